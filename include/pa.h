@@ -11,8 +11,11 @@
  *   pa_splitk_reduce       partition, then a log-sum-exp merge of partitions
  *   pa_decode_step         cache write + decode (+ merge) in one launch
  *   pa_copy_blocks         copy-on-write: copy shared blocks a branch writes into
- *   *_int8, *_fp8          the cache write and decode over an INT8 / FP8 KV cache
+ *   *_int8, *_fp8, *_int4  the cache write and decode over an INT8 / FP8 / 4-bit
+ *                          KV cache
+ *   pa_rope_reshape_and_cache*  rotary embedding of q and k and the cache write
  *   pa_prefill             causal attention of chunks of new tokens (prefill)
+ *   *_biased               decode and prefill with capped / biased / windowed scores
  *   pa_alloc_*             fixed-size block allocator with reference counts,
  *                          copy-on-write and automatic prefix caching (host
  *                          only, never on the GPU path)
@@ -100,7 +103,8 @@ typedef enum {
 #define PA_DEVERR_SLOT 0x4u         /* slot >= num_blocks * block_size */
 #define PA_DEVERR_WAIT_TIMEOUT 0x8u /* an asynchronous copy did not complete in time */
 #define PA_DEVERR_ORDER 0x10u       /* a work-order entry outside [0, num_seqs * max_partitions) */
-#define PA_DEVERR_PREFIX 0x20u      /* a sequence does not hold the shared prefix it was given */
+#define PA_DEVERR_PREFIX 0x20u      /* a sequence does not hold the prefix it was given */
+#define PA_DEVERR_POSITION 0x40u    /* a position outside the cosine / sine table */
 
 /* Static description of a status code; never NULL. */
 const char* pa_status_string(pa_status status);
@@ -267,6 +271,107 @@ pa_status pa_decode_splitk_fp8(float* ws_out, float* ws_m, float* ws_l,
                                int block_size, int num_blocks, float scale,
                                int partition_size, pa_stream_t stream);
 
+/*
+ * 4-bit KV cache (quantised KV at 4.5 bits a value).  Every (token, KV head)
+ * row is quantised in groups of 64 dims, each with an offset and a scale of
+ * its own, so a token is written once and never re-quantised:
+ *   lo = the group's least value (bf16, so exact),
+ *   scale = bf16((max - lo) / 15), round to nearest even (fp32 arithmetic; a
+ *           range past the largest float counts as that),
+ *   code = clamp(round_half_even((x - lo) / scale), 0, 15); 0 where scale is 0.
+ * The stored value is lo + scale * code, at most scale / 2 (and the rounding of
+ * scale, 15 * 2^-9 of it) from x.  Values must be finite (a NaN gets code 0).
+ * Pools (each one byte array, 16-byte aligned):
+ *   k_cache, v_cache : [num_blocks, num_kv_heads, 9 * head_dim] uint8, a tile of
+ *     8 * D bytes of codes and D bytes of parameters (D = head_dim).
+ * Parameters: 32-bit word t * (D / 64) + g holds token t's group g, lo in the
+ * low half, scale in the high half (bf16 bits).  Codes:
+ *   K: token t's row is the D / 2 bytes at t * D / 2; dim d is its nibble
+ *     (D / 4) * (e / 16) + e % 16 + 16 * (d / 64), e = d % 64 (nibble 2 i the
+ *     low, 2 i + 1 the high half of byte i).
+ *   V: dims 16 c + i (low nibble) and 16 c + i + 8 (high), i < 8, of token t are
+ *     the byte L * (D / 4) + 16 * u + 4 * (c % 4) + t / 8 + 2 * (t % 2) with
+ *     L = 4 * i + (t % 8) / 2 and u = (c / 4) XOR (i % 2) at D = 128, 0 at D = 64.
+ * (the places where the decode's tensor-core steps find them; two tokens share
+ * no byte).  Whole blocks can be copied with pa_copy_blocks, as bf16 pools of
+ * one head and one token: num_kv_heads 1, block_size 1, head_dim Hkv * 9 * D / 2.
+ * Decode keeps q unquantised (scaled by a power of two it is exact in f16) and
+ * takes QK and PV on the tensor cores over the codes, with fp32 accumulation;
+ * the softmax weights times a token's V scale enter PV as one f16 (11 bits).
+ * pa_reshape_and_cache_int4: head_dim 64 or 128, block_size 16; slots as
+ * pa_reshape_and_cache.  The decodes' shapes, checks and results otherwise as
+ * the bf16 calls'.
+ */
+pa_status pa_reshape_and_cache_int4(const void* key, const void* value, uint8_t* k_cache,
+                                    uint8_t* v_cache, const int64_t* slot_mapping,
+                                    int num_tokens, int num_kv_heads, int head_dim,
+                                    int block_size, int num_blocks, pa_stream_t stream);
+pa_status pa_decode_int4(void* out, const void* q, const uint8_t* k_cache,
+                         const uint8_t* v_cache, const int32_t* block_tables,
+                         int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                         int num_blocks, float scale, pa_stream_t stream);
+/* Split-K partition pass over a 4-bit cache; merge with pa_splitk_reduce. */
+pa_status pa_decode_splitk_int4(float* ws_out, float* ws_m, float* ws_l, int max_partitions,
+                                const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                float scale, int partition_size, pa_stream_t stream);
+
+/*
+ * Rotary position embedding of a step's new tokens and their cache write, one
+ * launch.  For token t at position p = positions[t] and every q and k head, the
+ * pair (a, b) of dims i < R / 2 (R = rotary_dim; a = x[i], b = x[i + R / 2], or
+ * with interleaved = 1 a = x[2 i], b = x[2 i + 1]) becomes
+ *   (a * c_i - b * s_i, b * c_i + a * s_i),  c_i = cos_sin[p, i],
+ *   s_i = cos_sin[p, R / 2 + i]
+ * in fp32 (products and sums rounded one by one), rounded to bf16 once; dims
+ * from R on pass through.  q goes to q_out; k goes, rotated, and v as it is, to
+ * the token's slot of the cache by the rule of the cache's kind: the bytes
+ * stored are those of pa_reshape_and_cache (_int8, _fp8, _int4) on the rotated
+ * k and v.
+ *   q, key, value : [num_tokens] rows of heads * head_dim bf16, stride elements
+ *     apart (a multiple of 8, at least the row): slices of one fused projection
+ *     need no copy.  q_out [num_tokens, num_q_heads, head_dim], contiguous; it
+ *     may be q itself (q_stride num_q_heads * head_dim), and overlaps no other
+ *     input.  num_q_heads 0: q and q_out are not read.
+ *   positions     : [num_tokens] int32.  Negative: a padding token, nothing of
+ *     it is read or written.  max_position or more: as padding, and sets
+ *     PA_DEVERR_POSITION.
+ *   cos_sin       : [max_position, rotary_dim] fp32, cosines then sines.
+ *   slot_mapping  : as pa_reshape_and_cache; a negative slot keeps k and v out
+ *     of the cache, q is rotated all the same.
+ * head_dim 64 or 128, rotary_dim a multiple of 16 up to head_dim, block_size 16
+ * for the quantised caches (else PA_ERR_UNSUPPORTED_SHAPE).
+ */
+pa_status pa_rope_reshape_and_cache(void* q_out, const void* q, int64_t q_stride,
+                                    const void* key, int64_t key_stride, const void* value,
+                                    int64_t value_stride, void* k_cache, void* v_cache,
+                                    const int64_t* slot_mapping, const int32_t* positions,
+                                    const float* cos_sin, int max_position, int rotary_dim,
+                                    int interleaved, int num_tokens, int num_q_heads,
+                                    int num_kv_heads, int head_dim, int block_size,
+                                    int num_blocks, pa_stream_t stream);
+pa_status pa_rope_reshape_and_cache_int8(
+    void* q_out, const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+    const void* value, int64_t value_stride, int8_t* k_cache, int8_t* v_cache, float* k_scales,
+    float* v_scales, const int64_t* slot_mapping, const int32_t* positions, const float* cos_sin,
+    int max_position, int rotary_dim, int interleaved, int num_tokens, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_stream_t stream);
+pa_status pa_rope_reshape_and_cache_fp8(
+    void* q_out, const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+    const void* value, int64_t value_stride, uint8_t* k_cache, uint8_t* v_cache, float* k_scales,
+    float* v_scales, const int64_t* slot_mapping, const int32_t* positions, const float* cos_sin,
+    int max_position, int rotary_dim, int interleaved, int num_tokens, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_stream_t stream);
+pa_status pa_rope_reshape_and_cache_int4(
+    void* q_out, const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+    const void* value, int64_t value_stride, uint8_t* k_cache, uint8_t* v_cache,
+    const int64_t* slot_mapping, const int32_t* positions, const float* cos_sin,
+    int max_position, int rotary_dim, int interleaved, int num_tokens, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_stream_t stream);
+
 /* Bytes of fp32 workspace pa_decode_splitk needs for contexts up to
  * max_context_len: ws_out [B, Hq, P, D] + ws_m [B, Hq, P] + ws_l [B, Hq, P]
  * with P = ceil(max_context_len / partition_size).  0 on invalid input. */
@@ -417,6 +522,41 @@ pa_status pa_decode_step_fp8(void* out, const void* q, const void* key, const vo
                              float* ws_m, float* ws_l, unsigned* counters, int max_partitions,
                              const int32_t* order, int flags, pa_stream_t stream);
 
+pa_status pa_decode_step_int4(void* out, const void* q, const void* key, const void* value,
+                              const int64_t* slot_mapping, uint8_t* k_cache, uint8_t* v_cache,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* context_lens, int num_seqs, int num_q_heads,
+                              int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                              float scale, int partition_size, float* ws_out, float* ws_m,
+                              float* ws_l, unsigned* counters, int max_partitions,
+                              const int32_t* order, int flags, pa_stream_t stream);
+
+/*
+ * The fused decode step with changed scores, over a bf16 cache: for the query
+ * at position p = context_lens[b] - 1 and the visible positions j <= p (with
+ * window > 0 only j > p - window),
+ *   x_j = scale * dot(q[b, h, :], K_j),
+ *   s_j = softcap * tanh(x_j / softcap) if softcap > 0, else x_j,
+ *   s_j -= alibi_slopes[h] * (p - j)    if alibi_slopes is not NULL,
+ * and the softmax and the mix of V are over s.  alibi_slopes: device fp32
+ * [num_q_heads] (or NULL); softcap 0: no cap; window 0: the whole context.
+ * Blocks that a window hides are not read, and their table entries may be
+ * stale.  The partitions of a split-K step then start at the first visible
+ * token's block: max_partitions needs to cover window + block_size - 1 tokens
+ * at most.  PA_ERR_INVALID_ARG for a negative or non-finite softcap, one so
+ * small that scale / softcap is not finite, or a negative window.  Everything
+ * else as pa_decode_step.
+ */
+pa_status pa_decode_step_biased(void* out, const void* q, const void* key, const void* value,
+                                const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                                const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                float scale, float softcap, const float* alibi_slopes, int window,
+                                int partition_size, float* ws_out, float* ws_m, float* ws_l,
+                                unsigned* counters, int max_partitions, const int32_t* order,
+                                int flags, pa_stream_t stream);
+
 /*
  * Fused decode step of a batch sharing a prefix [SH], [WALK] Step 8: every
  * sequence's first prefix_len tokens are the same blocks (block_tables[b][j]
@@ -498,6 +638,31 @@ pa_status pa_prefill(void* out, const void* q, const void* k_cache, const void* 
                      int num_blocks, float scale, pa_stream_t stream);
 
 /*
+ * Prefill with changed scores and masks.  The query at position p of sequence b
+ * sees the keys j with (j <= p or j < prefix_lens[b]) and, with window > 0,
+ * j > p - window; its scores are
+ *   s_j = softcap * tanh(x_j / softcap) - alibi_slopes[h] * |p - j|,
+ *   x_j = scale * dot(q_p, K_j)
+ * (softcap 0: x_j itself; alibi_slopes NULL: no second term).  prefix_lens:
+ * device int32 [num_seqs] (or NULL), leading positions that every query of the
+ * sequence sees (a bidirectional prefix; their K and V are in the cache before
+ * the call).  A prefix outside [0, context_lens[b]] sets PA_DEVERR_PREFIX and
+ * the sequence is skipped.  Blocks that a window hides from all queries of a
+ * tile of 128 / (Hq / Hkv) tokens are not read, and their table entries may be
+ * stale.  V of a position that any query of such a tile sees must be finite:
+ * a NaN or infinity there reaches the tile's other queries too.  Refusals as
+ * pa_decode_step_biased's; everything else as pa_prefill.
+ */
+pa_status pa_prefill_biased(void* out, const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_tables, int max_blocks_per_seq,
+                            const int32_t* context_lens, const int32_t* query_start_loc,
+                            int max_query_len, int num_seqs, int total_query_tokens,
+                            int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                            int num_blocks, float scale, float softcap,
+                            const float* alibi_slopes, int window, const int32_t* prefix_lens,
+                            pa_stream_t stream);
+
+/*
  * Split-K partition size for a decode batch (host): the size, from {256, 384,
  * 512, 640, 768, 1024, 1280, 1536, 1792, 2048, 4096} tokens, that minimises a
  * model of the split-K launch's time -- its CTAs handed in grid order to the first free
@@ -506,7 +671,7 @@ pa_status pa_prefill(void* out, const void* q, const void* k_cache, const void* 
  * share -- with ties going to the larger size; in grid order a 1-byte cache
  * (issue-bound kernels) whose batch has fewer (sequence, KV head) units than
  * CTA slots takes 512.  context_lens: host int32
- * [num_seqs]; kv_kind 0 = bf16 cache, 1 = INT8, 2 = FP8; num_sms the device's
+ * [num_seqs]; kv_kind 0 = bf16 cache, 1 = INT8, 2 = FP8, 4 = 4-bit; num_sms the device's
  * multiprocessor count; ordered != 0 models the launch with the
  * longest-first order of pa_splitk_order, 0 the plain grid order.  Returns 0
  * on invalid arguments.  The result is a

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
 #include <string>
 
 #include "../../include/pa.h"
@@ -36,6 +37,15 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool ok_ptr(const void* p, uintptr_t align) { return p != nullptr && aligned(p, align); }
 
 }  // namespace
+
+bool score_rule_ok(const ScoreRule& r, float scale) {
+  // a cap of 0 is none; one so small that scale / cap overflows bounds nothing
+  if (!(r.softcap >= 0.f) || !std::isfinite(r.softcap * 1.4426950408889634f) || r.window < 0)
+    return false;
+  if (r.softcap > 0.f && (!std::isfinite(scale / r.softcap) || !std::isfinite(1.f / r.softcap)))
+    return false;
+  return aligned(r.slopes, 4);
+}
 
 unsigned* device_error_word() {
   int dev = 0;
@@ -473,7 +483,8 @@ pa_status pa_decode_splitk_fp8(float* ws_out, float* ws_m, float* ws_l, int max_
 namespace {
 
 // pa_decode_step*: the cache write of each sequence's new token and its
-// attention in one launch (kv: 0 bf16, 1 INT8, 2 FP8).
+// attention in one launch (kv: 0 bf16, 1 INT8, 2 FP8, 3 4-bit; rule: the
+// scores are changed, bf16 only).
 pa_status decode_step_impl(void* out, const void* q, const void* key, const void* value,
                            const int64_t* slot_mapping, void* k_cache, void* v_cache,
                            float* k_scales, float* v_scales, const int32_t* block_tables,
@@ -481,7 +492,9 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
                            int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                            int num_blocks, float scale, int partition_size, float* ws_out,
                            float* ws_m, float* ws_l, unsigned* counters, int max_partitions,
-                           const int32_t* order, int flags, int kv, pa_stream_t stream) {
+                           const int32_t* order, int flags, int kv, pa_stream_t stream,
+                           const ScoreRule* rule = nullptr) {
+  if (rule && !score_rule_ok(*rule, scale)) return PA_ERR_INVALID_ARG;
   pa_status s = check_decode_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                                   context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim,
                                   block_size, num_blocks, scale);
@@ -498,7 +511,7 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
   if (split && (!ok_ptr(ws_out, 16) || !ok_ptr(ws_m, 4) || !ok_ptr(ws_l, 4) ||
                 !ok_ptr(counters, 4)))
     return PA_ERR_INVALID_ARG;
-  if (kv != 0 && (!ok_ptr(k_scales, 16) || !ok_ptr(v_scales, 16))) return PA_ERR_INVALID_ARG;
+  if ((kv == 1 || kv == 2) && (!ok_ptr(k_scales, 16) || !ok_ptr(v_scales, 16))) return PA_ERR_INVALID_ARG;
   if ((flags & ~PA_STEP_EARLY_READ) != 0) return PA_ERR_INVALID_ARG;
   if (order != nullptr) {
     if (!split || !ok_ptr(order, 4)) return PA_ERR_INVALID_ARG;
@@ -508,7 +521,10 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
   DecodeParams p = make_decode_params(q, kv ? nullptr : k_cache, kv ? nullptr : v_cache,
                                       block_tables, max_blocks_per_seq, context_lens, num_seqs,
                                       num_q_heads, num_kv_heads, num_blocks, scale);
-  if (kv != 0) {
+  if (kv == 3) {
+    p.k4 = static_cast<const uint8_t*>(k_cache);
+    p.v4 = static_cast<const uint8_t*>(v_cache);
+  } else if (kv != 0) {
     p.k8 = static_cast<const int8_t*>(k_cache);
     p.v8 = static_cast<const int8_t*>(v_cache);
     p.k_scales = k_scales;
@@ -543,7 +559,11 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
   p.err = device_error_word();
   if (!p.err) return cuda_fail(cudaGetLastError());
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_decode(p, head_dim, num_q_heads / num_kv_heads, split, st);
+  const int group = num_q_heads / num_kv_heads;
+  if (rule) p.rule = *rule;
+  cudaError_t e = kv == 3 ? launch_decode_int4(p, head_dim, group, split, st)
+                  : rule  ? launch_decode_biased(p, head_dim, group, split, st)
+                          : launch_decode(p, head_dim, group, split, st);
   if (e == cudaSuccess && merge_apart) {
     ReduceParams r{};
     r.out = p.out;
@@ -556,6 +576,7 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
     r.num_q_heads = num_q_heads;
     r.max_partitions = max_partitions;
     r.partition_size = partition_size;
+    r.window = rule ? rule->window : 0;
     e = launch_splitk_reduce(r, head_dim, st);
   }
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
@@ -678,6 +699,236 @@ pa_status pa_decode_step_fp8(void* out, const void* q, const void* key, const vo
                           block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
                           num_kv_heads, head_dim, block_size, num_blocks, scale, partition_size,
                           ws_out, ws_m, ws_l, counters, max_partitions, order, flags, 2, stream);
+}
+
+pa_status pa_decode_step_biased(void* out, const void* q, const void* key, const void* value,
+                                const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                                const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                float scale, float softcap, const float* alibi_slopes, int window,
+                                int partition_size, float* ws_out, float* ws_m, float* ws_l,
+                                unsigned* counters, int max_partitions, const int32_t* order,
+                                int flags, pa_stream_t stream) {
+  const ScoreRule rule{alibi_slopes, softcap, window};
+  return decode_step_impl(out, q, key, value, slot_mapping, k_cache, v_cache, nullptr, nullptr,
+                          block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                          num_kv_heads, head_dim, block_size, num_blocks, scale, partition_size,
+                          ws_out, ws_m, ws_l, counters, max_partitions, order, flags, 0, stream,
+                          &rule);
+}
+
+pa_status pa_decode_step_int4(void* out, const void* q, const void* key, const void* value,
+                              const int64_t* slot_mapping, uint8_t* k_cache, uint8_t* v_cache,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* context_lens, int num_seqs, int num_q_heads,
+                              int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                              float scale, int partition_size, float* ws_out, float* ws_m,
+                              float* ws_l, unsigned* counters, int max_partitions,
+                              const int32_t* order, int flags, pa_stream_t stream) {
+  return decode_step_impl(out, q, key, value, slot_mapping, k_cache, v_cache, nullptr, nullptr,
+                          block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                          num_kv_heads, head_dim, block_size, num_blocks, scale, partition_size,
+                          ws_out, ws_m, ws_l, counters, max_partitions, order, flags, 3, stream);
+}
+
+pa_status pa_decode_int4(void* out, const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                         const int32_t* block_tables, int max_blocks_per_seq,
+                         const int32_t* context_lens, int num_seqs, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                         float scale, pa_stream_t stream) {
+  return decode_step_impl(out, q, nullptr, nullptr, nullptr, const_cast<uint8_t*>(k_cache),
+                          const_cast<uint8_t*>(v_cache), nullptr, nullptr, block_tables,
+                          max_blocks_per_seq, context_lens, num_seqs, num_q_heads, num_kv_heads,
+                          head_dim, block_size, num_blocks, scale, 0, nullptr, nullptr, nullptr,
+                          nullptr, 0, nullptr, 0, 3, stream);
+}
+
+pa_status pa_decode_splitk_int4(float* ws_out, float* ws_m, float* ws_l, int max_partitions,
+                                const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                float scale, int partition_size, pa_stream_t stream) {
+  pa_status s = check_decode_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                                  context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                  block_size, num_blocks, scale);
+  if (s != PA_OK) return s;
+  if (max_partitions <= 0 || max_partitions > 65535 || partition_size <= 0 ||
+      partition_size % block_size != 0)
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  if (!ok_ptr(ws_out, 16) || !ok_ptr(ws_m, 4) || !ok_ptr(ws_l, 4)) return PA_ERR_INVALID_ARG;
+  DecodeParams p = make_decode_params(q, nullptr, nullptr, block_tables, max_blocks_per_seq,
+                                      context_lens, num_seqs, num_q_heads, num_kv_heads,
+                                      num_blocks, scale);
+  p.k4 = k_cache;
+  p.v4 = v_cache;
+  p.ws_o = ws_out;
+  p.ws_m = ws_m;
+  p.ws_l = ws_l;
+  p.max_partitions = max_partitions;
+  p.partition_blocks = partition_size / block_size;
+  p.err = device_error_word();
+  if (!p.err) return cuda_fail(cudaGetLastError());
+  cudaError_t e = launch_decode_int4(p, head_dim, num_q_heads / num_kv_heads, true,
+                                     reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // extern "C"
+
+namespace {
+
+// pa_rope_reshape_and_cache* and pa_reshape_and_cache_int4 (no q, no
+// rotation: positions null).  kind: 0 bf16, 1 INT8, 2 FP8, 3 4-bit.
+pa_status rope_append_impl(void* q_out, const void* q, int64_t q_stride, const void* key,
+                           int64_t key_stride, const void* value, int64_t value_stride,
+                           void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                           const int64_t* slot_mapping, const int32_t* positions,
+                           const float* cos_sin, int max_position, int rotary_dim,
+                           int interleaved, int num_tokens, int num_q_heads, int num_kv_heads,
+                           int head_dim, int block_size, int num_blocks, int kind, bool rope,
+                           pa_stream_t stream) {
+  if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      block_size <= 0 || num_blocks <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED_SHAPE;
+  if (kind != 0 && block_size != 16) return PA_ERR_UNSUPPORTED_SHAPE;
+  if (rope) {
+    if (max_position <= 0 || rotary_dim <= 0 || rotary_dim > head_dim ||
+        (interleaved != 0 && interleaved != 1))
+      return PA_ERR_INVALID_ARG;
+    if (rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED_SHAPE;
+  }
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * head_dim;
+  const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (num_q_heads > 0 && (q_stride < q_row || q_stride % 8 != 0)) return PA_ERR_INVALID_ARG;
+  if (key_stride < kv_row || key_stride % 8 != 0 || value_stride < kv_row ||
+      value_stride % 8 != 0)
+    return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  if (num_q_heads > 0 && (!ok_ptr(q, 16) || !ok_ptr(q_out, 16))) return PA_ERR_INVALID_ARG;
+  if (!ok_ptr(key, 16) || !ok_ptr(value, 16) || !ok_ptr(k_cache, 16) || !ok_ptr(v_cache, 16) ||
+      !ok_ptr(slot_mapping, 8))
+    return PA_ERR_INVALID_ARG;
+  if (rope && (!ok_ptr(positions, 4) || !ok_ptr(cos_sin, 16))) return PA_ERR_INVALID_ARG;
+  if ((kind == 1 || kind == 2) && (!ok_ptr(k_scales, 16) || !ok_ptr(v_scales, 16)))
+    return PA_ERR_INVALID_ARG;
+  if (num_q_heads > 0) {
+    // q may be rotated in place (each value is read by the thread that writes
+    // it); any other overlap of q_out with an input would be a race
+    auto overlap = [&](const void* in, int64_t stride, int64_t row) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(q_out);
+      const uintptr_t a1 = a + static_cast<uintptr_t>(num_tokens) * q_row * 2;
+      const uintptr_t c = reinterpret_cast<uintptr_t>(in);
+      const uintptr_t c1 = c + (static_cast<uintptr_t>(num_tokens - 1) * stride + row) * 2;
+      return a < c1 && c < a1;
+    };
+    if (q_out == q ? q_stride != q_row : overlap(q, q_stride, q_row)) return PA_ERR_INVALID_ARG;
+    if (overlap(key, key_stride, kv_row) || overlap(value, value_stride, kv_row))
+      return PA_ERR_INVALID_ARG;
+  }
+  RopeAppendParams p{};
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.key = static_cast<const __nv_bfloat16*>(key);
+  p.value = static_cast<const __nv_bfloat16*>(value);
+  p.q_stride = q_stride;
+  p.key_stride = key_stride;
+  p.value_stride = value_stride;
+  p.kind = kind;
+  if (kind == 0) {
+    p.k_cache = static_cast<__nv_bfloat16*>(k_cache);
+    p.v_cache = static_cast<__nv_bfloat16*>(v_cache);
+  } else if (kind == 3) {
+    p.k4 = static_cast<uint8_t*>(k_cache);
+    p.v4 = static_cast<uint8_t*>(v_cache);
+  } else {
+    p.k8 = static_cast<int8_t*>(k_cache);
+    p.v8 = static_cast<int8_t*>(v_cache);
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+  }
+  p.slot_mapping = slot_mapping;
+  p.positions = rope ? positions : nullptr;
+  p.cos_sin = rope ? cos_sin : nullptr;
+  p.max_position = rope ? max_position : 1;
+  p.rotary_dim = rope ? rotary_dim : 0;
+  p.interleaved = interleaved;
+  p.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.block_size = block_size;
+  p.err = device_error_word();
+  if (!p.err) return cuda_fail(cudaGetLastError());
+  cudaError_t e = launch_rope_append(p, head_dim, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_reshape_and_cache_int4(const void* key, const void* value, uint8_t* k_cache,
+                                    uint8_t* v_cache, const int64_t* slot_mapping,
+                                    int num_tokens, int num_kv_heads, int head_dim,
+                                    int block_size, int num_blocks, pa_stream_t stream) {
+  const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  return rope_append_impl(nullptr, nullptr, 0, key, row, value, row, k_cache, v_cache, nullptr,
+                          nullptr, slot_mapping, nullptr, nullptr, 0, 0, 0, num_tokens, 0,
+                          num_kv_heads, head_dim, block_size, num_blocks, 3, false, stream);
+}
+
+pa_status pa_rope_reshape_and_cache(void* q_out, const void* q, int64_t q_stride, const void* key,
+                                    int64_t key_stride, const void* value, int64_t value_stride,
+                                    void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                                    const int32_t* positions, const float* cos_sin,
+                                    int max_position, int rotary_dim, int interleaved,
+                                    int num_tokens, int num_q_heads, int num_kv_heads,
+                                    int head_dim, int block_size, int num_blocks,
+                                    pa_stream_t stream) {
+  return rope_append_impl(q_out, q, q_stride, key, key_stride, value, value_stride, k_cache,
+                          v_cache, nullptr, nullptr, slot_mapping, positions, cos_sin,
+                          max_position, rotary_dim, interleaved, num_tokens, num_q_heads,
+                          num_kv_heads, head_dim, block_size, num_blocks, 0, true, stream);
+}
+
+pa_status pa_rope_reshape_and_cache_int8(
+    void* q_out, const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+    const void* value, int64_t value_stride, int8_t* k_cache, int8_t* v_cache, float* k_scales,
+    float* v_scales, const int64_t* slot_mapping, const int32_t* positions, const float* cos_sin,
+    int max_position, int rotary_dim, int interleaved, int num_tokens, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_stream_t stream) {
+  return rope_append_impl(q_out, q, q_stride, key, key_stride, value, value_stride, k_cache,
+                          v_cache, k_scales, v_scales, slot_mapping, positions, cos_sin,
+                          max_position, rotary_dim, interleaved, num_tokens, num_q_heads,
+                          num_kv_heads, head_dim, block_size, num_blocks, 1, true, stream);
+}
+
+pa_status pa_rope_reshape_and_cache_fp8(
+    void* q_out, const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+    const void* value, int64_t value_stride, uint8_t* k_cache, uint8_t* v_cache, float* k_scales,
+    float* v_scales, const int64_t* slot_mapping, const int32_t* positions, const float* cos_sin,
+    int max_position, int rotary_dim, int interleaved, int num_tokens, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_stream_t stream) {
+  return rope_append_impl(q_out, q, q_stride, key, key_stride, value, value_stride, k_cache,
+                          v_cache, k_scales, v_scales, slot_mapping, positions, cos_sin,
+                          max_position, rotary_dim, interleaved, num_tokens, num_q_heads,
+                          num_kv_heads, head_dim, block_size, num_blocks, 2, true, stream);
+}
+
+pa_status pa_rope_reshape_and_cache_int4(
+    void* q_out, const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+    const void* value, int64_t value_stride, uint8_t* k_cache, uint8_t* v_cache,
+    const int64_t* slot_mapping, const int32_t* positions, const float* cos_sin,
+    int max_position, int rotary_dim, int interleaved, int num_tokens, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_stream_t stream) {
+  return rope_append_impl(q_out, q, q_stride, key, key_stride, value, value_stride, k_cache,
+                          v_cache, nullptr, nullptr, slot_mapping, positions, cos_sin,
+                          max_position, rotary_dim, interleaved, num_tokens, num_q_heads,
+                          num_kv_heads, head_dim, block_size, num_blocks, 3, true, stream);
 }
 
 }  // extern "C"

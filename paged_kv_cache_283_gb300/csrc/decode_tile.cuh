@@ -11,10 +11,26 @@
 #include <stdint.h>
 
 #include "device.cuh"
+#include "int4_row.cuh"
 
 namespace pa {
 
 constexpr int kBlockSize = 16;
+
+// How a launch changes its scores (base-2 units, one lane's head): capped by
+// cap2 * tanh(s / cap2) when cap2 > 0, then lowered by slope2 per token of
+// distance from the query.  Tokens before `first` are hidden.
+struct RuleLane {
+  float cap2 = 0.f, inv_cap2 = 0.f, slope2 = 0.f;
+  int last = 0;   // the query's position
+  int first = 0;  // the first visible position
+
+  // the score of the token at position j
+  __device__ __forceinline__ float operator()(float s, int j) const {
+    if (cap2 > 0.f) s = cap2 * tanhf(s * inv_cap2);
+    return fmaf(slope2, static_cast<float>(j - last), s);
+  }
+};
 
 template <int D, int G>
 struct Geometry {
@@ -30,13 +46,16 @@ struct Geometry {
   static_assert(NV % L == 0 && R >= 1 && P % R == 0, "score geometry");
 };
 
-// One K/V tile through QK, the online softmax update and PV.
-template <int D, int G, bool FULL>
+// One K/V tile through QK, the online softmax update and PV.  RULE: scores go
+// through `rule` (j0: the position of the tile's first token), and tokens
+// before rule.first are masked as those from nvalid on are.
+template <int D, int G, bool FULL, bool RULE = false>
 __device__ __forceinline__ void tile_step(const uint4* __restrict__ kt, const uint4* __restrict__ vt,
                                           float* ps, float* alpha_s, const float2 (&q2)[G][4],
                                           float2 (&acc)[G][4], float& m_run, float& l_run,
                                           int nvalid, int lane, int sub, int rg, int my_head,
-                                          int my_i0) {
+                                          int my_i0, const RuleLane& rule = RuleLane(),
+                                          int j0 = 0) {
   using Geo = Geometry<D, G>;
   constexpr int L = Geo::L, ROWS = Geo::ROWS, P = Geo::P, NV = Geo::NV, R = Geo::R;
 
@@ -79,7 +98,8 @@ __device__ __forceinline__ void tile_step(const uint4* __restrict__ kt, const ui
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int t = (my_i0 + r) * ROWS + rg;
-    s[r] = (FULL || t < nvalid) ? sc[r] : -INFINITY;
+    if constexpr (RULE) sc[r] = rule(sc[r], j0 + t);
+    s[r] = (FULL || (t < nvalid && (!RULE || j0 + t >= rule.first))) ? sc[r] : -INFINITY;
     mx = fmaxf(mx, s[r]);
   }
 #pragma unroll
@@ -115,7 +135,7 @@ __device__ __forceinline__ void tile_step(const uint4* __restrict__ kt, const ui
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int t = i * ROWS + rg;
-    if (FULL || t < nvalid) {
+    if (FULL || (t < nvalid && (!RULE || j0 + t >= rule.first))) {
       const uint4 w = vt[t * L + sub];
       const float2 v0 = bf16x2_to_float2(w.x), v1 = bf16x2_to_float2(w.y);
       const float2 v2 = bf16x2_to_float2(w.z), v3 = bf16x2_to_float2(w.w);
@@ -513,6 +533,191 @@ __device__ __forceinline__ void tile_step_1b(const unsigned char* __restrict__ k
     }
     mma_f16(acc[c], a0, a1, a2, a3, b0, b1);
     if constexpr (!C::PACKED) mma_f16(acc[c], a0, a1, a2, a3, l01, l23);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 4-bit KV cache (int4_row.cuh): value = lo + sc * code per token and group of
+// 64 dims, code 0..15.
+//
+// QK as the 1-byte step's, transposed: rows = the group's query heads, columns
+// = 8 tokens, and the codes enter the f16 MMAs as subnormals.  A mask leaves
+// two codes in a register as f16 subnormals: nibbles at bits 0 and 16 stand for
+// code * 2^-24, nibbles at bits 4 and 20 for code * 2^-20, so the second kind's
+// q carries a factor 2^-4 (exact) and one shift serves eight codes.  With sums
+// c_g of q . code over group g and qs_g = the sum of q over it,
+//   s = sum_g sc_g c_g + lo_g qs_g.
+// Group 0 uses the MMA's rows 0..7 and group 1 rows 8..15, so one accumulator
+// holds both.  PV: out^T = V^T . W with W's column = head, the weights of group
+// g being p * sc_g (one f16 each: 11 bits, so an output's error is about 2^-12
+// of its size, against the 2^-9 of its bf16 rounding), and the offsets' share,
+// sum p * lo_g, summed in fp32 beside it.  V nibbles of dims 16 c + gid are
+// scaled 2^-24 and those of dims 16 c + gid + 8 2^-20, undone once at the end.
+
+// The lane's words of q (qa), the head's group sums (qs, times the score
+// scale) and the factor of the MMA sums (qf).
+template <int D, int G, int NB, bool FULL, bool RULE>
+__device__ __forceinline__ void tile_step_4b(const unsigned char* __restrict__ stage,
+                                             const uint32_t (&qa)[D / 8], float qf,
+                                             const float (&qs)[D / kInt4Group],
+                                             float (&acc)[D / 16][4], float& m_run,
+                                             float& l_run, float (&zacc)[D / kInt4Group],
+                                             float& vbound, float& vinv, int nvalid, int lane,
+                                             const RuleLane& rule, int j0) {
+  constexpr int KT = int4_tile_bytes(D), NG = D / kInt4Group;
+  const int gid = lane >> 2, tig = lane & 3;
+  float s[NB][4];
+#pragma unroll
+  for (int u = 0; u < NB; ++u) {
+    const unsigned char* kt = stage + u * 2 * KT;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // tokens 8 h .. 8 h + 7
+      uint32_t k[D / 32];
+      const unsigned char* row = kt + (8 * h + gid) * (D / 2) + (D / 8) * tig;
+      if constexpr (D == 128) {
+        const uint4 x = *reinterpret_cast<const uint4*>(row);
+        k[0] = x.x; k[1] = x.y; k[2] = x.z; k[3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(row);
+        k[0] = x.x; k[1] = x.y;
+      }
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        const uint32_t x = k[w], y = k[w] >> 8;
+        if (w < 2) {
+          mma_f16(c, qa[4 * w], 0u, qa[4 * w + 1], 0u, x & 0x000F000Fu, x & 0x00F000F0u);
+          mma_f16(c, qa[4 * w + 2], 0u, qa[4 * w + 3], 0u, y & 0x000F000Fu, y & 0x00F000F0u);
+        } else {
+          mma_f16(c, 0u, qa[4 * w], 0u, qa[4 * w + 1], x & 0x000F000Fu, x & 0x00F000F0u);
+          mma_f16(c, 0u, qa[4 * w + 2], 0u, qa[4 * w + 3], y & 0x000F000Fu, y & 0x00F000F0u);
+        }
+      }
+      // tokens 8 h + 2 tig, + 1: their parameter words
+      const unsigned char* par = kt + 8 * D + (8 * h + 2 * tig) * NG * 4;
+      uint32_t w0[NG], w1[NG];
+      if constexpr (NG == 2) {
+        const uint4 x = *reinterpret_cast<const uint4*>(par);
+        w0[0] = x.x; w0[1] = x.y; w1[0] = x.z; w1[1] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(par);
+        w0[0] = x.x; w1[0] = x.y;
+      }
+      float d0 = 0.f, d1 = 0.f, z0 = 0.f, z1 = 0.f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        d0 = fmaf(__uint_as_float(w0[g] & 0xffff0000u), c[2 * g], d0);
+        d1 = fmaf(__uint_as_float(w1[g] & 0xffff0000u), c[2 * g + 1], d1);
+        z0 = fmaf(__uint_as_float(w0[g] << 16), qs[g], z0);
+        z1 = fmaf(__uint_as_float(w1[g] << 16), qs[g], z1);
+      }
+      float s0 = fmaf(d0, qf, z0), s1 = fmaf(d1, qf, z1);
+      const int t = 16 * u + 8 * h + 2 * tig;
+      if constexpr (RULE) {
+        s0 = rule(s0, j0 + t);
+        s1 = rule(s1, j0 + t + 1);
+      }
+      if constexpr (!FULL) {
+        if (!(t < nvalid && (!RULE || j0 + t >= rule.first))) s0 = -INFINITY;
+        if (!(t + 1 < nvalid && (!RULE || j0 + t + 1 >= rule.first))) s1 = -INFINITY;
+      }
+      s[u][2 * h] = s0;
+      s[u][2 * h + 1] = s1;
+    }
+  }
+  // the step's maximum for head(gid): over the lane's tokens, then the row's
+  // four lanes (the rows of one head, G <= 4, hold the same scores)
+  float mx = s[0][0];
+#pragma unroll
+  for (int u = 0; u < NB; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[u][i]);
+  mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
+  const float m_new = lazy_max(m_run, mx);
+  const float alpha = ex2_fast(m_run - m_new);
+  float psum = 0.f;
+#pragma unroll
+  for (int u = 0; u < NB; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[u][i] = ex2_fast(s[u][i] - m_new);
+      psum += s[u][i];
+    }
+  l_run = fmaf(l_run, alpha, psum);
+  m_run = m_new;
+
+  // V parameters of the lane's tokens: [u][h] tokens 8 h + 2 tig, + 1
+  uint32_t vw[NB][2][2][NG];
+  float vm = 0.f;
+#pragma unroll
+  for (int u = 0; u < NB; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const unsigned char* par =
+          stage + u * 2 * KT + KT + 8 * D + (8 * h + 2 * tig) * NG * 4;
+      if constexpr (NG == 2) {
+        const uint4 x = *reinterpret_cast<const uint4*>(par);
+        vw[u][h][0][0] = x.x; vw[u][h][0][1] = x.y;
+        vw[u][h][1][0] = x.z; vw[u][h][1][1] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(par);
+        vw[u][h][0][0] = x.x; vw[u][h][1][0] = x.y;
+      }
+      const int t = 16 * u + 8 * h + 2 * tig;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          if constexpr (!FULL) {  // a hidden token's parameters may be anything
+            if (!(t + e < nvalid && (!RULE || j0 + t + e >= rule.first))) vw[u][h][e][g] = 0u;
+          }
+          vm = fmaxf(vm, __uint_as_float(vw[u][h][e][g] & 0xffff0000u));
+        }
+    }
+  float r = 1.f;
+  if (__any_sync(kFullMask, vm > vbound)) {
+    vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 1));
+    vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 2));
+    r = raise_v_bound(vm, vbound, vinv);
+  }
+  if (__any_sync(kFullMask, alpha != 1.0f) || r != 1.0f) {
+    const float fa = __shfl_sync(kFullMask, alpha, 8 * tig) * r;
+    const float fb = __shfl_sync(kFullMask, alpha, 8 * tig + 4) * r;
+    scale_acc<D>(acc, fa, fb);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) zacc[g] *= alpha;
+  }
+  uint32_t b[NB][2][NG];
+#pragma unroll
+  for (int u = 0; u < NB; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float p0 = s[u][2 * h], p1 = s[u][2 * h + 1];
+      const float y0 = p0 * vinv, y1 = p1 * vinv;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        b[u][h][g] = f16x2_rn(y0 * __uint_as_float(vw[u][h][0][g] & 0xffff0000u),
+                              y1 * __uint_as_float(vw[u][h][1][g] & 0xffff0000u));
+        zacc[g] = fmaf(p0, __uint_as_float(vw[u][h][0][g] << 16), zacc[g]);
+        zacc[g] = fmaf(p1, __uint_as_float(vw[u][h][1][g] << 16), zacc[g]);
+      }
+    }
+#pragma unroll
+  for (int u = 0; u < NB; ++u) {
+    const unsigned char* base = stage + u * 2 * KT + KT + lane * (D / 4);
+#pragma unroll
+    for (int v = 0; v < D / 64; ++v) {
+      const uint4 x = *reinterpret_cast<const uint4*>(
+          base + 16 * (D == 128 ? (v ^ (gid & 1)) : 0));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t y = w[k] >> 8;
+        mma_f16(acc[4 * v + k], w[k] & 0x000F000Fu, w[k] & 0x00F000F0u, y & 0x000F000Fu,
+                y & 0x00F000F0u, b[u][0][v], b[u][1][v]);
+      }
+    }
   }
 }
 

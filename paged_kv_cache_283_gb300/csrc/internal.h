@@ -10,6 +10,18 @@
 
 namespace pa {
 
+// Changed scores (biased decode and prefill): s = softcap * tanh(scale q.k /
+// softcap) (softcap > 0), minus slopes[h] * distance (slopes non-null), over
+// the last `window` positions (window > 0).
+struct ScoreRule {
+  const float* slopes;  // [Hq] fp32
+  float softcap;
+  int window;
+};
+
+// Whether a rule's values make sense beside the score scale (api.cu).
+bool score_rule_ok(const ScoreRule& r, float scale);
+
 // Arguments of the decode kernels (plain and split-K).  Pointers are device
 // pointers, already validated on the host.
 struct DecodeParams {
@@ -22,6 +34,8 @@ struct DecodeParams {
   const __nv_bfloat16* v_cache;
   const int8_t* k8;        // int8 cache: codes [NB, Hkv, bs, D] (null for a bf16 cache)
   const int8_t* v8;
+  const uint8_t* k4;       // 4-bit cache: tiles of codes and parameters (int4_row.cuh)
+  const uint8_t* v4;
   const float* k_scales;   // int8 / fp8 cache: one scale per (block, head, token)
   const float* v_scales;
   int fp8;                 // 1-byte cache: codes are FP8 (E4M3), not INT8
@@ -55,6 +69,7 @@ struct DecodeParams {
   // partition_blocks blocks each from block prefix_blocks on.
   int first_partition;
   int prefix_blocks;
+  ScoreRule rule;        // RULE kernels only
 };
 
 struct ReduceParams {
@@ -68,6 +83,7 @@ struct ReduceParams {
   int num_q_heads;
   int max_partitions;
   int partition_size;
+  int window;            // > 0: the partitions cover the blocks of the last `window` tokens
 };
 
 struct CacheWriteParams {
@@ -89,6 +105,38 @@ struct CacheWriteParams {
   int fp8;            // codes are FP8 (E4M3), not INT8
 };
 
+// Rotary embedding + cache write (rope_append.cu).  Also the plain 4-bit
+// cache write: no q, rotary_dim 0, positions and cos_sin null.
+struct RopeAppendParams {
+  __nv_bfloat16* q_out;           // [T, Hq, D]
+  const __nv_bfloat16* q;         // [T] rows of Hq * D at q_stride
+  const __nv_bfloat16* key;       // [T] rows of Hkv * D at key_stride
+  const __nv_bfloat16* value;
+  int64_t q_stride, key_stride, value_stride;  // elements from token to token
+  __nv_bfloat16* k_cache;         // kind 0: bf16 pools
+  __nv_bfloat16* v_cache;
+  int8_t* k8;                     // kinds 1 (INT8), 2 (FP8): codes and scales
+  int8_t* v8;
+  float* k_scales;
+  float* v_scales;
+  uint8_t* k4;                    // kind 3: 4-bit tiles (int4_row.cuh)
+  uint8_t* v4;
+  const int64_t* slot_mapping;
+  const int32_t* positions;
+  const float* cos_sin;           // [max_position, R]: R / 2 cosines, R / 2 sines
+  unsigned* err;
+  int64_t num_slots;
+  int kind;
+  int max_position;
+  int rotary_dim;
+  int interleaved;
+  int num_tokens;
+  int num_q_heads;
+  int num_kv_heads;
+  int block_size;
+  int row_slots;                  // thread groups per token (set by the launcher)
+};
+
 // Pools of up to kCopyMaxLayers layers go to one copy_blocks launch.
 constexpr int kCopyMaxLayers = 64;
 
@@ -106,6 +154,11 @@ bool decode_shape_supported(int head_dim, int group, int block_size);
 
 cudaError_t launch_decode(const DecodeParams& p, int head_dim, int group, bool split,
                           cudaStream_t stream);
+// The same over a 4-bit cache, and over a bf16 cache with changed scores.
+cudaError_t launch_decode_int4(const DecodeParams& p, int head_dim, int group, bool split,
+                               cudaStream_t stream);
+cudaError_t launch_decode_biased(const DecodeParams& p, int head_dim, int group, bool split,
+                                 cudaStream_t stream);
 cudaError_t launch_splitk_reduce(const ReduceParams& p, int head_dim, cudaStream_t stream);
 // prefill.cu: the split-K partials of a decode batch's queries over a shared
 // prefix, partitions [0, splits) of split_blocks blocks each (head_dim 128);
@@ -120,6 +173,7 @@ cudaError_t launch_prefix_partials(const void* q, const void* k_cache, const voi
                                    cudaStream_t stream);
 cudaError_t launch_reshape_and_cache(const CacheWriteParams& p, cudaStream_t stream);
 cudaError_t launch_reshape_and_cache_int8(const CacheWriteParams& p, cudaStream_t stream);
+cudaError_t launch_rope_append(RopeAppendParams p, int head_dim, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const CopyBlocksParams& p, int num_pairs, int num_layers,
                                cudaStream_t stream);
 

@@ -128,6 +128,12 @@ struct PrefillParams {
   float* ws_m;
   float* ws_l;
   int max_partitions;
+  // Changed scores (RULE kernels): the rule, and per sequence how many leading
+  // positions every query of it sees (null: none).
+  ScoreRule rule;
+  const int32_t* prefix_lens;
+  float unit;    // base-2 units of a score as the softmax reads it
+  float cap_in;  // scale / softcap: the argument of the tanh per unit of q . k
 };
 
 // ---- tcgen05 / TMA wrappers -------------------------------------------------
@@ -253,6 +259,49 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// tanh of HK values times `k`, in place, to about 2e-7 of 1.  Where the warp's
+// values all stay within 0.3 -- caps lie well above the scores they bound -- an
+// odd polynomial (the first five terms of the series; the next is below 6e-8 of
+// the result there) in packed fused multiply-adds: 3.5 issue slots a score and
+// a maximum's half.  Elsewhere 1 - 2 / (1 + e^2z), two special-function
+// operations a score, which the softmax's own exponential already fills.
+template <int HK>
+__device__ __forceinline__ void tanh_scaled(uint32_t (&v)[HK], float k) {
+  float m4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < HK; ++j) m4[j & 3] = fmaxf(m4[j & 3], fabsf(__uint_as_float(v[j])));
+  const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+  // (a NaN or an infinity among the scores also takes the second form: fmaxf
+  // drops a NaN, and the polynomial of a NaN is a NaN too)
+  if (__all_sync(kFullMask, mx * k <= 0.3f)) {
+    const float2 k2 = make_float2(k, k);
+    const float2 a4 = make_float2(2.1869488e-2f, 2.1869488e-2f);    // 62 / 2835
+    const float2 a3 = make_float2(-5.3968254e-2f, -5.3968254e-2f);  // -17 / 315
+    const float2 a2 = make_float2(1.3333333e-1f, 1.3333333e-1f);    // 2 / 15
+    const float2 a1 = make_float2(-3.3333333e-1f, -3.3333333e-1f);  // -1 / 3
+    const float2 one = make_float2(1.f, 1.f);
+#pragma unroll
+    for (int j = 0; j < HK; j += 2) {
+      const float2 z = __fmul2_rn(
+          make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), k2);
+      const float2 u = __fmul2_rn(z, z);
+      float2 h = __ffma2_rn(u, a4, a3);
+      h = __ffma2_rn(u, h, a2);
+      h = __ffma2_rn(u, h, a1);
+      const float2 r = __fmul2_rn(z, __ffma2_rn(u, h, one));
+      v[j] = __float_as_uint(r.x);
+      v[j + 1] = __float_as_uint(r.y);
+    }
+  } else {
+    const float k2 = 2.8853900817779268f * k;  // 2 log2(e) k
+#pragma unroll
+    for (int j = 0; j < HK; ++j) {
+      const float e = ex2(__uint_as_float(v[j]) * k2);
+      v[j] = __float_as_uint(fmaf(-2.f, __fdividef(1.f, 1.f + e), 1.f));
+    }
+  }
+}
+
 // Barrier of the two warps that share a TMEM lane quarter (warps w, w + 4).
 __device__ __forceinline__ void pair_sync(int warp) {
   asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
@@ -290,7 +339,14 @@ __device__ __forceinline__ void pair_sync(int warp) {
 //   S[c%kSBuf]; arrive on p_ready[c%kSBuf].
 // No softmax thread leaves the loop early (the pair barriers must stay
 // matched): one whose wait timed out keeps iterating without waiting or working.
-template <int G>
+//
+// RULE: the scores are changed and the visible keys differ.  A score becomes
+// cap tanh(scale q.k / cap) - slope |p - j|; the query at p sees the keys j
+// with j <= p or j < prefix, and j > p - window.  The tile's chunks then start
+// at the block of the lowest key its first query sees (key0; blocks before it
+// are not read, and may be gone from the table), and positions below are
+// relative to it.
+template <int G, bool RULE>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tq,
                          const __grid_constant__ CUtensorMap tk,
@@ -318,8 +374,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
   const int i0 = tile * TQ;
   if (i0 >= n) return;
+  int key0 = 0, vlo = 0, prefix = 0;  // vlo: hidden keys of the first block
+  if constexpr (RULE) {
+    if (p.prefix_lens != nullptr) {
+      prefix = __ldg(p.prefix_lens + b);
+      if (prefix < 0 || prefix > ctx) {
+        if (tid == 0 && tile == 0 && kvh == 0) raise_error(p.err, PA_DEVERR_PREFIX);
+        return;
+      }
+    }
+    if (p.rule.window > 0) {
+      const int lo = max(0, ctx - n + i0 + 1 - p.rule.window);
+      key0 = lo / kBS * kBS;
+      vlo = lo - key0;
+    }
+  }
   // keys the tile's last query sees
-  const int nk = shared_prefix ? ctx : ctx - n + min(n, i0 + TQ);
+  const int nk = shared_prefix ? ctx : max(ctx - n + min(n, i0 + TQ), prefix) - key0;
   const int nchunks = (nk + kKeys - 1) / kKeys;
   const int nblk_all = (nk + kBS - 1) / kBS;
 
@@ -370,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // so one warp issuing both rings paced the whole pipeline.
     const bool vwarp = warp == kCopyWarp + 1;
     const int32_t* tbl = p.block_tables + static_cast<size_t>(b) * p.max_blocks_per_seq +
-                         static_cast<size_t>(split) * p.split_blocks;
+                         static_cast<size_t>(split) * p.split_blocks + key0 / kBS;
     int last_k = -1, last_v = -1;  // last chunk copied into each ring (for the drain)
     bool ok = true;                // lane 0: every wait so far succeeded
     auto uniform = [&](bool v) { return __shfl_sync(kFullMask, v ? 1 : 0, 0) != 0; };
@@ -546,8 +617,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int r = tid & (kRows - 1);  // row: token r / G of the tile, head r % G
     const int qi = i0 + r / G;
     const bool row_ok = qi < n;
-    const int pos = shared_prefix ? nk - 1 : ctx - n + qi;  // sees keys 0 .. pos
-    const float sl2 = p.scale_log2;
+    const int pos = shared_prefix ? nk - 1 : ctx - n + qi - key0;  // sees keys 0 .. pos
+    const float sl2 = RULE ? p.unit : p.scale_log2;
+    // the last key the row sees, the first, and its slope in the scores' unit
+    const int row_hi = RULE ? max(pos, prefix - 1 - key0) : pos;
+    const int row_lo = RULE && p.rule.window > 0 ? pos + 1 - p.rule.window : 0;
+    float slope = 0.f;
+    if constexpr (RULE) {
+      if (p.rule.slopes != nullptr)
+        slope = __ldg(p.rule.slopes + kvh * G + r % G) * 1.4426950408889634f / p.unit;
+    }
     float m_used = -INFINITY;  // reference maximum of the exponentials (base 2)
     float l_sum = 0.f;
     bool ok = true;  // sticky: this thread's waits all succeeded
@@ -558,22 +637,36 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       bool lok = ok && mbar_wait_bounded(&s_done[sb], (c / kSBuf) & 1, p.err);
       lok = __all_sync(kFullMask, lok);
       uint32_t sv[HK];
-      if (lok) {
-        tc_fence_after();
+      // causal mask
+      const int lim = row_ok ? row_hi - c * kKeys - HK * hcol : -1;  // visible: j <= lim
+      const int low = row_lo - c * kKeys - HK * hcol;               // and j >= low
+      const bool masked = !__all_sync(kFullMask, lim >= HK - 1 && (!RULE || low <= 0));
+      auto scores = [&]() {
 #pragma unroll
         for (int q4 = 0; q4 < HK / 32; ++q4) {
           uint32_t(&chunk)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * q4);
           tmem_ld32(tmem + lane_base + sb * kKeys + HK * hcol + 32 * q4, chunk);
         }
         tmem_wait_ld();
-      }
-      // causal mask
-      const int lim = row_ok ? pos - c * kKeys - HK * hcol : -1;  // visible: j <= lim
-      const bool masked = !__all_sync(kFullMask, lim >= HK - 1);
-      if (lok && masked) {
+        if constexpr (RULE) {
+          if (p.rule.softcap > 0.f) tanh_scaled<HK>(sv, p.cap_in);
+          if (p.rule.slopes != nullptr) {
+            const float at = static_cast<float>(c * kKeys + HK * hcol - pos);
 #pragma unroll
-        for (int j = 0; j < HK; ++j)
-          if (j > lim) sv[j] = __float_as_uint(-INFINITY);
+            for (int j = 0; j < HK; ++j)
+              sv[j] = __float_as_uint(fmaf(-slope, fabsf(at + static_cast<float>(j)),
+                                           __uint_as_float(sv[j])));
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < HK; ++j)
+            if (j > lim || (RULE && j < low)) sv[j] = __float_as_uint(-INFINITY);
+        }
+      };
+      if (lok) {
+        tc_fence_after();
+        scores();
       }
       // The weights against the current reference (none yet: offset 0, and a
       // row without a reference has only masked scores so far, which give
@@ -624,17 +717,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       if (__any_sync(kFullMask, row_want)) {
         float mx = -INFINITY;
         if (lok) {
-#pragma unroll
-          for (int q4 = 0; q4 < HK / 32; ++q4) {
-            uint32_t(&chunk)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * q4);
-            tmem_ld32(tmem + lane_base + sb * kKeys + HK * hcol + 32 * q4, chunk);
-          }
-          tmem_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < HK; ++j)
-              if (j > lim) sv[j] = __float_as_uint(-INFINITY);
-          }
+          scores();
           // eight independent partial maxima (max is exact in any order)
           float m8[8];
 #pragma unroll
@@ -718,10 +801,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       // (a partly filled block, or blocks not loaded); P is 0 there, but
       // 0 * NaN is not, so those rows are zeroed once the copies have landed.
       const int vk = nk - c * kKeys;  // valid keys in this chunk
-      if (lok && vk < kKeys) {
+      // (RULE: so may the keys of the first block that no query of the tile sees.)
+      if (lok && (vk < kKeys || (RULE && c == 0 && vlo > 0))) {
         const int st = c % kStages;
         lok = mbar_wait_bounded(&v_full[st], (c / kStages) & 1, p.err);
-        if (lok && r >= vk && r < kKeys) {
+        if (lok && (r >= vk || (RULE && c == 0 && r < vlo)) && r < kKeys) {
           const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int hh = hcol; hh < 2; hh += kRowThreads) {  // the 64-column halves
@@ -864,12 +948,12 @@ bool encode_q_map(CUtensorMap* map, const void* base, int total_q, int num_q_hea
          CUDA_SUCCESS;
 }
 
-template <int G>
+template <int G, bool RULE = false>
 cudaError_t launch_prefill_g(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const PrefillParams& p, int max_query_len, int num_seqs,
                              cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
-  auto kernel = paged_prefill_kernel<G>;
+  auto kernel = paged_prefill_kernel<G, RULE>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -933,17 +1017,22 @@ extern "C" int pa_prefill_supported(int head_dim, int group, int block_size) {
                                                   group == 8);
 }
 
-extern "C" pa_status pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
-                                const int32_t* block_tables, int max_blocks_per_seq,
-                                const int32_t* context_lens, const int32_t* query_start_loc,
-                                int max_query_len, int num_seqs, int total_query_tokens,
-                                int num_q_heads, int num_kv_heads, int head_dim, int block_size,
-                                int num_blocks, float scale, pa_stream_t stream) {
+namespace {
+
+// pa_prefill and pa_prefill_biased (rule non-null).
+pa_status prefill_impl(void* out, const void* q, const void* k_cache, const void* v_cache,
+                       const int32_t* block_tables, int max_blocks_per_seq,
+                       const int32_t* context_lens, const int32_t* query_start_loc,
+                       int max_query_len, int num_seqs, int total_query_tokens, int num_q_heads,
+                       int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                       float scale, const pa::ScoreRule* rule, const int32_t* prefix_lens,
+                       pa_stream_t stream) {
   using namespace pa;
   if (num_seqs < 0 || max_query_len < 0 || total_query_tokens < 0 || num_q_heads <= 0 ||
       num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || max_blocks_per_seq <= 0 ||
       num_blocks <= 0 || !(scale > 0.f) || num_seqs > 65535)
     return PA_ERR_INVALID_ARG;
+  if (rule && !score_rule_ok(*rule, scale)) return PA_ERR_INVALID_ARG;
   const int group = num_q_heads / num_kv_heads;
   if (!pa_prefill_supported(head_dim, group, block_size)) return PA_ERR_UNSUPPORTED_SHAPE;
   if (num_seqs == 0 || max_query_len == 0 || total_query_tokens == 0) return PA_OK;
@@ -972,11 +1061,53 @@ extern "C" pa_status pa_prefill(void* out, const void* q, const void* k_cache, c
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  switch (group) {
-    case 1: e = launch_prefill_g<1>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
-    case 2: e = launch_prefill_g<2>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
-    case 4: e = launch_prefill_g<4>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
-    default: e = launch_prefill_g<8>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
+  if (rule) {
+    p.rule = *rule;
+    p.prefix_lens = prefix_lens;
+    p.unit = rule->softcap > 0.f ? rule->softcap * 1.4426950408889634f : p.scale_log2;
+    p.cap_in = rule->softcap > 0.f ? scale / rule->softcap : 0.f;
+    switch (group) {
+      case 1: e = launch_prefill_g<1, true>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
+      case 2: e = launch_prefill_g<2, true>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
+      case 4: e = launch_prefill_g<4, true>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
+      default: e = launch_prefill_g<8, true>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
+    }
+  } else {
+    switch (group) {
+      case 1: e = launch_prefill_g<1>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
+      case 2: e = launch_prefill_g<2>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
+      case 4: e = launch_prefill_g<4>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
+      default: e = launch_prefill_g<8>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
+    }
   }
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" pa_status pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* context_lens, const int32_t* query_start_loc,
+                                int max_query_len, int num_seqs, int total_query_tokens,
+                                int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                int num_blocks, float scale, pa_stream_t stream) {
+  return prefill_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                      query_start_loc, max_query_len, num_seqs, total_query_tokens, num_q_heads,
+                      num_kv_heads, head_dim, block_size, num_blocks, scale, nullptr, nullptr,
+                      stream);
+}
+
+extern "C" pa_status pa_prefill_biased(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+    const int32_t* query_start_loc, int max_query_len, int num_seqs, int total_query_tokens,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    float softcap, const float* alibi_slopes, int window, const int32_t* prefix_lens,
+    pa_stream_t stream) {
+  if (reinterpret_cast<uintptr_t>(prefix_lens) % 4 != 0) return PA_ERR_INVALID_ARG;
+  const pa::ScoreRule rule{alibi_slopes, softcap, window};
+  return prefill_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                      query_start_loc, max_query_len, num_seqs, total_query_tokens, num_q_heads,
+                      num_kv_heads, head_dim, block_size, num_blocks, scale, &rule, prefix_lens,
+                      stream);
 }

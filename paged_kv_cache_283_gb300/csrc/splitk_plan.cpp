@@ -102,7 +102,8 @@ extern "C" int pa_splitk_partition_size(const int32_t* context_lens, int num_seq
                                         int num_q_heads, int num_kv_heads, int head_dim,
                                         int kv_kind, int num_sms, int ordered) {
   if (!context_lens || num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
-      num_q_heads % num_kv_heads != 0 || head_dim <= 0 || kv_kind < 0 || kv_kind > 2 ||
+      num_q_heads % num_kv_heads != 0 || head_dim <= 0 ||
+      (kv_kind != 4 && (kv_kind < 0 || kv_kind > 2)) ||
       num_sms <= 0)
     return 0;
   const int group = num_q_heads / num_kv_heads;

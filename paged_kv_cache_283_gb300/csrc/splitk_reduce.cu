@@ -44,6 +44,8 @@ __global__ void __launch_bounds__(D) splitk_reduce_kernel(const ReduceParams p) 
     }
   }
   int ctx = __ldg(p.context_lens + b);
+  if (p.window > 0 && ctx > p.window)  // the tokens from the first visible one's block on
+    ctx -= (ctx - p.window) / 16 * 16;
   const int64_t cap = static_cast<int64_t>(p.max_partitions) * p.partition_size;
   if (ctx < 0 || ctx > cap) {
     if (d == 0 && hq == 0) raise_error(p.err, PA_DEVERR_CONTEXT_LEN);

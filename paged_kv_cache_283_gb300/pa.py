@@ -27,6 +27,7 @@ PA_DEVERR_SLOT = 0x4
 PA_DEVERR_WAIT_TIMEOUT = 0x8
 PA_DEVERR_ORDER = 0x10
 PA_DEVERR_PREFIX = 0x20
+PA_DEVERR_POSITION = 0x40
 PA_STEP_EARLY_READ = 0x1
 
 # Every function include/pa.h declares: name -> (restype, argtypes).
@@ -71,11 +72,32 @@ SIGNATURES = {
     "pa_decode_step_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i,
                                 _i, _i, _i, _i, _i, _f, _i, _vp, _vp, _vp, _vp, _i, _vp, _i,
                                 _vp]),
+    "pa_reshape_and_cache_int4": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "pa_decode_int4": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _f, _vp]),
+    "pa_decode_splitk_int4": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i,
+                                   _i, _i, _i, _f, _i, _vp]),
+    "pa_decode_step_int4": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i,
+                                 _i, _i, _i, _f, _i, _vp, _vp, _vp, _vp, _i, _vp, _i, _vp]),
+    "pa_decode_step_biased": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i,
+                                   _i, _i, _i, _f, _f, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _vp,
+                                   _i, _vp]),
+    "pa_rope_reshape_and_cache": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
+                                       _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
+    "pa_rope_reshape_and_cache_int8": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                            _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
+                                            _i, _vp]),
+    "pa_rope_reshape_and_cache_fp8": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                           _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
+                                           _i, _vp]),
+    "pa_rope_reshape_and_cache_int4": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                            _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
     "pa_decode_splitk_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i,
                                       _f, _i, _i, _vp]),
     "pa_prefill_supported": (_i, [_i, _i, _i]),
     "pa_prefill": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
                         _f, _vp]),
+    "pa_prefill_biased": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                               _i, _i, _f, _f, _vp, _i, _vp, _vp]),
     "pa_plan_step": (_i, [_i, _i, _vp, _i, _vp, _pint]),
     "pa_alloc_create": (_i, [_i, _i, _vp, ctypes.POINTER(_vp)]),
     "pa_alloc_destroy": (None, [_vp]),
@@ -209,6 +231,179 @@ def pa_copy_blocks(k_caches, v_caches, block_mapping, stream=None):
     _check(st, "pa_copy_blocks")
 
 
+def _one_device(what, *tensors):
+    """Refuses tensors that do not all live on the current CUDA device, on whose
+    current stream the launch goes."""
+    cur = _torch().cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != cur:
+            raise ValueError(f"{what}: every tensor must be on the current CUDA device "
+                             f"(cuda:{cur}), got {t.device}")
+
+
+def _pool4(pool, name, hkv=None, d=None):
+    """Checked 4-bit pool [NB, Hkv, 9 * D] uint8: (pointer, NB, Hkv, D)."""
+    ptr = _dev(pool, _torch().uint8, name, 3)
+    nb, h, row = pool.shape
+    if row % 9 or (d is not None and row != 9 * d) or (hkv is not None and h != hkv):
+        raise ValueError(f"{name}: a 4-bit pool is [NB, Hkv, 9 * D] uint8, got "
+                         f"{tuple(pool.shape)}")
+    return ptr, nb, h, row // 9
+
+
+def int4_pool(num_blocks, num_kv_heads, head_dim, device="cuda"):
+    """A zeroed 4-bit K or V pool [NB, Hkv, 9 * D] uint8 (blocks of 16 tokens)."""
+    torch = _torch()
+    return torch.zeros((num_blocks, num_kv_heads, 9 * head_dim), dtype=torch.uint8,
+                       device=device)
+
+
+def pa_reshape_and_cache_int4(key, value, k_cache, v_cache, slot_mapping, stream=None):
+    """key/value [T, Hkv, D] bf16 quantised into 4-bit pools [NB, Hkv, 9 * D] uint8."""
+    torch = _torch()
+    T, hkv, d = key.shape
+    _one_device("pa_reshape_and_cache_int4", key, value, k_cache, v_cache, slot_mapping)
+    pk, nb, _, _ = _pool4(k_cache, "k_cache", hkv, d)
+    pv = _pool4(v_cache, "v_cache", hkv, d)[0]
+    if value.shape != key.shape or v_cache.shape != k_cache.shape or slot_mapping.shape != (T,):
+        raise ValueError("pa_reshape_and_cache_int4: inconsistent shapes")
+    st = lib().pa_reshape_and_cache_int4(
+        _dev(key, torch.bfloat16, "key", 3), _dev(value, torch.bfloat16, "value", 3), pk, pv,
+        _dev(slot_mapping, torch.int64, "slot_mapping", 1), T, hkv, d, 16, nb, _stream(stream))
+    _check(st, "pa_reshape_and_cache_int4")
+
+
+def rope_table(max_position, rotary_dim, base=10000.0, inv_freq=None, device="cuda"):
+    """The [max_position, rotary_dim] fp32 cosine / sine table of the rotary
+    embedding: angles p * base^(-2 i / rotary_dim) (or p * inv_freq[i]) taken in
+    float64, so far positions keep their angle, and rounded once."""
+    torch = _torch()
+    if inv_freq is None:
+        i = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+        inv_freq = float(base) ** (-i / rotary_dim)
+    f = torch.as_tensor(inv_freq, dtype=torch.float64, device=device)
+    if f.shape != (rotary_dim // 2,):
+        raise ValueError("rope_table: inv_freq must be [rotary_dim / 2]")
+    angle = torch.arange(max_position, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([angle.cos(), angle.sin()], 1).to(torch.float32).contiguous()
+
+
+def _heads(t, name):
+    """(pointer, token stride) of a [T, H, D] bf16 tensor whose tokens may be
+    strided (a slice of a fused projection) but whose rows are contiguous."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
+    T, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    stride = t.stride(0) if T > 1 else max(h * d, 8)
+    if stride < h * d or stride % 8:
+        raise ValueError(f"{name}: tokens must be a multiple of 8 elements apart and not overlap")
+    return ctypes.c_void_p(t.data_ptr()), stride
+
+
+def _rope_append_args(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                      interleaved, k_scales, v_scales):
+    """(C function, argument tuple without the stream) for pa_rope_reshape_and_cache*."""
+    torch = _torch()
+    what = "pa_rope_reshape_and_cache"
+    T, hkv, d = key.shape
+    _one_device(what, q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                k_scales, v_scales)
+    pk, ks = _heads(key, "key")
+    pv, vs = _heads(value, "value")
+    if value.shape != key.shape or slot_mapping.shape != (T,) or positions.shape != (T,):
+        raise ValueError(f"{what}: key / value [T, Hkv, D], slot_mapping and positions [T]")
+    if cos_sin.dim() != 2:
+        raise ValueError(f"{what}: cos_sin must be [max_position, rotary_dim]")
+    none = ctypes.c_void_p(None)
+    if (q is None) != (q_out is None):
+        raise ValueError(f"{what}: q and q_out go together")
+    if q is None:
+        qa, hq = (none, none, 0), 0
+    else:
+        hq = q.shape[1]
+        if q.shape != (T, hq, d) or q_out.shape != q.shape:
+            raise ValueError(f"{what}: q and q_out must be [T, Hq, D]")
+        pq, qs = _heads(q, "q")
+        qa = (_dev(q_out, torch.bfloat16, "q_out", 3), pq, qs)
+    bs = 16
+    if k_cache.dim() == 3:       # 4-bit
+        name, scales = "_int4", ()
+        ck, nb, _, _ = _pool4(k_cache, "k_cache", hkv, d)
+        pools = (ck, _pool4(v_cache, "v_cache", hkv, d)[0])
+        if k_scales is not None or v_scales is not None:
+            raise ValueError(f"{what}: a 4-bit pool keeps its parameters inside")
+    elif k_cache.dtype == torch.bfloat16:
+        name = ""
+        pools = (_dev(k_cache, torch.bfloat16, "k_cache", 4),
+                 _dev(v_cache, torch.bfloat16, "v_cache", 4))
+        nb, h2, bs, d2 = k_cache.shape
+        if (h2, d2) != (hkv, d):
+            raise ValueError(f"{what}: inconsistent key / cache shapes")
+        if k_scales is not None or v_scales is not None:
+            raise ValueError(f"{what}: a bf16 cache has no scales")
+    else:
+        fp8 = k_cache.dtype == torch.uint8
+        name = "_fp8" if fp8 else "_int8"
+        if k_scales is None or v_scales is None:
+            raise ValueError(f"{what}: a 1-byte cache needs k_scales and v_scales")
+        pools, (nb, h2, bs, d2) = _int8_pools(k_cache, v_cache, k_scales, v_scales, fp8)
+        if (h2, d2) != (hkv, d):
+            raise ValueError(f"{what}: inconsistent key / cache shapes")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError(f"{what}: k_cache and v_cache must have one shape")
+    args = qa + (pk, ks, pv, vs) + pools + (
+        _dev(slot_mapping, torch.int64, "slot_mapping", 1),
+        _dev(positions, torch.int32, "positions", 1), _dev(cos_sin, torch.float32, "cos_sin", 2),
+        cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, T, hq, hkv, d, bs, nb)
+    return getattr(lib(), "pa_rope_reshape_and_cache" + name), args
+
+
+def pa_rope_reshape_and_cache(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions,
+                              cos_sin, interleaved=False, k_scales=None, v_scales=None,
+                              stream=None):
+    """Rotary embedding of q (to q_out, which may be q) and key, and the cache
+    write of the rotated key and of value, in one launch (pa.h).
+
+    q / key / value [T, H, D] bf16, tokens strided or not; positions [T] int32;
+    cos_sin [max_position, rotary_dim] fp32 (rope_table).  The pools' type picks
+    the cache: bf16, int8 or uint8 (FP8 codes) [NB, Hkv, 16, D] with scales, or
+    4-bit [NB, Hkv, 9 * D] uint8.  q and q_out None: k and v only."""
+    fn, args = _rope_append_args(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions,
+                                 cos_sin, interleaved, k_scales, v_scales)
+    _check(fn(*args, _stream(stream)), "pa_rope_reshape_and_cache")
+
+
+class RopeAppend:
+    """pa_rope_reshape_and_cache of one layer on fixed device buffers, its
+    arguments checked and marshalled once; each call is one bare C call.  The
+    buffers' contents may change between calls, their shapes and addresses may
+    not."""
+
+    def __init__(self, q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                 interleaved=False, k_scales=None, v_scales=None, stream=None):
+        self._fn, self._args = _rope_append_args(q_out, q, key, value, k_cache, v_cache,
+                                                 slot_mapping, positions, cos_sin, interleaved,
+                                                 k_scales, v_scales)
+        self._stream = None if stream is None else ctypes.c_void_p(stream.cuda_stream)
+        self._keep = [q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                      k_scales, v_scales]
+
+    def __call__(self, stream=None):
+        s = self._stream if stream is None and self._stream is not None else _stream(stream)
+        st = self._fn(*self._args, s)
+        if st != PA_OK:
+            _check(st, "RopeAppend: pa_rope_reshape_and_cache")
+
+
 def _decode_common(q, k_cache, v_cache, block_tables, context_lens):
     torch = _torch()
     B, hq, d = q.shape
@@ -305,6 +500,50 @@ def pa_decode_splitk_int8(ws_out, ws_m, ws_l, q, k_cache, v_cache, k_scales, v_s
     _check(st, "pa_decode_splitk_int8")
 
 
+def _decode_int4_common(q, k_cache, v_cache, block_tables, context_lens):
+    torch = _torch()
+    B, hq, d = q.shape
+    _one_device("4-bit decode", q, k_cache, v_cache, block_tables, context_lens)
+    pk, nb, hkv, _ = _pool4(k_cache, "k_cache", None, d)
+    pv = _pool4(v_cache, "v_cache", hkv, d)[0]
+    if v_cache.shape != k_cache.shape or block_tables.dim() != 2 or \
+            block_tables.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError("4-bit decode: inconsistent shapes")
+    return (_dev(q, torch.bfloat16, "q", 3), pk, pv,
+            _dev(block_tables, torch.int32, "block_tables", 2),
+            _dev(context_lens, torch.int32, "context_lens", 1)), (B, hq, hkv, d, 16, nb,
+                                                                  block_tables.shape[1])
+
+
+def pa_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, scale, stream=None):
+    """out, q [B, Hq, D] bf16; 4-bit pools [NB, Hkv, 9 * D] uint8; block_tables [B, MB] int32."""
+    torch = _torch()
+    (pq, pk, pv, pt, pc), (B, hq, hkv, d, bs, nb, mb) = _decode_int4_common(
+        q, k_cache, v_cache, block_tables, context_lens)
+    if out.shape != q.shape:
+        raise ValueError("pa_decode_int4: out must match q")
+    _one_device("pa_decode_int4", out)
+    st = lib().pa_decode_int4(_dev(out, torch.bfloat16, "out", 3), pq, pk, pv, pt, mb, pc, B, hq,
+                              hkv, d, bs, nb, float(scale), _stream(stream))
+    _check(st, "pa_decode_int4")
+
+
+def pa_decode_splitk_int4(ws_out, ws_m, ws_l, q, k_cache, v_cache, block_tables, context_lens,
+                          scale, partition_size=512, stream=None):
+    torch = _torch()
+    (pq, pk, pv, pt, pc), (B, hq, hkv, d, bs, nb, mb) = _decode_int4_common(
+        q, k_cache, v_cache, block_tables, context_lens)
+    maxp = ws_m.shape[2]
+    if ws_out.shape != (B, hq, maxp, d) or ws_l.shape != ws_m.shape or ws_m.shape[:2] != (B, hq):
+        raise ValueError("pa_decode_splitk_int4: workspace shapes")
+    _one_device("pa_decode_splitk_int4", ws_out, ws_m, ws_l)
+    st = lib().pa_decode_splitk_int4(
+        _dev(ws_out, torch.float32, "ws_out", 4), _dev(ws_m, torch.float32, "ws_m", 3),
+        _dev(ws_l, torch.float32, "ws_l", 3), maxp, pq, pk, pv, pt, mb, pc, B, hq, hkv, d, bs, nb,
+        float(scale), int(partition_size), _stream(stream))
+    _check(st, "pa_decode_splitk_int4")
+
+
 def pa_splitk_workspace_bytes(num_seqs, num_q_heads, head_dim, max_context_len, partition_size):
     return int(lib().pa_splitk_workspace_bytes(num_seqs, num_q_heads, head_dim, max_context_len,
                                                partition_size))
@@ -360,7 +599,7 @@ def splitk_partition_size(context_lens, num_q_heads, num_kv_heads, head_dim, kv=
     if num_sms is None:
         torch = _torch()
         num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
-    kind = {"bf16": 0, "int8": 1, "fp8": 2}[kv]
+    kind = {"bf16": 0, "int8": 1, "fp8": 2, "int4": 4}[kv]
     r = lib().pa_splitk_partition_size(ctx.ctypes.data_as(ctypes.c_void_p), ctx.shape[0],
                                        num_q_heads, num_kv_heads, head_dim, kind, int(num_sms),
                                        1 if ordered else 0)
@@ -462,12 +701,25 @@ def recover_step_counters(counters):
 
 def _step_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, key, value,
                slot_mapping, partition_size, workspace, counters, k_scales, v_scales,
-               order=None, early_read=False):
+               order=None, early_read=False, softcap=0.0, alibi_slopes=None, window=0):
     """(C function, argument tuple without the stream) for pa_decode_step*."""
     torch = _torch()
-    fp8 = k_cache.dtype == torch.uint8
+    four = k_cache.dtype == torch.uint8 and k_cache.dim() == 3
+    fp8 = k_cache.dtype == torch.uint8 and not four
     one = fp8 or k_cache.dtype == torch.int8
-    if one:
+    ruled = bool(softcap) or alibi_slopes is not None or bool(window)
+    if ruled and (four or one):
+        raise ValueError("pa_decode_step: softcap, alibi_slopes and window need a bf16 cache")
+    if four or ruled:
+        _one_device("pa_decode_step", out, q, k_cache, v_cache, block_tables, context_lens, key,
+                    value, slot_mapping, counters, order, alibi_slopes, *(workspace or ()))
+    if four:
+        if k_scales is not None or v_scales is not None:
+            raise ValueError("pa_decode_step: a 4-bit pool keeps its parameters inside")
+        (pq, pk, pv, pt, pc), (B, hq, hkv, d, bs, nb, mb) = _decode_int4_common(
+            q, k_cache, v_cache, block_tables, context_lens)
+        pools = (pk, pv)
+    elif one:
         if k_scales is None or v_scales is None:
             raise ValueError("pa_decode_step: a 1-byte cache needs k_scales and v_scales")
         (pq, pk, pv, pks, pvs, pt, pc), (B, hq, hkv, d, bs, nb, mb) = _decode_int8_common(
@@ -508,10 +760,17 @@ def _step_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, key,
         if order is not None:
             raise ValueError("pa_decode_step: an order needs split-K")
     ordp = (none,) if order is None else (_dev(order, torch.int32, "order", 1),)
-    fn = lib().pa_decode_step_fp8 if fp8 else (lib().pa_decode_step_int8 if one
-                                                else lib().pa_decode_step)
+    rule = ()
+    if ruled:
+        if alibi_slopes is not None and alibi_slopes.shape != (hq,):
+            raise ValueError("pa_decode_step: alibi_slopes must be [Hq]")
+        rule = (float(softcap), none if alibi_slopes is None else
+                _dev(alibi_slopes, torch.float32, "alibi_slopes", 1), int(window))
+    fn = lib().pa_decode_step_biased if ruled else lib().pa_decode_step_int4 if four else (
+        lib().pa_decode_step_fp8 if fp8 else lib().pa_decode_step_int8 if one
+        else lib().pa_decode_step)
     args = (_dev(out, torch.bfloat16, "out", 3), pq) + kvs + pools + (
-        pt, mb, pc, B, hq, hkv, d, bs, nb, float(scale), ps) + wsa + ordp + (
+        pt, mb, pc, B, hq, hkv, d, bs, nb, float(scale)) + rule + (ps,) + wsa + ordp + (
         PA_STEP_EARLY_READ if early_read else 0,)
     return fn, args
 
@@ -519,19 +778,21 @@ def _step_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, key,
 def pa_decode_step(out, q, k_cache, v_cache, block_tables, context_lens, scale, key=None,
                    value=None, slot_mapping=None, partition_size=512, workspace=None,
                    counters=None, k_scales=None, v_scales=None, stream=None, order=None,
-                   early_read=False):
+                   early_read=False, softcap=0.0, alibi_slopes=None, window=0):
     """Cache write of each sequence's new token (key / value [B, Hkv, D] at
     slot_mapping [B], which must be the slot of position context_lens[b] - 1)
     and the decode, in one launch.  partition_size 0: whole-sequence CTAs;
     > 0: split-K merged in the same launch (workspace = splitk_workspace(...),
     counters = step_counters(...)).  The cache dtype picks bf16 / INT8 (int8)
-    / FP8 (uint8 codes, with k_scales / v_scales).  order: optional device
+    / FP8 (uint8 codes, with k_scales / v_scales) / 4-bit (uint8 [NB, Hkv, 9 *
+    D]).  softcap, alibi_slopes ([Hq] fp32) and window change the scores of a
+    bf16 cache's step (pa_decode_step_biased).  order: optional device
     int32 work order (splitk_order) for the split-K CTAs.  early_read: the
     caller's promise that tables, lengths, order and pools are not written by
     the kernel launched just before (PA_STEP_EARLY_READ in pa.h)."""
     fn, args = _step_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, key,
                           value, slot_mapping, partition_size, workspace, counters, k_scales,
-                          v_scales, order, early_read)
+                          v_scales, order, early_read, softcap, alibi_slopes, window)
     _check(fn(*args, _stream(stream)), "pa_decode_step")
 
 
@@ -737,6 +998,79 @@ def pa_prefill(out, q, k_cache, v_cache, block_tables, context_lens, query_start
     _check(st, "pa_prefill")
 
 
+def _prefill_biased_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                         max_query_len, scale, softcap, alibi_slopes, window, prefix_lens):
+    """Checked and marshalled arguments of pa_prefill_biased (without the stream)."""
+    torch = _torch()
+    T, hq, d = q.shape
+    _one_device("pa_prefill_biased", out, q, k_cache, v_cache, block_tables, context_lens,
+                query_start_loc, alibi_slopes, prefix_lens)
+    if out.shape != q.shape:
+        raise ValueError("pa_prefill_biased: out must match q")
+    nb, hkv, bs, d2 = k_cache.shape
+    if v_cache.shape != k_cache.shape or d2 != d:
+        raise ValueError("pa_prefill_biased: cache shapes")
+    B, mb = block_tables.shape
+    if context_lens.shape != (B,) or query_start_loc.shape != (B + 1,):
+        raise ValueError("pa_prefill_biased: context_lens / query_start_loc shapes")
+    if alibi_slopes is not None and alibi_slopes.shape != (hq,):
+        raise ValueError("pa_prefill_biased: alibi_slopes must be [Hq]")
+    if prefix_lens is not None and prefix_lens.shape != (B,):
+        raise ValueError("pa_prefill_biased: prefix_lens must be [B]")
+    none = ctypes.c_void_p(None)
+    return (_dev(out, torch.bfloat16, "out", 3), _dev(q, torch.bfloat16, "q", 3),
+            _dev(k_cache, torch.bfloat16, "k_cache", 4),
+            _dev(v_cache, torch.bfloat16, "v_cache", 4),
+            _dev(block_tables, torch.int32, "block_tables", 2), mb,
+            _dev(context_lens, torch.int32, "context_lens", 1),
+            _dev(query_start_loc, torch.int32, "query_start_loc", 1), int(max_query_len), B, T,
+            hq, hkv, d, bs, nb, float(scale), float(softcap),
+            none if alibi_slopes is None else
+            _dev(alibi_slopes, torch.float32, "alibi_slopes", 1), int(window),
+            none if prefix_lens is None else _dev(prefix_lens, torch.int32, "prefix_lens", 1))
+
+
+def pa_prefill_biased(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                      max_query_len, scale, softcap=0.0, alibi_slopes=None, window=0,
+                      prefix_lens=None, stream=None):
+    """pa_prefill with changed scores and masks (pa.h): scores capped by
+    softcap * tanh(s / softcap), lowered by alibi_slopes[h] * distance, keys
+    limited to a window, and leading prefix_lens[b] positions seen by every
+    query.  alibi_slopes [Hq] fp32, prefix_lens [B] int32, both on the device."""
+    args = _prefill_biased_args(out, q, k_cache, v_cache, block_tables, context_lens,
+                                query_start_loc, max_query_len, scale, softcap, alibi_slopes,
+                                window, prefix_lens)
+    _check(lib().pa_prefill_biased(*args, _stream(stream)), "pa_prefill_biased")
+
+
+class PrefillStep:
+    """One prefill call of one layer on fixed device buffers, its arguments
+    checked and marshalled once; each call is one bare C call: pa_prefill, or
+    pa_prefill_biased when softcap, alibi_slopes, window or prefix_lens is
+    given.  The buffers' contents may change between calls, their shapes and
+    addresses may not."""
+
+    def __init__(self, out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                 max_query_len, scale, softcap=0.0, alibi_slopes=None, window=0,
+                 prefix_lens=None, stream=None):
+        args = _prefill_biased_args(out, q, k_cache, v_cache, block_tables, context_lens,
+                                    query_start_loc, max_query_len, scale, softcap,
+                                    alibi_slopes, window, prefix_lens)
+        if softcap or alibi_slopes is not None or window or prefix_lens is not None:
+            self._fn, self._args = lib().pa_prefill_biased, args
+        else:
+            self._fn, self._args = lib().pa_prefill, args[:17]
+        self._stream = None if stream is None else ctypes.c_void_p(stream.cuda_stream)
+        self._keep = [out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                      alibi_slopes, prefix_lens]
+
+    def __call__(self, stream=None):
+        s = self._stream if stream is None and self._stream is not None else _stream(stream)
+        st = self._fn(*self._args, s)
+        if st != PA_OK:
+            _check(st, "PrefillStep: prefill")
+
+
 def pa_plan_step(budget, num_decodes, prefill_remaining):
     """(decodes scheduled, numpy int32 tokens per queued prefill) for one step."""
     import numpy as np
@@ -763,7 +1097,10 @@ class DecodeStep:
     tables' capacity, max_blocks_per_seq * block_size); any lengths up to that
     stay correct as they grow from call to call, only the speed may differ.
     After a launch that raised PA_DEVERR_ORDER or PA_DEVERR_WAIT_TIMEOUT,
-    call recover() before the next one.
+    call recover() before the next one.  softcap, alibi_slopes and window change
+    the scores (pa_decode_step_biased); with a window the plan, the workspace
+    and the order cover the window only.  key, value and slot_mapping None:
+    attention only.
 
     Every argument is checked and marshalled once, here; each call then makes
     two or three bare C calls, which keeps the host ahead of the GPU when a
@@ -776,9 +1113,14 @@ class DecodeStep:
                  context_lens, out, scale, split=True, partition_size=512,
                  max_context_len=None, workspace=None, stream=None, k_scales=None,
                  v_scales=None, fused=True, counters=None, order=None, early_read=False,
-                 host_context_lens=None):
+                 host_context_lens=None, softcap=0.0, alibi_slopes=None, window=0):
         torch = _torch()
         self.fused = bool(fused)
+        four = k_cache.dtype == torch.uint8 and k_cache.dim() == 3
+        block = 16 if four else k_cache.shape[2]
+        if not self.fused and (four or softcap or alibi_slopes is not None or window):
+            raise ValueError("DecodeStep: a 4-bit cache, softcap, alibi_slopes and window need "
+                             "fused=True")
         if self.fused:
             # one pa_decode_step* launch: write + attention (+ merge)
             self._stream = None if stream is None else ctypes.c_void_p(stream.cuda_stream)
@@ -791,10 +1133,14 @@ class DecodeStep:
                 # workspace and the order cover the block tables' capacity
                 # unless max_context_len says less, so the contexts may grow
                 # from call to call up to that capacity.
-                kind = ("fp8" if k_cache.dtype == torch.uint8 else
+                kind = ("int4" if four else "fp8" if k_cache.dtype == torch.uint8 else
                         "int8" if k_cache.dtype == torch.int8 else "bf16")
                 if max_context_len is None:
-                    max_context_len = block_tables.shape[1] * k_cache.shape[2]
+                    max_context_len = block_tables.shape[1] * block
+                if window:  # what a step reads: the window, from a block's start
+                    import numpy as np
+                    host_context_lens = np.minimum(host_context_lens, int(window) + block - 1)
+                    max_context_len = min(int(max_context_len), int(window) + block - 1)
                 plan = plan_decode_step(
                     host_context_lens, hq, hkv, d, kind,
                     torch.cuda.get_device_properties(q.device).multi_processor_count,
@@ -808,7 +1154,9 @@ class DecodeStep:
             if self.split:
                 if workspace is None:
                     mc = (int(max_context_len) if max_context_len is not None
-                          else block_tables.shape[1] * k_cache.shape[2])
+                          else block_tables.shape[1] * block)
+                    if window:
+                        mc = min(mc, int(window) + block - 1)
                     workspace = splitk_workspace(B, hq, d, mc, partition_size, q.device)
                 if counters is None:
                     counters = step_counters(B, hkv, q.device)
@@ -816,9 +1164,10 @@ class DecodeStep:
             self._fn, self._args = _step_args(
                 out, q, k_cache, v_cache, block_tables, context_lens, scale, key, value,
                 slot_mapping, partition_size if self.split else 0, workspace, counters,
-                k_scales, v_scales, order, early_read)
+                k_scales, v_scales, order, early_read, softcap, alibi_slopes, window)
             self._keep = [key, value, k_cache, v_cache, slot_mapping, q, block_tables,
-                          context_lens, out, workspace, counters, k_scales, v_scales, order]
+                          context_lens, out, workspace, counters, k_scales, v_scales, order,
+                          alibi_slopes]
             return
         if partition_size is None:
             partition_size = 512
