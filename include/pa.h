@@ -276,8 +276,8 @@ pa_status pa_decode_splitk_fp8(float* ws_out, float* ws_m, float* ws_l,
  * row is quantised in groups of 64 dims, each with an offset and a scale of
  * its own, so a token is written once and never re-quantised:
  *   lo = the group's least value (bf16, so exact),
- *   scale = bf16((max - lo) / 15), round to nearest even (fp32 arithmetic; a
- *           range past the largest float counts as that),
+ *   scale = bf16((max - lo) * r), r the float nearest 1 / 15, round to nearest
+ *           even (fp32 arithmetic; a range past the largest float counts as that),
  *   code = clamp(round_half_even((x - lo) / scale), 0, 15); 0 where scale is 0.
  * The stored value is lo + scale * code, at most scale / 2 (and the rounding of
  * scale, 15 * 2^-9 of it) from x.  Values must be finite (a NaN gets code 0).
@@ -329,15 +329,17 @@ pa_status pa_decode_splitk_int4(float* ws_out, float* ws_m, float* ws_l, int max
  * in fp32 (products and sums rounded one by one), rounded to bf16 once; dims
  * from R on pass through.  q goes to q_out; k goes, rotated, and v as it is, to
  * the token's slot of the cache by the rule of the cache's kind: the bytes
- * stored are those of pa_reshape_and_cache (_int8, _fp8, _int4) on the rotated
- * k and v.
+ * stored in a bf16 or 4-bit cache are those of pa_reshape_and_cache (_int4) on
+ * the rotated k and v; INT8 and FP8 rows take their scale as max|x| times the
+ * float nearest 1 / 127 or 1 / 448 (one rounding step from the plain writes'
+ * quotient at most), and their codes from it by the plain writes' rule.
  *   q, key, value : [num_tokens] rows of heads * head_dim bf16, stride elements
  *     apart (a multiple of 8, at least the row): slices of one fused projection
  *     need no copy.  q_out [num_tokens, num_q_heads, head_dim], contiguous; it
  *     may be q itself (q_stride num_q_heads * head_dim), and overlaps no other
  *     input.  num_q_heads 0: q and q_out are not read.
  *   positions     : [num_tokens] int32.  Negative: a padding token, nothing of
- *     it is read or written.  max_position or more: as padding, and sets
+ *     it is written.  max_position or more: as padding, and sets
  *     PA_DEVERR_POSITION.
  *   cos_sin       : [max_position, rotary_dim] fp32, cosines then sines.
  *   slot_mapping  : as pa_reshape_and_cache; a negative slot keeps k and v out

@@ -3,7 +3,7 @@
 Each (token, KV head) row is quantised in groups of 64 dims:
 
     lo    = min of the group            (a bf16 value)
-    scale = bf16((max - lo) / 15)       (float32 arithmetic, nearest even)
+    scale = bf16((max - lo) * fl(1 / 15))   (float32 arithmetic, nearest even)
     code  = clamp(round_half_even((x - lo) / scale), 0, 15), 0 where scale is 0
     x    ~= lo + scale * code
 
@@ -25,7 +25,7 @@ def quantize(x_bits):
     lo, hi = g.min(-1), g.max(-1)
     with np.errstate(over="ignore"):
         rng = np.minimum(hi - lo, np.finfo(np.float32).max)
-    sc_bits = to_bf16_bits(rng / np.float32(15.0))
+    sc_bits = to_bf16_bits(rng * np.float32(1.0 / 15.0))
     sc = bf16_bits_to_f64(sc_bits).astype(np.float32)
     safe = np.where(sc > 0, sc, np.float32(1.0))[..., None]
     with np.errstate(over="ignore"):

@@ -793,7 +793,8 @@ pa_status rope_append_impl(void* q_out, const void* q, int64_t q_stride, const v
   if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       block_size <= 0 || num_blocks <= 0)
     return PA_ERR_INVALID_ARG;
-  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED_SHAPE;
+  if ((head_dim != 64 && head_dim != 128) || num_q_heads > 32767 || num_kv_heads > 8191)
+    return PA_ERR_UNSUPPORTED_SHAPE;
   if (kind != 0 && block_size != 16) return PA_ERR_UNSUPPORTED_SHAPE;
   if (rope) {
     if (max_position <= 0 || rotary_dim <= 0 || rotary_dim > head_dim ||

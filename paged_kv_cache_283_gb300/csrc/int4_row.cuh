@@ -43,13 +43,13 @@ __host__ __device__ __forceinline__ int v4_byte(int t, int c, int i) {
 }
 
 // A group's parameters from its least and largest value: the offset is the
-// least value (a bf16 value, so stored exactly), the scale a fifteenth of the
-// range rounded to bf16 (the codes are taken with the rounded scale; at most
-// 2^-9 above or below the exact one, so the largest code stays 15).  A range
-// past the largest float counts as that.
+// least value (a bf16 value, so stored exactly), the scale the range times the
+// float nearest 1 / 15, rounded to bf16 (the codes are taken with the rounded
+// scale; at most 2^-8 above or below the exact one, so the largest code stays
+// 15).  A range past the largest float counts as that.
 __device__ __forceinline__ uint32_t int4_params(float lo, float hi, float* scale) {
   const float range = fminf(__fsub_rn(hi, lo), FLT_MAX);
-  const uint32_t sc = __bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(range, 15.0f)));
+  const uint32_t sc = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(range, 1.0f / 15.0f)));
   *scale = __uint_as_float(sc << 16);
   return (sc << 16) | (__float_as_uint(lo) >> 16);
 }

@@ -173,7 +173,7 @@ cudaError_t launch_prefix_partials(const void* q, const void* k_cache, const voi
                                    cudaStream_t stream);
 cudaError_t launch_reshape_and_cache(const CacheWriteParams& p, cudaStream_t stream);
 cudaError_t launch_reshape_and_cache_int8(const CacheWriteParams& p, cudaStream_t stream);
-cudaError_t launch_rope_append(RopeAppendParams p, int head_dim, cudaStream_t stream);
+cudaError_t launch_rope_append(const RopeAppendParams& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const CopyBlocksParams& p, int num_pairs, int num_layers,
                                cudaStream_t stream);
 

@@ -259,24 +259,23 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// tanh of HK values times `k`, in place, to about 2e-7 of 1.  Where the warp's
-// values all stay within 0.3 -- caps lie well above the scores they bound -- an
-// odd polynomial (the first five terms of the series; the next is below 6e-8 of
-// the result there) in packed fused multiply-adds: 3.5 issue slots a score and
-// a maximum's half.  Elsewhere 1 - 2 / (1 + e^2z), two special-function
-// operations a score, which the softmax's own exponential already fills.
+// tanh of HK values times `k`, in place, to about 2e-7 of 1, or 1e-7 of the
+// result while the warp's values are small.  Caps lie well above the scores
+// they bound, so two terms of the odd series beside z serve while every |z| of
+// the warp is at most 0.1 (the next term, 17/315 z^6, is below 6e-8 there):
+// five packed multiply-adds a pair and half a maximum a score.  Elsewhere
+// 1 - 2 / (1 + e^2z), two special-function operations a score.
 template <int HK>
 __device__ __forceinline__ void tanh_scaled(uint32_t (&v)[HK], float k) {
   float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < HK; ++j) m4[j & 3] = fmaxf(m4[j & 3], fabsf(__uint_as_float(v[j])));
+  for (int j = 0; j < HK; j += 2)
+    m4[(j >> 1) & 3] = fmaxf(fmaxf(m4[(j >> 1) & 3], fabsf(__uint_as_float(v[j]))),
+                             fabsf(__uint_as_float(v[j + 1])));
   const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-  // (a NaN or an infinity among the scores also takes the second form: fmaxf
-  // drops a NaN, and the polynomial of a NaN is a NaN too)
-  if (__all_sync(kFullMask, mx * k <= 0.3f)) {
+  // (a NaN among the scores stays one in both forms; fmaxf drops it)
+  if (__all_sync(kFullMask, mx * k <= 0.1f)) {
     const float2 k2 = make_float2(k, k);
-    const float2 a4 = make_float2(2.1869488e-2f, 2.1869488e-2f);    // 62 / 2835
-    const float2 a3 = make_float2(-5.3968254e-2f, -5.3968254e-2f);  // -17 / 315
     const float2 a2 = make_float2(1.3333333e-1f, 1.3333333e-1f);    // 2 / 15
     const float2 a1 = make_float2(-3.3333333e-1f, -3.3333333e-1f);  // -1 / 3
     const float2 one = make_float2(1.f, 1.f);
@@ -285,10 +284,7 @@ __device__ __forceinline__ void tanh_scaled(uint32_t (&v)[HK], float k) {
       const float2 z = __fmul2_rn(
           make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), k2);
       const float2 u = __fmul2_rn(z, z);
-      float2 h = __ffma2_rn(u, a4, a3);
-      h = __ffma2_rn(u, h, a2);
-      h = __ffma2_rn(u, h, a1);
-      const float2 r = __fmul2_rn(z, __ffma2_rn(u, h, one));
+      const float2 r = __fmul2_rn(z, __ffma2_rn(u, __ffma2_rn(u, a2, a1), one));
       v[j] = __float_as_uint(r.x);
       v[j + 1] = __float_as_uint(r.y);
     }
@@ -345,7 +341,10 @@ __device__ __forceinline__ void pair_sync(int warp) {
 // with j <= p or j < prefix, and j > p - window.  The tile's chunks then start
 // at the block of the lowest key its first query sees (key0; blocks before it
 // are not read, and may be gone from the table), and positions below are
-// relative to it.
+// relative to it.  Chunks run from the last to the first: a distance bias
+// makes the nearest keys the heaviest, so the reference maximum is found at
+// once and does not climb chunk by chunk (each climb rescales O and takes the
+// weights twice).  The tiles of a sequence run from the last (the longest).
 template <int G, bool RULE>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tq,
@@ -357,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   griddep_wait();
   griddep_launch_dependents();
   const bool shared_prefix = p.split_blocks > 0;  // CTA-uniform
-  const int tile = blockIdx.x, kvh = blockIdx.y, b = shared_prefix ? 0 : blockIdx.z;
+  const int tile = RULE ? gridDim.x - 1 - blockIdx.x : blockIdx.x, kvh = blockIdx.y, b = shared_prefix ? 0 : blockIdx.z;
   const int split = shared_prefix ? blockIdx.z : 0;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -393,6 +392,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const int nk = shared_prefix ? ctx : max(ctx - n + min(n, i0 + TQ), prefix) - key0;
   const int nchunks = (nk + kKeys - 1) / kKeys;
   const int nblk_all = (nk + kBS - 1) / kBS;
+  // the keys' chunk that step c of the loops takes
+  auto chunk_at = [&](int c) -> int { return RULE ? nchunks - 1 - c : c; };
 
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(
@@ -448,13 +449,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // Lane j < 8: the raw table entry of block j of chunk c (checked at use),
     // fetched a chunk ahead so that the table's latency stays off the copies.
     auto fetch_id = [&](int c) -> int {
-      if (c >= nchunks || lane >= min(kChunkBlocks, nblk_all - c * kChunkBlocks)) return 0;
-      return __ldg(tbl + c * kChunkBlocks + lane);
+      const int kc = chunk_at(c);
+      if (c >= nchunks || lane >= min(kChunkBlocks, nblk_all - kc * kChunkBlocks)) return 0;
+      return __ldg(tbl + kc * kChunkBlocks + lane);
     };
     // K (or V) of chunk c into stage c % 3, one block per lane
     auto load = [&](int c, bool is_v, int id) {
       const int st = c % kStages;
-      const int nb = min(kChunkBlocks, nblk_all - c * kChunkBlocks);
+      const int nb = min(kChunkBlocks, nblk_all - chunk_at(c) * kChunkBlocks);
       uint64_t* bar = is_v ? &v_full[st] : &k_full[st];
       unsigned char* dst = sm + (is_v ? kV : kK) + 2 * st * kKVHalf + lane * kBox;
       if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(nb * 2 * kBox));
@@ -622,11 +624,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // the last key the row sees, the first, and its slope in the scores' unit
     const int row_hi = RULE ? max(pos, prefix - 1 - key0) : pos;
     const int row_lo = RULE && p.rule.window > 0 ? pos + 1 - p.rule.window : 0;
-    float slope = 0.f;
+    // (far_bias), or with every visible key at or before the row's position the
+    // bias as slope2 (j - p) in base-2 units, added with the reference
+    float slope = 0.f, slope2 = 0.f;
+    const bool far_bias = RULE && p.rule.slopes != nullptr && prefix > ctx - n + i0 + 1;
     if constexpr (RULE) {
-      if (p.rule.slopes != nullptr)
-        slope = __ldg(p.rule.slopes + kvh * G + r % G) * 1.4426950408889634f / p.unit;
+      if (p.rule.slopes != nullptr) {
+        const float s = __ldg(p.rule.slopes + kvh * G + r % G) * 1.4426950408889634f;
+        if (far_bias) slope = s / p.unit;
+        else slope2 = s;
+      }
     }
+    const bool near_bias = RULE && p.rule.slopes != nullptr && !far_bias;
     float m_used = -INFINITY;  // reference maximum of the exponentials (base 2)
     float l_sum = 0.f;
     bool ok = true;  // sticky: this thread's waits all succeeded
@@ -637,9 +646,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       bool lok = ok && mbar_wait_bounded(&s_done[sb], (c / kSBuf) & 1, p.err);
       lok = __all_sync(kFullMask, lok);
       uint32_t sv[HK];
+      const int kc = chunk_at(c);
       // causal mask
-      const int lim = row_ok ? row_hi - c * kKeys - HK * hcol : -1;  // visible: j <= lim
-      const int low = row_lo - c * kKeys - HK * hcol;               // and j >= low
+      const int lim = row_ok ? row_hi - kc * kKeys - HK * hcol : -1;  // visible: j <= lim
+      const int low = row_lo - kc * kKeys - HK * hcol;               // and j >= low
       const bool masked = !__all_sync(kFullMask, lim >= HK - 1 && (!RULE || low <= 0));
       auto scores = [&]() {
 #pragma unroll
@@ -650,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         tmem_wait_ld();
         if constexpr (RULE) {
           if (p.rule.softcap > 0.f) tanh_scaled<HK>(sv, p.cap_in);
-          if (p.rule.slopes != nullptr) {
-            const float at = static_cast<float>(c * kKeys + HK * hcol - pos);
+          if (far_bias) {  // keys after the row's own are visible: |p - j|
+            const float at = static_cast<float>(kc * kKeys + HK * hcol - pos);
 #pragma unroll
             for (int j = 0; j < HK; ++j)
               sv[j] = __float_as_uint(fmaf(-slope, fabsf(at + static_cast<float>(j)),
@@ -678,13 +688,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       float psum = 0.f;
       auto weights = [&]() {
         const bool live = m_used != -INFINITY;
-        const float2 neg2 = make_float2(live ? -m_used : 0.f, live ? -m_used : 0.f);
+        float2 neg2 = make_float2(live ? -m_used : 0.f, live ? -m_used : 0.f);
+        // RULE: neg2 of pair j is neg2 + slope2 (j, j + 1)
+        const float2 slope22 = make_float2(slope2, slope2);
+        if constexpr (RULE) {
+          if (near_bias) {
+            const float at = slope2 * static_cast<float>(kc * kKeys + HK * hcol - pos);
+            neg2 = make_float2(neg2.x + at, neg2.y + at);
+          }
+        }
         float2 ps4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                          make_float2(0.f, 0.f)};  // independent partial sums
 #pragma unroll
         for (int j = 0; j < HK; j += 2) {
+          float2 off = neg2;
+          if constexpr (RULE)
+            if (near_bias)
+              off = __ffma2_rn(make_float2(static_cast<float>(j), static_cast<float>(j + 1)),
+                               slope22, neg2);
           const float2 x = __ffma2_rn(
-              make_float2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), sl2x2, neg2);
+              make_float2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), sl2x2, off);
           const float2 e = make_float2(ex2(x.x), ex2(x.y));
           ps4[(j >> 1) & 3] = __fadd2_rn(ps4[(j >> 1) & 3], e);
           sv[j] = __float_as_uint(e.x);
@@ -718,6 +741,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         float mx = -INFINITY;
         if (lok) {
           scores();
+          if constexpr (RULE) {
+            if (near_bias) {  // with its bias, in the scores' unit
+              const float per = slope2 / sl2;
+              const float at = per * static_cast<float>(kc * kKeys + HK * hcol - pos);
+#pragma unroll
+              for (int j = 0; j < HK; ++j)
+                sv[j] = __float_as_uint(__uint_as_float(sv[j]) +
+                                        fmaf(per, static_cast<float>(j), at));
+            }
+          }
           // eight independent partial maxima (max is exact in any order)
           float m8[8];
 #pragma unroll
@@ -747,6 +780,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               alpha = ex2(m_used - mx);
               m_used = mx;
             }
+          }
+          if constexpr (RULE) {
+            if (near_bias) scores();  // without the bias, which weights() adds
           }
           weights();  // the scores were read again: weights against the reference
         }
@@ -800,12 +836,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       // V of the final chunk: keys past the last visible one may hold anything
       // (a partly filled block, or blocks not loaded); P is 0 there, but
       // 0 * NaN is not, so those rows are zeroed once the copies have landed.
-      const int vk = nk - c * kKeys;  // valid keys in this chunk
+      const int vk = nk - kc * kKeys;  // valid keys in this chunk
       // (RULE: so may the keys of the first block that no query of the tile sees.)
-      if (lok && (vk < kKeys || (RULE && c == 0 && vlo > 0))) {
+      if (lok && (vk < kKeys || (RULE && kc == 0 && vlo > 0))) {
         const int st = c % kStages;
         lok = mbar_wait_bounded(&v_full[st], (c / kStages) & 1, p.err);
-        if (lok && (r >= vk || (RULE && c == 0 && r < vlo)) && r < kKeys) {
+        if (lok && (r >= vk || (RULE && kc == 0 && r < vlo)) && r < kKeys) {
           const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int hh = hcol; hh < 2; hh += kRowThreads) {  // the 64-column halves

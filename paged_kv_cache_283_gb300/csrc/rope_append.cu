@@ -7,9 +7,8 @@
 // with the cosines and sines of the caller's table; dims from R on pass
 // through.  Products and sums are fp32, each rounded by itself (no fused
 // multiply-add), so that a result does not depend on which of a pair's two
-// products the compiler would fuse; a rotated value is rounded to bf16 once.
-// Quantised caches quantise those bf16 values, so that this launch stores the
-// bytes that the rotation followed by the plain cache write would.
+// products the compiler would fuse; a rotated value is rounded to bf16 once,
+// and quantised caches quantise those bf16 values.
 //
 // What bounds it: bytes (each value is read and written once; three
 // operations per value), or the launch itself for a decode step's few tokens.
@@ -35,6 +34,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlock = 16;  // tokens of a block of the 1-byte and 4-bit caches
+constexpr int64_t kOneRowThreads = 152 * 2048;  // the GPU's resident threads
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
   const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
@@ -148,7 +148,7 @@ __device__ __forceinline__ void store_quantised(const RopeAppendParams& p, bool 
     for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
     for (int m = L / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, m));
-    const float scale = __fdiv_rn(amax, Q == 2 ? 448.0f : 127.0f);
+    const float scale = __fmul_rn(amax, Q == 2 ? 1.0f / 448.0f : 1.0f / 127.0f);
     uint32_t w[4] = {0, 0, 0, 0};  // chunk ca's 8 codes, chunk cb's 8 codes
     if (scale > 0.f) {
 #pragma unroll
@@ -187,25 +187,43 @@ __device__ __forceinline__ void store_quantised(const RopeAppendParams& p, bool 
   }
 }
 
-// U rows at a time per thread; slots of a token (p.row_slots) take its rows
-// s, s + row_slots, ...  All L lanes of a row follow the same path.
+// grid (tokens, thread blocks per token); thread group s of a token (L lanes)
+// takes its rows s, s + row_slots, ..., U of them at most, loaded together and
+// before the position and the slot are known (their round trips overlap).  All
+// L lanes of a row follow the same path.
 template <int D, int Q, int U>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendParams p) {
   constexpr int L = D / 16;
   griddep_wait();  // the producer of q / key / value is complete
   griddep_launch_dependents();
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int j = static_cast<int>(id % L);
-  const int64_t group = id / L;
-  const int64_t t = group / p.row_slots;
-  const int s = static_cast<int>(group % p.row_slots);
-  if (t >= p.num_tokens) return;
+  const int j = threadIdx.x % L;
+  const int64_t t = blockIdx.x;
+  const int s = (blockIdx.y * blockDim.x + threadIdx.x) / L;
   const unsigned mask = ((1u << L) - 1u) << (threadIdx.x & 31 & ~(L - 1));
   const int rot_lanes = p.rotary_dim / 16;
   const int rows = p.num_q_heads + 2 * p.num_kv_heads;
+  if (s >= p.row_slots) return;
 
+  // this lane's chunks of a rotated row
+  const bool rot = j < rot_lanes;
+  const int ra = rot ? j : 2 * rot_lanes + 2 * (j - rot_lanes);
+  const int rb = rot ? j + rot_lanes : ra + 1;
+  uint4 wa[U], wb[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int r = s + u * p.row_slots;
+    if (r >= rows) break;
+    const int h = r - p.num_q_heads;
+    const bool is_v = h >= p.num_kv_heads;
+    const __nv_bfloat16* src =
+        h < 0 ? p.q + t * p.q_stride + r * D
+              : is_v ? p.value + t * p.value_stride + (h - p.num_kv_heads) * D
+                     : p.key + t * p.key_stride + h * D;
+    wa[u] = load16(src + 8 * (is_v ? 2 * j : ra));
+    wb[u] = load16(src + 8 * (is_v ? 2 * j + 1 : rb));
+  }
   const int pos = p.positions != nullptr ? __ldg(p.positions + t) : 0;
-  const int64_t slot = p.slot_mapping != nullptr ? __ldg(p.slot_mapping + t) : -1;
+  const int64_t slot = __ldg(p.slot_mapping + t);
   if (pos < 0) return;  // a padding token
   if (pos >= p.max_position) {
     if (s == 0 && j == 0) raise_error(p.err, PA_DEVERR_POSITION);
@@ -214,14 +232,14 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendP
   const bool bad_slot = slot >= p.num_slots;
   if (bad_slot && s == 0 && j == 0) raise_error(p.err, PA_DEVERR_SLOT);
   const bool put = slot >= 0 && !bad_slot;
-  const int64_t blk = put ? slot / p.block_size : 0;
-  const int off = put ? static_cast<int>(slot % p.block_size) : 0;
+  int64_t blk = slot >> 4;
+  int off = static_cast<int>(slot & 15);
+  if (p.block_size != 16 && put) {
+    blk = slot / p.block_size;
+    off = static_cast<int>(slot % p.block_size);
+  }
 
-  // this lane's chunks of a rotated row, and their cosines and sines
-  const bool rot = j < rot_lanes;
-  const int ra = rot ? j : 2 * rot_lanes + 2 * (j - rot_lanes);
-  const int rb = rot ? j + rot_lanes : ra + 1;
-  float cs[8], sn[8];
+  float cs[8], sn[8];  // the lane's cosines and sines
   if (rot) {
     const float* tab = p.cos_sin + static_cast<int64_t>(pos) * p.rotary_dim;
     const int half = p.rotary_dim / 2;
@@ -240,75 +258,66 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendP
     }
   }
 
-  for (int r0 = s; r0 < rows; r0 += U * p.row_slots) {
-    uint4 wa[U], wb[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * p.row_slots;
-      const int h = r - p.num_q_heads;
-      if (r >= rows || (h >= 0 && !put)) continue;
-      const bool is_v = h >= p.num_kv_heads;
-      const __nv_bfloat16* src =
-          h < 0 ? p.q + t * p.q_stride + static_cast<int64_t>(r) * D
-                : is_v ? p.value + t * p.value_stride + static_cast<int64_t>(h - p.num_kv_heads) * D
-                       : p.key + t * p.key_stride + static_cast<int64_t>(h) * D;
-      wa[u] = load16(src + 8 * (is_v ? 2 * j : ra));
-      wb[u] = load16(src + 8 * (is_v ? 2 * j + 1 : rb));
-    }
+  for (int u = 0; u < U; ++u) {
+    const int r = s + u * p.row_slots;
+    const int h = r - p.num_q_heads;
+    if (r >= rows || (h >= 0 && !put)) continue;
+    const bool is_v = h >= p.num_kv_heads;
+    if (rot && !is_v) {
+      float a[8], b[8];
+      unpack8(wa[u], a);
+      unpack8(wb[u], b);
+      if (p.interleaved) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * p.row_slots;
-      const int h = r - p.num_q_heads;
-      if (r >= rows || (h >= 0 && !put)) continue;
-      const bool is_v = h >= p.num_kv_heads;
-      if (rot && !is_v) {
-        float a[8], b[8];
-        unpack8(wa[u], a);
-        unpack8(wb[u], b);
-        if (p.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            rotate(a[2 * i], a[2 * i + 1], cs[i], sn[i]);
-            rotate(b[2 * i], b[2 * i + 1], cs[4 + i], sn[4 + i]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) rotate(a[i], b[i], cs[i], sn[i]);
+        for (int i = 0; i < 4; ++i) {
+          rotate(a[2 * i], a[2 * i + 1], cs[i], sn[i]);
+          rotate(b[2 * i], b[2 * i + 1], cs[4 + i], sn[4 + i]);
         }
-        wa[u] = pack8(a);
-        wb[u] = pack8(b);
-      }
-      const int ca = is_v ? 2 * j : ra, cb = is_v ? 2 * j + 1 : rb;
-      if (h < 0) {
-        __nv_bfloat16* dst = p.q_out + (t * p.num_q_heads + r) * static_cast<int64_t>(D);
-        *reinterpret_cast<uint4*>(dst + 8 * ca) = wa[u];
-        *reinterpret_cast<uint4*>(dst + 8 * cb) = wb[u];
-        continue;
-      }
-      const int64_t tile = blk * p.num_kv_heads + (is_v ? h - p.num_kv_heads : h);
-      if constexpr (Q == 0) {
-        __nv_bfloat16* dst =
-            (is_v ? p.v_cache : p.k_cache) + (tile * p.block_size + off) * static_cast<int64_t>(D);
-        *reinterpret_cast<uint4*>(dst + 8 * ca) = wa[u];
-        *reinterpret_cast<uint4*>(dst + 8 * cb) = wb[u];
       } else {
-        float x[16];
-        unpack8(wa[u], *reinterpret_cast<float(*)[8]>(x));
-        unpack8(wb[u], *reinterpret_cast<float(*)[8]>(x + 8));
-        store_quantised<D, Q>(p, is_v, x, ca, cb, tile, off, j, mask);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rotate(a[i], b[i], cs[i], sn[i]);
       }
+      wa[u] = pack8(a);
+      wb[u] = pack8(b);
+    }
+    const int ca = is_v ? 2 * j : ra, cb = is_v ? 2 * j + 1 : rb;
+    if (h < 0) {
+      __nv_bfloat16* dst = p.q_out + (t * p.num_q_heads + r) * static_cast<int64_t>(D);
+      *reinterpret_cast<uint4*>(dst + 8 * ca) = wa[u];
+      *reinterpret_cast<uint4*>(dst + 8 * cb) = wb[u];
+      continue;
+    }
+    const int64_t tile = blk * p.num_kv_heads + (is_v ? h - p.num_kv_heads : h);
+    if constexpr (Q == 0) {
+      __nv_bfloat16* dst =
+          (is_v ? p.v_cache : p.k_cache) + (tile * p.block_size + off) * static_cast<int64_t>(D);
+      *reinterpret_cast<uint4*>(dst + 8 * ca) = wa[u];
+      *reinterpret_cast<uint4*>(dst + 8 * cb) = wb[u];
+    } else {
+      float x[16];
+      unpack8(wa[u], *reinterpret_cast<float(*)[8]>(x));
+      unpack8(wb[u], *reinterpret_cast<float(*)[8]>(x + 8));
+      store_quantised<D, Q>(p, is_v, x, ca, cb, tile, off, j, mask);
     }
   }
 }
 
 template <int D, int Q>
 cudaError_t launch_t(const RopeAppendParams& p, cudaStream_t stream) {
-  constexpr int L = D / 16;
-  const int64_t threads = static_cast<int64_t>(p.num_tokens) * p.row_slots * L;
-  const int64_t blocks = (threads + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_pdl(rope_append_kernel<D, Q, 2>, dim3(static_cast<unsigned>(blocks)),
-                    dim3(kThreads), 0, stream, p);
+  constexpr int L = D / 16, U = 4;
+  const int rows = p.num_q_heads + 2 * p.num_kv_heads;
+  // While one row per thread fills less than the GPU's threads, the call is a
+  // chain of round trips and a row to a thread is the shortest; past that a
+  // thread takes up to U rows, which share its cosines and sines.
+  const bool one = static_cast<int64_t>(p.num_tokens) * rows * L <= kOneRowThreads;
+  RopeAppendParams r = p;
+  r.row_slots = one ? rows : (rows + U - 1) / U;
+  const int threads = (r.row_slots * L + 31) / 32 * 32;
+  const dim3 block(threads < kThreads ? threads : kThreads);
+  const dim3 grid(p.num_tokens, (threads + block.x - 1) / block.x);
+  return one ? launch_pdl(rope_append_kernel<D, Q, 1>, grid, block, 0, stream, r)
+             : launch_pdl(rope_append_kernel<D, Q, U>, grid, block, 0, stream, r);
 }
 
 template <int D>
@@ -323,11 +332,8 @@ cudaError_t launch_d(const RopeAppendParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_rope_append(RopeAppendParams p, int head_dim, cudaStream_t stream) {
+cudaError_t launch_rope_append(const RopeAppendParams& p, int head_dim, cudaStream_t stream) {
   if (p.num_tokens == 0) return cudaSuccess;
-  const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-  // one thread per row and lane: nothing waits but on its own loads
-  p.row_slots = rows;
   if (head_dim == 128) return launch_d<128>(p, stream);
   if (head_dim == 64) return launch_d<64>(p, stream);
   return cudaErrorInvalidValue;

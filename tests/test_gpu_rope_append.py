@@ -1,6 +1,7 @@
 """Rotary embedding + cache write on the GPU: q and the bf16 pools bit-exact
-against the float32 definition and near the float64 rotation; the quantised pools
-the bytes that the plain cache writes give for the rotated k; padding, bad
+against the float32 definition and near the float64 rotation; the 4-bit pools
+the bytes that the plain cache write gives for the rotated k, the INT8 and FP8
+pools those of their rule; padding, bad
 positions and slots, strided inputs, in-place q, graph replay."""
 import numpy as np
 import pytest
@@ -11,7 +12,7 @@ from oracle import rope as OR
 from paged_kv_cache_283_gb300 import pa
 from paged_kv_cache_283_gb300.inputs import normal_bf16
 
-from gpu_helpers import bf16_to_f64, dev_bf16, host_bits
+from gpu_helpers import bf16_to_f64, dev_bf16, host_bits, v_pool_logical, v_pool_stored
 
 pytestmark = pytest.mark.gpu
 
@@ -30,8 +31,28 @@ def _pools(kind, nb, hkv, d, rng):
                               for _ in "kv"]
 
 
-PLAIN = {"bf16": pa.pa_reshape_and_cache, "int8": pa.pa_reshape_and_cache_int8,
-         "fp8": pa.pa_reshape_and_cache_fp8, "int4": pa.pa_reshape_and_cache_int4}
+def _write_1byte(key, value, kp, vp, ks, vs, slots):
+    """INT8 / FP8 rows in float32: scale = amax * fl(1 / 127 or 1 / 448), codes by
+    division, round half to even (E4M3: torch's conversion of the quotient)."""
+    fp8 = kp.dtype == torch.uint8
+    r = np.float32(1.0 / (448.0 if fp8 else 127.0))
+    logical = [kp.cpu().numpy(), v_pool_logical(vp.cpu().numpy(), fp8)]
+    for pool, sc, x in zip(logical, (ks, vs), (key, value)):
+        f = x.float().cpu().numpy()
+        scale = np.abs(f).max(-1) * r
+        y = torch.from_numpy(f / np.where(scale > 0, scale, np.float32(1))[..., None])
+        codes = y.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else \
+            y.round().clamp(-127, 127).to(torch.int8)
+        for t, s in enumerate(slots.tolist()):
+            if s >= 0:
+                pool[s // 16, :, s % 16] = codes[t].numpy()
+                sc[s // 16, :, s % 16] = torch.from_numpy(scale[t]).cuda()
+    kp.copy_(torch.from_numpy(logical[0]))
+    vp.copy_(torch.from_numpy(v_pool_stored(logical[1], fp8)))
+
+
+PLAIN = {"bf16": pa.pa_reshape_and_cache, "int8": _write_1byte, "fp8": _write_1byte,
+         "int4": pa.pa_reshape_and_cache_int4}
 
 
 def _inputs(seed, T, hq, hkv, d, strided):
