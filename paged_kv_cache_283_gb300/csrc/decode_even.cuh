@@ -1,0 +1,608 @@
+// Paged decode attention with the batch's work cut evenly among the GPU's
+// warps, sm_103a: for the 4-bit cache (Q = 3) and, with changed scores, the
+// bf16 cache (Q = 0, RULE).
+//
+// The partitioned kernel (decode_kernel.cuh) gives every CTA a partition of one
+// sequence; CTAs of a second wave, the tail of the longest, and each CTA's
+// start and merge cost it a third to a half of its time on a 4-bit cache, whose
+// tiles are quickly read.  Here the launch is one wave of resident CTAs.  A unit is the
+// context of one (sequence, KV head), counted in steps (32 tokens of a 4-bit
+// cache, 16 of a bf16 one); the units stand in a row, and warp w of N takes the
+// steps [w W / N, (w + 1) W / N) of all W: every warp the same number, whatever
+// the lengths, with no plan made on the host.  Warps work alone: each finds its
+// place from the context lengths, copies its tiles through its own ring of
+// bulk copies that runs on over the ends of units, and keeps its own softmax.
+//
+// A unit inside one warp's range goes straight to the output.  A unit that
+// spans several leaves one partial (m, l, sum p v) per warp in the workspace,
+// and the last warp to arrive at it merges them in warp order (so the result
+// does not depend on who is last): up to 16 warps at one counter; a longer unit
+// first inside groups of 16 consecutive warps, then over the groups.  Nobody
+// waits for another warp, and every counter is left at zero.
+#pragma once
+
+#include "decode_kernel.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kEvenWarps = 4;   // warps of a CTA
+constexpr int kEvenGroup = 16;  // warps whose partials one warp merges at once
+// fewer steps than this to a warp (while every unit has one) do not pay
+constexpr int kEvenMinSteps = 4;
+
+template <int D, int G, int Q>
+struct Even {
+  static constexpr int S = D == 128 ? 2 : 4;  // ring stages of a warp
+  static constexpr int CTAS = Q == 3 ? (G <= 4 ? 4 : 3) : (G <= 4 ? 3 : 2);  // per SM
+  using Lay = SmemLayout<D, G, kEvenWarps, S, Q>;
+  static constexpr int PATCH = Q == 3 ? 512 : 4 * D;
+  static constexpr int WARP = (Lay::TILES + Lay::PS + Lay::ALPHA + PATCH + Lay::BARS + 127) / 128 * 128;
+  static constexpr int SMEM = kEvenWarps * WARP;
+  // a lane's share of a unit's result: V values and the (m, l) of H heads
+  using Geo = Geometry<D, G>;
+  static constexpr int H = Q == 3 ? 2 : (G / Geo::ROWS > 0 ? G / Geo::ROWS : 1);
+  static constexpr int V = Q == 3 ? 4 * Out4<D, G>::TILES : 8 * H;
+  static constexpr int SLOT = 32 * (V + 2 * H);  // floats of a partial in the workspace
+};
+
+struct EvenArgs {
+  float* ws;           // [2 * warps][SLOT]
+  unsigned* unit_cnt;  // [num_seqs * num_kv_heads]
+  unsigned* group_cnt; // [2 * groups]
+  int warps;           // of the grid
+};
+
+template <int D, int G, int Q, bool RULE>
+__global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
+    paged_decode_even_kernel(const DecodeParams p, const EvenArgs ev) {
+  using E = Even<D, G, Q>;
+  using Lay = typename E::Lay;
+  using Geo = Geometry<D, G>;
+  constexpr int S = E::S, SB = kStepBlocks<Q>, BS = kBlockSize, WS = 32 / SB;
+  constexpr int L = Geo::L, R = Geo::R, P = Geo::P;
+  extern __shared__ __align__(128) unsigned char smem[];
+  if (!p.early_read) griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;       // Q = 3
+  const int sub = lane % L, rg = lane / L;         // Q = 0
+  // consecutive ranges go to different SMs: a small batch spreads over them
+  const int me = warp * gridDim.x + blockIdx.x;
+  unsigned char* wbase = smem + warp * E::WARP;
+  unsigned char* tiles = wbase;
+  float* ps = reinterpret_cast<float*>(wbase + Lay::TILES);
+  float* alpha_s = reinterpret_cast<float*>(wbase + Lay::TILES + Lay::PS);
+  unsigned char* patch = wbase + Lay::TILES + Lay::PS + Lay::ALPHA;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(patch + E::PATCH);
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+
+  // A sequence's context, clamped to its table; the first visible token; the
+  // block that holds it; the steps from there on.
+  const int B = p.num_seqs, hkv = p.num_kv_heads;
+  const int cap = p.max_blocks_per_seq * BS;
+  struct Seq {
+    int ctx, lo, wb, nblk, T;
+  };
+  auto seq_at = [&](int b) {
+    Seq q;
+    q.ctx = max(0, min(__ldg(p.context_lens + b), cap));
+    q.lo = 0;
+    if constexpr (RULE) {
+      if (p.rule.window > 0) q.lo = max(0, q.ctx - p.rule.window);
+    }
+    q.wb = q.lo / BS;
+    q.nblk = (q.ctx + BS - 1) / BS;
+    q.T = (q.nblk - q.wb + SB - 1) / SB;
+    return q;
+  };
+  // Lane l sums the sequences [l K, (l + 1) K): their steps, and how many are
+  // not empty.
+  const int K = (B + 31) / 32;
+  int sum = 0, some = 0;
+  bool bad = false;
+  for (int i = 0; i < K; ++i) {
+    const int b = lane * K + i;
+    if (b < B) {
+      const int T = seq_at(b).T;
+      sum += T;
+      some += T > 0;
+      if (me == 0) {
+        const int c = __ldg(p.context_lens + b);
+        bad |= c < 0 || c > cap;
+      }
+    }
+  }
+  if (bad) raise_error(p.err, PA_DEVERR_CONTEXT_LEN);
+  int incl = sum;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int up = __shfl_up_sync(kFullMask, incl, m);
+    if (lane >= m) incl += up;
+    some += __shfl_xor_sync(kFullMask, some, m);
+  }
+  const int excl = incl - sum;
+  // (W fits 31 bits: the launcher bounds the tables' steps)
+  const int W = __shfl_sync(kFullMask, incl, 31) * hkv;
+  const int N = min(ev.warps, max(W / kEvenMinSteps, some * hkv));
+  auto start_of = [&](int w) {  // warp w's first step (N >= 1)
+    return static_cast<int>(static_cast<int64_t>(w) * W / N);
+  };
+  auto warp_of = [&](int step) {  // the last warp that starts at or before a step
+    return static_cast<int>(((step + 1ll) * N - 1) / W);
+  };
+  const bool work = me < N;  // then W >= N >= 1
+  const int w0 = work ? start_of(me) : 0;
+  const int n = work ? start_of(me + 1) - w0 : 0;
+
+  // A place in the row of units: step s of the T of unit (b, h); rem: blocks from
+  // the unit's first on.
+  struct Place {
+    int b, h, s, T, rem;
+  };
+  auto set_seq = [&](Place& x) {
+    const Seq q = seq_at(x.b);
+    x.T = q.T;
+    x.rem = q.nblk - q.wb;
+  };
+  Place at{};
+  if (work) {
+    const int tb = w0 / hkv;  // steps of one head before it
+    const int owner = __ffs(__ballot_sync(kFullMask, excl <= tb && tb < excl + sum)) - 1;
+    int run = __shfl_sync(kFullMask, excl, owner);
+    at.b = owner * K;
+    set_seq(at);
+    while (tb >= run + at.T) {
+      run += at.T;
+      ++at.b;
+      set_seq(at);
+    }
+    const int r = w0 - run * hkv;
+    at.h = r / at.T;
+    at.s = r - at.h * at.T;
+  }
+  // the first step of the next unit (b = B past the last)
+  auto next_unit = [&](Place& x) {
+    x.s = 0;
+    if (++x.h < hkv) return;
+    x.h = 0;
+    do {
+      ++x.b;
+      if (x.b >= B) return;
+      set_seq(x);
+    } while (x.T == 0);
+  };
+
+  // The copies run ahead of the sums, over unit ends.  Their block ids come in
+  // windows of 32 (lane l: block l of the window), fetched one window ahead.
+  auto load_ids = [&](const Place& x) -> int {
+    const int j = x.s * SB + lane;
+    return x.b < B && j < x.rem
+               ? __ldg(p.block_tables + static_cast<size_t>(x.b) * p.max_blocks_per_seq +
+                       (RULE ? seq_at(x.b).wb : 0) + j)
+               : 0;
+  };
+  // the window in use: head, first step, end, blocks from its first on
+  int win_h = 0, win_s = 0, win_end = 0, win_rem = 0, ids = 0;
+  // the next one, and its ids
+  Place nwin = at;
+  int nids = 0;
+  auto fetch_window = [&]() { nids = load_ids(nwin); };
+  auto take_window = [&]() {
+    win_h = nwin.h;
+    win_s = nwin.s;
+    win_end = min(nwin.T, nwin.s + WS);
+    win_rem = nwin.rem - nwin.s * SB;
+    ids = nids;
+    if (win_end < nwin.T)
+      nwin.s = win_end;
+    else
+      next_unit(nwin);
+  };
+  const uint64_t policy = l2_policy_evict_first();
+  int is = 0, issued = 0;
+  if (n > 0) {
+    fetch_window();
+    take_window();
+    is = win_s;
+    fetch_window();
+  }
+  auto issue = [&](int st) {
+    if (is == win_end) {
+      take_window();
+      is = win_s;
+      if (issued + (win_end - win_s) < n) fetch_window();  // it will be read
+    }
+    // lanes 2 u and 2 u + 1 copy the K and the V tile of the step's block u
+    const int u = lane >> 1;
+    int id = __shfl_sync(kFullMask, ids, ((is - win_s) * SB + (u & (SB - 1))) & 31);
+    const int here = min(SB, win_rem - (is - win_s) * SB);  // blocks in the step
+    if (u < here) {
+      if (id < 0 || id >= p.num_blocks) {  // never dereferenced: block 0 is read instead
+        if ((lane & 1) == 0) raise_error(p.err, PA_DEVERR_BLOCK_ID);
+        id = 0;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&bars[st], here * 2 * Lay::KT);
+      const size_t tile = static_cast<size_t>(id) * hkv + win_h;
+      const unsigned char* src;
+      if constexpr (Q == 3)
+        src = (lane & 1) ? p.v4 : p.k4;
+      else
+        src = reinterpret_cast<const unsigned char*>((lane & 1) ? p.v_cache : p.k_cache);
+      bulk_copy_g2s(tiles + st * Lay::STAGE + lane * Lay::KT, src + tile * Lay::KT, Lay::KT,
+                    &bars[st], policy);
+    }
+    ++is;
+    ++issued;
+  };
+  for (int i = 0; i < S && i < n; ++i) issue(i);
+  if (p.early_read) griddep_wait();
+
+  // an empty sequence's output is zeros, and a new token has no place there
+  for (int b = me; b < B; b += ev.warps) {
+    if (__ldg(p.context_lens + b) > 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<size_t>(b) * p.num_q_heads * D);
+    for (int i = lane; i < p.num_q_heads * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
+    if (p.slot_mapping != nullptr && lane == 0 && __ldg(p.slot_mapping + b) >= 0)
+      raise_error(p.err, PA_DEVERR_SLOT);
+  }
+
+  // the unit being summed: q, softmax state, sums
+  uint32_t qa[D / 8];
+  float qf = 0.f;
+  float qs4[D / kInt4Group];
+  float2 q2[Q == 0 ? G : 1][4];
+  float acc8[Q == 3 ? D / 16 : 1][4];
+  float zacc[Cols4<D, G>::NZ];
+  float2 acc[Q == 0 ? G : 1][4];
+  float m_run = -INFINITY, l_run = 0.f, vbound = 0x1p-126f, vinv = 0x1p126f;
+  RuleLane rule;
+  const int my_head = (sub * R) / P, my_i0 = (sub * R) % P;  // Q = 0
+  bool patched = false;
+  Seq unit_seq{};
+
+  auto begin = [&](bool reaches_end) {
+    unit_seq = seq_at(at.b);
+    m_run = -INFINITY;
+    l_run = 0.f;
+    if constexpr (Q == 3) {
+      load_q_4b<D, G>(p, at.b, at.h, lane, qa, qf, qs4);
+      vbound = 0x1p-126f;
+      vinv = 0x1p126f;
+#pragma unroll
+      for (int g = 0; g < Cols4<D, G>::NZ; ++g) zacc[g] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc8[c][k] = 0.f;
+    } else {
+      load_q_bf16<D, G>(p, at.b, at.h, sub, q2);
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[g][k] = make_float2(0.f, 0.f);
+    }
+    if constexpr (RULE) {
+      if (p.rule.slopes != nullptr)
+        rule.slope2 = 1.4426950408889634f * __ldg(p.rule.slopes + at.h * G + my_head);
+      rule.last = unit_seq.ctx - 1;
+      rule.first = unit_seq.lo;
+    }
+    // the warp that reads the unit's last step writes the sequence's new token
+    patched = p.slot_mapping != nullptr && reaches_end &&
+              fused_cache_write<D, Q>(
+                  p, at.b, at.h, unit_seq.ctx,
+                  p.block_tables + static_cast<size_t>(at.b) * p.max_blocks_per_seq, lane, patch);
+    if (patched) __syncwarp();
+  };
+  if constexpr (RULE) {
+    rule.cap2 = p.rule.softcap * 1.4426950408889634f;
+    rule.inv_cap2 = rule.cap2 > 0.f ? 1.f / rule.cap2 : 0.f;
+  }
+
+  // A finished piece: v, the lane's V sums, and (m, l) of its H heads; which of
+  // them v[e] belongs to.
+  float v[E::V];
+  float2 ml[E::H];
+  auto head_of = [](int e) { return Q == 3 ? e & 1 : e >> 3; };
+  auto gather = [&]() {
+    if constexpr (Q == 3) {
+      l_run += __shfl_xor_sync(kFullMask, l_run, 1);
+      l_run += __shfl_xor_sync(kFullMask, l_run, 2);
+      finish_4b<D, G>(acc8, zacc, vbound, lane, v);
+      ml[0] = make_float2(__shfl_sync(kFullMask, m_run, 8 * tig),
+                          __shfl_sync(kFullMask, l_run, 8 * tig));
+      ml[1] = make_float2(__shfl_sync(kFullMask, m_run, 8 * tig + 4),
+                          __shfl_sync(kFullMask, l_run, 8 * tig + 4));
+    } else {
+#pragma unroll
+      for (int m = 1; m < Geo::HEAD_LANES; m <<= 1)
+        l_run += __shfl_xor_sync(kFullMask, l_run, m);
+#pragma unroll
+      for (int m = L; m < 32; m <<= 1) {
+        l_run += __shfl_xor_sync(kFullMask, l_run, m);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            acc[g][k].x += __shfl_xor_sync(kFullMask, acc[g][k].x, m);
+            acc[g][k].y += __shfl_xor_sync(kFullMask, acc[g][k].y, m);
+          }
+      }
+      // row group rg keeps heads rg H .. rg H + H - 1
+#pragma unroll
+      for (int h = 0; h < E::H; ++h) {
+#pragma unroll
+        for (int g = 0; g < Geo::ROWS; ++g) {
+          if (rg == g) {
+            constexpr int H = E::H;
+            const float2(&a)[4] = acc[(g * H + h) % G];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              v[8 * h + 2 * k] = a[k].x;
+              v[8 * h + 2 * k + 1] = a[k].y;
+            }
+          }
+        }
+        const int src = (rg * E::H + h) % G * Geo::HEAD_LANES;
+        ml[h] = make_float2(__shfl_sync(kFullMask, m_run, src),
+                            __shfl_sync(kFullMask, l_run, src));
+      }
+    }
+  };
+  auto write_out = [&]() {
+    float inv[E::H];
+#pragma unroll
+    for (int h = 0; h < E::H; ++h) inv[h] = 1.0f / ml[h].y;
+    __nv_bfloat16* o =
+        p.out + (static_cast<size_t>(at.b) * p.num_q_heads + static_cast<size_t>(at.h) * G) * D;
+    if constexpr (Q == 3) {
+      if (Cols4<D, G>::owner(tig)) {
+        o += QCols<G>::head(2 * tig) * D + 16 * Out4<D, G>::first(tig) + gid;
+#pragma unroll
+        for (int c = 0; c < Out4<D, G>::TILES; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            o[(k & 1) * D + 16 * c + 8 * (k >> 1)] =
+                __float2bfloat16_rn(v[4 * c + k] * inv[k & 1]);
+      }
+    } else if (rg * E::H < G) {
+#pragma unroll
+      for (int h = 0; h < E::H; ++h) {
+        __nv_bfloat162 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = __float22bfloat162_rn(
+              make_float2(v[8 * h + 2 * k] * inv[h], v[8 * h + 2 * k + 1] * inv[h]));
+        *reinterpret_cast<uint4*>(o + (rg * E::H + h) * D + sub * 8) =
+            *reinterpret_cast<const uint4*>(w);
+      }
+    }
+  };
+  auto store_partial = [&](float* slot) {
+#pragma unroll
+    for (int i = 0; i < E::V / 4; ++i)
+      __stcg(reinterpret_cast<float4*>(slot) + 32 * i + lane,
+             make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+#pragma unroll
+    for (int h = 0; h < E::H; ++h)
+      __stcg(reinterpret_cast<float2*>(slot + 32 * E::V) + 32 * h + lane, ml[h]);
+  };
+  // v, ml: `count` partials merged in order, each weighed against the running
+  // maximum.  slot_at(i): the i-th.
+  auto merge = [&](int count, auto slot_at) {
+    constexpr int U = 2;  // loaded together
+#pragma unroll
+    for (int e = 0; e < E::V; ++e) v[e] = 0.f;
+#pragma unroll
+    for (int h = 0; h < E::H; ++h) ml[h] = make_float2(-INFINITY, 0.f);
+    for (int i0 = 0; i0 < count; i0 += U) {
+      float4 x[U][E::V / 4];
+      float2 y[U][E::H];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i0 + u >= count) break;
+        const float* slot = slot_at(i0 + u);
+#pragma unroll
+        for (int i = 0; i < E::V / 4; ++i)
+          x[u][i] = __ldcg(reinterpret_cast<const float4*>(slot) + 32 * i + lane);
+#pragma unroll
+        for (int h = 0; h < E::H; ++h)
+          y[u][h] = __ldcg(reinterpret_cast<const float2*>(slot + 32 * E::V) + 32 * h + lane);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i0 + u >= count) break;
+        float a[E::H], c[E::H];
+#pragma unroll
+        for (int h = 0; h < E::H; ++h) {
+          const float m = fmaxf(ml[h].x, y[u][h].x);
+          a[h] = ml[h].x == m ? 1.f : exp2f(ml[h].x - m);  // (both -inf: 1)
+          c[h] = y[u][h].x == m ? 1.f : exp2f(y[u][h].x - m);
+          ml[h] = make_float2(m, ml[h].y * a[h] + y[u][h].y * c[h]);
+        }
+#pragma unroll
+        for (int i = 0; i < E::V / 4; ++i) {
+          const float xs[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int e = 4 * i + k;
+            v[e] = v[e] * a[head_of(e)] + xs[k] * c[head_of(e)];
+          }
+        }
+      }
+    }
+  };
+  // One arrival of `expected` at a counter, after the warp's writes; the last
+  // sees all the others' writes and leaves the counter at zero.
+  auto arrive = [&](unsigned* cnt, int expected) -> bool {
+    __threadfence();
+    __syncwarp();
+    unsigned old = 0;
+    if (lane == 0) old = atomicAdd(cnt, 1u);
+    old = __shfl_sync(kFullMask, old, 0);
+    if (old + 1u != static_cast<unsigned>(expected)) return false;
+    __threadfence();
+    if (lane == 0) *cnt = 0u;
+    return true;
+  };
+
+  bool ok = true;  // every wait so far succeeded (warp-uniform)
+  int st = 0, k = 0;
+  unsigned ph = 0;
+  while (k < n) {
+    const int len = min(at.T - at.s, n - k);
+    const bool ends = at.s + len == at.T;
+    begin(ends);
+#pragma unroll 1
+    for (int i = 0; i < len; ++i, ++k) {
+      if (ok) ok = __all_sync(kFullMask, mbar_wait_bounded(&bars[st], ph, p.err));
+      if (!ok) continue;
+      const int j0 = (unit_seq.wb + (at.s + i) * SB) * BS;  // the step's first token
+      const int nvalid = min(BS * SB, unit_seq.ctx - j0);
+      unsigned char* stage = tiles + st * Lay::STAGE;
+      if (patched && i + 1 == len) {
+        patch_tile<D, Q>(stage + (SB > 1 ? (nvalid - 1) / BS * 2 * Lay::KT : 0), Lay::KT, patch,
+                         (nvalid - 1) % BS, lane);
+        __syncwarp();
+      }
+      const bool full = nvalid == BS * SB && (!RULE || j0 >= unit_seq.lo);
+      if constexpr (Q == 3) {
+        if (full)
+          tile_step_4b<D, G, SB, true, RULE>(stage, qa, qf, qs4, acc8, m_run, l_run, zacc,
+                                             vbound, vinv, nvalid, lane, rule, j0);
+        else
+          tile_step_4b<D, G, SB, false, RULE>(stage, qa, qf, qs4, acc8, m_run, l_run, zacc,
+                                              vbound, vinv, nvalid, lane, rule, j0);
+      } else {
+        const uint4* kt = reinterpret_cast<const uint4*>(stage);
+        const uint4* vt = reinterpret_cast<const uint4*>(stage + Lay::KT);
+        if (full)
+          tile_step<D, G, true, RULE>(kt, vt, ps, alpha_s, q2, acc, m_run, l_run, nvalid, lane,
+                                      sub, rg, my_head, my_i0, rule, j0);
+        else
+          tile_step<D, G, false, RULE>(kt, vt, ps, alpha_s, q2, acc, m_run, l_run, nvalid, lane,
+                                       sub, rg, my_head, my_i0, rule, j0);
+      }
+      __syncwarp();  // every lane is done with the stage
+      if (issued < n) issue(st);
+      if (++st == S) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+    gather();
+    bool done = at.s == 0 && ends;  // the whole unit is this warp's
+    if (!done) {
+      // the unit's warps, and this one's place among them
+      const int u0 = w0 + k - len - at.s;
+      const int wf = warp_of(u0), wl = warp_of(u0 + at.T - 1);
+      auto slot_of = [&](int w) {
+        return ev.ws + static_cast<size_t>(2 * w + (w == wf ? 1 : 0)) * E::SLOT;
+      };
+      // level 0: the warps of one group of a unit that spans several (a group
+      // holds at most one unit that comes in from the group before, and at most
+      // one that begins in it and goes on into the next); level 1: a unit's
+      // groups, or its warps where one group holds them all
+      const int g0 = wf / kEvenGroup, g1 = wl / kEvenGroup, g = me / kEvenGroup;
+      float* mine = slot_of(me);
+#pragma unroll 1
+      for (int level = g0 == g1 ? 1 : 0; level < 2; ++level) {
+        store_partial(mine);
+        unsigned* cnt;
+        int first, stride, count;
+        if (level == 0) {
+          first = max(wf, g * kEvenGroup);
+          stride = 1;
+          count = min(wl, g * kEvenGroup + kEvenGroup - 1) - first + 1;
+          cnt = ev.group_cnt + 2 * g + (g > g0 ? 0 : 1);
+        } else {
+          first = g0 == g1 ? wf : g0 * kEvenGroup;
+          stride = g0 == g1 ? 1 : kEvenGroup;
+          count = g0 == g1 ? wl - wf + 1 : g1 - g0 + 1;
+          cnt = ev.unit_cnt + static_cast<size_t>(at.b) * hkv + at.h;
+        }
+        if (!arrive(cnt, count)) break;
+        merge(count, [&](int i) { return slot_of(max(wf, first + i * stride)); });
+        mine = slot_of(max(wf, first));
+        done = level == 1;
+      }
+    }
+    if (done) write_out();
+    if (ends)
+      next_unit(at);
+    else
+      at.s += len;
+  }
+  // Only after a timed-out wait: copies still in flight land (bounded) before
+  // the shared memory can be reused.
+  if (!ok)
+    for (int i = 0; i < S; ++i) mbar_wait_bounded(&bars[i], ph ^ (i < st ? 1u : 0u), p.err);
+}
+
+// Warps of a launch on the current device: one wave of resident CTAs.
+template <int D, int G, int Q>
+cudaError_t even_grid(int* ctas) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) *ctas = sms * Even<D, G, Q>::CTAS;
+  return e;
+}
+
+template <int D, int G, int Q, bool RULE>
+cudaError_t launch_even_t(const DecodeParams& p, cudaStream_t stream) {
+  using E = Even<D, G, Q>;
+  static std::atomic<uint64_t> smem_set{0};
+  auto kernel = paged_decode_even_kernel<D, G, Q, RULE>;
+  cudaError_t e = allow_smem(kernel, E::SMEM, smem_set);
+  int ctas = 0;
+  if (e == cudaSuccess) e = even_grid<D, G, Q>(&ctas);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than the tables hold steps
+  const int64_t steps = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads *
+                        ((p.max_blocks_per_seq + kStepBlocks<Q> - 1) / kStepBlocks<Q>);
+  if (steps > 0x7fffffff) return cudaErrorInvalidValue;
+  if (steps < ctas) ctas = static_cast<int>(steps);
+  EvenArgs ev;
+  ev.ws = p.ws_o;
+  ev.unit_cnt = p.counters;
+  ev.group_cnt = p.counters + static_cast<size_t>(p.num_seqs) * p.num_kv_heads;
+  ev.warps = ctas * kEvenWarps;
+  return launch_pdl(kernel, dim3(ctas), dim3(kEvenWarps * 32), E::SMEM, stream, p, ev);
+}
+
+template <int D, int Q, bool RULE>
+cudaError_t launch_even_d(const DecodeParams& p, int group, cudaStream_t stream) {
+  switch (group) {
+    case 2: return launch_even_t<D, 2, Q, RULE>(p, stream);
+    case 4: return launch_even_t<D, 4, Q, RULE>(p, stream);
+    case 8: return launch_even_t<D, 8, Q, RULE>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+// Floats of workspace a launch may use on the current device (0: no device).
+template <int D, int Q>
+size_t even_floats_d(int group) {
+  auto of = [](cudaError_t e, int ctas, size_t slot) {
+    return e == cudaSuccess ? static_cast<size_t>(ctas) * kEvenWarps * 2 * slot : 0;
+  };
+  int ctas = 0;
+  switch (group) {
+    case 2: { const auto e = even_grid<D, 2, Q>(&ctas); return of(e, ctas, Even<D, 2, Q>::SLOT); }
+    case 4: { const auto e = even_grid<D, 4, Q>(&ctas); return of(e, ctas, Even<D, 4, Q>::SLOT); }
+    case 8: { const auto e = even_grid<D, 8, Q>(&ctas); return of(e, ctas, Even<D, 8, Q>::SLOT); }
+    default: return 0;
+  }
+}
+
+}  // namespace
+
+}  // namespace pa

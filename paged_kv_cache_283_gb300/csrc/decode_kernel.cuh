@@ -265,6 +265,79 @@ __device__ __forceinline__ void patch_tile(unsigned char* tile, int kt_bytes,
   }
 }
 
+// q of (sequence b, KV head kvh) for tile_step_4b: the lane's words, the factor
+// of the MMA sums and the head's group sums.
+template <int D, int G>
+__device__ __forceinline__ void load_q_4b(const DecodeParams& p, int b, int kvh, int lane,
+                                          uint32_t (&qa)[D / 8], float& qf,
+                                          float (&qs4)[D / kInt4Group]) {
+  // Lane (gid, tig): head(gid)'s dims 16 tig .. 16 tig + 15 of every group,
+  // times a power of two 2^k that brings the head's largest |q| to
+  // [2^13, 2^14): a bf16 value has 8 significant bits, so its f16 is exact
+  // down to 2^-28 of that (with the factor 2^-4 of the odd nibbles).
+  using C = QCols<G>;
+  const int gid = lane >> 2, tig = lane & 3;
+  const __nv_bfloat16* qh =
+      p.q + (static_cast<size_t>(b) * p.num_q_heads + static_cast<size_t>(kvh) * G +
+             C::head(gid)) * D + 16 * tig;
+  float f[D / 4];
+#pragma unroll
+  for (int u = 0; u < D / 32; ++u) {  // 8 dims: half u % 2 of group u / 2's sixteen
+    const uint4 w =
+        __ldg(reinterpret_cast<const uint4*>(qh + kInt4Group * (u / 2) + 8 * (u % 2)));
+    const float2 a = bf16x2_to_float2(w.x), c = bf16x2_to_float2(w.y);
+    const float2 d = bf16x2_to_float2(w.z), e = bf16x2_to_float2(w.w);
+    f[8 * u] = a.x; f[8 * u + 1] = a.y; f[8 * u + 2] = c.x; f[8 * u + 3] = c.y;
+    f[8 * u + 4] = d.x; f[8 * u + 5] = d.y; f[8 * u + 6] = e.x; f[8 * u + 7] = e.y;
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < D / 4; ++k) amax = fmaxf(amax, fabsf(f[k]));
+  amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
+  const int ebits = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu);
+  const int kexp = min(127, max(-126, 140 - ebits));
+  const float up = __uint_as_float(static_cast<uint32_t>(kexp + 127) << 23);
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) {  // nibbles 0..7 of word w: dims f[8 w ..]
+    qa[4 * w] = f16x2_rn(f[8 * w] * up, f[8 * w + 4] * up);
+    qa[4 * w + 1] = f16x2_rn(f[8 * w + 1] * up * 0.0625f, f[8 * w + 5] * up * 0.0625f);
+    qa[4 * w + 2] = f16x2_rn(f[8 * w + 2] * up, f[8 * w + 6] * up);
+    qa[4 * w + 3] = f16x2_rn(f[8 * w + 3] * up * 0.0625f, f[8 * w + 7] * up * 0.0625f);
+  }
+#pragma unroll
+  for (int g = 0; g < D / kInt4Group; ++g) {
+    float x = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x += f[16 * g + k];
+    x += __shfl_xor_sync(kFullMask, x, 1);
+    x += __shfl_xor_sync(kFullMask, x, 2);
+    qs4[g] = x * p.scale_log2;
+  }
+  qf = ldexpf(p.scale_log2, 24 - kexp);
+}
+
+// q of (sequence b, KV head kvh) for tile_step: the lane's 8 dims of each head,
+// times the score scale.
+template <int D, int G>
+__device__ __forceinline__ void load_q_bf16(const DecodeParams& p, int b, int kvh, int sub,
+                                            float2 (&q2)[G][4]) {
+  const __nv_bfloat16* qb =
+      p.q + (static_cast<size_t>(b) * p.num_q_heads + static_cast<size_t>(kvh) * G) * D + sub * 8;
+  uint4 qw[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+    qw[g] = __ldg(reinterpret_cast<const uint4*>(qb + static_cast<size_t>(g) * D));
+  const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    q2[g][0] = __fmul2_rn(bf16x2_to_float2(qw[g].x), sc2);
+    q2[g][1] = __fmul2_rn(bf16x2_to_float2(qw[g].y), sc2);
+    q2[g][2] = __fmul2_rn(bf16x2_to_float2(qw[g].z), sc2);
+    q2[g][3] = __fmul2_rn(bf16x2_to_float2(qw[g].w), sc2);
+  }
+}
+
 // Q: the cache's element type: 0 = bf16, 1 = INT8, 2 = FP8 (E4M3).  INT8 and
 // FP8 share the 1-byte-code tile layout (codes + per-token scales) and the
 // tile step (tile_step_1b: QK and PV on the tensor cores, weights in
@@ -423,65 +496,9 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
       }
       qf = ldexpf(p.scale_log2, -kexp);
     } else if constexpr (Q == 3) {
-      // Lane (gid, tig): head(gid)'s dims 16 tig .. 16 tig + 15 of every group,
-      // times a power of two 2^k that brings the head's largest |q| to
-      // [2^13, 2^14): a bf16 value has 8 significant bits, so its f16 is exact
-      // down to 2^-28 of that (with the factor 2^-4 of the odd nibbles).
-      using C = QCols<G>;
-      const int gid = lane >> 2, tig = lane & 3;
-      const __nv_bfloat16* qh =
-          p.q + (static_cast<size_t>(b) * p.num_q_heads + static_cast<size_t>(kvh) * G +
-                 C::head(gid)) * D + 16 * tig;
-      float f[D / 4];
-  #pragma unroll
-      for (int u = 0; u < D / 32; ++u) {  // 8 dims: half u % 2 of group u / 2's sixteen
-        const uint4 w =
-            __ldg(reinterpret_cast<const uint4*>(qh + kInt4Group * (u / 2) + 8 * (u % 2)));
-        const float2 a = bf16x2_to_float2(w.x), c = bf16x2_to_float2(w.y);
-        const float2 d = bf16x2_to_float2(w.z), e = bf16x2_to_float2(w.w);
-        f[8 * u] = a.x; f[8 * u + 1] = a.y; f[8 * u + 2] = c.x; f[8 * u + 3] = c.y;
-        f[8 * u + 4] = d.x; f[8 * u + 5] = d.y; f[8 * u + 6] = e.x; f[8 * u + 7] = e.y;
-      }
-      float amax = 0.f;
-  #pragma unroll
-      for (int k = 0; k < D / 4; ++k) amax = fmaxf(amax, fabsf(f[k]));
-      amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
-      const int ebits = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu);
-      const int kexp = min(127, max(-126, 140 - ebits));
-      const float up = __uint_as_float(static_cast<uint32_t>(kexp + 127) << 23);
-  #pragma unroll
-      for (int w = 0; w < D / 32; ++w) {  // nibbles 0..7 of word w: dims f[8 w ..]
-        qa[4 * w] = f16x2_rn(f[8 * w] * up, f[8 * w + 4] * up);
-        qa[4 * w + 1] = f16x2_rn(f[8 * w + 1] * up * 0.0625f, f[8 * w + 5] * up * 0.0625f);
-        qa[4 * w + 2] = f16x2_rn(f[8 * w + 2] * up, f[8 * w + 6] * up);
-        qa[4 * w + 3] = f16x2_rn(f[8 * w + 3] * up * 0.0625f, f[8 * w + 7] * up * 0.0625f);
-      }
-  #pragma unroll
-      for (int g = 0; g < D / kInt4Group; ++g) {
-        float x = 0.f;
-  #pragma unroll
-        for (int k = 0; k < 16; ++k) x += f[16 * g + k];
-        x += __shfl_xor_sync(kFullMask, x, 1);
-        x += __shfl_xor_sync(kFullMask, x, 2);
-        qs4[g] = x * p.scale_log2;
-      }
-      qf = ldexpf(p.scale_log2, 24 - kexp);
+      load_q_4b<D, G>(p, b, kvh, lane, qa, qf, qs4);
     } else if constexpr (Q == 0) {
-      const __nv_bfloat16* qb =
-          p.q + (static_cast<size_t>(b) * p.num_q_heads + static_cast<size_t>(kvh) * G) * D + sub * 8;
-      uint4 qw[G];
-  #pragma unroll
-      for (int g = 0; g < G; ++g)
-        qw[g] = __ldg(reinterpret_cast<const uint4*>(qb + static_cast<size_t>(g) * D));
-      const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-  #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        q2[g][0] = __fmul2_rn(bf16x2_to_float2(qw[g].x), sc2);
-        q2[g][1] = __fmul2_rn(bf16x2_to_float2(qw[g].y), sc2);
-        q2[g][2] = __fmul2_rn(bf16x2_to_float2(qw[g].z), sc2);
-        q2[g][3] = __fmul2_rn(bf16x2_to_float2(qw[g].w), sc2);
-      }
+      load_q_bf16<D, G>(p, b, kvh, sub, q2);
     } else {
       // q of each head to int8 codes with one fp32 scale, by the cache's rule
       // (scale = amax / 127, code = round-half-even(q / scale)), once per CTA:
@@ -698,9 +715,9 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
   // 1-byte caches: the warp's power-of-two bound on the V scales it has
   // weighted (raise_v_bound) and its reciprocal; acc8 is in units of it
   float vbound = 0x1p-126f, vinv = 0x1p126f;
-  float zacc[D / kInt4Group];  // 4-bit cache: the lane's share of head gid's sums p * lo
+  float zacc[Cols4<D, G>::NZ];  // 4-bit cache: the lane's share of head gid's sums p * lo
 #pragma unroll
-  for (int g = 0; g < D / kInt4Group; ++g) zacc[g] = 0.f;
+  for (int g = 0; g < Cols4<D, G>::NZ; ++g) zacc[g] = 0.f;
   const int my_head = (sub * R) / P;  // bf16 cache: the lane's score head and first pass
   const int my_i0 = (sub * R) % P;
   RuleLane rule;
@@ -861,26 +878,20 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
       }
     }
     if constexpr (Q == 3) {
-      // codes were fed as code * 2^-24 (dims 16 c + gid) and code * 2^-20 (+ 8);
-      // the offsets' sums of heads 2 tig, 2 tig + 1 come from rows 2 tig, 2 tig + 1
-      const float up = vbound * 0x1p20f;
+      float o4[4 * Out4<D, G>::TILES];
+      finish_4b<D, G>(acc8, zacc, vbound, lane, o4);
+      if (Cols4<D, G>::owner(tig)) {
+        const int ha = C::head(2 * tig);
 #pragma unroll
-      for (int g = 0; g < D / kInt4Group; ++g) {
-        zacc[g] += __shfl_xor_sync(kFullMask, zacc[g], 1);
-        zacc[g] += __shfl_xor_sync(kFullMask, zacc[g], 2);
-        const float za = __shfl_sync(kFullMask, zacc[g], 8 * tig);
-        const float zb = __shfl_sync(kFullMask, zacc[g], 8 * tig + 4);
-#pragma unroll
-        for (int c = 4 * g; c < 4 * g + 4; ++c) {
-          acc8[c][0] = fmaf(acc8[c][0] * 16.f, up, za);
-          acc8[c][1] = fmaf(acc8[c][1] * 16.f, up, zb);
-          acc8[c][2] = fmaf(acc8[c][2], up, za);
-          acc8[c][3] = fmaf(acc8[c][3], up, zb);
+        for (int c = 0; c < Out4<D, G>::TILES; ++c) {
+          const int d0 = 16 * (Out4<D, G>::first(tig) + c) + gid;
+          mrg[ha * D + d0] = o4[4 * c];
+          mrg[(ha + 1) * D + d0] = o4[4 * c + 1];
+          mrg[ha * D + d0 + 8] = o4[4 * c + 2];
+          mrg[(ha + 1) * D + d0 + 8] = o4[4 * c + 3];
         }
       }
-      vbound = 1.f;
-    }
-    if (C::part0(tig)) {
+    } else if (C::part0(tig)) {
       const int ha = C::head(2 * tig);
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {

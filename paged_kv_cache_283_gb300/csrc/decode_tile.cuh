@@ -548,11 +548,27 @@ __device__ __forceinline__ void tile_step_1b(const unsigned char* __restrict__ k
 // c_g of q . code over group g and qs_g = the sum of q over it,
 //   s = sum_g sc_g c_g + lo_g qs_g.
 // Group 0 uses the MMA's rows 0..7 and group 1 rows 8..15, so one accumulator
-// holds both.  PV: out^T = V^T . W with W's column = head, the weights of group
-// g being p * sc_g (one f16 each: 11 bits, so an output's error is about 2^-12
-// of its size, against the 2^-9 of its bf16 rounding), and the offsets' share,
-// sum p * lo_g, summed in fp32 beside it.  V nibbles of dims 16 c + gid are
-// scaled 2^-24 and those of dims 16 c + gid + 8 2^-20, undone once at the end.
+// holds both.  PV: out^T = V^T . W with the weights of group g being p * sc_g
+// (one f16 each: 11 bits, so an output's error is about 2^-12 of its size,
+// against the 2^-9 of its bf16 rounding), and the offsets' share, sum p * lo_g,
+// summed in fp32 beside it.  V nibbles of dims 16 c + gid are scaled 2^-24 and
+// those of dims 16 c + gid + 8 2^-20, undone once at the end.
+//
+// W's 8 columns: one head each for G = 8, two MMA operands for two groups.  For
+// G <= 4 and two groups, column n is head n % G with the weights of group
+// n / G % 2, so one operand serves both groups (an m-tile's other columns are
+// not read), and a lane weighs its tokens for one group only.
+template <int D, int G>
+struct Cols4 {
+  static constexpr int NG = D / kInt4Group;
+  static constexpr bool PACK = G < 8 && NG == 2;
+  static constexpr int NZ = PACK ? 1 : NG;  // weight operands, offset sums per lane
+  static __device__ __forceinline__ int group(int n) { return PACK ? n / G % 2 : 0; }
+  // whether PV columns 2 tig, 2 tig + 1 hold results no other lane holds
+  static __device__ __forceinline__ bool owner(int tig) {
+    return G == 8 || 2 * tig < (PACK ? 2 * G : G);
+  }
+};
 
 // The lane's words of q (qa), the head's group sums (qs, times the score
 // scale) and the factor of the MMA sums (qf).
@@ -561,11 +577,13 @@ __device__ __forceinline__ void tile_step_4b(const unsigned char* __restrict__ s
                                              const uint32_t (&qa)[D / 8], float qf,
                                              const float (&qs)[D / kInt4Group],
                                              float (&acc)[D / 16][4], float& m_run,
-                                             float& l_run, float (&zacc)[D / kInt4Group],
+                                             float& l_run, float (&zacc)[Cols4<D, G>::NZ],
                                              float& vbound, float& vinv, int nvalid, int lane,
                                              const RuleLane& rule, int j0) {
   constexpr int KT = int4_tile_bytes(D), NG = D / kInt4Group;
+  constexpr int NZ = Cols4<D, G>::NZ;
   const int gid = lane >> 2, tig = lane & 3;
+  const int my_group = Cols4<D, G>::group(gid);
   float s[NB][4];
 #pragma unroll
   for (int u = 0; u < NB; ++u) {
@@ -648,7 +666,7 @@ __device__ __forceinline__ void tile_step_4b(const unsigned char* __restrict__ s
   m_run = m_new;
 
   // V parameters of the lane's tokens: [u][h] tokens 8 h + 2 tig, + 1
-  uint32_t vw[NB][2][2][NG];
+  uint32_t vw[NB][2][2][NZ];
   float vm = 0.f;
 #pragma unroll
   for (int u = 0; u < NB; ++u)
@@ -656,7 +674,10 @@ __device__ __forceinline__ void tile_step_4b(const unsigned char* __restrict__ s
     for (int h = 0; h < 2; ++h) {
       const unsigned char* par =
           stage + u * 2 * KT + KT + 8 * D + (8 * h + 2 * tig) * NG * 4;
-      if constexpr (NG == 2) {
+      if constexpr (Cols4<D, G>::PACK) {
+        vw[u][h][0][0] = *reinterpret_cast<const uint32_t*>(par + 4 * my_group);
+        vw[u][h][1][0] = *reinterpret_cast<const uint32_t*>(par + 4 * my_group + 8);
+      } else if constexpr (NG == 2) {
         const uint4 x = *reinterpret_cast<const uint4*>(par);
         vw[u][h][0][0] = x.x; vw[u][h][0][1] = x.y;
         vw[u][h][1][0] = x.z; vw[u][h][1][1] = x.w;
@@ -668,7 +689,7 @@ __device__ __forceinline__ void tile_step_4b(const unsigned char* __restrict__ s
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < NZ; ++g) {
           if constexpr (!FULL) {  // a hidden token's parameters may be anything
             if (!(t + e < nvalid && (!RULE || j0 + t + e >= rule.first))) vw[u][h][e][g] = 0u;
           }
@@ -679,6 +700,8 @@ __device__ __forceinline__ void tile_step_4b(const unsigned char* __restrict__ s
   if (__any_sync(kFullMask, vm > vbound)) {
     vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 1));
     vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 2));
+    if constexpr (Cols4<D, G>::PACK)  // the other group's rows
+      vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 4 * G));
     r = raise_v_bound(vm, vbound, vinv);
   }
   if (__any_sync(kFullMask, alpha != 1.0f) || r != 1.0f) {
@@ -686,9 +709,9 @@ __device__ __forceinline__ void tile_step_4b(const unsigned char* __restrict__ s
     const float fb = __shfl_sync(kFullMask, alpha, 8 * tig + 4) * r;
     scale_acc<D>(acc, fa, fb);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) zacc[g] *= alpha;
+    for (int g = 0; g < NZ; ++g) zacc[g] *= alpha;
   }
-  uint32_t b[NB][2][NG];
+  uint32_t b[NB][2][NZ];
 #pragma unroll
   for (int u = 0; u < NB; ++u)
 #pragma unroll
@@ -696,7 +719,7 @@ __device__ __forceinline__ void tile_step_4b(const unsigned char* __restrict__ s
       const float p0 = s[u][2 * h], p1 = s[u][2 * h + 1];
       const float y0 = p0 * vinv, y1 = p1 * vinv;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+      for (int g = 0; g < NZ; ++g) {
         b[u][h][g] = f16x2_rn(y0 * __uint_as_float(vw[u][h][0][g] & 0xffff0000u),
                               y1 * __uint_as_float(vw[u][h][1][g] & 0xffff0000u));
         zacc[g] = fmaf(p0, __uint_as_float(vw[u][h][0][g] << 16), zacc[g]);
@@ -715,8 +738,48 @@ __device__ __forceinline__ void tile_step_4b(const unsigned char* __restrict__ s
       for (int k = 0; k < 4; ++k) {
         const uint32_t y = w[k] >> 8;
         mma_f16(acc[4 * v + k], w[k] & 0x000F000Fu, w[k] & 0x00F000F0u, y & 0x000F000Fu,
-                y & 0x00F000F0u, b[u][0][v], b[u][1][v]);
+                y & 0x00F000F0u, b[u][0][NZ == 2 ? v : 0], b[u][1][NZ == 2 ? v : 0]);
       }
+    }
+  }
+}
+
+// The lane's sums of a finished run of tile_step_4b: out[k] (before the division
+// by l) of the m-tiles it owns (Cols4::owner), in order: (dim 16 c + gid; column
+// 2 tig), (same; 2 tig + 1), (dim 16 c + gid + 8; the two columns), for the
+// owned c; zacc is reduced over the row's lanes.  All 32 lanes must call it.
+template <int D, int G>
+struct Out4 {
+  static constexpr int TILES = Cols4<D, G>::PACK ? 4 : D / 16;  // owned m-tiles
+  static __device__ __forceinline__ int first(int tig) {        // the first of them
+    return Cols4<D, G>::PACK ? 4 * Cols4<D, G>::group(2 * tig) : 0;
+  }
+};
+template <int D, int G>
+__device__ __forceinline__ void finish_4b(float (&acc)[D / 16][4],
+                                          float (&zacc)[Cols4<D, G>::NZ], float vbound, int lane,
+                                          float (&out)[4 * Out4<D, G>::TILES]) {
+  const int tig = lane & 3;
+  // codes were fed as code * 2^-24 (dims 16 c + gid) and code * 2^-20 (+ 8)
+  const float up = vbound * 0x1p20f;
+  float za[Cols4<D, G>::NZ], zb[Cols4<D, G>::NZ];
+#pragma unroll
+  for (int g = 0; g < Cols4<D, G>::NZ; ++g) {
+    zacc[g] += __shfl_xor_sync(kFullMask, zacc[g], 1);
+    zacc[g] += __shfl_xor_sync(kFullMask, zacc[g], 2);
+    // the offsets' sums of columns 2 tig, 2 tig + 1 come from those rows
+    za[g] = __shfl_sync(kFullMask, zacc[g], 8 * tig);
+    zb[g] = __shfl_sync(kFullMask, zacc[g], 8 * tig + 4);
+  }
+  const bool second = Out4<D, G>::first(tig) != 0;
+#pragma unroll
+  for (int c = 0; c < Out4<D, G>::TILES; ++c) {
+    const int g = Cols4<D, G>::NZ == 2 ? c / 4 : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float x = acc[c][k];
+      if constexpr (Cols4<D, G>::PACK) x = second ? acc[c + 4][k] : x;
+      out[4 * c + k] = fmaf(k < 2 ? x * 16.f : x, up, k % 2 == 0 ? za[g] : zb[g]);
     }
   }
 }

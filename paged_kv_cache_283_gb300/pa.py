@@ -29,6 +29,8 @@ PA_DEVERR_ORDER = 0x10
 PA_DEVERR_PREFIX = 0x20
 PA_DEVERR_POSITION = 0x40
 PA_STEP_EARLY_READ = 0x1
+PA_SPLIT_EVEN = -1
+PA_EVEN_MAX_SEQS = 4096
 
 # Every function include/pa.h declares: name -> (restype, argtypes).
 _vp, _i, _u, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_float, ctypes.c_size_t
@@ -81,6 +83,8 @@ SIGNATURES = {
     "pa_decode_step_biased": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i,
                                    _i, _i, _i, _f, _f, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _vp,
                                    _i, _vp]),
+    "pa_even_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "pa_even_counters": (_sz, [_i, _i]),
     "pa_rope_reshape_and_cache": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
                                        _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
     "pa_rope_reshape_and_cache_int8": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
@@ -640,6 +644,29 @@ def step_counters(num_seqs, num_kv_heads, device="cuda"):
     return torch.zeros(num_seqs * num_kv_heads, dtype=torch.int32, device=device)
 
 
+def even_workspace(num_q_heads, num_kv_heads, head_dim, kv, device="cuda"):
+    """(workspace float tensor, None, None) for a pa_decode_step with
+    partition_size PA_SPLIT_EVEN over a "bf16" (changed scores) or "int4" cache:
+    its size does not depend on the batch."""
+    torch = _torch()
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        n = lib().pa_even_workspace_bytes(num_q_heads, num_kv_heads, head_dim,
+                                          {"bf16": 0, "int4": 4}[kv])
+    if n == 0:
+        raise ValueError("even_workspace: unsupported shape")
+    return torch.empty(n // 4, dtype=torch.float32, device=device), None, None
+
+
+def even_counters(num_seqs, num_kv_heads, device="cuda"):
+    """Zeroed counters for a pa_decode_step with partition_size PA_SPLIT_EVEN."""
+    torch = _torch()
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        n = lib().pa_even_counters(num_seqs, num_kv_heads)
+    return torch.zeros(n, dtype=torch.int32, device=device)
+
+
 # Past this many partitions per sequence a split-K pa_decode_step merges in a
 # second launch, the items are nearly all full partitions and the
 # longest-first order has nothing to balance (long contexts measured slower
@@ -754,7 +781,20 @@ def _step_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, key,
         kvs = (_dev(key, torch.bfloat16, "key", 3), _dev(value, torch.bfloat16, "value", 3),
                _dev(slot_mapping, torch.int64, "slot_mapping", 1))
     ps = int(partition_size)
-    if ps > 0:
+    if ps == PA_SPLIT_EVEN:
+        if not (four or ruled):
+            raise ValueError("pa_decode_step: PA_SPLIT_EVEN needs a 4-bit cache or changed scores")
+        if workspace is None or counters is None:
+            raise ValueError("pa_decode_step: PA_SPLIT_EVEN needs a workspace and counters")
+        if order is not None:
+            raise ValueError("pa_decode_step: PA_SPLIT_EVEN takes no order")
+        need = lib().pa_even_workspace_bytes(hq, hkv, d, 4 if four else 0)
+        if need == 0 or workspace[0].numel() * 4 < need or \
+                counters.numel() < lib().pa_even_counters(B, hkv):
+            raise ValueError("pa_decode_step: even_workspace / even_counters of this shape")
+        wsa = (_dev(workspace[0], torch.float32, "workspace", 1), none, none,
+               _dev(counters, torch.int32, "counters", 1), 0)
+    elif ps > 0:
         if workspace is None or counters is None:
             raise ValueError("pa_decode_step: split-K needs a workspace and counters")
         ws_o, ws_m, ws_l = workspace
@@ -794,6 +834,8 @@ def pa_decode_step(out, q, k_cache, v_cache, block_tables, context_lens, scale, 
     """Cache write of each sequence's new token (key / value [B, Hkv, D] at
     slot_mapping [B], which must be the slot of position context_lens[b] - 1)
     and the decode, in one launch.  partition_size 0: whole-sequence CTAs;
+    PA_SPLIT_EVEN (4-bit cache, changed scores): cut evenly among the GPU's
+    warps (workspace = even_workspace(...), counters = even_counters(...));
     > 0: split-K merged in the same launch (workspace = splitk_workspace(...),
     counters = step_counters(...)).  The cache dtype picks bf16 / INT8 (int8)
     / FP8 (uint8 codes, with k_scales / v_scales) / 4-bit (uint8 [NB, Hkv, 9 *
@@ -1111,7 +1153,9 @@ class DecodeStep:
     After a launch that raised PA_DEVERR_ORDER or PA_DEVERR_WAIT_TIMEOUT,
     call recover() before the next one.  softcap, alibi_slopes and window change
     the scores (pa_decode_step_biased); with a window the plan, the workspace
-    and the order cover the window only.  key, value and slot_mapping None:
+    and the order cover the window only.  Over a 4-bit cache, or with changed
+    scores, partition_size None cuts the work evenly among the GPU's warps
+    (PA_SPLIT_EVEN), which needs no plan.  key, value and slot_mapping None:
     attention only.
 
     Every argument is checked and marshalled once, here; each call then makes
@@ -1139,7 +1183,18 @@ class DecodeStep:
             self.split = bool(split)
             B, hq, d = q.shape
             hkv = k_cache.shape[1]
-            if self.split and host_context_lens is not None and partition_size is None:
+            ruled = bool(softcap) or alibi_slopes is not None or bool(window)
+            even = self.split and (four or ruled) and order is None and (
+                partition_size == PA_SPLIT_EVEN or
+                (partition_size is None and workspace is None and B <= PA_EVEN_MAX_SEQS))
+            if even:
+                # every warp the same share of the batch: nothing to plan
+                partition_size = PA_SPLIT_EVEN
+                if workspace is None:
+                    workspace = even_workspace(hq, hkv, d, "int4" if four else "bf16", q.device)
+                if counters is None:
+                    counters = even_counters(B, hkv, q.device)
+            elif self.split and host_context_lens is not None and partition_size is None:
                 # chosen for these contexts (plan_decode_step): the partition
                 # size for a longest-first launch, and that order.  The
                 # workspace and the order cover the block tables' capacity

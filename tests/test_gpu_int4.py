@@ -88,6 +88,15 @@ def _all_ways(case, scale, parts=(512,), what=""):
                               counters=counters, early_read=early)
             _gate(out, ref, V, f"{what} step {part}")
         assert not counters.any()
+    ws, counters = pa.even_workspace(hq, dk.shape[1], d, "int4"), pa.even_counters(B, dk.shape[1])
+    ws[0].fill_(float("nan"))
+    for early in (False, True):
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        pa.pa_decode_step(out, dq, dk, dv, t, c, scale, partition_size=pa.PA_SPLIT_EVEN,
+                          workspace=ws, counters=counters, early_read=early)
+        _gate(out, ref, V, f"{what} even")
+        assert not counters.any()
     assert pa.pa_get_device_error() == 0
 
 
@@ -115,6 +124,15 @@ def test_int4_cache_write_bit_exact(d):
 def test_int4_decode(hq, hkv, d):
     case = _case(hq + d, [1, 0, 15, 16, 17, 31, 32, 33, 500, 1023], hq, hkv, d)
     _all_ways(case, d ** -0.5, (16, 48, 256, 512), f"hq={hq} hkv={hkv} d={d}")
+
+
+@pytest.mark.parametrize("ctx,hq,hkv", [
+    ([5000], 8, 1), ([40000], 8, 2), ([20000, 7, 0, 30000], 8, 1), ([2047] * 40, 8, 2),
+    (list(range(0, 1300, 13)), 4, 2), ([33] * 700, 4, 1)])
+def test_int4_even_split_shares(ctx, hq, hkv):
+    # units over many warps and groups of warps, warps over many units
+    case = _case(len(ctx), ctx, hq, hkv, 64 if hq == 4 else 128)
+    _all_ways(case, 0.088, (), f"{len(ctx)} sequences")
 
 
 def test_int4_decode_more_than_sixteen_partitions():
@@ -177,7 +195,7 @@ def test_int4_bad_block_ids_and_lengths():
 
 
 @pytest.mark.parametrize("d", [128, 64])
-@pytest.mark.parametrize("part", [0, 16, 48, 256])
+@pytest.mark.parametrize("part", [0, 16, 48, 256, pa.PA_SPLIT_EVEN])
 def test_int4_step_writes_and_attends(d, part):
     rng, ctx, tables, pools, q = _case(8 + d, [1, 16, 17, 33, 400], 8, 2, d)
     B = len(ctx)
@@ -189,7 +207,9 @@ def test_int4_step_writes_and_attends(d, part):
     out = torch.empty(B, 8, d, dtype=torch.bfloat16, device="cuda")
     pa.pa_clear_device_error()
     kw = {}
-    if part:
+    if part == pa.PA_SPLIT_EVEN:
+        kw = dict(workspace=pa.even_workspace(8, 2, d, "int4"), counters=pa.even_counters(B, 2))
+    elif part:
         kw = dict(workspace=pa.splitk_workspace(B, 8, d, 400, part),
                   counters=pa.step_counters(B, 2))
     pa.pa_decode_step(out, dev_bf16(q), dk, dv, _dev(tables, np.int32), _dev(ctx, np.int32), 0.1,
