@@ -25,6 +25,7 @@ SOURCES = ["api.cu", "decode.cu", "decode_int4.cu", "decode_biased.cu", "decode_
            "prefill.cu", "prefill_biased.cu", "allocator.cpp", "sha256.cpp", "scheduler.cpp", "splitk_plan.cpp"]
 HEADERS = [os.path.join(ROOT, "include", "pa.h"), os.path.join(CSRC, "internal.h"),
            os.path.join(CSRC, "device.cuh"), os.path.join(CSRC, "decode_tile.cuh"),
+           os.path.join(CSRC, "decode_tile4.cuh"),
            os.path.join(CSRC, "decode_kernel.cuh"), os.path.join(CSRC, "decode_even.cuh"),
            os.path.join(CSRC, "prefill_kernel.cuh"),
            os.path.join(CSRC, "int4_row.cuh"),

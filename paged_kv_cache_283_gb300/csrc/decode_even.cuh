@@ -42,8 +42,8 @@ struct Even {
   static constexpr int SMEM = kEvenWarps * WARP;
   // a lane's share of a unit's result: V values and the (m, l) of H heads
   using Geo = Geometry<D, G>;
-  static constexpr int H = Q == 3 ? 2 : (G / Geo::ROWS > 0 ? G / Geo::ROWS : 1);
-  static constexpr int V = Q == 3 ? 4 * Out4<D, G>::TILES : 8 * H;
+  static constexpr int H = Q == 3 ? Warp4<D, G>::H : (G / Geo::ROWS > 0 ? G / Geo::ROWS : 1);
+  static constexpr int V = Q == 3 ? Warp4<D, G>::V : 8 * H;
   static constexpr int SLOT = 32 * (V + 2 * H);  // floats of a partial in the workspace
 };
 
@@ -254,14 +254,10 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
   }
 
   // the unit being summed: q, softmax state, sums
-  uint32_t qa[D / 8];
-  float qf = 0.f;
-  float qs4[D / kInt4Group];
-  float2 q2[Q == 0 ? G : 1][4];
-  float acc8[Q == 3 ? D / 16 : 1][4];
-  float zacc[Cols4<D, G>::NZ];
+  Warp4<D, G> w4;                // Q = 3
+  float2 q2[Q == 0 ? G : 1][4];  // Q = 0
   float2 acc[Q == 0 ? G : 1][4];
-  float m_run = -INFINITY, l_run = 0.f, vbound = 0x1p-126f, vinv = 0x1p126f;
+  float m_run = -INFINITY, l_run = 0.f;
   RuleLane rule;
   const int my_head = (sub * R) / P, my_i0 = (sub * R) % P;  // Q = 0
   bool patched = false;
@@ -269,19 +265,13 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
 
   auto begin = [&](bool reaches_end) {
     unit_seq = seq_at(at.b);
-    m_run = -INFINITY;
-    l_run = 0.f;
     if constexpr (Q == 3) {
-      load_q_4b<D, G>(p, at.b, at.h, lane, qa, qf, qs4);
-      vbound = 0x1p-126f;
-      vinv = 0x1p126f;
-#pragma unroll
-      for (int g = 0; g < Cols4<D, G>::NZ; ++g) zacc[g] = 0.f;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc8[c][k] = 0.f;
+      w4.begin(p.q + (static_cast<size_t>(at.b) * p.num_q_heads +
+                      static_cast<size_t>(at.h) * G) * D,
+               p.scale_log2, lane);
     } else {
+      m_run = -INFINITY;
+      l_run = 0.f;
       load_q_bf16<D, G>(p, at.b, at.h, sub, q2);
 #pragma unroll
       for (int g = 0; g < G; ++g)
@@ -310,16 +300,10 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
   // them v[e] belongs to.
   float v[E::V];
   float2 ml[E::H];
-  auto head_of = [](int e) { return Q == 3 ? e & 1 : e >> 3; };
+  auto head_of = [](int e) { return Q == 3 ? e % E::H : e >> 3; };
   auto gather = [&]() {
     if constexpr (Q == 3) {
-      l_run += __shfl_xor_sync(kFullMask, l_run, 1);
-      l_run += __shfl_xor_sync(kFullMask, l_run, 2);
-      finish_4b<D, G>(acc8, zacc, vbound, lane, v);
-      ml[0] = make_float2(__shfl_sync(kFullMask, m_run, 8 * tig),
-                          __shfl_sync(kFullMask, l_run, 8 * tig));
-      ml[1] = make_float2(__shfl_sync(kFullMask, m_run, 8 * tig + 4),
-                          __shfl_sync(kFullMask, l_run, 8 * tig + 4));
+      w4.finish(lane, v, ml);
     } else {
 #pragma unroll
       for (int m = 1; m < Geo::HEAD_LANES; m <<= 1)
@@ -363,14 +347,14 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
     __nv_bfloat16* o =
         p.out + (static_cast<size_t>(at.b) * p.num_q_heads + static_cast<size_t>(at.h) * G) * D;
     if constexpr (Q == 3) {
-      if (Cols4<D, G>::owner(tig)) {
-        o += QCols<G>::head(2 * tig) * D + 16 * Out4<D, G>::first(tig) + gid;
+      if (Warp4<D, G>::owner(tig)) {
 #pragma unroll
-        for (int c = 0; c < Out4<D, G>::TILES; ++c)
+        for (int h = 0; h < E::H; ++h) {
+          __nv_bfloat16* oh = o + Warp4<D, G>::head(tig, h) * D + gid;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            o[(k & 1) * D + 16 * c + 8 * (k >> 1)] =
-                __float2bfloat16_rn(v[4 * c + k] * inv[k & 1]);
+          for (int c = 0; c < D / 8; ++c)
+            oh[8 * c] = __float2bfloat16_rn(v[c * E::H + h] * inv[h]);
+        }
       }
     } else if (rg * E::H < G) {
 #pragma unroll
@@ -475,11 +459,9 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
       const bool full = nvalid == BS * SB && (!RULE || j0 >= unit_seq.lo);
       if constexpr (Q == 3) {
         if (full)
-          tile_step_4b<D, G, SB, true, RULE>(stage, qa, qf, qs4, acc8, m_run, l_run, zacc,
-                                             vbound, vinv, nvalid, lane, rule, j0);
+          w4.template step<SB, true>(stage, nvalid, lane);
         else
-          tile_step_4b<D, G, SB, false, RULE>(stage, qa, qf, qs4, acc8, m_run, l_run, zacc,
-                                              vbound, vinv, nvalid, lane, rule, j0);
+          w4.template step<SB, false>(stage, nvalid, lane);
       } else {
         const uint4* kt = reinterpret_cast<const uint4*>(stage);
         const uint4* vt = reinterpret_cast<const uint4*>(stage + Lay::KT);

@@ -46,6 +46,7 @@
 
 #include "cache_row.cuh"
 #include "decode_tile.cuh"
+#include "decode_tile4.cuh"
 #include "device.cuh"
 #include "int4_row.cuh"
 #include "internal.h"
@@ -265,58 +266,6 @@ __device__ __forceinline__ void patch_tile(unsigned char* tile, int kt_bytes,
   }
 }
 
-// q of (sequence b, KV head kvh) for tile_step_4b: the lane's words, the factor
-// of the MMA sums and the head's group sums.
-template <int D, int G>
-__device__ __forceinline__ void load_q_4b(const DecodeParams& p, int b, int kvh, int lane,
-                                          uint32_t (&qa)[D / 8], float& qf,
-                                          float (&qs4)[D / kInt4Group]) {
-  // Lane (gid, tig): head(gid)'s dims 16 tig .. 16 tig + 15 of every group,
-  // times a power of two 2^k that brings the head's largest |q| to
-  // [2^13, 2^14): a bf16 value has 8 significant bits, so its f16 is exact
-  // down to 2^-28 of that (with the factor 2^-4 of the odd nibbles).
-  using C = QCols<G>;
-  const int gid = lane >> 2, tig = lane & 3;
-  const __nv_bfloat16* qh =
-      p.q + (static_cast<size_t>(b) * p.num_q_heads + static_cast<size_t>(kvh) * G +
-             C::head(gid)) * D + 16 * tig;
-  float f[D / 4];
-#pragma unroll
-  for (int u = 0; u < D / 32; ++u) {  // 8 dims: half u % 2 of group u / 2's sixteen
-    const uint4 w =
-        __ldg(reinterpret_cast<const uint4*>(qh + kInt4Group * (u / 2) + 8 * (u % 2)));
-    const float2 a = bf16x2_to_float2(w.x), c = bf16x2_to_float2(w.y);
-    const float2 d = bf16x2_to_float2(w.z), e = bf16x2_to_float2(w.w);
-    f[8 * u] = a.x; f[8 * u + 1] = a.y; f[8 * u + 2] = c.x; f[8 * u + 3] = c.y;
-    f[8 * u + 4] = d.x; f[8 * u + 5] = d.y; f[8 * u + 6] = e.x; f[8 * u + 7] = e.y;
-  }
-  float amax = 0.f;
-#pragma unroll
-  for (int k = 0; k < D / 4; ++k) amax = fmaxf(amax, fabsf(f[k]));
-  amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
-  const int ebits = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu);
-  const int kexp = min(127, max(-126, 140 - ebits));
-  const float up = __uint_as_float(static_cast<uint32_t>(kexp + 127) << 23);
-#pragma unroll
-  for (int w = 0; w < D / 32; ++w) {  // nibbles 0..7 of word w: dims f[8 w ..]
-    qa[4 * w] = f16x2_rn(f[8 * w] * up, f[8 * w + 4] * up);
-    qa[4 * w + 1] = f16x2_rn(f[8 * w + 1] * up * 0.0625f, f[8 * w + 5] * up * 0.0625f);
-    qa[4 * w + 2] = f16x2_rn(f[8 * w + 2] * up, f[8 * w + 6] * up);
-    qa[4 * w + 3] = f16x2_rn(f[8 * w + 3] * up * 0.0625f, f[8 * w + 7] * up * 0.0625f);
-  }
-#pragma unroll
-  for (int g = 0; g < D / kInt4Group; ++g) {
-    float x = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) x += f[16 * g + k];
-    x += __shfl_xor_sync(kFullMask, x, 1);
-    x += __shfl_xor_sync(kFullMask, x, 2);
-    qs4[g] = x * p.scale_log2;
-  }
-  qf = ldexpf(p.scale_log2, 24 - kexp);
-}
-
 // q of (sequence b, KV head kvh) for tile_step: the lane's 8 dims of each head,
 // times the score scale.
 template <int D, int G>
@@ -343,7 +292,7 @@ __device__ __forceinline__ void load_q_bf16(const DecodeParams& p, int b, int kv
 // tile step (tile_step_1b: QK and PV on the tensor cores, weights in
 // registers); INT8 quantises q and its QK is exact in integers (f16 MMAs on
 // the codes), FP8 takes QK in E4M3 on two exact parts of q.
-// Q 3: a 4-bit cache (tile_step_4b, two blocks per step).  RULE: the scores are
+// Q 3: a 4-bit cache (Warp4::step, two blocks per step).  RULE: the scores are
 // changed (ScoreRule) and a window may hide the context's start.
 template <int D, int G, int NW, int S, bool SPLIT, int Q, bool RULE = false>
 __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
@@ -433,7 +382,7 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
   // factor (tile_step_1b)
   uint32_t qa[D / 8];
   float qf = 0.f;
-  float qs4[D / kInt4Group];  // 4-bit cache: the head's q summed over each group, scaled
+  Warp4<D, G> w4;  // 4-bit cache: q, softmax state and sums
   float qoff = 0.f;  // int8 cache: 128 * the sum of head(gid)'s q codes (tile_step_1b)
   // q of the group into this lane's registers (or, for the int8 cache,
   // quantised through shared memory): the inputs a preceding kernel may
@@ -496,7 +445,8 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
       }
       qf = ldexpf(p.scale_log2, -kexp);
     } else if constexpr (Q == 3) {
-      load_q_4b<D, G>(p, b, kvh, lane, qa, qf, qs4);
+      w4.begin(p.q + (static_cast<size_t>(b) * p.num_q_heads + static_cast<size_t>(kvh) * G) * D,
+               p.scale_log2, lane);
     } else if constexpr (Q == 0) {
       load_q_bf16<D, G>(p, b, kvh, sub, q2);
     } else {
@@ -715,9 +665,6 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
   // 1-byte caches: the warp's power-of-two bound on the V scales it has
   // weighted (raise_v_bound) and its reciprocal; acc8 is in units of it
   float vbound = 0x1p-126f, vinv = 0x1p126f;
-  float zacc[Cols4<D, G>::NZ];  // 4-bit cache: the lane's share of head gid's sums p * lo
-#pragma unroll
-  for (int g = 0; g < Cols4<D, G>::NZ; ++g) zacc[g] = 0.f;
   const int my_head = (sub * R) / P;  // bf16 cache: the lane's score head and first pass
   const int my_i0 = (sub * R) % P;
   RuleLane rule;
@@ -774,12 +721,11 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
         tile_step<D, G, false>(kt, vt, ps, alpha_s, q2, acc, m_run, l_run, nvalid, lane, sub,
                                rg, my_head, my_i0);
     } else if constexpr (Q == 3) {
-      if (nvalid == SB * BS && (!RULE || j * BS >= lo_tok))
-        tile_step_4b<D, G, SB, true, RULE>(stage, qa, qf, qs4, acc8, m_run, l_run, zacc, vbound,
-                                           vinv, nvalid, lane, rule, j * BS);
+      static_assert(!RULE, "changed scores: bf16 only");
+      if (nvalid == SB * BS)
+        w4.template step<SB, true>(stage, nvalid, lane);
       else
-        tile_step_4b<D, G, SB, false, RULE>(stage, qa, qf, qs4, acc8, m_run, l_run, zacc, vbound,
-                                            vinv, nvalid, lane, rule, j * BS);
+        w4.template step<SB, false>(stage, nvalid, lane);
     } else {
       const float* ksc = reinterpret_cast<const float*>(stage + 2 * Lay::KT);
       const float* vsc = ksc + BS;
@@ -819,7 +765,9 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
                  : "memory");
 
   // Per-warp totals: l over the lanes of each head, acc over row groups.
-  if constexpr (I8) {  // the 4 lanes of each row of the QK MMA
+  if constexpr (Q == 3) {
+    // (finish() below)
+  } else if constexpr (I8) {  // the 4 lanes of each row of the QK MMA
     l_run += __shfl_xor_sync(kFullMask, l_run, 1);
     l_run += __shfl_xor_sync(kFullMask, l_run, 2);
   } else {
@@ -849,12 +797,30 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
         dst[1] = make_float4(acc[g][2].x, acc[g][2].y, acc[g][3].x, acc[g][3].y);
       }
     }
+  } else if constexpr (Q == 3) {
+    using W4 = Warp4<D, G>;
+    float v4[W4::V];
+    float2 ml[W4::H];
+    w4.finish(lane, v4, ml);
+    const int gid = lane >> 2, tig = lane & 3;
+    if (W4::owner(tig)) {
+#pragma unroll
+      for (int h = 0; h < W4::H; ++h) {
+        const int hd = W4::head(tig, h);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) mrg[hd * D + 8 * c + gid] = v4[c * W4::H + h];
+        if (gid == 0) {
+          mrg[G * D + hd] = ml[h].x;
+          mrg[G * D + G + hd] = ml[h].y;
+        }
+      }
+    }
   } else {
     // acc8: (dims 16c + gid, 16c + gid + 8; columns 2 tig, 2 tig + 1), in
     // units of the warp's V-scale bound; G <= 4: each head's hi and lo parts
     // sit in the lanes tig and tig ^ G / 2 and are summed here
     using C = QCols<G>;
-    if constexpr (C::PACKED && Q != 3) {
+    if constexpr (C::PACKED) {
 #pragma unroll
       for (int c = 0; c < D / 16; ++c)
 #pragma unroll
@@ -877,21 +843,7 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
         acc8[c][3] = fmaf(acc8[c][3], 0x1p24f, -wb);
       }
     }
-    if constexpr (Q == 3) {
-      float o4[4 * Out4<D, G>::TILES];
-      finish_4b<D, G>(acc8, zacc, vbound, lane, o4);
-      if (Cols4<D, G>::owner(tig)) {
-        const int ha = C::head(2 * tig);
-#pragma unroll
-        for (int c = 0; c < Out4<D, G>::TILES; ++c) {
-          const int d0 = 16 * (Out4<D, G>::first(tig) + c) + gid;
-          mrg[ha * D + d0] = o4[4 * c];
-          mrg[(ha + 1) * D + d0] = o4[4 * c + 1];
-          mrg[ha * D + d0 + 8] = o4[4 * c + 2];
-          mrg[(ha + 1) * D + d0 + 8] = o4[4 * c + 3];
-        }
-      }
-    } else if (C::part0(tig)) {
+    if (C::part0(tig)) {
       const int ha = C::head(2 * tig);
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
@@ -903,7 +855,9 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
       }
     }
   }
-  if constexpr (I8) {  // head gid's state, from its part-0 row
+  if constexpr (Q == 3) {
+    // (written above)
+  } else if constexpr (I8) {  // head gid's state, from its part-0 row
     if (lane % 4 == 0 && lane / 4 < G) {
       mrg[G * D + lane / 4] = m_run;
       mrg[G * D + G + lane / 4] = l_run;

@@ -11,7 +11,6 @@
 #include <stdint.h>
 
 #include "device.cuh"
-#include "int4_row.cuh"
 
 namespace pa {
 
@@ -533,254 +532,6 @@ __device__ __forceinline__ void tile_step_1b(const unsigned char* __restrict__ k
     }
     mma_f16(acc[c], a0, a1, a2, a3, b0, b1);
     if constexpr (!C::PACKED) mma_f16(acc[c], a0, a1, a2, a3, l01, l23);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// 4-bit KV cache (int4_row.cuh): value = lo + sc * code per token and group of
-// 64 dims, code 0..15.
-//
-// QK as the 1-byte step's, transposed: rows = the group's query heads, columns
-// = 8 tokens, and the codes enter the f16 MMAs as subnormals.  A mask leaves
-// two codes in a register as f16 subnormals: nibbles at bits 0 and 16 stand for
-// code * 2^-24, nibbles at bits 4 and 20 for code * 2^-20, so the second kind's
-// q carries a factor 2^-4 (exact) and one shift serves eight codes.  With sums
-// c_g of q . code over group g and qs_g = the sum of q over it,
-//   s = sum_g sc_g c_g + lo_g qs_g.
-// Group 0 uses the MMA's rows 0..7 and group 1 rows 8..15, so one accumulator
-// holds both.  PV: out^T = V^T . W with the weights of group g being p * sc_g
-// (one f16 each: 11 bits, so an output's error is about 2^-12 of its size,
-// against the 2^-9 of its bf16 rounding), and the offsets' share, sum p * lo_g,
-// summed in fp32 beside it.  V nibbles of dims 16 c + gid are scaled 2^-24 and
-// those of dims 16 c + gid + 8 2^-20, undone once at the end.
-//
-// W's 8 columns: one head each for G = 8, two MMA operands for two groups.  For
-// G <= 4 and two groups, column n is head n % G with the weights of group
-// n / G % 2, so one operand serves both groups (an m-tile's other columns are
-// not read), and a lane weighs its tokens for one group only.
-template <int D, int G>
-struct Cols4 {
-  static constexpr int NG = D / kInt4Group;
-  static constexpr bool PACK = G < 8 && NG == 2;
-  static constexpr int NZ = PACK ? 1 : NG;  // weight operands, offset sums per lane
-  static __device__ __forceinline__ int group(int n) { return PACK ? n / G % 2 : 0; }
-  // whether PV columns 2 tig, 2 tig + 1 hold results no other lane holds
-  static __device__ __forceinline__ bool owner(int tig) {
-    return G == 8 || 2 * tig < (PACK ? 2 * G : G);
-  }
-};
-
-// The lane's words of q (qa), the head's group sums (qs, times the score
-// scale) and the factor of the MMA sums (qf).
-template <int D, int G, int NB, bool FULL, bool RULE>
-__device__ __forceinline__ void tile_step_4b(const unsigned char* __restrict__ stage,
-                                             const uint32_t (&qa)[D / 8], float qf,
-                                             const float (&qs)[D / kInt4Group],
-                                             float (&acc)[D / 16][4], float& m_run,
-                                             float& l_run, float (&zacc)[Cols4<D, G>::NZ],
-                                             float& vbound, float& vinv, int nvalid, int lane,
-                                             const RuleLane& rule, int j0) {
-  constexpr int KT = int4_tile_bytes(D), NG = D / kInt4Group;
-  constexpr int NZ = Cols4<D, G>::NZ;
-  const int gid = lane >> 2, tig = lane & 3;
-  const int my_group = Cols4<D, G>::group(gid);
-  float s[NB][4];
-#pragma unroll
-  for (int u = 0; u < NB; ++u) {
-    const unsigned char* kt = stage + u * 2 * KT;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {  // tokens 8 h .. 8 h + 7
-      uint32_t k[D / 32];
-      const unsigned char* row = kt + (8 * h + gid) * (D / 2) + (D / 8) * tig;
-      if constexpr (D == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(row);
-        k[0] = x.x; k[1] = x.y; k[2] = x.z; k[3] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(row);
-        k[0] = x.x; k[1] = x.y;
-      }
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        const uint32_t x = k[w], y = k[w] >> 8;
-        if (w < 2) {
-          mma_f16(c, qa[4 * w], 0u, qa[4 * w + 1], 0u, x & 0x000F000Fu, x & 0x00F000F0u);
-          mma_f16(c, qa[4 * w + 2], 0u, qa[4 * w + 3], 0u, y & 0x000F000Fu, y & 0x00F000F0u);
-        } else {
-          mma_f16(c, 0u, qa[4 * w], 0u, qa[4 * w + 1], x & 0x000F000Fu, x & 0x00F000F0u);
-          mma_f16(c, 0u, qa[4 * w + 2], 0u, qa[4 * w + 3], y & 0x000F000Fu, y & 0x00F000F0u);
-        }
-      }
-      // tokens 8 h + 2 tig, + 1: their parameter words
-      const unsigned char* par = kt + 8 * D + (8 * h + 2 * tig) * NG * 4;
-      uint32_t w0[NG], w1[NG];
-      if constexpr (NG == 2) {
-        const uint4 x = *reinterpret_cast<const uint4*>(par);
-        w0[0] = x.x; w0[1] = x.y; w1[0] = x.z; w1[1] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(par);
-        w0[0] = x.x; w1[0] = x.y;
-      }
-      float d0 = 0.f, d1 = 0.f, z0 = 0.f, z1 = 0.f;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        d0 = fmaf(__uint_as_float(w0[g] & 0xffff0000u), c[2 * g], d0);
-        d1 = fmaf(__uint_as_float(w1[g] & 0xffff0000u), c[2 * g + 1], d1);
-        z0 = fmaf(__uint_as_float(w0[g] << 16), qs[g], z0);
-        z1 = fmaf(__uint_as_float(w1[g] << 16), qs[g], z1);
-      }
-      float s0 = fmaf(d0, qf, z0), s1 = fmaf(d1, qf, z1);
-      const int t = 16 * u + 8 * h + 2 * tig;
-      if constexpr (RULE) {
-        s0 = rule(s0, j0 + t);
-        s1 = rule(s1, j0 + t + 1);
-      }
-      if constexpr (!FULL) {
-        if (!(t < nvalid && (!RULE || j0 + t >= rule.first))) s0 = -INFINITY;
-        if (!(t + 1 < nvalid && (!RULE || j0 + t + 1 >= rule.first))) s1 = -INFINITY;
-      }
-      s[u][2 * h] = s0;
-      s[u][2 * h + 1] = s1;
-    }
-  }
-  // the step's maximum for head(gid): over the lane's tokens, then the row's
-  // four lanes (the rows of one head, G <= 4, hold the same scores)
-  float mx = s[0][0];
-#pragma unroll
-  for (int u = 0; u < NB; ++u)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[u][i]);
-  mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 2));
-  const float m_new = lazy_max(m_run, mx);
-  const float alpha = ex2_fast(m_run - m_new);
-  float psum = 0.f;
-#pragma unroll
-  for (int u = 0; u < NB; ++u)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[u][i] = ex2_fast(s[u][i] - m_new);
-      psum += s[u][i];
-    }
-  l_run = fmaf(l_run, alpha, psum);
-  m_run = m_new;
-
-  // V parameters of the lane's tokens: [u][h] tokens 8 h + 2 tig, + 1
-  uint32_t vw[NB][2][2][NZ];
-  float vm = 0.f;
-#pragma unroll
-  for (int u = 0; u < NB; ++u)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const unsigned char* par =
-          stage + u * 2 * KT + KT + 8 * D + (8 * h + 2 * tig) * NG * 4;
-      if constexpr (Cols4<D, G>::PACK) {
-        vw[u][h][0][0] = *reinterpret_cast<const uint32_t*>(par + 4 * my_group);
-        vw[u][h][1][0] = *reinterpret_cast<const uint32_t*>(par + 4 * my_group + 8);
-      } else if constexpr (NG == 2) {
-        const uint4 x = *reinterpret_cast<const uint4*>(par);
-        vw[u][h][0][0] = x.x; vw[u][h][0][1] = x.y;
-        vw[u][h][1][0] = x.z; vw[u][h][1][1] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(par);
-        vw[u][h][0][0] = x.x; vw[u][h][1][0] = x.y;
-      }
-      const int t = 16 * u + 8 * h + 2 * tig;
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int g = 0; g < NZ; ++g) {
-          if constexpr (!FULL) {  // a hidden token's parameters may be anything
-            if (!(t + e < nvalid && (!RULE || j0 + t + e >= rule.first))) vw[u][h][e][g] = 0u;
-          }
-          vm = fmaxf(vm, __uint_as_float(vw[u][h][e][g] & 0xffff0000u));
-        }
-    }
-  float r = 1.f;
-  if (__any_sync(kFullMask, vm > vbound)) {
-    vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 1));
-    vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 2));
-    if constexpr (Cols4<D, G>::PACK)  // the other group's rows
-      vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 4 * G));
-    r = raise_v_bound(vm, vbound, vinv);
-  }
-  if (__any_sync(kFullMask, alpha != 1.0f) || r != 1.0f) {
-    const float fa = __shfl_sync(kFullMask, alpha, 8 * tig) * r;
-    const float fb = __shfl_sync(kFullMask, alpha, 8 * tig + 4) * r;
-    scale_acc<D>(acc, fa, fb);
-#pragma unroll
-    for (int g = 0; g < NZ; ++g) zacc[g] *= alpha;
-  }
-  uint32_t b[NB][2][NZ];
-#pragma unroll
-  for (int u = 0; u < NB; ++u)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float p0 = s[u][2 * h], p1 = s[u][2 * h + 1];
-      const float y0 = p0 * vinv, y1 = p1 * vinv;
-#pragma unroll
-      for (int g = 0; g < NZ; ++g) {
-        b[u][h][g] = f16x2_rn(y0 * __uint_as_float(vw[u][h][0][g] & 0xffff0000u),
-                              y1 * __uint_as_float(vw[u][h][1][g] & 0xffff0000u));
-        zacc[g] = fmaf(p0, __uint_as_float(vw[u][h][0][g] << 16), zacc[g]);
-        zacc[g] = fmaf(p1, __uint_as_float(vw[u][h][1][g] << 16), zacc[g]);
-      }
-    }
-#pragma unroll
-  for (int u = 0; u < NB; ++u) {
-    const unsigned char* base = stage + u * 2 * KT + KT + lane * (D / 4);
-#pragma unroll
-    for (int v = 0; v < D / 64; ++v) {
-      const uint4 x = *reinterpret_cast<const uint4*>(
-          base + 16 * (D == 128 ? (v ^ (gid & 1)) : 0));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t y = w[k] >> 8;
-        mma_f16(acc[4 * v + k], w[k] & 0x000F000Fu, w[k] & 0x00F000F0u, y & 0x000F000Fu,
-                y & 0x00F000F0u, b[u][0][NZ == 2 ? v : 0], b[u][1][NZ == 2 ? v : 0]);
-      }
-    }
-  }
-}
-
-// The lane's sums of a finished run of tile_step_4b: out[k] (before the division
-// by l) of the m-tiles it owns (Cols4::owner), in order: (dim 16 c + gid; column
-// 2 tig), (same; 2 tig + 1), (dim 16 c + gid + 8; the two columns), for the
-// owned c; zacc is reduced over the row's lanes.  All 32 lanes must call it.
-template <int D, int G>
-struct Out4 {
-  static constexpr int TILES = Cols4<D, G>::PACK ? 4 : D / 16;  // owned m-tiles
-  static __device__ __forceinline__ int first(int tig) {        // the first of them
-    return Cols4<D, G>::PACK ? 4 * Cols4<D, G>::group(2 * tig) : 0;
-  }
-};
-template <int D, int G>
-__device__ __forceinline__ void finish_4b(float (&acc)[D / 16][4],
-                                          float (&zacc)[Cols4<D, G>::NZ], float vbound, int lane,
-                                          float (&out)[4 * Out4<D, G>::TILES]) {
-  const int tig = lane & 3;
-  // codes were fed as code * 2^-24 (dims 16 c + gid) and code * 2^-20 (+ 8)
-  const float up = vbound * 0x1p20f;
-  float za[Cols4<D, G>::NZ], zb[Cols4<D, G>::NZ];
-#pragma unroll
-  for (int g = 0; g < Cols4<D, G>::NZ; ++g) {
-    zacc[g] += __shfl_xor_sync(kFullMask, zacc[g], 1);
-    zacc[g] += __shfl_xor_sync(kFullMask, zacc[g], 2);
-    // the offsets' sums of columns 2 tig, 2 tig + 1 come from those rows
-    za[g] = __shfl_sync(kFullMask, zacc[g], 8 * tig);
-    zb[g] = __shfl_sync(kFullMask, zacc[g], 8 * tig + 4);
-  }
-  const bool second = Out4<D, G>::first(tig) != 0;
-#pragma unroll
-  for (int c = 0; c < Out4<D, G>::TILES; ++c) {
-    const int g = Cols4<D, G>::NZ == 2 ? c / 4 : 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float x = acc[c][k];
-      if constexpr (Cols4<D, G>::PACK) x = second ? acc[c + 4][k] : x;
-      out[4 * c + k] = fmaf(k < 2 ? x * 16.f : x, up, k % 2 == 0 ? za[g] : zb[g]);
-    }
   }
 }
 

@@ -1,0 +1,355 @@
+// The 4-bit cache's share of the paged decode kernels: q's operands, one step
+// over NB blocks of 16 tokens, and a warp's finished sums.
+//
+// A cached value is lo + sc * code per token and group of 64 dims (int4_row.cuh).
+// Everything that does not depend on the head is done once for the warp, and
+// everything that does once per (token, head):
+//
+// QK: S = K q, the MMA's rows the block's 16 tokens, in E4M3 (m16n8k32): a
+// nibble in a byte IS the E4M3 value code * 2^-9 (codes 0..15 run through the
+// subnormals and the first binade, which have one spacing), so a mask, and a
+// shift and a mask, turn a 32-bit word into its 8 codes.  q comes in two E4M3
+// parts, x = q1 + 2^-5 q2 (x: q times a power of two that brings the head's
+// largest |q| to [128, 256)): q1 keeps 4 of a bf16's 8 bits and 32 (x - q1) is
+// exact in q2 but for what falls under E4M3's normal range, 2^-21 of the head's
+// largest.  The parts of head h are columns 2 h and 2 h + 1, so lane (gid, tig)
+// receives both sums of head tig with tokens gid and gid + 8.  With c_g those
+// sums over group g and qs_g the sum of q over it,
+//   s = sum_g sc_g c_g + lo_g qs_g.
+//
+// PV: out^T = V^T W in f16 (m16n8k16), V's codes as f16 subnormals: a nibble at
+// bit 0 or 16 is code * 2^-24, one at bit 4 or 20 code * 2^-20 (undone once at
+// the end).  W holds p * sc_g, one f16 each (11 bits: an output's error is about
+// 2^-12 of its size, against the 2^-9 of its bf16 rounding); the offsets' share,
+// sum p * lo_g, is summed in fp32 beside it.  W's columns: for G <= 4, 2 h + g;
+// for G = 8, heads tig and tig + 4 at 2 tig and 2 tig + 1, one operand per group.
+// A lane computes its tokens' row of W; a matrix transpose of 8 x 8 halves
+// (movmatrix) makes the operand.  So the lane that weighs head tig also holds
+// the columns of head tig of the result, and its own rescale factor.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "decode_tile.cuh"
+#include "device.cuh"
+#include "int4_row.cuh"
+
+namespace pa {
+
+template <int D, int G>
+struct Warp4 {
+  static constexpr int NG = D / kInt4Group;
+  static constexpr int H = G == 8 ? 2 : 1;      // heads per lane: tig (+ 4)
+  static constexpr int NW = G == 8 ? NG : 1;    // W operands per 16 tokens
+  static constexpr int KT = int4_tile_bytes(D);
+  // results per lane: its heads' dims 16 c + gid and 16 c + gid + 8
+  static constexpr int V = D / 16 * 2 * H;
+
+  uint32_t qw[H][D / 16];  // q's columns: head gid / 2 (+ 4), part gid % 2
+  float qf[H];             // factor of the MMA sums of the lane's heads
+  float qs[H][NG];         // their q summed over each group, times the score scale
+  float m[H], l[H];        // softmax reference (base 2), the lane's share of the sum
+  float z[H][NG];          // the lane's share of sum p * lo
+  float acc[D / 16][4];
+  float vbound, vinv;      // the warp's bound on the V scales it has weighed
+
+  static __device__ __forceinline__ int head(int tig, int h) { return (tig + 4 * h) % G; }
+  // whether no other lane of the row holds the same results
+  static __device__ __forceinline__ bool owner(int tig) { return G >= 4 || tig < G; }
+
+  // q: the G heads of the group, D values each.
+  __device__ __forceinline__ void begin(const __nv_bfloat16* q, float scale_log2, int lane) {
+    const int gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const __nv_bfloat16* qh = q + static_cast<size_t>(head(gid / 2, h)) * D + 16 * tig;
+      float f[D / 4];  // dims 16 tig .. 16 tig + 15 of every group
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) {
+        const uint4 w =
+            __ldg(reinterpret_cast<const uint4*>(qh + kInt4Group * (u / 2) + 8 * (u % 2)));
+        const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
+        const float2 c = bf16x2_to_float2(w.z), d = bf16x2_to_float2(w.w);
+        f[8 * u] = a.x; f[8 * u + 1] = a.y; f[8 * u + 2] = b.x; f[8 * u + 3] = b.y;
+        f[8 * u + 4] = c.x; f[8 * u + 5] = c.y; f[8 * u + 6] = d.x; f[8 * u + 7] = d.y;
+      }
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 4; ++k) amax = fmaxf(amax, fabsf(f[k]));
+      amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
+      // biased exponent of amax (0 for 0 and subnormals); k = 7 - unbiased
+      const int ebits = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu);
+      const int kexp = min(127, max(-126, 134 - ebits));
+      const float up = __uint_as_float(static_cast<uint32_t>(kexp + 127) << 23);
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {  // the word's even, odd nibbles
+          uint32_t r = 0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float x0 = f[8 * w + 4 * i + o] * up, x1 = f[8 * w + 4 * i + 2 + o] * up;
+            __nv_fp8x2_storage_t c =
+                __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+            if (gid & 1) {
+              const __half2_raw c1 = __nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3);
+              const float2 q1 = __half22float2(*reinterpret_cast<const __half2*>(&c1));
+              c = __nv_cvt_float2_to_fp8x2(
+                  make_float2((x0 - q1.x) * 32.f, (x1 - q1.y) * 32.f), __NV_SATFINITE, __NV_E4M3);
+            }
+            r |= static_cast<uint32_t>(c) << (16 * i);
+          }
+          qw[h][2 * w + o] = r;
+        }
+      // the lane's scores are those of head(tig): its factors come from row 2 tig
+      qf[h] = __shfl_sync(kFullMask, ldexpf(scale_log2, 9 - kexp), 8 * tig);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float x = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x += f[16 * g + k];
+        x += __shfl_xor_sync(kFullMask, x, 1);
+        x += __shfl_xor_sync(kFullMask, x, 2);
+        qs[h][g] = __shfl_sync(kFullMask, x * scale_log2, 8 * tig);
+        z[h][g] = 0.f;
+      }
+      m[h] = -INFINITY;
+      l[h] = 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[c][k] = 0.f;
+    vbound = 0x1p-126f;
+    vinv = 0x1p126f;
+  }
+
+  static __device__ __forceinline__ float hi16(uint32_t w) {
+    return __uint_as_float(w & 0xffff0000u);
+  }
+  static __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+
+  // d = a . b, the first step of a sum
+  static __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1,
+                                                   uint32_t a2, uint32_t a3, uint32_t b0,
+                                                   uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  }
+  static __device__ __forceinline__ uint32_t transpose(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+  }
+
+  // One step: NB blocks, K tile then V tile each, of which the first nvalid
+  // tokens count (FULL: all).  A hidden token's bytes may be anything.
+  template <int NB, bool FULL>
+  __device__ __forceinline__ void step(const unsigned char* __restrict__ stage, int nvalid,
+                                       int lane) {
+    const int gid = lane >> 2, tig = lane & 3;
+    float2 s[NB][H];  // scores, then weights: tokens gid, gid + 8 of each block
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const unsigned char* kt = stage + u * 2 * KT;
+      uint32_t k0[D / 32], k1[D / 32];
+      const unsigned char* row = kt + gid * (D / 2) + (D / 8) * tig;
+      if constexpr (D == 128) {
+        const uint4 x = *reinterpret_cast<const uint4*>(row);
+        const uint4 y = *reinterpret_cast<const uint4*>(row + 8 * (D / 2));
+        k0[0] = x.x; k0[1] = x.y; k0[2] = x.z; k0[3] = x.w;
+        k1[0] = y.x; k1[1] = y.y; k1[2] = y.z; k1[3] = y.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(row);
+        const uint2 y = *reinterpret_cast<const uint2*>(row + 8 * (D / 2));
+        k0[0] = x.x; k0[1] = x.y;
+        k1[0] = y.x; k1[1] = y.y;
+      }
+      float c[H][NG][4];
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {  // two words of codes to a group
+        const uint32_t a0 = k0[w] & 0x0F0F0F0Fu, a2 = (k0[w] >> 4) & 0x0F0F0F0Fu;
+        const uint32_t a1 = k1[w] & 0x0F0F0F0Fu, a3 = (k1[w] >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          if (w % 2 == 0)
+            mma_first(c[h][w / 2], a0, a1, a2, a3, qw[h][2 * w], qw[h][2 * w + 1]);
+          else
+            mma_e4m3(c[h][w / 2], a0, a1, a2, a3, qw[h][2 * w], qw[h][2 * w + 1]);
+        }
+      }
+      uint32_t p0[NG], p1[NG];  // parameters of tokens gid, gid + 8
+      load_params(kt, gid, p0);
+      load_params(kt, gid + 8, p1);
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        float2 d, zz;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float2 e = __ffma2_rn(make_float2(c[h][g][1], c[h][g][3]),
+                                      make_float2(0.03125f, 0.03125f),
+                                      make_float2(c[h][g][0], c[h][g][2]));
+          const float2 sc = make_float2(hi16(p0[g]), hi16(p1[g]));
+          const float2 lo = make_float2(lo16(p0[g]), lo16(p1[g]));
+          const float2 q2 = make_float2(qs[h][g], qs[h][g]);
+          d = g == 0 ? __fmul2_rn(e, sc) : __ffma2_rn(e, sc, d);
+          zz = g == 0 ? __fmul2_rn(lo, q2) : __ffma2_rn(lo, q2, zz);
+        }
+        s[u][h] = __ffma2_rn(d, make_float2(qf[h], qf[h]), zz);
+        if constexpr (!FULL) {
+          if (!(16 * u + gid < nvalid)) s[u][h].x = -INFINITY;
+          if (!(16 * u + gid + 8 < nvalid)) s[u][h].y = -INFINITY;
+        }
+      }
+    }
+    // each head's maximum over the step: the lane's tokens, then the 8 rows
+    float alpha[H];
+    bool moved = false;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      float mx = fmaxf(s[0][h].x, s[0][h].y);
+#pragma unroll
+      for (int u = 1; u < NB; ++u) mx = fmaxf(mx, fmaxf(s[u][h].x, s[u][h].y));
+      mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, 16));
+      const float m_new = lazy_max(m[h], mx);
+      alpha[h] = 1.f;
+      if (m_new != m[h]) {
+        alpha[h] = ex2_fast(m[h] - m_new);
+        m[h] = m_new;
+        moved = true;
+      }
+      const float2 neg = make_float2(-m[h], -m[h]);
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        const float2 x = __fadd2_rn(s[u][h], neg);
+        s[u][h] = make_float2(ex2_fast(x.x), ex2_fast(x.y));
+        sum = u == 0 ? s[u][h] : __fadd2_rn(sum, s[u][h]);
+      }
+      l[h] = fmaf(l[h], alpha[h], sum.x + sum.y);
+    }
+    // V's parameters, and whether a scale passes the warp's bound (the words
+    // order as their scales do: scales are not negative)
+    uint32_t w0[NB][NG], w1[NB][NG];
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const unsigned char* vt = stage + u * 2 * KT + KT;
+      load_params(vt, gid, w0[u]);
+      load_params(vt, gid + 8, w1[u]);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        if constexpr (!FULL) {
+          if (!(16 * u + gid < nvalid)) w0[u][g] = 0u;
+          if (!(16 * u + gid + 8 < nvalid)) w1[u][g] = 0u;
+        }
+        top = max(top, max(w0[u][g], w1[u][g]));
+      }
+    }
+    float r = 1.f;
+    if (__any_sync(kFullMask, (top & 0xffff0000u) > __float_as_uint(vbound))) {
+      float vm = hi16(top);
+      vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 4));
+      vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 8));
+      vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 16));
+      r = raise_v_bound(vm, vbound, vinv);
+      moved = true;
+    }
+    if (__any_sync(kFullMask, moved)) {
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) z[h][g] *= alpha[h];
+      const float fa = alpha[0] * r, fb = alpha[H - 1] * r;
+      scale_acc<D>(acc, fa, fb);  // columns 2 tig and 2 tig + 1 are the lane's heads
+    }
+    uint32_t b0[NB][NW], b1[NB][NW];
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      float2 y[H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        y[h] = __fmul2_rn(s[u][h], make_float2(vinv, vinv));
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          z[h][g] = fmaf(s[u][h].x, lo16(w0[u][g]), fmaf(s[u][h].y, lo16(w1[u][g]), z[h][g]));
+      }
+      if constexpr (G == 8) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          b0[u][g] = transpose(f16x2_rn(y[0].x * hi16(w0[u][g]), y[H - 1].x * hi16(w0[u][g])));
+          b1[u][g] = transpose(f16x2_rn(y[0].y * hi16(w1[u][g]), y[H - 1].y * hi16(w1[u][g])));
+        }
+      } else {  // column 2 h + g (one group: the odd columns are not read)
+        b0[u][0] =
+            transpose(f16x2_rn(y[0].x * hi16(w0[u][0]), y[0].x * hi16(w0[u][NG - 1])));
+        b1[u][0] =
+            transpose(f16x2_rn(y[0].y * hi16(w1[u][0]), y[0].y * hi16(w1[u][NG - 1])));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const unsigned char* base = stage + u * 2 * KT + KT + lane * (D / 4);
+#pragma unroll
+      for (int v = 0; v < D / 64; ++v) {  // dims of group v
+        const uint4 x = *reinterpret_cast<const uint4*>(
+            base + 16 * (D == 128 ? (v ^ (gid & 1)) : 0));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const int o = NW == 2 ? v : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t y = w[k] >> 8;
+          mma_f16(acc[4 * v + k], w[k] & 0x000F000Fu, w[k] & 0x00F000F0u, y & 0x000F000Fu,
+                  y & 0x00F000F0u, b0[u][o], b1[u][o]);
+        }
+      }
+    }
+  }
+
+  // The warp's sums: v[(2 c + j) * H + h] = sum p v of head(tig, h), dim 16 c +
+  // gid + 8 j; ml[h] = (m, l).  All 32 lanes must call it.
+  __device__ __forceinline__ void finish(int lane, float (&v)[V], float2 (&ml)[H]) {
+    const float up = vbound * 0x1p20f;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        l[h] += __shfl_xor_sync(kFullMask, l[h], x);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) z[h][g] += __shfl_xor_sync(kFullMask, z[h][g], x);
+      }
+      ml[h] = make_float2(m[h], l[h]);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const int g = c / 4;
+        const int col = G == 8 ? h : g;  // 2 tig or 2 tig + 1
+        v[2 * c * H + h] = fmaf(acc[c][col] * 16.f, up, z[h][g]);
+        v[(2 * c + 1) * H + h] = fmaf(acc[c][2 + col], up, z[h][g]);
+      }
+    }
+  }
+
+ private:
+  static __device__ __forceinline__ void load_params(const unsigned char* tile, int t,
+                                                     uint32_t (&w)[NG]) {
+    const unsigned char* par = tile + 8 * D + t * NG * 4;
+    if constexpr (NG == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(par);
+      w[0] = x.x; w[1] = x.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(par);
+    }
+  }
+};
+
+}  // namespace pa
