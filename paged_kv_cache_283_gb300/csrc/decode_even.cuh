@@ -7,9 +7,10 @@
 // start and merge cost it a third to a half of its time on a 4-bit cache, whose
 // tiles are quickly read.  Here the launch is one wave of resident CTAs.  A unit is the
 // context of one (sequence, KV head), counted in steps (32 tokens of a 4-bit
-// cache, 16 of a bf16 one); the units stand in a row, and warp w of N takes the
-// steps [w W / N, (w + 1) W / N) of all W: every warp the same number, whatever
-// the lengths, with no plan made on the host.  Warps work alone: each finds its
+// cache, 16 of a bf16 one) after kEvenUnitSteps more that stand for its beginning
+// and end; the units stand in a row, and warp w of N takes the places [w W / N,
+// (w + 1) W / N) of all W: every warp the same number, whatever the lengths, with
+// no plan made on the host.  Warps work alone: each finds its
 // place from the context lengths, copies its tiles through its own ring of
 // bulk copies that runs on over the ends of units, and keeps its own softmax.
 //
@@ -31,14 +32,22 @@ constexpr int kEvenWarps = 4;   // warps of a CTA
 constexpr int kEvenGroup = 16;  // warps whose partials one warp merges at once
 // fewer steps than this to a warp (while every unit has one) do not pay
 constexpr int kEvenMinSteps = 4;
+// what beginning a unit (its q, its result) costs a warp, in steps
+constexpr int kEvenUnitSteps = 2;
+// blocks per step
+template <int Q>
+constexpr int kEvenBlocks = Q == 3 ? 2 : 1;
 
 template <int D, int G, int Q>
 struct Even {
   static constexpr int S = D == 128 ? 2 : 4;  // ring stages of a warp
   static constexpr int CTAS = Q == 3 ? (G <= 4 ? 4 : 3) : (G <= 4 ? 3 : 2);  // per SM
   using Lay = SmemLayout<D, G, kEvenWarps, S, Q>;
+  static constexpr int SB = kEvenBlocks<Q>;
+  static constexpr int STAGE = SB * 2 * Lay::KT;
+  static constexpr int RING = S * STAGE;
   static constexpr int PATCH = Q == 3 ? 512 : 4 * D;
-  static constexpr int WARP = (Lay::TILES + Lay::PS + Lay::ALPHA + PATCH + Lay::BARS + 127) / 128 * 128;
+  static constexpr int WARP = (RING + Lay::PS + Lay::ALPHA + PATCH + Lay::BARS + 127) / 128 * 128;
   static constexpr int SMEM = kEvenWarps * WARP;
   // a lane's share of a unit's result: V values and the (m, l) of H heads
   using Geo = Geometry<D, G>;
@@ -54,13 +63,137 @@ struct EvenArgs {
   int warps;           // of the grid
 };
 
+// A lane's share of a result is v (Even::V sums of p v) and ml ((m, l) of its H
+// heads); which of the heads v[e] belongs to:
+template <int D, int G, int Q>
+__device__ __forceinline__ constexpr int even_head_of(int e) {
+  return Q == 3 ? e % Even<D, G, Q>::H : e >> 3;
+}
+
+// The result of unit (b, h) written out; o: its first head's row.
+template <int D, int G, int Q>
+__device__ __forceinline__ void even_write_out(__nv_bfloat16* o, int lane,
+                                               const float (&v)[Even<D, G, Q>::V],
+                                               const float2 (&ml)[Even<D, G, Q>::H]) {
+  using E = Even<D, G, Q>;
+  float inv[E::H];
+#pragma unroll
+  for (int h = 0; h < E::H; ++h) inv[h] = 1.0f / ml[h].y;
+  if constexpr (Q == 3) {
+    const int gid = lane >> 2, tig = lane & 3;
+    if (Warp4<D, G>::owner(tig)) {
+#pragma unroll
+      for (int h = 0; h < E::H; ++h) {
+        __nv_bfloat16* oh = o + Warp4<D, G>::head(tig, h) * D + gid;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          oh[8 * c] = __float2bfloat16_rn(v[c * E::H + h] * inv[h]);
+      }
+    }
+  } else {
+    const int sub = lane % E::Geo::L, rg = lane / E::Geo::L;
+    if (rg * E::H < G) {
+#pragma unroll
+      for (int h = 0; h < E::H; ++h) {
+        __nv_bfloat162 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = __float22bfloat162_rn(
+              make_float2(v[8 * h + 2 * k] * inv[h], v[8 * h + 2 * k + 1] * inv[h]));
+        *reinterpret_cast<uint4*>(o + (rg * E::H + h) * D + sub * 8) =
+            *reinterpret_cast<const uint4*>(w);
+      }
+    }
+  }
+}
+
+template <int D, int G, int Q>
+__device__ __forceinline__ void even_store(float* slot, int lane,
+                                           const float (&v)[Even<D, G, Q>::V],
+                                           const float2 (&ml)[Even<D, G, Q>::H]) {
+  using E = Even<D, G, Q>;
+#pragma unroll
+  for (int i = 0; i < E::V / 4; ++i)
+    __stcg(reinterpret_cast<float4*>(slot) + 32 * i + lane,
+           make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+#pragma unroll
+  for (int h = 0; h < E::H; ++h)
+    __stcg(reinterpret_cast<float2*>(slot + 32 * E::V) + 32 * h + lane, ml[h]);
+}
+
+// The slot of warp w's partial of the unit that begins in warp wf.
+template <int D, int G, int Q>
+__device__ __forceinline__ float* even_slot(float* ws, int wf, int w) {
+  return ws + static_cast<size_t>(2 * w + (w == wf ? 1 : 0)) * Even<D, G, Q>::SLOT;
+}
+
+// `count` partials of one unit, of the warps max(wf, first + i stride), merged in
+// order, each weighed against the running maximum; the result goes out (o), or
+// (o null) into the first of their slots.  A call of its own, so that the many
+// loads it has in flight take no registers from the loop over the steps.
+template <int D, int G, int Q>
+__device__ __noinline__ void even_merge(float* ws, int wf, int first, int stride, int count,
+                                        __nv_bfloat16* o) {
+  using E = Even<D, G, Q>;
+  constexpr int U = E::V >= 32 ? 2 : 4;  // loaded together
+  const int lane = threadIdx.x & 31;
+  float v[E::V];
+  float2 ml[E::H];
+#pragma unroll
+  for (int e = 0; e < E::V; ++e) v[e] = 0.f;
+#pragma unroll
+  for (int h = 0; h < E::H; ++h) ml[h] = make_float2(-INFINITY, 0.f);
+  for (int i0 = 0; i0 < count; i0 += U) {
+    float4 x[U][E::V / 4];
+    float2 y[U][E::H];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // (past the last: the last again, not counted below)
+      const int i = min(i0 + u, count - 1);
+      const float* slot = even_slot<D, G, Q>(ws, wf, max(wf, first + i * stride));
+#pragma unroll
+      for (int k = 0; k < E::V / 4; ++k)
+        x[u][k] = __ldcg(reinterpret_cast<const float4*>(slot) + 32 * k + lane);
+#pragma unroll
+      for (int h = 0; h < E::H; ++h)
+        y[u][h] = __ldcg(reinterpret_cast<const float2*>(slot + 32 * E::V) + 32 * h + lane);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u >= count) break;
+      float a[E::H], c[E::H];
+#pragma unroll
+      for (int h = 0; h < E::H; ++h) {
+        const float m = fmaxf(ml[h].x, y[u][h].x);
+        a[h] = ml[h].x == m ? 1.f : exp2f(ml[h].x - m);  // (both -inf: 1)
+        c[h] = y[u][h].x == m ? 1.f : exp2f(y[u][h].x - m);
+        ml[h] = make_float2(m, ml[h].y * a[h] + y[u][h].y * c[h]);
+      }
+#pragma unroll
+      for (int i = 0; i < E::V / 4; ++i) {
+        const float xs[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int e = 4 * i + k, h = even_head_of<D, G, Q>(e);
+          v[e] = v[e] * a[h] + xs[k] * c[h];
+        }
+      }
+    }
+  }
+  if (o != nullptr)
+    even_write_out<D, G, Q>(o, lane, v, ml);
+  else
+    even_store<D, G, Q>(even_slot<D, G, Q>(ws, wf, max(wf, first)), lane, v, ml);
+}
+
 template <int D, int G, int Q, bool RULE>
 __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
     paged_decode_even_kernel(const DecodeParams p, const EvenArgs ev) {
   using E = Even<D, G, Q>;
   using Lay = typename E::Lay;
   using Geo = Geometry<D, G>;
-  constexpr int S = E::S, SB = kStepBlocks<Q>, BS = kBlockSize, WS = 32 / SB;
+  constexpr int S = E::S, SB = E::SB, BS = kBlockSize, WS = 32 / SB;
+  constexpr int C = kEvenUnitSteps;
   constexpr int L = Geo::L, R = Geo::R, P = Geo::P;
   extern __shared__ __align__(128) unsigned char smem[];
   if (!p.early_read) griddep_wait();
@@ -72,9 +205,9 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
   const int me = warp * gridDim.x + blockIdx.x;
   unsigned char* wbase = smem + warp * E::WARP;
   unsigned char* tiles = wbase;
-  float* ps = reinterpret_cast<float*>(wbase + Lay::TILES);
-  float* alpha_s = reinterpret_cast<float*>(wbase + Lay::TILES + Lay::PS);
-  unsigned char* patch = wbase + Lay::TILES + Lay::PS + Lay::ALPHA;
+  float* ps = reinterpret_cast<float*>(wbase + E::RING);
+  float* alpha_s = reinterpret_cast<float*>(wbase + E::RING + Lay::PS);
+  unsigned char* patch = wbase + E::RING + Lay::PS + Lay::ALPHA;
   uint64_t* bars = reinterpret_cast<uint64_t*>(patch + E::PATCH);
   if (lane == 0) {
 #pragma unroll
@@ -111,7 +244,7 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
     const int b = lane * K + i;
     if (b < B) {
       const int T = seq_at(b).T;
-      sum += T;
+      sum += T > 0 ? T + C : 0;
       some += T > 0;
       if (me == 0) {
         const int c = __ldg(p.context_lens + b);
@@ -138,13 +271,12 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
     return static_cast<int>(((step + 1ll) * N - 1) / W);
   };
   const bool work = me < N;  // then W >= N >= 1
-  const int w0 = work ? start_of(me) : 0;
-  const int n = work ? start_of(me + 1) - w0 : 0;
+  const int v0 = work ? start_of(me) : 0, v1 = work ? start_of(me + 1) : 0;
 
-  // A place in the row of units: step s of the T of unit (b, h); rem: blocks from
-  // the unit's first on.
+  // A unit (b, h) in the row: its T steps stand at the places v + C .. v + C + T -
+  // 1; rem: its blocks.
   struct Place {
-    int b, h, s, T, rem;
+    int b, h, v, T, rem;
   };
   auto set_seq = [&](Place& x) {
     const Seq q = seq_at(x.b);
@@ -153,23 +285,22 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
   };
   Place at{};
   if (work) {
-    const int tb = w0 / hkv;  // steps of one head before it
+    const int tb = v0 / hkv;  // places of one head before it
     const int owner = __ffs(__ballot_sync(kFullMask, excl <= tb && tb < excl + sum)) - 1;
     int run = __shfl_sync(kFullMask, excl, owner);
     at.b = owner * K;
     set_seq(at);
-    while (tb >= run + at.T) {
-      run += at.T;
+    while (at.T == 0 || tb >= run + at.T + C) {
+      run += at.T > 0 ? at.T + C : 0;
       ++at.b;
       set_seq(at);
     }
-    const int r = w0 - run * hkv;
-    at.h = r / at.T;
-    at.s = r - at.h * at.T;
+    at.h = (v0 - run * hkv) / (at.T + C);
+    at.v = run * hkv + at.h * (at.T + C);
   }
-  // the first step of the next unit (b = B past the last)
+  // the next unit (b = B past the last)
   auto next_unit = [&](Place& x) {
-    x.s = 0;
+    x.v += x.T + C;
     if (++x.h < hkv) return;
     x.h = 0;
     do {
@@ -178,70 +309,83 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
       set_seq(x);
     } while (x.T == 0);
   };
+  // this warp's steps of a unit: [first_step, end_step), maybe none
+  auto first_step = [&](const Place& x) { return max(0, v0 - x.v - C); };
+  auto end_step = [&](const Place& x) { return min(x.T, v1 - x.v - C); };
 
   // The copies run ahead of the sums, over unit ends.  Their block ids come in
   // windows of 32 (lane l: block l of the window), fetched one window ahead.
-  auto load_ids = [&](const Place& x) -> int {
-    const int j = x.s * SB + lane;
-    return x.b < B && j < x.rem
-               ? __ldg(p.block_tables + static_cast<size_t>(x.b) * p.max_blocks_per_seq +
-                       (RULE ? seq_at(x.b).wb : 0) + j)
+  // Place of the copies' unit, and the window after the one in use: its first
+  // step (within cu) and ids.
+  Place cu = at;
+  int cs = 0, nids = 0;
+  auto fetch_window = [&]() {
+    const int j = cs * SB + lane;
+    nids = cu.b < B && j < cu.rem
+               ? __ldg(p.block_tables + static_cast<size_t>(cu.b) * p.max_blocks_per_seq +
+                       (RULE ? seq_at(cu.b).wb : 0) + j)
                : 0;
   };
-  // the window in use: head, first step, end, blocks from its first on
-  int win_h = 0, win_s = 0, win_end = 0, win_rem = 0, ids = 0;
-  // the next one, and its ids
-  Place nwin = at;
-  int nids = 0;
-  auto fetch_window = [&]() { nids = load_ids(nwin); };
+  // to the next unit that holds steps of this warp, or past its range
+  auto settle = [&]() {
+    while (cu.b < B && cu.v + C < v1 && cs >= end_step(cu)) {
+      next_unit(cu);
+      cs = 0;
+    }
+  };
+  // The window in use: what is left of its steps and blocks; the lane that holds
+  // the next block's id; and this lane's source without the block (lanes 2 u and
+  // 2 u + 1 copy the K and the V tile of a step's block u).
+  int ids = 0, left = 0, blocks = 0, id_at = 0;
+  const unsigned char* src = nullptr;
+  const uint64_t tile_stride = static_cast<uint64_t>(hkv) * Lay::KT;
+  const unsigned char* pool;
+  if constexpr (Q == 3)
+    pool = (lane & 1) ? p.v4 : p.k4;
+  else
+    pool = reinterpret_cast<const unsigned char*>((lane & 1) ? p.v_cache : p.k_cache);
   auto take_window = [&]() {
-    win_h = nwin.h;
-    win_s = nwin.s;
-    win_end = min(nwin.T, nwin.s + WS);
-    win_rem = nwin.rem - nwin.s * SB;
     ids = nids;
-    if (win_end < nwin.T)
-      nwin.s = win_end;
-    else
-      next_unit(nwin);
+    left = min(WS, end_step(cu) - cs);
+    blocks = cu.rem - cs * SB;
+    id_at = (lane >> 1) & (SB - 1);
+    src = pool + static_cast<uint32_t>(cu.h) * Lay::KT;
+    cs += left;
+    settle();
   };
   const uint64_t policy = l2_policy_evict_first();
-  int is = 0, issued = 0;
-  if (n > 0) {
-    fetch_window();
-    take_window();
-    is = win_s;
-    fetch_window();
+  const uint32_t ring_u = smem_u32(wbase) + lane * Lay::KT, bars_u = smem_u32(bars);
+  // whether a step is left to copy
+  auto more = [&]() { return left > 0 || (cu.b < B && cu.v + C < v1); };
+  if (work) {
+    cs = first_step(cu);
+    settle();
+    if (more()) {
+      fetch_window();
+      take_window();
+      if (cu.b < B) fetch_window();
+    }
   }
   auto issue = [&](int st) {
-    if (is == win_end) {
+    if (left == 0) {
       take_window();
-      is = win_s;
-      if (issued + (win_end - win_s) < n) fetch_window();  // it will be read
+      if (cu.b < B && cu.v + C < v1) fetch_window();
     }
-    // lanes 2 u and 2 u + 1 copy the K and the V tile of the step's block u
-    const int u = lane >> 1;
-    int id = __shfl_sync(kFullMask, ids, ((is - win_s) * SB + (u & (SB - 1))) & 31);
-    const int here = min(SB, win_rem - (is - win_s) * SB);  // blocks in the step
-    if (u < here) {
-      if (id < 0 || id >= p.num_blocks) {  // never dereferenced: block 0 is read instead
+    int id = __shfl_sync(kFullMask, ids, id_at);
+    if (lane < 2 * min(SB, blocks)) {
+      if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) {
         if ((lane & 1) == 0) raise_error(p.err, PA_DEVERR_BLOCK_ID);
-        id = 0;
+        id = 0;  // never dereferenced: block 0 is read instead
       }
-      if (lane == 0) mbar_arrive_expect_tx(&bars[st], here * 2 * Lay::KT);
-      const size_t tile = static_cast<size_t>(id) * hkv + win_h;
-      const unsigned char* src;
-      if constexpr (Q == 3)
-        src = (lane & 1) ? p.v4 : p.k4;
-      else
-        src = reinterpret_cast<const unsigned char*>((lane & 1) ? p.v_cache : p.k_cache);
-      bulk_copy_g2s(tiles + st * Lay::STAGE + lane * Lay::KT, src + tile * Lay::KT, Lay::KT,
-                    &bars[st], policy);
+      if (lane == 0) mbar_expect_u32(bars_u + 8 * st, min(SB, blocks) * 2 * Lay::KT);
+      bulk_copy_u32(ring_u + st * E::STAGE, src + static_cast<uint32_t>(id) * tile_stride,
+                    Lay::KT, bars_u + 8 * st, policy);
     }
-    ++is;
-    ++issued;
+    id_at += SB;
+    blocks -= SB;
+    --left;
   };
-  for (int i = 0; i < S && i < n; ++i) issue(i);
+  for (int i = 0; i < S && more(); ++i) issue(i);
   if (p.early_read) griddep_wait();
 
   // an empty sequence's output is zeros, and a new token has no place there
@@ -296,11 +440,9 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
     rule.inv_cap2 = rule.cap2 > 0.f ? 1.f / rule.cap2 : 0.f;
   }
 
-  // A finished piece: v, the lane's V sums, and (m, l) of its H heads; which of
-  // them v[e] belongs to.
+  // A finished piece: the lane's share of its result.
   float v[E::V];
   float2 ml[E::H];
-  auto head_of = [](int e) { return Q == 3 ? e % E::H : e >> 3; };
   auto gather = [&]() {
     if constexpr (Q == 3) {
       w4.finish(lane, v, ml);
@@ -340,89 +482,6 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
       }
     }
   };
-  auto write_out = [&]() {
-    float inv[E::H];
-#pragma unroll
-    for (int h = 0; h < E::H; ++h) inv[h] = 1.0f / ml[h].y;
-    __nv_bfloat16* o =
-        p.out + (static_cast<size_t>(at.b) * p.num_q_heads + static_cast<size_t>(at.h) * G) * D;
-    if constexpr (Q == 3) {
-      if (Warp4<D, G>::owner(tig)) {
-#pragma unroll
-        for (int h = 0; h < E::H; ++h) {
-          __nv_bfloat16* oh = o + Warp4<D, G>::head(tig, h) * D + gid;
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            oh[8 * c] = __float2bfloat16_rn(v[c * E::H + h] * inv[h]);
-        }
-      }
-    } else if (rg * E::H < G) {
-#pragma unroll
-      for (int h = 0; h < E::H; ++h) {
-        __nv_bfloat162 w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w[k] = __float22bfloat162_rn(
-              make_float2(v[8 * h + 2 * k] * inv[h], v[8 * h + 2 * k + 1] * inv[h]));
-        *reinterpret_cast<uint4*>(o + (rg * E::H + h) * D + sub * 8) =
-            *reinterpret_cast<const uint4*>(w);
-      }
-    }
-  };
-  auto store_partial = [&](float* slot) {
-#pragma unroll
-    for (int i = 0; i < E::V / 4; ++i)
-      __stcg(reinterpret_cast<float4*>(slot) + 32 * i + lane,
-             make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-#pragma unroll
-    for (int h = 0; h < E::H; ++h)
-      __stcg(reinterpret_cast<float2*>(slot + 32 * E::V) + 32 * h + lane, ml[h]);
-  };
-  // v, ml: `count` partials merged in order, each weighed against the running
-  // maximum.  slot_at(i): the i-th.
-  auto merge = [&](int count, auto slot_at) {
-    constexpr int U = 2;  // loaded together
-#pragma unroll
-    for (int e = 0; e < E::V; ++e) v[e] = 0.f;
-#pragma unroll
-    for (int h = 0; h < E::H; ++h) ml[h] = make_float2(-INFINITY, 0.f);
-    for (int i0 = 0; i0 < count; i0 += U) {
-      float4 x[U][E::V / 4];
-      float2 y[U][E::H];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i0 + u >= count) break;
-        const float* slot = slot_at(i0 + u);
-#pragma unroll
-        for (int i = 0; i < E::V / 4; ++i)
-          x[u][i] = __ldcg(reinterpret_cast<const float4*>(slot) + 32 * i + lane);
-#pragma unroll
-        for (int h = 0; h < E::H; ++h)
-          y[u][h] = __ldcg(reinterpret_cast<const float2*>(slot + 32 * E::V) + 32 * h + lane);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i0 + u >= count) break;
-        float a[E::H], c[E::H];
-#pragma unroll
-        for (int h = 0; h < E::H; ++h) {
-          const float m = fmaxf(ml[h].x, y[u][h].x);
-          a[h] = ml[h].x == m ? 1.f : exp2f(ml[h].x - m);  // (both -inf: 1)
-          c[h] = y[u][h].x == m ? 1.f : exp2f(y[u][h].x - m);
-          ml[h] = make_float2(m, ml[h].y * a[h] + y[u][h].y * c[h]);
-        }
-#pragma unroll
-        for (int i = 0; i < E::V / 4; ++i) {
-          const float xs[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int e = 4 * i + k;
-            v[e] = v[e] * a[head_of(e)] + xs[k] * c[head_of(e)];
-          }
-        }
-      }
-    }
-  };
   // One arrival of `expected` at a counter, after the warp's writes; the last
   // sees all the others' writes and leaves the counter at zero.
   auto arrive = [&](unsigned* cnt, int expected) -> bool {
@@ -438,20 +497,24 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
   };
 
   bool ok = true;  // every wait so far succeeded (warp-uniform)
-  int st = 0, k = 0;
+  int st = 0;
   unsigned ph = 0;
-  while (k < n) {
-    const int len = min(at.T - at.s, n - k);
-    const bool ends = at.s + len == at.T;
+  while (work && at.b < B && at.v + C < v1) {
+    const int s0 = first_step(at), s1 = end_step(at);
+    if (s0 >= s1) {
+      next_unit(at);
+      continue;
+    }
+    const bool ends = s1 == at.T;
     begin(ends);
+    int j0 = (unit_seq.wb + s0 * SB) * BS;  // the step's first token
 #pragma unroll 1
-    for (int i = 0; i < len; ++i, ++k) {
+    for (int s = s0; s < s1; ++s, j0 += SB * BS) {
       if (ok) ok = __all_sync(kFullMask, mbar_wait_bounded(&bars[st], ph, p.err));
       if (!ok) continue;
-      const int j0 = (unit_seq.wb + (at.s + i) * SB) * BS;  // the step's first token
       const int nvalid = min(BS * SB, unit_seq.ctx - j0);
-      unsigned char* stage = tiles + st * Lay::STAGE;
-      if (patched && i + 1 == len) {
+      unsigned char* stage = tiles + st * E::STAGE;
+      if (patched && s + 1 == s1) {
         patch_tile<D, Q>(stage + (SB > 1 ? (nvalid - 1) / BS * 2 * Lay::KT : 0), Lay::KT, patch,
                          (nvalid - 1) % BS, lane);
         __syncwarp();
@@ -473,54 +536,40 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
                                        sub, rg, my_head, my_i0, rule, j0);
       }
       __syncwarp();  // every lane is done with the stage
-      if (issued < n) issue(st);
+      if (more()) issue(st);
       if (++st == S) {
         st = 0;
         ph ^= 1u;
       }
     }
     gather();
-    bool done = at.s == 0 && ends;  // the whole unit is this warp's
-    if (!done) {
+    __nv_bfloat16* o =
+        p.out + (static_cast<size_t>(at.b) * p.num_q_heads + static_cast<size_t>(at.h) * G) * D;
+    if (s0 == 0 && ends) {  // the whole unit is this warp's
+      even_write_out<D, G, Q>(o, lane, v, ml);
+    } else {
       // the unit's warps, and this one's place among them
-      const int u0 = w0 + k - len - at.s;
-      const int wf = warp_of(u0), wl = warp_of(u0 + at.T - 1);
-      auto slot_of = [&](int w) {
-        return ev.ws + static_cast<size_t>(2 * w + (w == wf ? 1 : 0)) * E::SLOT;
-      };
-      // level 0: the warps of one group of a unit that spans several (a group
-      // holds at most one unit that comes in from the group before, and at most
-      // one that begins in it and goes on into the next); level 1: a unit's
-      // groups, or its warps where one group holds them all
+      const int wf = warp_of(at.v + C), wl = warp_of(at.v + C + at.T - 1);
       const int g0 = wf / kEvenGroup, g1 = wl / kEvenGroup, g = me / kEvenGroup;
-      float* mine = slot_of(me);
-#pragma unroll 1
-      for (int level = g0 == g1 ? 1 : 0; level < 2; ++level) {
-        store_partial(mine);
-        unsigned* cnt;
-        int first, stride, count;
-        if (level == 0) {
-          first = max(wf, g * kEvenGroup);
-          stride = 1;
-          count = min(wl, g * kEvenGroup + kEvenGroup - 1) - first + 1;
-          cnt = ev.group_cnt + 2 * g + (g > g0 ? 0 : 1);
-        } else {
-          first = g0 == g1 ? wf : g0 * kEvenGroup;
-          stride = g0 == g1 ? 1 : kEvenGroup;
-          count = g0 == g1 ? wl - wf + 1 : g1 - g0 + 1;
-          cnt = ev.unit_cnt + static_cast<size_t>(at.b) * hkv + at.h;
+      unsigned* unit = ev.unit_cnt + static_cast<size_t>(at.b) * hkv + at.h;
+      even_store<D, G, Q>(even_slot<D, G, Q>(ev.ws, wf, me), lane, v, ml);
+      if (g0 == g1) {  // one group holds them all
+        if (arrive(unit, wl - wf + 1))
+          even_merge<D, G, Q>(ev.ws, wf, wf, 1, wl - wf + 1, o);
+      } else {
+        // first this group's warps (a group holds at most one unit that comes in
+        // from the group before, and at most one that begins in it and goes on
+        // into the next), then the groups
+        const int first = max(wf, g * kEvenGroup);
+        const int count = min(wl, g * kEvenGroup + kEvenGroup - 1) - first + 1;
+        if (arrive(ev.group_cnt + 2 * g + (g > g0 ? 0 : 1), count)) {
+          if (count > 1) even_merge<D, G, Q>(ev.ws, wf, first, 1, count, nullptr);
+          if (arrive(unit, g1 - g0 + 1))
+            even_merge<D, G, Q>(ev.ws, wf, g0 * kEvenGroup, kEvenGroup, g1 - g0 + 1, o);
         }
-        if (!arrive(cnt, count)) break;
-        merge(count, [&](int i) { return slot_of(max(wf, first + i * stride)); });
-        mine = slot_of(max(wf, first));
-        done = level == 1;
       }
     }
-    if (done) write_out();
-    if (ends)
-      next_unit(at);
-    else
-      at.s += len;
+    next_unit(at);  // (past this warp's range where the unit goes on)
   }
   // Only after a timed-out wait: copies still in flight land (bounded) before
   // the shared memory can be reused.
@@ -549,8 +598,9 @@ cudaError_t launch_even_t(const DecodeParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // no more CTAs than the tables hold steps
   const int64_t steps = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads *
-                        ((p.max_blocks_per_seq + kStepBlocks<Q> - 1) / kStepBlocks<Q>);
-  if (steps > 0x7fffffff) return cudaErrorInvalidValue;
+                        ((p.max_blocks_per_seq + kEvenBlocks<Q> - 1) / kEvenBlocks<Q>);
+  if (steps + static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * kEvenUnitSteps > 0x7fffffff)
+    return cudaErrorInvalidValue;
   if (steps < ctas) ctas = static_cast<int>(steps);
   EvenArgs ev;
   ev.ws = p.ws_o;
