@@ -17,8 +17,9 @@
 // A unit inside one warp's range goes straight to the output.  A unit that
 // spans several leaves one partial (m, l, sum p v) per warp in the workspace,
 // and the last warp to arrive at it merges them in warp order (so the result
-// does not depend on who is last): up to 16 warps at one counter; a longer unit
-// first inside groups of 16 consecutive warps, then over the groups.  Nobody
+// does not depend on who is last): up to 32 partials at one counter; those of a
+// longer unit first inside groups of 16 consecutive warps, then over the groups.
+// Nobody
 // waits for another warp, and every counter is left at zero.
 #pragma once
 
@@ -29,19 +30,22 @@ namespace pa {
 namespace {
 
 constexpr int kEvenWarps = 4;   // warps of a CTA
-constexpr int kEvenGroup = 16;  // warps whose partials one warp merges at once
+// A unit's partials are merged by one warp up to kEvenFlat of them; past that
+// first in groups of kEvenGroup consecutive warps, then group by group.
+constexpr int kEvenFlat = 32;
+constexpr int kEvenGroup = 16;
 // fewer steps than this to a warp (while every unit has one) do not pay
 constexpr int kEvenMinSteps = 4;
 // what beginning a unit (its q, its result) costs a warp, in steps
 constexpr int kEvenUnitSteps = 2;
 // blocks per step
 template <int Q>
-constexpr int kEvenBlocks = Q == 3 ? 2 : 1;
+constexpr int kEvenBlocks = Q == 3 ? 4 : 1;
 
 template <int D, int G, int Q>
 struct Even {
-  static constexpr int S = D == 128 ? 2 : 4;  // ring stages of a warp
-  static constexpr int CTAS = Q == 3 ? (G <= 4 ? 4 : 3) : (G <= 4 ? 3 : 2);  // per SM
+  static constexpr int S = Q == 3 && G == 8 ? 3 : Q == 3 || D == 128 ? 2 : 4;  // ring stages of a warp
+  static constexpr int CTAS = Q == 3 ? (G == 8 ? 2 : 3) : (G <= 4 ? 3 : 2);  // per SM
   using Lay = SmemLayout<D, G, kEvenWarps, S, Q>;
   static constexpr int SB = kEvenBlocks<Q>;
   static constexpr int STAGE = SB * 2 * Lay::KT;
@@ -553,12 +557,12 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G, Q>::CTAS))
       const int g0 = wf / kEvenGroup, g1 = wl / kEvenGroup, g = me / kEvenGroup;
       unsigned* unit = ev.unit_cnt + static_cast<size_t>(at.b) * hkv + at.h;
       even_store<D, G, Q>(even_slot<D, G, Q>(ev.ws, wf, me), lane, v, ml);
-      if (g0 == g1) {  // one group holds them all
+      if (wl - wf < kEvenFlat) {
         if (arrive(unit, wl - wf + 1))
           even_merge<D, G, Q>(ev.ws, wf, wf, 1, wl - wf + 1, o);
       } else {
-        // first this group's warps (a group holds at most one unit that comes in
-        // from the group before, and at most one that begins in it and goes on
+        // first this group's warps (a group holds at most one such unit that comes
+        // in from the group before, and at most one that begins in it and goes on
         // into the next), then the groups
         const int first = max(wf, g * kEvenGroup);
         const int count = min(wl, g * kEvenGroup + kEvenGroup - 1) - first + 1;
