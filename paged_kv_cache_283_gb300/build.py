@@ -20,14 +20,12 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpa.so")
 
 SOURCES = ["api.cu", "decode.cu", "decode_int4.cu", "decode_biased.cu", "decode_int4_even.cu",
-           "decode_biased_even.cu", "splitk_reduce.cu",
-           "reshape_and_cache.cu", "rope_append.cu", "copy_blocks.cu", "noalloc.cu",
+           "splitk_reduce.cu", "reshape_and_cache.cu", "rope_append.cu", "copy_blocks.cu", "noalloc.cu",
            "prefill.cu", "prefill_biased.cu", "allocator.cpp", "sha256.cpp", "scheduler.cpp", "splitk_plan.cpp"]
 HEADERS = [os.path.join(ROOT, "include", "pa.h"), os.path.join(CSRC, "internal.h"),
            os.path.join(CSRC, "device.cuh"), os.path.join(CSRC, "decode_tile.cuh"),
            os.path.join(CSRC, "decode_tile4.cuh"),
-           os.path.join(CSRC, "decode_kernel.cuh"), os.path.join(CSRC, "decode_even.cuh"),
-           os.path.join(CSRC, "prefill_kernel.cuh"),
+           os.path.join(CSRC, "decode_kernel.cuh"), os.path.join(CSRC, "prefill_kernel.cuh"),
            os.path.join(CSRC, "int4_row.cuh"),
            os.path.join(CSRC, "sha256.h"), os.path.join(CSRC, "cache_row.cuh")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

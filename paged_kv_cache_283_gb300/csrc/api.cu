@@ -500,7 +500,7 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
                                   block_size, num_blocks, scale);
   if (s != PA_OK) return s;
   const bool write = key != nullptr || value != nullptr || slot_mapping != nullptr;
-  const bool even = partition_size == PA_SPLIT_EVEN && (kv == 3 || rule);
+  const bool even = partition_size == PA_SPLIT_EVEN && kv == 3;
   const bool split = partition_size != 0 && !even;
   if ((partition_size < 0 && !even) || (split && (partition_size % block_size != 0 || max_partitions <= 0 ||
                                        max_partitions > 65535)))
@@ -513,7 +513,7 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
                 !ok_ptr(counters, 4)))
     return PA_ERR_INVALID_ARG;
   if (even && (!ok_ptr(ws_out, 16) || !ok_ptr(counters, 4))) return PA_ERR_INVALID_ARG;
-  if (even && (num_seqs > PA_EVEN_MAX_SEQS ||
+  if (even && (num_seqs > PA_EVEN_MAX_SEQS || num_q_heads / num_kv_heads > 4 ||
                static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq > 0x7fffffff))
     return PA_ERR_UNSUPPORTED_SHAPE;
   if ((kv == 1 || kv == 2) && (!ok_ptr(k_scales, 16) || !ok_ptr(v_scales, 16))) return PA_ERR_INVALID_ARG;
@@ -571,8 +571,7 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
   if (rule) p.rule = *rule;
   cudaError_t e;
   if (even)
-    e = kv == 3 ? launch_decode_int4_even(p, head_dim, group, st)
-                : launch_decode_biased_even(p, head_dim, group, st);
+    e = launch_decode_int4_even(p, head_dim, group, st);
   else
     e = kv == 3 ? launch_decode_int4(p, head_dim, group, split, st)
         : rule  ? launch_decode_biased(p, head_dim, group, split, st)
@@ -745,13 +744,9 @@ pa_status pa_decode_step_int4(void* out, const void* q, const void* key, const v
                           ws_out, ws_m, ws_l, counters, max_partitions, order, flags, 3, stream);
 }
 
-size_t pa_even_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int kv_kind) {
-  if (pa_decode_supported(num_q_heads, num_kv_heads, head_dim, 16) != PA_OK ||
-      (kv_kind != 0 && kv_kind != 4))
-    return 0;
-  const int group = num_q_heads / num_kv_heads;
-  return sizeof(float) *
-         (kv_kind == 4 ? even_floats_int4(head_dim, group) : even_floats_biased(head_dim, group));
+size_t pa_even_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim) {
+  if (pa_decode_supported(num_q_heads, num_kv_heads, head_dim, 16) != PA_OK) return 0;
+  return sizeof(float) * even_floats_int4(head_dim, num_q_heads / num_kv_heads);
 }
 
 size_t pa_even_counters(int num_seqs, int num_kv_heads) {
@@ -760,7 +755,7 @@ size_t pa_even_counters(int num_seqs, int num_kv_heads) {
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
-  // two for each group of 16 warps, of which an SM holds one at most
+  // two for each group of 16 warps, of which an SM holds less than one
   return static_cast<size_t>(num_seqs) * num_kv_heads + 2 * static_cast<size_t>(sms) + 2;
 }
 

@@ -83,7 +83,7 @@ SIGNATURES = {
     "pa_decode_step_biased": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i,
                                    _i, _i, _i, _f, _f, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _vp,
                                    _i, _vp]),
-    "pa_even_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "pa_even_workspace_bytes": (_sz, [_i, _i, _i]),
     "pa_even_counters": (_sz, [_i, _i]),
     "pa_rope_reshape_and_cache": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
                                        _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
@@ -644,15 +644,13 @@ def step_counters(num_seqs, num_kv_heads, device="cuda"):
     return torch.zeros(num_seqs * num_kv_heads, dtype=torch.int32, device=device)
 
 
-def even_workspace(num_q_heads, num_kv_heads, head_dim, kv, device="cuda"):
-    """(workspace float tensor, None, None) for a pa_decode_step with
-    partition_size PA_SPLIT_EVEN over a "bf16" (changed scores) or "int4" cache:
-    its size does not depend on the batch."""
+def even_workspace(num_q_heads, num_kv_heads, head_dim, device="cuda"):
+    """(workspace float tensor, None, None) for a 4-bit pa_decode_step with
+    partition_size PA_SPLIT_EVEN: its size does not depend on the batch."""
     torch = _torch()
     device = torch.device(device)
     with torch.cuda.device(device):
-        n = lib().pa_even_workspace_bytes(num_q_heads, num_kv_heads, head_dim,
-                                          {"bf16": 0, "int4": 4}[kv])
+        n = lib().pa_even_workspace_bytes(num_q_heads, num_kv_heads, head_dim)
     if n == 0:
         raise ValueError("even_workspace: unsupported shape")
     return torch.empty(n // 4, dtype=torch.float32, device=device), None, None
@@ -724,6 +722,26 @@ def plan_decode_step(context_lens, num_q_heads, num_kv_heads, head_dim, kv="bf16
     return StepPlan(partition_size, maxp, arr, chosen)
 
 
+# From this many (token, KV head) pairs on, a 4-bit step is cut evenly among the
+# warps.  Below it a warp's share (a dozen 64-token steps at the border) does not
+# outweigh its partial's way through the workspace: 64 contexts of 128 to 2048
+# tokens x 8 KV heads (0.55 M) take 24.9 us evenly cut and 22.8 in partitions, 8 of
+# 8K to 128K (1.55 M) 50.7 and 61.0, 33 of up to 5880 x 16 KV heads of 64 dims
+# (1.65 M) 32.8 and 48.4.  Groups of 8 have no such kernel: their state leaves it
+# two CTAs an SM, and it was the same or slower (4.2 M pairs: 147.4 and 148.8 us).
+EVEN_MIN_PAIRS = 1000000
+
+
+def int4_split_evenly(context_lens, num_q_heads, num_kv_heads):
+    """Whether a 4-bit step over these host context lengths is better cut evenly
+    among the GPU's warps (PA_SPLIT_EVEN) than in partitions.  A performance
+    choice only: both give the same attention whatever the lengths."""
+    import numpy as np
+    ctx = np.asarray(context_lens, dtype=np.int64)
+    return num_q_heads // num_kv_heads in (2, 4) and ctx.shape[0] <= PA_EVEN_MAX_SEQS and \
+        int(ctx.sum()) * num_kv_heads >= EVEN_MIN_PAIRS
+
+
 def recover_step_counters(counters):
     """Re-zeroes a split-K pa_decode_step's arrival counters and clears the
     device error word when it holds PA_DEVERR_ORDER or PA_DEVERR_WAIT_TIMEOUT
@@ -782,13 +800,13 @@ def _step_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, key,
                _dev(slot_mapping, torch.int64, "slot_mapping", 1))
     ps = int(partition_size)
     if ps == PA_SPLIT_EVEN:
-        if not (four or ruled):
-            raise ValueError("pa_decode_step: PA_SPLIT_EVEN needs a 4-bit cache or changed scores")
+        if not four:
+            raise ValueError("pa_decode_step: PA_SPLIT_EVEN needs a 4-bit cache")
         if workspace is None or counters is None:
             raise ValueError("pa_decode_step: PA_SPLIT_EVEN needs a workspace and counters")
         if order is not None:
             raise ValueError("pa_decode_step: PA_SPLIT_EVEN takes no order")
-        need = lib().pa_even_workspace_bytes(hq, hkv, d, 4 if four else 0)
+        need = lib().pa_even_workspace_bytes(hq, hkv, d)
         if need == 0 or workspace[0].numel() * 4 < need or \
                 counters.numel() < lib().pa_even_counters(B, hkv):
             raise ValueError("pa_decode_step: even_workspace / even_counters of this shape")
@@ -834,7 +852,7 @@ def pa_decode_step(out, q, k_cache, v_cache, block_tables, context_lens, scale, 
     """Cache write of each sequence's new token (key / value [B, Hkv, D] at
     slot_mapping [B], which must be the slot of position context_lens[b] - 1)
     and the decode, in one launch.  partition_size 0: whole-sequence CTAs;
-    PA_SPLIT_EVEN (4-bit cache, changed scores): cut evenly among the GPU's
+    PA_SPLIT_EVEN (4-bit cache, groups of 2 and 4): cut evenly among the GPU's
     warps (workspace = even_workspace(...), counters = even_counters(...));
     > 0: split-K merged in the same launch (workspace = splitk_workspace(...),
     counters = step_counters(...)).  The cache dtype picks bf16 / INT8 (int8)
@@ -1153,9 +1171,8 @@ class DecodeStep:
     After a launch that raised PA_DEVERR_ORDER or PA_DEVERR_WAIT_TIMEOUT,
     call recover() before the next one.  softcap, alibi_slopes and window change
     the scores (pa_decode_step_biased); with a window the plan, the workspace
-    and the order cover the window only.  Over a 4-bit cache, or with changed
-    scores, partition_size None cuts the work evenly among the GPU's warps
-    (PA_SPLIT_EVEN), which needs no plan.  key, value and slot_mapping None:
+    and the order cover the window only.  Over a 4-bit cache the choice may be
+    to cut the work evenly among the GPU's warps (int4_split_evenly).  key, value and slot_mapping None:
     attention only.
 
     Every argument is checked and marshalled once, here; each call then makes
@@ -1183,15 +1200,12 @@ class DecodeStep:
             self.split = bool(split)
             B, hq, d = q.shape
             hkv = k_cache.shape[1]
-            ruled = bool(softcap) or alibi_slopes is not None or bool(window)
-            even = self.split and (four or ruled) and order is None and (
-                partition_size == PA_SPLIT_EVEN or
-                (partition_size is None and workspace is None and B <= PA_EVEN_MAX_SEQS))
-            if even:
-                # every warp the same share of the batch: nothing to plan
+            if self.split and four and order is None and workspace is None and (
+                    partition_size == PA_SPLIT_EVEN or (
+                        partition_size is None and host_context_lens is not None and
+                        int4_split_evenly(host_context_lens, hq, hkv))):
                 partition_size = PA_SPLIT_EVEN
-                if workspace is None:
-                    workspace = even_workspace(hq, hkv, d, "int4" if four else "bf16", q.device)
+                workspace = even_workspace(hq, hkv, d, q.device)
                 if counters is None:
                     counters = even_counters(B, hkv, q.device)
             elif self.split and host_context_lens is not None and partition_size is None:

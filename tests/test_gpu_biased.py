@@ -100,7 +100,7 @@ def test_biased_step(rule, d, hq, hkv):
                           counters=counters, **kw)
         assert_close(bf16_to_f64(out), ref, f"split {part} {rule}")
         assert not counters.any()
-    for part in (None, 256):          # evenly cut, and in partitions
+    for part in (None, 256):          # chosen, and given
         out.fill_(float("nan"))
         step = pa.DecodeStep(None, None, dk, dv, None, dq, t, c, out, d ** -0.5,
                              partition_size=part, host_context_lens=ctx, **kw)
@@ -109,29 +109,6 @@ def test_biased_step(rule, d, hq, hkv):
         assert_close(bf16_to_f64(out), ref, f"handle {part} {rule}")
         assert not step.counters.any()
     assert pa.pa_get_device_error() == 0
-
-
-@pytest.mark.parametrize("ctx,hq,hkv,d,window", [
-    ([30000], 8, 1, 128, 0), ([9000, 3, 0, 17000], 16, 4, 64, 0), ([5000] * 30, 8, 2, 128, 333),
-    (list(range(0, 900, 9)), 4, 2, 64, 50)])
-def test_biased_even_split_shares(ctx, hq, hkv, d, window):
-    case = _case(len(ctx) + d, [(max(c - 1, 0), min(c, 1)) for c in ctx], hq, hkv, d, window)
-    c, n, tables, kc, vc, _ = case
-    q = normal_bf16(np.random.default_rng(1), (len(ctx), hq, d))
-    ref = np.concatenate([OB.sequence(q[b:b + 1], kc, vc, tables[b], int(c[b]), 0.1, softcap=30.0,
-                                      slopes=_slopes(hq), window=window)
-                          for b in range(len(ctx))])
-    out = torch.full((len(ctx), hq, d), float("nan"), dtype=torch.bfloat16, device="cuda")
-    step = pa.DecodeStep(None, None, dev_bf16(kc), dev_bf16(vc), None, dev_bf16(q),
-                         _dev(tables, np.int32), _dev(c, np.int32), out, 0.1,
-                         partition_size=None, softcap=30.0,
-                         alibi_slopes=_dev(_slopes(hq), np.float32), window=window)
-    assert step.partition_size == pa.PA_SPLIT_EVEN
-    pa.pa_clear_device_error()
-    for _ in range(2):
-        step()
-    assert_close(bf16_to_f64(out), ref, "even split")
-    assert pa.pa_get_device_error() == 0 and not step.counters.any()
 
 
 def test_biased_step_large_scores():
@@ -146,7 +123,7 @@ def test_biased_step_large_scores():
 
 
 @pytest.mark.parametrize("window", [0, 1, 40])
-@pytest.mark.parametrize("part", [0, 32, pa.PA_SPLIT_EVEN])
+@pytest.mark.parametrize("part", [0, 32])
 def test_biased_step_writes(window, part):
     ctx, n, tables, kc, vc, q = _case(4, [(c - 1, 1) for c in (1, 16, 17, 300)], 8, 2, 128,
                                       window)
@@ -159,9 +136,7 @@ def test_biased_step_writes(window, part):
     ref = OB.batch(q, kc, vc, tables, ctx, n, 0.1, window=window, softcap=30.0)
     out = torch.empty(4, 8, 128, dtype=torch.bfloat16, device="cuda")
     kw = {}
-    if part == pa.PA_SPLIT_EVEN:
-        kw = dict(workspace=pa.even_workspace(8, 2, 128, "bf16"), counters=pa.even_counters(4, 2))
-    elif part:
+    if part:
         kw = dict(workspace=pa.splitk_workspace(4, 8, 128, 300, part),
                   counters=pa.step_counters(4, 2))
     pa.pa_clear_device_error()
@@ -178,10 +153,9 @@ def test_biased_step_empty_and_bad_lengths():
     ctx, n, tables, kc, vc, q = _case(6, [(99, 1), (20, 1)], 8, 2, hide=False)
     out = torch.full((2, 8, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
     pa.pa_clear_device_error()
-    for part in (0, 32, pa.PA_SPLIT_EVEN):
+    for part in (0, 32):
         kw = {} if not part else dict(workspace=pa.splitk_workspace(2, 8, 128, 112, part),
-                                      counters=pa.step_counters(2, 2)) if part > 0 else \
-            dict(workspace=pa.even_workspace(8, 2, 128, "bf16"), counters=pa.even_counters(2, 2))
+                                      counters=pa.step_counters(2, 2))
         pa.pa_decode_step(out, dev_bf16(q), dev_bf16(kc), dev_bf16(vc), _dev(tables, np.int32),
                           _dev([100, 0], np.int32), 0.1, partition_size=part, window=10, **kw)
         assert pa.pa_get_device_error() == 0

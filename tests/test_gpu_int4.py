@@ -88,9 +88,11 @@ def _all_ways(case, scale, parts=(512,), what=""):
                               counters=counters, early_read=early)
             _gate(out, ref, V, f"{what} step {part}")
         assert not counters.any()
-    ws, counters = pa.even_workspace(hq, dk.shape[1], d, "int4"), pa.even_counters(B, dk.shape[1])
-    ws[0].fill_(float("nan"))
-    for early in (False, True):
+    even = hq // dk.shape[1] <= 4
+    if even:
+        ws, counters = pa.even_workspace(hq, dk.shape[1], d), pa.even_counters(B, dk.shape[1])
+        ws[0].fill_(float("nan"))
+    for early in (False, True) if even else ():
         out.fill_(float("nan"))
         torch.cuda.synchronize()
         pa.pa_decode_step(out, dq, dk, dv, t, c, scale, partition_size=pa.PA_SPLIT_EVEN,
@@ -127,7 +129,7 @@ def test_int4_decode(hq, hkv, d):
 
 
 @pytest.mark.parametrize("ctx,hq,hkv", [
-    ([5000], 8, 1), ([40000], 8, 2), ([20000, 7, 0, 30000], 8, 1), ([2047] * 40, 8, 2),
+    ([5000], 4, 1), ([40000], 8, 2), ([20000, 7, 0, 30000], 4, 1), ([2047] * 40, 8, 2),
     (list(range(0, 1300, 13)), 4, 2), ([33] * 700, 4, 1)])
 def test_int4_even_split_shares(ctx, hq, hkv):
     # units over many warps and groups of warps, warps over many units
@@ -208,7 +210,7 @@ def test_int4_step_writes_and_attends(d, part):
     pa.pa_clear_device_error()
     kw = {}
     if part == pa.PA_SPLIT_EVEN:
-        kw = dict(workspace=pa.even_workspace(8, 2, d, "int4"), counters=pa.even_counters(B, 2))
+        kw = dict(workspace=pa.even_workspace(8, 2, d), counters=pa.even_counters(B, 2))
     elif part:
         kw = dict(workspace=pa.splitk_workspace(B, 8, d, 400, part),
                   counters=pa.step_counters(B, 2))
@@ -244,6 +246,25 @@ def test_int4_decode_step_handle_plans_and_replays():
         torch.cuda.synchronize()
         ref, V = _ref((rng, ctx, tables, pools, q), 0.088, now)
         _gate(out, ref, V, f"replay {less}")
+
+
+def test_int4_handle_picks_the_even_split_for_long_batches():
+    assert not pa.int4_split_evenly([2048] * 10, 32, 8)
+    assert pa.int4_split_evenly([40000] * 4, 32, 8) and not pa.int4_split_evenly(
+        [40000] * 4, 64, 8)
+    rng, ctx, tables, pools, q = _case(15, [70000, 60000, 5], 32, 8, 64)
+    dk, dv = (torch.from_numpy(p).cuda() for p in pools)
+    out = torch.full((3, 32, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    step = pa.DecodeStep(None, None, dk, dv, None, dev_bf16(q), _dev(tables, np.int32),
+                         _dev(ctx, np.int32), out, 0.125, partition_size=None,
+                         host_context_lens=ctx)
+    assert step.partition_size == pa.PA_SPLIT_EVEN
+    pa.pa_clear_device_error()
+    for _ in range(2):
+        step()
+    ref, V = _ref((rng, ctx, tables, pools, q), 0.125)
+    _gate(out, ref, V, "even split of long contexts")
+    assert pa.pa_get_device_error() == 0 and not step.counters.any()
 
 
 def test_int4_blocks_copy_as_bf16():
@@ -291,6 +312,14 @@ def test_int4_binding_refusals():
             pa.pa_decode_int4(**{**ok, **bad})
     with pytest.raises(ValueError):
         pa.pa_decode_step(**ok, softcap=30.0)       # rules need a bf16 cache
+    with pytest.raises(ValueError):                 # no counters; too small; groups of 8
+        pa.pa_decode_step(**ok, partition_size=pa.PA_SPLIT_EVEN)
+    with pytest.raises(ValueError):
+        pa.pa_decode_step(**ok, partition_size=pa.PA_SPLIT_EVEN,
+                          workspace=(torch.empty(4, device="cuda"), None, None),
+                          counters=pa.even_counters(2, 2))
+    with pytest.raises(ValueError):
+        pa.even_workspace(16, 2, 128)
     with pytest.raises(ValueError):
         pa.pa_decode_step(**ok, k_scales=torch.zeros(3, 2, 16, device="cuda"))
     with pytest.raises(ValueError):
