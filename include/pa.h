@@ -686,6 +686,43 @@ pa_status pa_prefill_biased(void* out, const void* q, const void* k_cache, const
                             pa_stream_t stream);
 
 /*
+ * Prepared calls: a call on fixed device buffers checked once and launched many
+ * times.  pa_prepare_* takes the arguments of the call without the stream, checks
+ * them as the call does, and on PA_OK leaves an object in *prepared (on an error
+ * NULL) that pa_run launches: the same kernels with the same arguments, whatever
+ * the buffers then hold.  It keeps no device memory of its own.  kv_kind: 0 =
+ * bf16 cache, 1 = INT8, 2 = FP8 (with scales), 4 = 4-bit; softcap, alibi_slopes,
+ * window and prefix_lens as the _biased calls (all 0 / NULL: the plain ones).
+ * pa_run needs the device that was current at the preparation to be current
+ * (else PA_ERR_INVALID_ARG).  A prepared call holds the addresses of its buffers:
+ * they must stay valid while it may run.
+ */
+typedef struct pa_prepared pa_prepared;
+pa_status pa_prepare_rope_reshape_and_cache(
+    pa_prepared** prepared, int kv_kind, void* q_out, const void* q, int64_t q_stride,
+    const void* key, int64_t key_stride, const void* value, int64_t value_stride, void* k_cache,
+    void* v_cache, float* k_scales, float* v_scales, const int64_t* slot_mapping,
+    const int32_t* positions, const float* cos_sin, int max_position, int rotary_dim,
+    int interleaved, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks);
+pa_status pa_prepare_decode_step(
+    pa_prepared** prepared, int kv_kind, void* out, const void* q, const void* key,
+    const void* value, const int64_t* slot_mapping, void* k_cache, void* v_cache,
+    float* k_scales, float* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, float scale, float softcap, const float* alibi_slopes,
+    int window, int partition_size, float* ws_out, float* ws_m, float* ws_l, unsigned* counters,
+    int max_partitions, const int32_t* order, int flags);
+pa_status pa_prepare_prefill(
+    pa_prepared** prepared, void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+    const int32_t* query_start_loc, int max_query_len, int num_seqs, int total_query_tokens,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    float softcap, const float* alibi_slopes, int window, const int32_t* prefix_lens);
+pa_status pa_run(const pa_prepared* prepared, pa_stream_t stream);
+void pa_prepared_destroy(pa_prepared* prepared);
+
+/*
  * Split-K partition size for a decode batch (host): the size, from {256, 384,
  * 512, 640, 768, 1024, 1280, 1536, 1792, 2048, 4096} tokens, that minimises a
  * model of the split-K launch's time -- its CTAs handed in grid order to the first free

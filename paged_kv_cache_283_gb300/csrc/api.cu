@@ -493,7 +493,7 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
                            int num_blocks, float scale, int partition_size, float* ws_out,
                            float* ws_m, float* ws_l, unsigned* counters, int max_partitions,
                            const int32_t* order, int flags, int kv, pa_stream_t stream,
-                           const ScoreRule* rule = nullptr) {
+                           const ScoreRule* rule = nullptr, pa_prepared** keep = nullptr) {
   if (rule && !score_rule_ok(*rule, scale)) return PA_ERR_INVALID_ARG;
   pa_status s = check_decode_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                                   context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim,
@@ -505,7 +505,7 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
   if ((partition_size < 0 && !even) || (split && (partition_size % block_size != 0 || max_partitions <= 0 ||
                                        max_partitions > 65535)))
     return PA_ERR_INVALID_ARG;
-  if (num_seqs == 0) return PA_OK;
+  if (num_seqs == 0) return keep ? nothing_to_do(keep) : PA_OK;
   if (!ok_ptr(out, 16)) return PA_ERR_INVALID_ARG;
   if (write && (!ok_ptr(key, 16) || !ok_ptr(value, 16) || !ok_ptr(slot_mapping, 8)))
     return PA_ERR_INVALID_ARG;
@@ -566,32 +566,34 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
   }
   p.err = device_error_word();
   if (!p.err) return cuda_fail(cudaGetLastError());
-  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int group = num_q_heads / num_kv_heads;
-  if (rule) p.rule = *rule;
-  cudaError_t e;
-  if (even)
-    e = launch_decode_int4_even(p, head_dim, group, st);
-  else
-    e = kv == 3 ? launch_decode_int4(p, head_dim, group, split, st)
-        : rule  ? launch_decode_biased(p, head_dim, group, split, st)
-                : launch_decode(p, head_dim, group, split, st);
-  if (e == cudaSuccess && merge_apart) {
-    ReduceParams r{};
-    r.out = p.out;
-    r.ws_o = ws_out;
-    r.ws_m = ws_m;
-    r.ws_l = ws_l;
-    r.context_lens = context_lens;
-    r.err = p.err;
-    r.num_seqs = num_seqs;
-    r.num_q_heads = num_q_heads;
-    r.max_partitions = max_partitions;
-    r.partition_size = partition_size;
-    r.window = rule ? rule->window : 0;
-    e = launch_splitk_reduce(r, head_dim, st);
-  }
-  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+  const bool ruled = rule != nullptr;
+  if (ruled) p.rule = *rule;
+  const int window = ruled ? rule->window : 0;
+  return launch_or_keep(
+      [=](cudaStream_t st) {
+        if (even) return launch_decode_int4_even(p, head_dim, group, st);
+        cudaError_t e = kv == 3 ? launch_decode_int4(p, head_dim, group, split, st)
+                        : ruled ? launch_decode_biased(p, head_dim, group, split, st)
+                                : launch_decode(p, head_dim, group, split, st);
+        if (e == cudaSuccess && merge_apart) {
+          ReduceParams r{};
+          r.out = p.out;
+          r.ws_o = p.ws_o;
+          r.ws_m = p.ws_m;
+          r.ws_l = p.ws_l;
+          r.context_lens = p.context_lens;
+          r.err = p.err;
+          r.num_seqs = p.num_seqs;
+          r.num_q_heads = p.num_q_heads;
+          r.max_partitions = p.max_partitions;
+          r.partition_size = partition_size;
+          r.window = window;
+          e = launch_splitk_reduce(r, head_dim, st);
+        }
+        return e;
+      },
+      keep, stream);
 }
 
 }  // namespace
@@ -816,7 +818,7 @@ pa_status rope_append_impl(void* q_out, const void* q, int64_t q_stride, const v
                            const float* cos_sin, int max_position, int rotary_dim,
                            int interleaved, int num_tokens, int num_q_heads, int num_kv_heads,
                            int head_dim, int block_size, int num_blocks, int kind, bool rope,
-                           pa_stream_t stream) {
+                           pa_stream_t stream, pa_prepared** keep = nullptr) {
   if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       block_size <= 0 || num_blocks <= 0)
     return PA_ERR_INVALID_ARG;
@@ -835,7 +837,7 @@ pa_status rope_append_impl(void* q_out, const void* q, int64_t q_stride, const v
   if (key_stride < kv_row || key_stride % 8 != 0 || value_stride < kv_row ||
       value_stride % 8 != 0)
     return PA_ERR_INVALID_ARG;
-  if (num_tokens == 0) return PA_OK;
+  if (num_tokens == 0) return keep ? nothing_to_do(keep) : PA_OK;
   if (num_q_heads > 0 && (!ok_ptr(q, 16) || !ok_ptr(q_out, 16))) return PA_ERR_INVALID_ARG;
   if (!ok_ptr(key, 16) || !ok_ptr(value, 16) || !ok_ptr(k_cache, 16) || !ok_ptr(v_cache, 16) ||
       !ok_ptr(slot_mapping, 8))
@@ -891,8 +893,8 @@ pa_status rope_append_impl(void* q_out, const void* q, int64_t q_stride, const v
   p.block_size = block_size;
   p.err = device_error_word();
   if (!p.err) return cuda_fail(cudaGetLastError());
-  cudaError_t e = launch_rope_append(p, head_dim, reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+  return launch_or_keep(
+      [=](cudaStream_t st) { return launch_rope_append(p, head_dim, st); }, keep, stream);
 }
 
 }  // namespace
@@ -958,5 +960,57 @@ pa_status pa_rope_reshape_and_cache_int4(
                           max_position, rotary_dim, interleaved, num_tokens, num_q_heads,
                           num_kv_heads, head_dim, block_size, num_blocks, 3, true, stream);
 }
+
+// kv_kind of the C ABI (0 bf16, 1 INT8, 2 FP8, 4 4-bit) to this file's (3).
+static int kind_of(int kv_kind) { return kv_kind == 4 ? 3 : kv_kind; }
+static bool kind_ok(int kv_kind) { return kv_kind == 4 || (kv_kind >= 0 && kv_kind <= 2); }
+
+pa_status pa_prepare_rope_reshape_and_cache(
+    pa_prepared** prepared, int kv_kind, void* q_out, const void* q, int64_t q_stride,
+    const void* key, int64_t key_stride, const void* value, int64_t value_stride, void* k_cache,
+    void* v_cache, float* k_scales, float* v_scales, const int64_t* slot_mapping,
+    const int32_t* positions, const float* cos_sin, int max_position, int rotary_dim,
+    int interleaved, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks) {
+  if (!prepared || !kind_ok(kv_kind)) return PA_ERR_INVALID_ARG;
+  *prepared = nullptr;
+  return rope_append_impl(q_out, q, q_stride, key, key_stride, value, value_stride, k_cache,
+                          v_cache, k_scales, v_scales, slot_mapping, positions, cos_sin,
+                          max_position, rotary_dim, interleaved, num_tokens, num_q_heads,
+                          num_kv_heads, head_dim, block_size, num_blocks, kind_of(kv_kind), true,
+                          nullptr, prepared);
+}
+
+pa_status pa_prepare_decode_step(
+    pa_prepared** prepared, int kv_kind, void* out, const void* q, const void* key,
+    const void* value, const int64_t* slot_mapping, void* k_cache, void* v_cache,
+    float* k_scales, float* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, float scale, float softcap, const float* alibi_slopes,
+    int window, int partition_size, float* ws_out, float* ws_m, float* ws_l, unsigned* counters,
+    int max_partitions, const int32_t* order, int flags) {
+  if (!prepared || !kind_ok(kv_kind)) return PA_ERR_INVALID_ARG;
+  *prepared = nullptr;
+  const bool ruled = softcap != 0.f || alibi_slopes != nullptr || window != 0;
+  if (ruled && kv_kind != 0) return PA_ERR_INVALID_ARG;
+  const ScoreRule rule{alibi_slopes, softcap, window};
+  return decode_step_impl(out, q, key, value, slot_mapping, k_cache, v_cache, k_scales, v_scales,
+                          block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                          num_kv_heads, head_dim, block_size, num_blocks, scale, partition_size,
+                          ws_out, ws_m, ws_l, counters, max_partitions, order, flags,
+                          kind_of(kv_kind), nullptr, ruled ? &rule : nullptr, prepared);
+}
+
+pa_status pa_run(const pa_prepared* prepared, pa_stream_t stream) {
+  if (!prepared) return PA_ERR_INVALID_ARG;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev != prepared->device) return PA_ERR_INVALID_ARG;
+  e = prepared->launch(reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+void pa_prepared_destroy(pa_prepared* prepared) { delete prepared; }
 
 }  // extern "C"

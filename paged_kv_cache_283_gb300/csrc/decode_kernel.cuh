@@ -89,7 +89,7 @@ struct Pipe<128, SPLIT, Q> {
 };
 // Blocks per pipeline stage (and tile step): a 4-bit block is small, and two
 // at a time halve the per-step costs that do not grow with the tokens.
-template <int Q>
+template <int Q, int G>
 constexpr int kStepBlocks = Q == 3 ? 2 : 1;
 // Small bf16 CTAs share an SM three at a time (<= 168 registers); groups of 8
 // heads need more registers than that and get one CTA's worth.  The 1-byte
@@ -114,7 +114,7 @@ struct SmemLayout {
   static constexpr int KT =      // bytes of one K (or V) tile
       Q == 3 ? int4_tile_bytes(D) : I8 ? Geo::BS * D : Geo::TILE;
   static constexpr int STAGE =
-      Q == 3 ? kStepBlocks<Q> * 2 * KT : I8 ? 2 * KT + 2 * Geo::BS * 4 : 2 * KT;
+      Q == 3 ? kStepBlocks<Q, G> * 2 * KT : I8 ? 2 * KT + 2 * Geo::BS * 4 : 2 * KT;
   static constexpr int TILES = S * STAGE;
   // bf16: softmax weights of one tile and the heads' rescale factors (the
   // 1-byte caches keep both in registers)
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
   constexpr bool I8 = Q != 0;   // 1-byte codes + scales
   using Geo = Geometry<D, G>;
   using Lay = SmemLayout<D, G, NW, S, Q>;
-  constexpr int SB = kStepBlocks<Q>;
+  constexpr int SB = kStepBlocks<Q, G>;
   constexpr int BS = Geo::BS, L = Geo::L, P = Geo::P, R = Geo::R;
   extern __shared__ __align__(128) unsigned char smem[];
 

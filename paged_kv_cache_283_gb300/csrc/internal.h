@@ -6,7 +6,17 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <functional>
+#include <new>
+#include <utility>
+
 #include "../../include/pa.h"
+
+// A checked call, kept to be launched again (pa_prepare_*, pa_run).
+struct pa_prepared {
+  int device;
+  std::function<cudaError_t(cudaStream_t)> launch;
+};
 
 namespace pa {
 
@@ -189,5 +199,27 @@ unsigned* device_error_word();
 // Records e as the calling thread's last CUDA error (pa_last_cuda_error) and
 // returns PA_ERR_CUDA.
 pa_status cuda_fail(cudaError_t e);
+
+// A checked call's end: launched on `stream`, or (keep non-null) kept.
+template <typename Launch>
+pa_status launch_or_keep(Launch&& launch, pa_prepared** keep, pa_stream_t stream) {
+  if (!keep) {
+    const cudaError_t e = launch(reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+  }
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  try {
+    *keep = new pa_prepared{dev, std::forward<Launch>(launch)};
+  } catch (const std::bad_alloc&) {
+    return PA_ERR_INVALID_ARG;
+  }
+  return PA_OK;
+}
+// The same for a call with nothing to do.
+inline pa_status nothing_to_do(pa_prepared** keep) {
+  return launch_or_keep([](cudaStream_t) { return cudaSuccess; }, keep, nullptr);
+}
 
 }  // namespace pa

@@ -125,7 +125,7 @@ pa_status prefill_impl(void* out, const void* q, const void* k_cache, const void
                        int max_query_len, int num_seqs, int total_query_tokens, int num_q_heads,
                        int num_kv_heads, int head_dim, int block_size, int num_blocks,
                        float scale, const pa::ScoreRule* rule, const int32_t* prefix_lens,
-                       pa_stream_t stream) {
+                       pa_stream_t stream, pa_prepared** keep = nullptr) {
   using namespace pa;
   if (num_seqs < 0 || max_query_len < 0 || total_query_tokens < 0 || num_q_heads <= 0 ||
       num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || max_blocks_per_seq <= 0 ||
@@ -134,7 +134,8 @@ pa_status prefill_impl(void* out, const void* q, const void* k_cache, const void
   if (rule && !score_rule_ok(*rule, scale)) return PA_ERR_INVALID_ARG;
   const int group = num_q_heads / num_kv_heads;
   if (!pa_prefill_supported(head_dim, group, block_size)) return PA_ERR_UNSUPPORTED_SHAPE;
-  if (num_seqs == 0 || max_query_len == 0 || total_query_tokens == 0) return PA_OK;
+  if (num_seqs == 0 || max_query_len == 0 || total_query_tokens == 0)
+    return keep ? nothing_to_do(keep) : PA_OK;
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
       !block_tables || !context_lens || !query_start_loc)
     return PA_ERR_INVALID_ARG;
@@ -158,22 +159,23 @@ pa_status prefill_impl(void* out, const void* q, const void* k_cache, const void
   p.num_blocks = num_blocks;
   p.total_q = total_query_tokens;
   p.scale_log2 = scale * 1.4426950408889634f;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (rule) {
+  const bool ruled = rule != nullptr;
+  if (ruled) {
     p.rule = *rule;
     p.prefix_lens = prefix_lens;
     p.cap_in = rule->softcap > 0.f ? scale / rule->softcap : 0.f;
-    e = launch_prefill_biased(tq, tk, tv, p, group, max_query_len, num_seqs, s);
-  } else {
-    switch (group) {
-      case 1: e = launch_prefill_g<1>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
-      case 2: e = launch_prefill_g<2>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
-      case 4: e = launch_prefill_g<4>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
-      default: e = launch_prefill_g<8>(tq, tk, tv, p, max_query_len, num_seqs, s); break;
-    }
   }
-  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+  return launch_or_keep(
+      [=](cudaStream_t s) {
+        if (ruled) return launch_prefill_biased(tq, tk, tv, p, group, max_query_len, num_seqs, s);
+        switch (group) {
+          case 1: return launch_prefill_g<1>(tq, tk, tv, p, max_query_len, num_seqs, s);
+          case 2: return launch_prefill_g<2>(tq, tk, tv, p, max_query_len, num_seqs, s);
+          case 4: return launch_prefill_g<4>(tq, tk, tv, p, max_query_len, num_seqs, s);
+          default: return launch_prefill_g<8>(tq, tk, tv, p, max_query_len, num_seqs, s);
+        }
+      },
+      keep, stream);
 }
 
 }  // namespace
@@ -203,4 +205,20 @@ extern "C" pa_status pa_prefill_biased(
                       query_start_loc, max_query_len, num_seqs, total_query_tokens, num_q_heads,
                       num_kv_heads, head_dim, block_size, num_blocks, scale, &rule, prefix_lens,
                       stream);
+}
+
+extern "C" pa_status pa_prepare_prefill(
+    pa_prepared** prepared, void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+    const int32_t* query_start_loc, int max_query_len, int num_seqs, int total_query_tokens,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    float softcap, const float* alibi_slopes, int window, const int32_t* prefix_lens) {
+  if (!prepared || reinterpret_cast<uintptr_t>(prefix_lens) % 4 != 0) return PA_ERR_INVALID_ARG;
+  *prepared = nullptr;
+  const pa::ScoreRule rule{alibi_slopes, softcap, window};
+  const bool ruled = softcap != 0.f || alibi_slopes != nullptr || window != 0 || prefix_lens;
+  return prefill_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                      query_start_loc, max_query_len, num_seqs, total_query_tokens, num_q_heads,
+                      num_kv_heads, head_dim, block_size, num_blocks, scale,
+                      ruled ? &rule : nullptr, prefix_lens, nullptr, prepared);
 }

@@ -102,6 +102,17 @@ SIGNATURES = {
                         _f, _vp]),
     "pa_prefill_biased": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i,
                                _i, _i, _f, _f, _vp, _i, _vp, _vp]),
+    "pa_prepare_rope_reshape_and_cache": (
+        _i, [ctypes.POINTER(_vp), _i, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
+             _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i]),
+    "pa_prepare_decode_step": (
+        _i, [ctypes.POINTER(_vp), _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp,
+             _i, _i, _i, _i, _i, _i, _f, _f, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _i]),
+    "pa_prepare_prefill": (
+        _i, [ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i,
+             _i, _i, _f, _f, _vp, _i, _vp]),
+    "pa_run": (_i, [_vp, _vp]),
+    "pa_prepared_destroy": (None, [_vp]),
     "pa_plan_step": (_i, [_i, _i, _vp, _i, _vp, _pint]),
     "pa_alloc_create": (_i, [_i, _i, _vp, ctypes.POINTER(_vp)]),
     "pa_alloc_destroy": (None, [_vp]),
@@ -247,6 +258,32 @@ def pa_copy_blocks(k_caches, v_caches, block_mapping, stream=None):
     _check(st, "pa_copy_blocks")
 
 
+class _Prepared:
+    """A prepared call (pa_prepare_*, pa_run): checked and marshalled once, each
+    run two arguments.  Passing a step's two dozen through ctypes takes 2 us of the
+    5 that a small call lasts."""
+
+    def __init__(self, prepare, *args):
+        h = ctypes.c_void_p()
+        fn = getattr(lib(), prepare)
+        _check(fn(ctypes.byref(h), *args), prepare)
+        self._h = h
+        self._run = lib().pa_run
+
+    def __call__(self, stream, where):
+        st = self._run(self._h, stream)
+        if st != PA_OK:
+            _check(st, where)
+
+    def __del__(self):
+        try:
+            if self._h:
+                lib().pa_prepared_destroy(self._h)
+                self._h = None
+        except Exception:
+            pass
+
+
 def _one_device(what, *tensors):
     """Refuses tensors that do not all live on the current CUDA device, on whose
     current stream the launch goes."""
@@ -327,7 +364,8 @@ def _heads(t, name):
 
 def _rope_append_args(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
                       interleaved, k_scales, v_scales):
-    """(C function, argument tuple without the stream) for pa_rope_reshape_and_cache*."""
+    """(name suffix of the C function, its arguments without the stream) for
+    pa_rope_reshape_and_cache*."""
     torch = _torch()
     what = "pa_rope_reshape_and_cache"
     T, hkv, d = key.shape
@@ -380,7 +418,7 @@ def _rope_append_args(q_out, q, key, value, k_cache, v_cache, slot_mapping, posi
         _dev(slot_mapping, torch.int64, "slot_mapping", 1),
         _dev(positions, torch.int32, "positions", 1), _dev(cos_sin, torch.float32, "cos_sin", 2),
         cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, T, hq, hkv, d, bs, nb)
-    return getattr(lib(), "pa_rope_reshape_and_cache" + name), args
+    return name, args
 
 
 def pa_rope_reshape_and_cache(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions,
@@ -393,31 +431,33 @@ def pa_rope_reshape_and_cache(q_out, q, key, value, k_cache, v_cache, slot_mappi
     cos_sin [max_position, rotary_dim] fp32 (rope_table).  The pools' type picks
     the cache: bf16, int8 or uint8 (FP8 codes) [NB, Hkv, 16, D] with scales, or
     4-bit [NB, Hkv, 9 * D] uint8.  q and q_out None: k and v only."""
-    fn, args = _rope_append_args(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions,
-                                 cos_sin, interleaved, k_scales, v_scales)
-    _check(fn(*args, _stream(stream)), "pa_rope_reshape_and_cache")
+    name, args = _rope_append_args(q_out, q, key, value, k_cache, v_cache, slot_mapping,
+                                   positions, cos_sin, interleaved, k_scales, v_scales)
+    _check(getattr(lib(), "pa_rope_reshape_and_cache" + name)(*args, _stream(stream)),
+           "pa_rope_reshape_and_cache")
 
 
 class RopeAppend:
     """pa_rope_reshape_and_cache of one layer on fixed device buffers, its
-    arguments checked and marshalled once; each call is one bare C call.  The
+    arguments checked and marshalled once; each call is one bare launch.  The
     buffers' contents may change between calls, their shapes and addresses may
     not."""
 
     def __init__(self, q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
                  interleaved=False, k_scales=None, v_scales=None, stream=None):
-        self._fn, self._args = _rope_append_args(q_out, q, key, value, k_cache, v_cache,
-                                                 slot_mapping, positions, cos_sin, interleaved,
-                                                 k_scales, v_scales)
+        name, args = _rope_append_args(q_out, q, key, value, k_cache, v_cache, slot_mapping,
+                                       positions, cos_sin, interleaved, k_scales, v_scales)
+        if name in ("", "_int4"):       # no scales
+            args = args[:9] + (None, None) + args[9:]
+        self._call = _Prepared("pa_prepare_rope_reshape_and_cache",
+                               {"": 0, "_int8": 1, "_fp8": 2, "_int4": 4}[name], *args)
         self._stream = None if stream is None else ctypes.c_void_p(stream.cuda_stream)
         self._keep = [q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
                       k_scales, v_scales]
 
     def __call__(self, stream=None):
         s = self._stream if stream is None and self._stream is not None else _stream(stream)
-        st = self._fn(*self._args, s)
-        if st != PA_OK:
-            _check(st, "RopeAppend: pa_rope_reshape_and_cache")
+        self._call(s, "RopeAppend: pa_rope_reshape_and_cache")
 
 
 def _decode_common(q, k_cache, v_cache, block_tables, context_lens):
@@ -1117,7 +1157,7 @@ def pa_prefill_biased(out, q, k_cache, v_cache, block_tables, context_lens, quer
 
 class PrefillStep:
     """One prefill call of one layer on fixed device buffers, its arguments
-    checked and marshalled once; each call is one bare C call: pa_prefill, or
+    checked and marshalled once; each call is one bare launch: pa_prefill, or
     pa_prefill_biased when softcap, alibi_slopes, window or prefix_lens is
     given.  The buffers' contents may change between calls, their shapes and
     addresses may not."""
@@ -1128,19 +1168,14 @@ class PrefillStep:
         args = _prefill_biased_args(out, q, k_cache, v_cache, block_tables, context_lens,
                                     query_start_loc, max_query_len, scale, softcap,
                                     alibi_slopes, window, prefix_lens)
-        if softcap or alibi_slopes is not None or window or prefix_lens is not None:
-            self._fn, self._args = lib().pa_prefill_biased, args
-        else:
-            self._fn, self._args = lib().pa_prefill, args[:17]
+        self._call = _Prepared("pa_prepare_prefill", *args)
         self._stream = None if stream is None else ctypes.c_void_p(stream.cuda_stream)
         self._keep = [out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
                       alibi_slopes, prefix_lens]
 
     def __call__(self, stream=None):
         s = self._stream if stream is None and self._stream is not None else _stream(stream)
-        st = self._fn(*self._args, s)
-        if st != PA_OK:
-            _check(st, "PrefillStep: prefill")
+        self._call(s, "PrefillStep: prefill")
 
 
 def pa_plan_step(budget, num_decodes, prefill_remaining):
@@ -1249,6 +1284,14 @@ class DecodeStep:
             self._keep = [key, value, k_cache, v_cache, slot_mapping, q, block_tables,
                           context_lens, out, workspace, counters, k_scales, v_scales, order,
                           alibi_slopes]
+            self._call = None
+            if four or softcap or alibi_slopes is not None or window:
+                # out q key value slots | pools | tables .. scale | rule | the rest
+                a = self._args
+                rule = (0.0, None, 0) if four else a[17:20]
+                self._call = _Prepared(
+                    "pa_prepare_decode_step", 4 if four else 0, *a[:7], None, None, *a[7:17],
+                    *rule, *a[17 if four else 20:])
             return
         if partition_size is None:
             partition_size = 512
@@ -1321,6 +1364,9 @@ class DecodeStep:
     def __call__(self, stream=None):
         s = self._stream if stream is None and self._stream is not None else _stream(stream)
         if self.fused:
+            if self._call is not None:
+                self._call(s, "DecodeStep: pa_decode_step")
+                return
             st = self._fn(*self._args, s)
             if st != PA_OK:
                 _check(st, "DecodeStep: pa_decode_step")

@@ -308,3 +308,28 @@ def test_binding_refuses_without_a_gpu():
         pa.pa_reshape_and_cache_int4(x, x, torch.zeros(3, 4, 1152, dtype=torch.uint8),
                                      torch.zeros(3, 4, 1152, dtype=torch.uint8),
                                      torch.zeros(2, dtype=torch.int64))
+
+
+def test_prepared_calls_check_as_the_calls_do(lib):
+    h = ctypes.c_void_p(123)
+    bad, shape = pa.PA_ERR_INVALID_ARG, pa.PA_ERR_UNSUPPORTED_SHAPE
+
+    def step(kind=4, part=512, cap=0.0, window=0, out=F):
+        return lib.pa_prepare_decode_step(
+            ctypes.byref(h), kind, out, F, None, None, None, F, F, None, None, F, 4, F, 2, 32, 8,
+            128, 16, 10, 0.1, cap, None, window, part, F, F, F, F, 4, None, 0)
+
+    assert step(kind=3) == bad and step(kind=-1) == bad and step(out=None) == bad
+    assert h.value is None                          # an error leaves no object
+    assert step(part=100) == bad and step(cap=30.0) == bad      # rules: bf16 only
+    assert step(kind=1) == bad                      # INT8 needs scales
+    assert step(kind=0, window=-1) == bad
+    assert lib.pa_prepare_rope_reshape_and_cache(
+        ctypes.byref(h), 0, None, None, 0, F, 1024, F, 1024, F, F, None, None, F, F, F, 100, 24,
+        0, 3, 0, 8, 128, 16, 10) == shape
+    assert lib.pa_prepare_prefill(ctypes.byref(h), F, F, F, F, F, 4, F, F, 8, 2, 16, 32, 8, 64,
+                                  16, 10, 0.1, 0.0, None, 0, None) == shape
+    assert lib.pa_prepare_prefill(None, F, F, F, F, F, 4, F, F, 8, 2, 16, 32, 8, 128, 16, 10,
+                                  0.1, 0.0, None, 0, None) == bad
+    assert lib.pa_run(None, None) == bad
+    lib.pa_prepared_destroy(None)
