@@ -731,7 +731,8 @@ void pa_prepared_destroy(pa_prepared* prepared);
  * share -- with ties going to the larger size; in grid order a 1-byte cache
  * (issue-bound kernels) whose batch has fewer (sequence, KV head) units than
  * CTA slots takes 512.  context_lens: host int32
- * [num_seqs]; kv_kind 0 = bf16 cache, 1 = INT8, 2 = FP8, 4 = 4-bit; num_sms the device's
+ * [num_seqs]; kv_kind 0 = bf16 cache, 1 = INT8, 2 = FP8, 4 = 4-bit,
+ * 5 = bf16 with changed scores (pa_decode_step_biased); num_sms the device's
  * multiprocessor count; ordered != 0 models the launch with the
  * longest-first order of pa_splitk_order, 0 the plain grid order.  Returns 0
  * on invalid arguments.  The result is a

@@ -26,6 +26,12 @@
 // head) units than slots they take 512-token partitions in grid order, the
 // measured best there.  Longest first, the model's choice matched the
 // measured best for them too (batch 64: 1024; 32 layers: 2048).
+//
+// The 4-bit cache and the bf16 cache with changed scores have costs of their
+// own, fitted to 26 and 33 batches of 1 to 156 sequences and 16 to 49,796 tokens
+// (the sizes' mean time over the best size's: 1.020 and 1.006; with the constants
+// above 1.029 and 1.033, and 54.2 instead of 48.7 us for 64 windows of 1024
+// tokens, which 768 splits and 1280 does not).
 
 #include <stdint.h>
 
@@ -40,29 +46,32 @@ namespace {
 
 // Costs (µs) fitted per dispatch order: grid order, and longest first.
 struct Costs {
-  double token_bf16;  // per token and KV head, head_dim 128, bf16 cache
-  double token_1byte;
+  double token;  // per token and KV head, head_dim 128
   double cta;
   double merge;
 };
-constexpr Costs kGridCosts = {0.025, 0.019, 4.0, 2.0};
-constexpr Costs kOrderedCosts = {0.022, 0.0167, 7.0, 3.0};
+// kv_kind: 0 bf16, 1 INT8, 2 FP8, 4 4-bit, 5 bf16 with changed scores
+Costs costs_of(int kv_kind, bool ordered) {
+  if (kv_kind == 4) return {0.006, 2.0, 1.0};
+  if (kv_kind == 5) return {0.022, 4.0, 1.0};
+  if (ordered) return {kv_kind == 0 ? 0.022 : 0.0167, 7.0, 3.0};
+  return {kv_kind == 0 ? 0.025 : 0.019, 4.0, 2.0};
+}
 constexpr double kApartUs = 3.0;
 constexpr int kMergeInKernelParts = 16;  // as pa_decode_step
 constexpr int kCandidates[] = {256, 384, 512, 640, 768, 1024, 1280, 1536, 1792, 2048, 4096};
 
 // CTAs per SM of the split-K kernels (their __launch_bounds__ minimum).
 int ctas_per_sm(int group, int kv_kind) {
-  if (kv_kind == 0) return group <= 4 ? 3 : 1;
+  if (kv_kind == 0 || kv_kind == 5) return group <= 4 ? 3 : 1;
   return group <= 4 ? 4 : 3;
 }
 
 // Tokens of item (b, z) of a split into `part`-token partitions.
 int item_tokens(int n, int z, int part) { return std::max(0, std::min(part, n - z * part)); }
 
-double makespan(const int32_t* ctx, int num_seqs, int hkv, int part, int slots, double token_us,
-                bool ordered) {
-  const Costs& k = ordered ? kOrderedCosts : kGridCosts;
+double makespan(const int32_t* ctx, int num_seqs, int hkv, int part, int slots, const Costs& k,
+                double token_us, bool ordered) {
   int maxp = 1;
   for (int b = 0; b < num_seqs; ++b) maxp = std::max(maxp, (std::max(ctx[b], 0) + part - 1) / part);
   const bool apart = maxp > kMergeInKernelParts;
@@ -103,16 +112,16 @@ extern "C" int pa_splitk_partition_size(const int32_t* context_lens, int num_seq
                                         int kv_kind, int num_sms, int ordered) {
   if (!context_lens || num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
       num_q_heads % num_kv_heads != 0 || head_dim <= 0 ||
-      (kv_kind != 4 && (kv_kind < 0 || kv_kind > 2)) ||
+      (!(kv_kind >= 0 && kv_kind <= 2) && kv_kind != 4 && kv_kind != 5) ||
       num_sms <= 0)
     return 0;
   const int group = num_q_heads / num_kv_heads;
   const int slots = num_sms * ctas_per_sm(group, kv_kind);
-  const Costs& k = ordered ? kOrderedCosts : kGridCosts;
-  const double token_us = (kv_kind == 0 ? k.token_bf16 : k.token_1byte) * head_dim / 128.0;
+  const Costs k = costs_of(kv_kind, ordered != 0);
+  const double token_us = k.token * head_dim / 128.0;
   int max_ctx = 0;
   for (int b = 0; b < num_seqs; ++b) max_ctx = std::max(max_ctx, context_lens[b]);
-  if (!ordered && kv_kind != 0 && static_cast<int64_t>(num_seqs) * num_kv_heads < slots &&
+  if (!ordered && (kv_kind == 1 || kv_kind == 2) && static_cast<int64_t>(num_seqs) * num_kv_heads < slots &&
       (static_cast<int64_t>(max_ctx) + 511) / 512 <= 65535)
     return 512;
   int best = 0;
@@ -120,7 +129,7 @@ extern "C" int pa_splitk_partition_size(const int32_t* context_lens, int num_seq
   for (int part : kCandidates) {
     if ((static_cast<int64_t>(max_ctx) + part - 1) / part > 65535) continue;  // grid z
     const double t =
-        makespan(context_lens, num_seqs, num_kv_heads, part, slots, token_us, ordered != 0);
+        makespan(context_lens, num_seqs, num_kv_heads, part, slots, k, token_us, ordered != 0);
     // ties go to the larger partition: fewer CTAs, less workspace
     if (best == 0 || t <= best_t + 1e-9) {
       best = part;

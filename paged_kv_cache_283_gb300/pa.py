@@ -655,7 +655,7 @@ def splitk_partition_size(context_lens, num_q_heads, num_kv_heads, head_dim, kv=
     if num_sms is None:
         torch = _torch()
         num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
-    kind = {"bf16": 0, "int8": 1, "fp8": 2, "int4": 4}[kv]
+    kind = {"bf16": 0, "int8": 1, "fp8": 2, "int4": 4, "bf16-biased": 5}[kv]
     r = lib().pa_splitk_partition_size(ctx.ctypes.data_as(ctypes.c_void_p), ctx.shape[0],
                                        num_q_heads, num_kv_heads, head_dim, kind, int(num_sms),
                                        1 if ordered else 0)
@@ -1249,8 +1249,10 @@ class DecodeStep:
                 # workspace and the order cover the block tables' capacity
                 # unless max_context_len says less, so the contexts may grow
                 # from call to call up to that capacity.
+                ruled = bool(softcap) or alibi_slopes is not None or bool(window)
                 kind = ("int4" if four else "fp8" if k_cache.dtype == torch.uint8 else
-                        "int8" if k_cache.dtype == torch.int8 else "bf16")
+                        "int8" if k_cache.dtype == torch.int8 else
+                        "bf16-biased" if ruled else "bf16")
                 if max_context_len is None:
                     max_context_len = block_tables.shape[1] * block
                 if window:  # what a step reads: the window, from a block's start
