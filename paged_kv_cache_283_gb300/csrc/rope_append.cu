@@ -74,6 +74,33 @@ __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
   return v;
 }
 
+// The quantisers' codes are defined by the rounded quotient x / scale.  A row's 16
+// quotients a lane were most of a quantising launch; here a quotient is x times
+// the rounded reciprocal, off by less than 2^-22 of itself, which rounds to the
+// same code unless it lies that near a border between two codes, and there (or
+// for a scale whose reciprocal is no normal number) the division is made.
+constexpr float kMinScale = 1e-30f, kMaxScale = 1e30f;  // of which the reciprocal is used
+
+// round_half_even(x / scale), within +-2^21.
+__device__ __forceinline__ float round_quotient(float x, float scale, float inv, bool divide) {
+  const float t = __fmul_rn(x, inv);
+  const float magic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+  float c = __fsub_rn(__fadd_rn(t, magic), magic);
+  // (|t| up to 127: an error below 3e-5)
+  if (divide || fabsf(fabsf(__fsub_rn(t, c)) - 0.5f) < 1e-4f) c = rintf(__fdiv_rn(x, scale));
+  return c;
+}
+
+// x / scale as E4M3 takes it: the quotient, exact wherever its E4M3 code could
+// depend on its last bits.
+__device__ __forceinline__ float e4m3_quotient(float x, float scale, float inv, bool divide) {
+  const float t = __fmul_rn(x, inv);
+  // a border between two codes: the 20 bits below E4M3's 3 are half a step
+  const uint32_t low = __float_as_uint(t) & 0xFFFFFu;
+  if (divide || !(fabsf(t) >= 0.015625f) || low - 0x7FFF0u <= 0x20u) return __fdiv_rn(x, scale);
+  return t;
+}
+
 // Two chunks (ca, cb: 8-dim chunk indices) of one row quantised and stored.
 // The L lanes of the row call it together; mask: those lanes.  x: the 16
 // values, chunk ca's then chunk cb's.
@@ -120,11 +147,18 @@ __device__ __forceinline__ void store_quantised(const RopeAppendParams& p, bool 
     }
     uint32_t c[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int g = (i < 8 ? ca : cb) / 8;
+    for (int h = 0; h < 2; ++h) {
+      const int g = (h == 0 ? ca : cb) / 8;
       const float l = NG == 1 || g == 0 ? lo[0] : lo[NG - 1];
       const float s = NG == 1 || g == 0 ? scale[0] : scale[NG - 1];
-      c[i] = int4_code(x[i], l, s);
+      const float inv = __frcp_rn(s);
+      const bool divide = !(s >= kMinScale && s <= kMaxScale);
+#pragma unroll
+      for (int i = 8 * h; i < 8 * h + 8; ++i) {
+        // int4_code: clamped to 0..15 (a NaN to 0), 0 where the scale is 0
+        const float q = round_quotient(__fsub_rn(x[i], l), s, inv, divide);
+        c[i] = s > 0.f ? static_cast<uint32_t>(fminf(15.f, fmaxf(0.f, q))) : 0u;
+      }
     }
     if (is_v) {  // chunks 2 j, 2 j + 1: dims 16 j + i and 16 j + i + 8
 #pragma unroll
@@ -150,19 +184,22 @@ __device__ __forceinline__ void store_quantised(const RopeAppendParams& p, bool 
     for (int m = L / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, m));
     const float scale = __fmul_rn(amax, Q == 2 ? 1.0f / 448.0f : 1.0f / 127.0f);
     uint32_t w[4] = {0, 0, 0, 0};  // chunk ca's 8 codes, chunk cb's 8 codes
+    const float inv = __frcp_rn(scale);
+    const bool divide = !(scale >= kMinScale && scale <= kMaxScale);
     if (scale > 0.f) {
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
         uint32_t two;
         if constexpr (Q == 2) {
           two = __nv_cvt_float2_to_fp8x2(
-              make_float2(__fdiv_rn(x[i], scale), __fdiv_rn(x[i + 1], scale)), __NV_SATFINITE,
-              __NV_E4M3);
+              make_float2(e4m3_quotient(x[i], scale, inv, divide),
+                          e4m3_quotient(x[i + 1], scale, inv, divide)),
+              __NV_SATFINITE, __NV_E4M3);
         } else {
           const int a = static_cast<int>(
-              fminf(127.f, fmaxf(-127.f, rintf(__fdiv_rn(x[i], scale)))));
+              fminf(127.f, fmaxf(-127.f, round_quotient(x[i], scale, inv, divide))));
           const int b = static_cast<int>(
-              fminf(127.f, fmaxf(-127.f, rintf(__fdiv_rn(x[i + 1], scale)))));
+              fminf(127.f, fmaxf(-127.f, round_quotient(x[i + 1], scale, inv, divide))));
           two = (static_cast<uint32_t>(a) & 0xffu) | ((static_cast<uint32_t>(b) & 0xffu) << 8);
         }
         w[i / 4] |= two << (8 * (i % 4));
@@ -305,7 +342,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendP
 
 template <int D, int Q>
 cudaError_t launch_t(const RopeAppendParams& p, cudaStream_t stream) {
-  constexpr int L = D / 16, U = 4;
+  constexpr int L = D / 16, U = 3;
   const int rows = p.num_q_heads + 2 * p.num_kv_heads;
   // While one row per thread fills less than the GPU's threads, the call is a
   // chain of round trips and a row to a thread is the shortest; past that a
