@@ -527,8 +527,8 @@ pa_status pa_decode_step_fp8(void* out, const void* q, const void* key, const vo
 /*
  * partition_size PA_SPLIT_EVEN (pa_decode_step_int4): one launch in which every
  * warp of the GPU takes the same share of the whole batch's context, whatever the
- * lengths; no partition size, no work order.  Faster than partitions where a
- * warp's share is long (from about a million (token, KV head) pairs on).
+ * lengths; no partition size, no work order.  Faster than partitions for a few
+ * long contexts (from about a million (token, KV head) pairs on, 32K tokens in one).
  *   ws_out  : pa_even_workspace_bytes(...) bytes, its size the same for every
  *             batch; ws_m, ws_l, max_partitions and order are ignored.
  *   counters: device uint32 [pa_even_counters(num_seqs, num_kv_heads)], all zero

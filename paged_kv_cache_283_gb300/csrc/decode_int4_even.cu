@@ -20,12 +20,14 @@
 // longer unit first inside groups of 16 consecutive warps, then over the groups.
 // Nobody waits for another warp, and every counter is left at zero.
 //
-// Measured (32 query / 8 KV heads, D = 128): 8 contexts of 8K to 128K tokens
-// 50.7 us against 61.0 in partitions (33.0 at the copy rate); 8 of 128K tokens
-// 201 us (178); 64 of 128 to 2048 tokens 24.9 against 22.8: a warp's share must
+// Measured (32 query / 8 KV heads, D = 128): 8 contexts of 8K to 50K tokens 47.6
+// us against 53.7 in the best partitions (33.0 at the copy rate); 8 of 128K tokens
+// 193 us (178); 64 of 128 to 2048 tokens 22.0 against 20.1: a warp's share must
 // outweigh its merges, see the binding's rule.  Steps of 64 tokens with three
-// CTAs an SM (168 registers a thread) against 32 with four (128 registers): 201
-// against 225 us; of 96 with two: 204.
+// CTAs an SM (168 registers a thread); 32 with four (128 registers) take 196 us
+// for the 8 x 128K and 69.8 against 66.9 for 8 x 40,000; 96 with two 187 for the
+// former, but 122 against 106 for 500 short ones and, with D = 64, 93 against 71
+// for 64 of 4K to 16K tokens.
 #include "decode_kernel.cuh"
 
 namespace pa {
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(kEvenWarps * 32, (Even<D, G>::CTAS))
     ids = nids;
     left = min(WS, end_step(cu) - cs);
     blocks = cu.rem - cs * SB;
-    id_at = (lane >> 1) & (SB - 1);
+    id_at = min(lane >> 1, SB - 1);
     src = pool + static_cast<uint32_t>(cu.h) * E::KT;
     cs += left;
     settle();

@@ -5,20 +5,23 @@
 // Everything that does not depend on the head is done once for the warp, and
 // everything that does once per (token, head):
 //
-// QK: S = K q, the MMA's rows the block's 16 tokens, in E4M3 (m16n8k32): a
-// nibble in a byte IS the E4M3 value code * 2^-9 (codes 0..15 run through the
-// subnormals and the first binade, which have one spacing), so a mask, and a
-// shift and a mask, turn a 32-bit word into its 8 codes.  q comes in two E4M3
-// parts, x = q1 + 2^-5 q2 (x: q times a power of two that brings the head's
-// largest |q| to [128, 256)): q1 keeps 4 of a bf16's 8 bits and 32 (x - q1) is
-// exact in q2 but for what falls under E4M3's normal range, 2^-21 of the head's
-// largest.  The parts of head h are columns 2 h and 2 h + 1, so lane (gid, tig)
-// receives both sums of head tig with tokens gid and gid + 8.  With c_g those
-// sums over group g and qs_g the sum of q over it,
+// QK: S = K q, the f16 MMA's rows the block's 16 tokens.  A mask leaves two codes
+// in a register as f16 subnormals: nibbles at bits 0 and 16 stand for code *
+// 2^-24, nibbles at bits 4 and 20 for code * 2^-20 (the second kind's q carries a
+// factor 2^-4, exact), so five operations make the four operands of eight codes.
+// (An E4M3 MMA would take the nibbles of a word by two masks and a shift, codes
+// 0..15 being E4M3 values as they are; but mma.sync's E4M3 forms cost 125 ALU
+// operations a 32-token step here against 80 -- 416 instructions and 1078 cycles
+// against 352 and 1002, one warp alone, G = 4, D = 128.)  q,
+// times a power of two that brings the head's largest |q| to [2^13, 2^14), is
+// exact in f16 down to 2^-26 of that.  The columns, for G <= 4 and two groups: 2
+// h + g holds head h's q of group g and zeros for the other group's dims, so one
+// chain of MMAs leaves both groups' sums of head tig, tokens gid and gid + 8, in
+// lane (gid, tig); for G = 8 heads tig and tig + 4 are columns 2 tig and 2 tig +
+// 1, one chain per group.  With c_g those sums and qs_g the sum of q over group g,
 //   s = sum_g sc_g c_g + lo_g qs_g.
 //
-// PV: out^T = V^T W in f16 (m16n8k16), V's codes as f16 subnormals: a nibble at
-// bit 0 or 16 is code * 2^-24, one at bit 4 or 20 code * 2^-20 (undone once at
+// PV: out^T = V^T W, V's codes as f16 subnormals in the same way (undone once at
 // the end).  W holds p * sc_g, one f16 each (11 bits: an output's error is about
 // 2^-12 of its size, against the 2^-9 of its bf16 rounding); the offsets' share,
 // sum p * lo_g, is summed in fp32 beside it.  W's columns: for G <= 4, 2 h + g;
@@ -49,8 +52,9 @@ struct Warp4 {
   static constexpr int KT = int4_tile_bytes(D);
   // results per lane: its heads' dims 16 c + gid and 16 c + gid + 8
   static constexpr int V = D / 16 * 2 * H;
+  static constexpr int NC = G == 8 ? NG : 1;    // QK accumulators
 
-  uint32_t qw[H][D / 16];  // q's columns: head gid / 2 (+ 4), part gid % 2
+  uint32_t qw[D / 8];      // q's column gid
   float qf[H];             // factor of the MMA sums of the lane's heads
   float qs[H][NG];         // their q summed over each group, times the score scale
   float m[H], l[H];        // softmax reference (base 2), the lane's share of the sum
@@ -65,58 +69,57 @@ struct Warp4 {
   // q: the G heads of the group, D values each.
   __device__ __forceinline__ void begin(const __nv_bfloat16* q, float scale_log2, int lane) {
     const int gid = lane >> 2, tig = lane & 3;
+    // the column's head, and the one group of its dims that it holds (-1: all)
+    const int hn = G == 8 ? gid / 2 + 4 * (gid % 2) : gid / 2 % G;
+    const int only = G < 8 && NG == 2 ? gid % 2 : -1;
+    const __nv_bfloat16* qh = q + static_cast<size_t>(hn) * D + 16 * tig;
+    float f[D / 4];  // dims 16 tig .. 16 tig + 15 of every group
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+      const uint4 w =
+          __ldg(reinterpret_cast<const uint4*>(qh + kInt4Group * (u / 2) + 8 * (u % 2)));
+      const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
+      const float2 c = bf16x2_to_float2(w.z), d = bf16x2_to_float2(w.w);
+      f[8 * u] = a.x; f[8 * u + 1] = a.y; f[8 * u + 2] = b.x; f[8 * u + 3] = b.y;
+      f[8 * u + 4] = c.x; f[8 * u + 5] = c.y; f[8 * u + 6] = d.x; f[8 * u + 7] = d.y;
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 4; ++k) amax = fmaxf(amax, fabsf(f[k]));
+    amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
+    // biased exponent of amax (0 for 0 and subnormals); k = 13 - unbiased
+    const int ebits = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu);
+    const int kexp = min(127, max(-126, 140 - ebits));
+    const float up = __uint_as_float(static_cast<uint32_t>(kexp + 127) << 23);
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {  // nibbles 0 .. 7 of word w: f[8 w ..]
+      const float x = only < 0 || only == w / 2 ? up : 0.f, y = x * 0.0625f;
+      qw[4 * w] = f16x2_rn(f[8 * w] * x, f[8 * w + 4] * x);
+      qw[4 * w + 1] = f16x2_rn(f[8 * w + 1] * y, f[8 * w + 5] * y);
+      qw[4 * w + 2] = f16x2_rn(f[8 * w + 2] * x, f[8 * w + 6] * x);
+      qw[4 * w + 3] = f16x2_rn(f[8 * w + 3] * y, f[8 * w + 7] * y);
+    }
+    // the lane's scores are those of its heads: their factors come from the rows
+    // that hold them as columns
+    float sum[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      float x = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x += f[16 * g + k];
+      x += __shfl_xor_sync(kFullMask, x, 1);
+      x += __shfl_xor_sync(kFullMask, x, 2);
+      sum[g] = x * scale_log2;
+    }
+    const float factor = ldexpf(scale_log2, 24 - kexp);
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      const __nv_bfloat16* qh = q + static_cast<size_t>(head(gid / 2, h)) * D + 16 * tig;
-      float f[D / 4];  // dims 16 tig .. 16 tig + 15 of every group
-#pragma unroll
-      for (int u = 0; u < D / 32; ++u) {
-        const uint4 w =
-            __ldg(reinterpret_cast<const uint4*>(qh + kInt4Group * (u / 2) + 8 * (u % 2)));
-        const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
-        const float2 c = bf16x2_to_float2(w.z), d = bf16x2_to_float2(w.w);
-        f[8 * u] = a.x; f[8 * u + 1] = a.y; f[8 * u + 2] = b.x; f[8 * u + 3] = b.y;
-        f[8 * u + 4] = c.x; f[8 * u + 5] = c.y; f[8 * u + 6] = d.x; f[8 * u + 7] = d.y;
-      }
-      float amax = 0.f;
-#pragma unroll
-      for (int k = 0; k < D / 4; ++k) amax = fmaxf(amax, fabsf(f[k]));
-      amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
-      // biased exponent of amax (0 for 0 and subnormals); k = 7 - unbiased
-      const int ebits = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu);
-      const int kexp = min(127, max(-126, 134 - ebits));
-      const float up = __uint_as_float(static_cast<uint32_t>(kexp + 127) << 23);
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w)
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {  // the word's even, odd nibbles
-          uint32_t r = 0;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float x0 = f[8 * w + 4 * i + o] * up, x1 = f[8 * w + 4 * i + 2 + o] * up;
-            __nv_fp8x2_storage_t c =
-                __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-            if (gid & 1) {
-              const __half2_raw c1 = __nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3);
-              const float2 q1 = __half22float2(*reinterpret_cast<const __half2*>(&c1));
-              c = __nv_cvt_float2_to_fp8x2(
-                  make_float2((x0 - q1.x) * 32.f, (x1 - q1.y) * 32.f), __NV_SATFINITE, __NV_E4M3);
-            }
-            r |= static_cast<uint32_t>(c) << (16 * i);
-          }
-          qw[h][2 * w + o] = r;
-        }
-      // the lane's scores are those of head(tig): its factors come from row 2 tig
-      qf[h] = __shfl_sync(kFullMask, ldexpf(scale_log2, 9 - kexp), 8 * tig);
+      const int src = 8 * tig + 4 * h;  // column 2 tig + h
+      qf[h] = __shfl_sync(kFullMask, factor, src);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        float x = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x += f[16 * g + k];
-        x += __shfl_xor_sync(kFullMask, x, 1);
-        x += __shfl_xor_sync(kFullMask, x, 2);
-        qs[h][g] = __shfl_sync(kFullMask, x * scale_log2, 8 * tig);
+        qs[h][g] = __shfl_sync(kFullMask, sum[g], src);
         z[h][g] = 0.f;
       }
       m[h] = -INFINITY;
@@ -139,7 +142,7 @@ struct Warp4 {
   static __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1,
                                                    uint32_t a2, uint32_t a3, uint32_t b0,
                                                    uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -173,18 +176,19 @@ struct Warp4 {
         k0[0] = x.x; k0[1] = x.y;
         k1[0] = y.x; k1[1] = y.y;
       }
-      float c[H][NG][4];
+      float c[NC][4];
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {  // two words of codes to a group
-        const uint32_t a0 = k0[w] & 0x0F0F0F0Fu, a2 = (k0[w] >> 4) & 0x0F0F0F0Fu;
-        const uint32_t a1 = k1[w] & 0x0F0F0F0Fu, a3 = (k1[w] >> 4) & 0x0F0F0F0Fu;
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          if (w % 2 == 0)
-            mma_first(c[h][w / 2], a0, a1, a2, a3, qw[h][2 * w], qw[h][2 * w + 1]);
-          else
-            mma_e4m3(c[h][w / 2], a0, a1, a2, a3, qw[h][2 * w], qw[h][2 * w + 1]);
-        }
+        const int o = NC == 2 ? w / 2 : 0;
+        const uint32_t x0 = k0[w], x1 = k1[w], y0 = k0[w] >> 8, y1 = k1[w] >> 8;
+        if (w == 0 || (NC == 2 && w == 2))
+          mma_first(c[o], x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u,
+                    x1 & 0x00F000F0u, qw[4 * w], qw[4 * w + 1]);
+        else
+          mma_f16(c[o], x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u,
+                  x1 & 0x00F000F0u, qw[4 * w], qw[4 * w + 1]);
+        mma_f16(c[o], y0 & 0x000F000Fu, y1 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x00F000F0u,
+                qw[4 * w + 2], qw[4 * w + 3]);
       }
       uint32_t p0[NG], p1[NG];  // parameters of tokens gid, gid + 8
       load_params(kt, gid, p0);
@@ -194,9 +198,9 @@ struct Warp4 {
         float2 d, zz;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const float2 e = __ffma2_rn(make_float2(c[h][g][1], c[h][g][3]),
-                                      make_float2(0.03125f, 0.03125f),
-                                      make_float2(c[h][g][0], c[h][g][2]));
+          // column 2 tig + (G = 8: the head, else the group), both tokens
+          const int o = NC == 2 ? g : 0, col = G == 8 ? h : g;
+          const float2 e = make_float2(c[o][col], c[o][2 + col]);
           const float2 sc = make_float2(hi16(p0[g]), hi16(p1[g]));
           const float2 lo = make_float2(lo16(p0[g]), lo16(p1[g]));
           const float2 q2 = make_float2(qs[h][g], qs[h][g]);
@@ -253,7 +257,7 @@ struct Warp4 {
           if (!(16 * u + gid < nvalid)) w0[u][g] = 0u;
           if (!(16 * u + gid + 8 < nvalid)) w1[u][g] = 0u;
         }
-        top = max(top, max(w0[u][g], w1[u][g]));
+        top = __vimax3_u32(top, w0[u][g], w1[u][g]);
       }
     }
     float r = 1.f;

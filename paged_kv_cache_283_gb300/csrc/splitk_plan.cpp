@@ -28,9 +28,9 @@
 // measured best for them too (batch 64: 1024; 32 layers: 2048).
 //
 // The 4-bit cache and the bf16 cache with changed scores have costs of their
-// own, fitted to 26 and 33 batches of 1 to 156 sequences and 16 to 49,796 tokens
-// (the sizes' mean time over the best size's: 1.020 and 1.006; with the constants
-// above 1.029 and 1.033, and 54.2 instead of 48.7 us for 64 windows of 1024
+// own, fitted to 40 and 33 batches of 1 to 256 sequences and 16 to 49,796 tokens
+// (the sizes' mean time over the best size's: 1.023 and 1.006; with the constants
+// above 1.031 and 1.033, and 54.2 instead of 48.7 us for 64 windows of 1024
 // tokens, which 768 splits and 1280 does not).
 
 #include <stdint.h>

@@ -762,14 +762,21 @@ def plan_decode_step(context_lens, num_q_heads, num_kv_heads, head_dim, kv="bf16
     return StepPlan(partition_size, maxp, arr, chosen)
 
 
-# From this many (token, KV head) pairs on, a 4-bit step is cut evenly among the
-# warps.  Below it a warp's share (a dozen 64-token steps at the border) does not
-# outweigh its partial's way through the workspace: 64 contexts of 128 to 2048
-# tokens x 8 KV heads (0.55 M) take 24.9 us evenly cut and 22.8 in partitions, 8 of
-# 8K to 128K (1.55 M) 50.7 and 61.0, 33 of up to 5880 x 16 KV heads of 64 dims
-# (1.65 M) 32.8 and 48.4.  Groups of 8 have no such kernel: their state leaves it
-# two CTAs an SM, and it was the same or slower (4.2 M pairs: 147.4 and 148.8 us).
+# A 4-bit step is cut evenly among the warps from this many (token, KV head) pairs
+# on, if a context is this long.  With fewer pairs a warp's share (a dozen 64-token
+# steps at the border) does not outweigh its partial's way through the workspace;
+# without a long context partitions, some of them whole contexts, balance as well
+# and one CTA's four warps share a unit's beginning and end.  Evenly cut and in the
+# best partitions, us (contexts x their tokens; 8 KV heads, D = 128, G = 4):
+#   2 x 131059         54.8  63.7      64 x 128 to 2016        22.0  20.1
+#   4 x 58643 and less 46.8  49.4      32 x 15340 and less     37.3  33.6
+#   8 x 8K to 50K      47.6  53.7      16 x 29521 and less     60.4  58.4
+#   4 x 65536          56.8  59.7      64 x 15763 and less    113.5 113.4
+#   8 x 131072        193.0 196.6     256 x 4068 and less      98.3  92.9
+# (32 x 15340: G = 2).  Groups of 8 have no such kernel: their
+# state leaves it two CTAs an SM, and it was not faster.
 EVEN_MIN_PAIRS = 1000000
+EVEN_MIN_CONTEXT = 32768
 
 
 def int4_split_evenly(context_lens, num_q_heads, num_kv_heads):
@@ -778,7 +785,8 @@ def int4_split_evenly(context_lens, num_q_heads, num_kv_heads):
     choice only: both give the same attention whatever the lengths."""
     import numpy as np
     ctx = np.asarray(context_lens, dtype=np.int64)
-    return num_q_heads // num_kv_heads in (2, 4) and ctx.shape[0] <= PA_EVEN_MAX_SEQS and \
+    return num_q_heads // num_kv_heads in (2, 4) and \
+        0 < ctx.shape[0] <= PA_EVEN_MAX_SEQS and int(ctx.max()) >= EVEN_MIN_CONTEXT and \
         int(ctx.sum()) * num_kv_heads >= EVEN_MIN_PAIRS
 
 
