@@ -568,8 +568,9 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
   if (!p.err) return cuda_fail(cudaGetLastError());
   const int group = num_q_heads / num_kv_heads;
   const bool ruled = rule != nullptr;
-  if (ruled) p.rule = *rule;
-  const int window = ruled ? rule->window : 0;
+  if (ruled)
+    p.rule = within_capacity(*rule, static_cast<int64_t>(max_blocks_per_seq) * block_size);
+  const int window = p.rule.window;
   return launch_or_keep(
       [=](cudaStream_t st) {
         if (even) return launch_decode_int4_even(p, head_dim, group, st);

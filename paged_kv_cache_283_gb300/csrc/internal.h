@@ -29,6 +29,13 @@ struct ScoreRule {
   int window;
 };
 
+// The rule for contexts of up to `capacity` tokens: a window of that many hides
+// nothing, and without it no position of the kernels' arithmetic passes 32 bits.
+inline ScoreRule within_capacity(ScoreRule r, int64_t capacity) {
+  if (r.window >= capacity) r.window = 0;
+  return r;
+}
+
 // Whether a rule's values make sense beside the score scale (api.cu).
 bool score_rule_ok(const ScoreRule& r, float scale);
 

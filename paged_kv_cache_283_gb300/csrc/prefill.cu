@@ -161,7 +161,7 @@ pa_status prefill_impl(void* out, const void* q, const void* k_cache, const void
   p.scale_log2 = scale * 1.4426950408889634f;
   const bool ruled = rule != nullptr;
   if (ruled) {
-    p.rule = *rule;
+    p.rule = within_capacity(*rule, static_cast<int64_t>(max_blocks_per_seq) * block_size);
     p.prefix_lens = prefix_lens;
     p.cap_in = rule->softcap > 0.f ? scale / rule->softcap : 0.f;
   }

@@ -206,6 +206,24 @@ def test_biased_prefill_prefix(rule):
     assert_close(got, ref, f"prefix {rule}")
 
 
+@pytest.mark.parametrize("window", [1200, 2 ** 31 - 1])
+def test_biased_windows_past_every_context(window):
+    # nothing is hidden: also where a prefix reaches far past the first queries
+    slopes = _slopes(16)
+    case = _case(14, [(0, 1100), (30, 200)], 16, 8)
+    got, ref = _prefill(case, 0.088, [1100, 230], slopes=slopes, window=window)
+    assert_close(got, ref, f"prefill window {window}")
+    ctx, n, tables, kc, vc, q = case
+    last = q[[1099, 1299]]
+    out = torch.empty(2, 16, 128, dtype=torch.bfloat16, device="cuda")
+    step = pa.DecodeStep(None, None, dev_bf16(kc), dev_bf16(vc), None, dev_bf16(last),
+                         _dev(tables, np.int32), _dev(ctx, np.int32), out, 0.088,
+                         partition_size=64, alibi_slopes=_dev(slopes, np.float32), window=window)
+    step()
+    full = OB.batch(last, kc, vc, tables, ctx, np.array([1, 1]), 0.088, slopes=slopes)
+    assert_close(bf16_to_f64(out), full, f"step window {window}")
+
+
 def test_biased_prefill_large_scores():
     for cap, gain in ((5.0, 64.0), (1000.0, 64.0), (0.01, 1.0), (2.0, 4.0)):
         case = _case(9, [(40, 30), (0, 150)], 8, 2, gain=gain)
