@@ -343,7 +343,8 @@ pa_status pa_decode_splitk_int4(float* ws_out, float* ws_m, float* ws_l, int max
  *     PA_DEVERR_POSITION.
  *   cos_sin       : [max_position, rotary_dim] fp32, cosines then sines.
  *   slot_mapping  : as pa_reshape_and_cache; a negative slot keeps k and v out
- *     of the cache, q is rotated all the same.
+ *     of the cache, q is rotated all the same.  Two tokens of a call must not
+ *     have one slot (its bytes would mix both).
  * head_dim 64 or 128, rotary_dim a multiple of 16 up to head_dim, block_size 16
  * for the quantised caches (else PA_ERR_UNSUPPORTED_SHAPE).
  */

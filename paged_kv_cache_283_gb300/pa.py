@@ -1214,9 +1214,10 @@ class DecodeStep:
     After a launch that raised PA_DEVERR_ORDER or PA_DEVERR_WAIT_TIMEOUT,
     call recover() before the next one.  softcap, alibi_slopes and window change
     the scores (pa_decode_step_biased); with a window the plan, the workspace
-    and the order cover the window only.  Over a 4-bit cache the choice may be
-    to cut the work evenly among the GPU's warps (int4_split_evenly).  key, value and slot_mapping None:
-    attention only.
+    and the order cover the window only.  Over a 4-bit cache, where neither a
+    workspace nor counters or an order are passed, the choice may be to cut the
+    work evenly among the GPU's warps (int4_split_evenly).  key, value and
+    slot_mapping None: attention only.
 
     Every argument is checked and marshalled once, here; each call then makes
     two or three bare C calls, which keeps the host ahead of the GPU when a
@@ -1243,9 +1244,11 @@ class DecodeStep:
             self.split = bool(split)
             B, hq, d = q.shape
             hkv = k_cache.shape[1]
+            made = workspace is None or counters is None  # on the stream that is current now
             if self.split and four and order is None and workspace is None and (
                     partition_size == PA_SPLIT_EVEN or (
-                        partition_size is None and host_context_lens is not None and
+                        partition_size is None and counters is None and
+                        host_context_lens is not None and
                         int4_split_evenly(host_context_lens, hq, hkv))):
                 partition_size = PA_SPLIT_EVEN
                 workspace = even_workspace(hq, hkv, d, q.device)
@@ -1286,6 +1289,9 @@ class DecodeStep:
                     workspace = splitk_workspace(B, hq, d, mc, partition_size, q.device)
                 if counters is None:
                     counters = step_counters(B, hkv, q.device)
+                if made and not torch.cuda.is_current_stream_capturing():
+                    # the first call may go to another stream
+                    torch.cuda.current_stream(q.device).synchronize()
             self.workspace, self.counters = workspace, counters
             self._fn, self._args = _step_args(
                 out, q, k_cache, v_cache, block_tables, context_lens, scale, key, value,

@@ -267,6 +267,38 @@ def test_int4_handle_picks_the_even_split_for_long_batches():
     assert pa.pa_get_device_error() == 0 and not step.counters.any()
 
 
+def test_int4_handle_with_its_own_counters_and_another_stream():
+    rng, ctx, tables, pools, q = _case(16, [50000, 60000, 70000], 32, 8, 64)
+    assert pa.int4_split_evenly(ctx, 32, 8)
+    dk, dv = (torch.from_numpy(p).cuda() for p in pools)
+    dq, t, c = dev_bf16(q), _dev(tables, np.int32), _dev(ctx, np.int32)
+    ref, V = _ref((rng, ctx, tables, pools, q), 0.125)
+    # partitions' counters are given: the lengths do not change that choice
+    out = torch.full((3, 32, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    step = pa.DecodeStep(None, None, dk, dv, None, dq, t, c, out, 0.125, partition_size=None,
+                         host_context_lens=ctx, counters=pa.step_counters(3, 8))
+    assert step.partition_size != pa.PA_SPLIT_EVEN
+    step()
+    _gate(out, ref, V, "counters given")
+    # a handle made behind other work on one stream and run on another: its
+    # counters are zeros before that
+    other = torch.cuda.Stream()
+    for ps in (None, 4096):
+        out.fill_(float("nan"))
+        dirty = [torch.full((n,), -1, dtype=torch.int32, device="cuda") for n in (24, 512)]
+        torch.cuda.synchronize()
+        del dirty                               # (the handle's counters may take its place)
+        work = torch.randn(4096, 4096, device="cuda")
+        for _ in range(20):
+            work = work @ work * 1e-2
+        step = pa.DecodeStep(None, None, dk, dv, None, dq, t, c, out, 0.125, partition_size=ps,
+                             host_context_lens=ctx, stream=other)
+        step()
+        other.synchronize()
+        _gate(out, ref, V, f"another stream {ps}")
+        torch.cuda.synchronize()
+
+
 def test_int4_blocks_copy_as_bf16():
     # pa_copy_blocks on a 4-bit pool seen as [NB, 1, 1, bytes / 2] bf16
     rng = np.random.default_rng(10)
