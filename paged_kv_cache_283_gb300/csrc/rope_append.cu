@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlock = 16;  // tokens of a block of the 1-byte and 4-bit caches
-constexpr int64_t kOneRowThreads = 152 * 2048;  // the GPU's resident threads
+constexpr int64_t kOneRowThreads = 152 * 512;  // two CTAs an SM
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
   const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
@@ -344,9 +344,16 @@ template <int D, int Q>
 cudaError_t launch_t(const RopeAppendParams& p, cudaStream_t stream) {
   constexpr int L = D / 16, U = 3;
   const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-  // While one row per thread fills less than the GPU's threads, the call is a
-  // chain of round trips and a row to a thread is the shortest; past that a
-  // thread takes up to U rows, which share its cosines and sines.
+  // While one row per thread makes few threads, the call is a chain of round
+  // trips and a row to a thread is the shortest; past that a thread takes up to U
+  // rows, which share its cosines and sines and overlap their loads.  In us, one
+  // row and U (D = 128; bf16 with 32 + 16 rows a token, 4-bit with 16 + 8):
+  //   bf16   64 tokens,   25K threads   1.8   2.1      128,  49K  2.1  2.1
+  //         256,          98K           2.7   2.3     8192, 3.1M 44.8 34.2
+  //   4-bit 400,          77K           3.6   3.8      512,  98K  4.1  3.9
+  //        1024,         197K           6.4   5.2     8192, 1.6M 35.3 29.7
+  // U: 8192 bf16 tokens take 36.6 us with 2 rows, 34.6 with 3, 34.7 with 4, 37.8
+  // with 6.
   const bool one = static_cast<int64_t>(p.num_tokens) * rows * L <= kOneRowThreads;
   RopeAppendParams r = p;
   r.row_slots = one ? rows : (rows + U - 1) / U;
