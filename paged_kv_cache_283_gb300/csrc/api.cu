@@ -567,9 +567,9 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
   p.err = device_error_word();
   if (!p.err) return cuda_fail(cudaGetLastError());
   const int group = num_q_heads / num_kv_heads;
-  const bool ruled = rule != nullptr;
-  if (ruled)
+  if (rule)
     p.rule = within_capacity(*rule, static_cast<int64_t>(max_blocks_per_seq) * block_size);
+  const bool ruled = p.rule.any();
   const int window = p.rule.window;
   return launch_or_keep(
       [=](cudaStream_t st) {

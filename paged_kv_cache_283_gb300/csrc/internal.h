@@ -27,6 +27,7 @@ struct ScoreRule {
   const float* slopes;  // [Hq] fp32
   float softcap;
   int window;
+  bool any() const { return slopes != nullptr || softcap > 0.f || window > 0; }
 };
 
 // The rule for contexts of up to `capacity` tokens: a window of that many hides

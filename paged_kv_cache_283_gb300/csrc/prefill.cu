@@ -159,12 +159,12 @@ pa_status prefill_impl(void* out, const void* q, const void* k_cache, const void
   p.num_blocks = num_blocks;
   p.total_q = total_query_tokens;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const bool ruled = rule != nullptr;
-  if (ruled) {
+  if (rule) {
     p.rule = within_capacity(*rule, static_cast<int64_t>(max_blocks_per_seq) * block_size);
     p.prefix_lens = prefix_lens;
     p.cap_in = rule->softcap > 0.f ? scale / rule->softcap : 0.f;
   }
+  const bool ruled = p.rule.any() || p.prefix_lens != nullptr;
   return launch_or_keep(
       [=](cudaStream_t s) {
         if (ruled) return launch_prefill_biased(tq, tk, tv, p, group, max_query_len, num_seqs, s);

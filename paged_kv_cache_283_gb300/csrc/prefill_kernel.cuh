@@ -275,11 +275,19 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// tanh(z) / z as polynomials in z^2: |z| <= 0.2 and |z| <= 0.6
+enum Reach { kNear, kMid, kFar };
+__device__ constexpr float kTanhNear[3] = {0.99999989f, -0.33328591f, 0.13015408f};
+__device__ constexpr float kTanhMid[5] = {0.99999993f, -0.3333231f, 0.13310174f, -0.05210148f,
+                                          0.01547543f};
+
 // How a softmax row changes its raw scores s = q . k into base-2 units.
 struct RuleRow {
   float unit;    // scale log2(e)
-  float c1, c2;  // the cap's series: unit s (1 + c1 / unit s^2 + c2 / unit s^4)
-  float k2;      // 2 log2(e) scale / cap
+  float k2;      // (scale / cap)^2
+  float n0, n1, c2;  // near: s (n0 + n1 s^2 + c2 s^4)
+  float c4;      // mid: the last coefficient
+  float twice;   // 2 log2(e) scale / cap
   float cap2;    // cap log2(e)
   float slope2;  // slope log2(e)
 };
@@ -300,20 +308,25 @@ __device__ __forceinline__ float max_abs(const uint32_t (&v)[HK]) {
 // largest x, or the weights 2^x in place of the scores and their sum.  `at` is
 // the distance of the first key from the query (negative before it).
 //
-// The cap.  Caps lie well above the scores they bound, so while every
-// |s scale / cap| of the warp is at most 0.1 (`small`), tanh's series to the
-// fifth power serves (the next term, 17/315 z^6, is below 6e-8 of the result):
-// x = s (unit + s^2 (c1 + c2 s^2)) - m, three packed multiply-adds a pair beside
-// the one that x takes anyway.  Elsewhere 1 - 2 / (1 + e^2z), two more
-// special-function operations a score, to 2e-7 of the cap.  A masked score,
-// -inf, stays one: c2 > 0.
+// The cap.  Caps lie above the scores they bound: with z = s scale / cap, tanh(z)
+// is z times a polynomial in z^2, the minimax one (relative error, Remez), of
+// degree 2 while every |z| of the warp is at most 0.2 (kNear: 1.1e-7 of the
+// result, x = s (c0 + c1 s^2 + c2 s^4) - m, three packed operations a pair beside
+// the one that x takes anyway) and of degree 4 up to 0.6 (kMid: 8e-8; five).
+// Elsewhere (kFar), and for maxima, 1 - 2 / (1 + e^2z), two more special-function
+// operations a score, to 2e-7 of the cap.  A masked score, -inf, stays one: the
+// last coefficients are positive.  16 x 512 new tokens after up to 3450 (32 query
+// / 8 KV heads; uncapped 328 us): every score near
+// 375, mid 403, far 537.  Packed multiply-adds have the rate of two single ones,
+// so mid without near makes the small scores 395; near and far alone 366 and 522,
+// which leaves scores of a fifth of the cap at 522.
 //
 // The bias, slope (j - p) where no key after the query is visible, runs along
 // the keys in four chains of additions (a packed multiply-add would want its
 // 32 constant pairs in registers); `far` takes |p - j| key by key.
 template <int HK, int RULE, bool MAX>
 __device__ __forceinline__ float rule_pass(uint32_t (&sv)[HK], const RuleRow& r, float m,
-                                           float at, bool small, bool far) {
+                                           float at, int reach, bool far) {
   float2 acc[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q)
@@ -334,24 +347,35 @@ __device__ __forceinline__ float rule_pass(uint32_t (&sv)[HK], const RuleRow& r,
       }
     }
   };
-  const float2 unit2 = make_float2(r.unit, r.unit);
-  const float2 c12 = make_float2(r.c1, r.c1), c22 = make_float2(r.c2, r.c2);
+  auto both = [](float c) { return make_float2(c, c); };
+  const float2 near0 = both(r.n0), near1 = both(r.n1), near2 = both(r.c2);
   auto curves = [&](auto offset) {
+    auto away = [&](float s, float o) {
+      const float e = ex2(s * r.twice);
+      const float x = fmaf(fmaf(-2.f, __fdividef(1.f, 1.f + e), 1.f), r.cap2, o);
+      return s == -INFINITY ? s : x;
+    };
     if constexpr ((RULE & kCap) == 0) {
-      pass([&](float2 s, float2 o) { return __ffma2_rn(s, unit2, o); }, offset);
-    } else if (small) {
+      const float2 unit = both(r.unit);
+      pass([&](float2 s, float2 o) { return __ffma2_rn(s, unit, o); }, offset);
+    } else if (MAX || reach == kFar) {
+      pass([&](float2 s, float2 o) { return make_float2(away(s.x, o.x), away(s.y, o.y)); },
+           offset);
+    } else if (reach == kNear) {
       pass([&](float2 s, float2 o) {
         const float2 v = __fmul2_rn(s, s);
-        return __ffma2_rn(s, __ffma2_rn(v, __ffma2_rn(v, c22, c12), unit2), o);
+        return __ffma2_rn(s, __ffma2_rn(v, __ffma2_rn(v, near2, near1), near0), o);
       }, offset);
     } else {
-      auto one = [&](float s, float o) {
-        const float e = ex2(s * r.k2);
-        const float x = fmaf(fmaf(-2.f, __fdividef(1.f, 1.f + e), 1.f), r.cap2, o);
-        return s == -INFINITY ? s : x;
-      };
-      pass([&](float2 s, float2 o) { return make_float2(one(s.x, o.x), one(s.y, o.y)); },
-           offset);
+      const float2 c0 = both(r.unit * kTanhMid[0]), c1 = both(r.unit * r.k2 * kTanhMid[1]),
+                   c2 = both(r.unit * r.k2 * r.k2 * kTanhMid[2]),
+                   c3 = both(r.unit * r.k2 * r.k2 * r.k2 * kTanhMid[3]), c4 = both(r.c4);
+      pass([&](float2 s, float2 o) {
+        const float2 v = __fmul2_rn(s, s);
+        float2 y = __ffma2_rn(v, __ffma2_rn(v, c4, c3), c2);
+        y = __ffma2_rn(v, __ffma2_rn(v, y, c1), c0);
+        return __ffma2_rn(s, y, o);
+      }, offset);
     }
   };
   if constexpr ((RULE & kBias) == 0) {
@@ -740,9 +764,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if constexpr (RULE != 0) {
       const float k = p.cap_in;  // scale / cap
       rr.unit = sl2;
-      rr.c1 = -sl2 * k * k / 3.f;
-      rr.c2 = fmaxf(sl2 * k * k * (k * k) * (2.f / 15.f), 1.2e-38f);
-      rr.k2 = 2.8853900817779268f * k;
+      rr.k2 = k * k;
+      rr.n0 = sl2 * kTanhNear[0];
+      rr.n1 = sl2 * rr.k2 * kTanhNear[1];
+      rr.c2 = fmaxf(sl2 * rr.k2 * rr.k2 * kTanhNear[2], 1.2e-38f);
+      rr.c4 = sl2 * rr.k2 * rr.k2 * rr.k2 * rr.k2 * kTanhMid[4];
+      rr.twice = 2.8853900817779268f * k;
       rr.cap2 = p.rule.softcap * 1.4426950408889634f;
       if constexpr ((RULE & kBias) != 0)
         rr.slope2 = __ldg(p.rule.slopes + kvh * G + r % G) * 1.4426950408889634f;
@@ -801,6 +828,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // true maxima taken and the reference moved, before any weight.
         const uint32_t tS = tmem + lane_base + sb * kKeys;
         const float at = static_cast<float>(kc * kKeys - pos);  // the first key's distance
+        // some row of the warp sees a key after its own
+        const bool far = far_bias && __any_sync(kFullMask, at + (HK - 1) > 0.f);
         float alpha = 1.f;
         if (lok) {
           tc_fence_after();
@@ -810,14 +839,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             tmem_ld32(tS + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * h));
           tmem_wait_ld();
           const float mabs = max_abs<HK>(sv);
-          bool small = true;
+          int reach = kNear;
           float top = mabs * sl2;
           if constexpr ((RULE & kCap) != 0) {
-            small = __all_sync(kFullMask, mabs * p.cap_in <= 0.1f) && rr.c2 < 1e37f;
+            // (c2's floor stays below 1e-9 of its sum while |s| < 1e7, and no
+            // coefficient leaves the normal numbers)
+            if (!__all_sync(kFullMask, mabs * p.cap_in <= 0.2f && mabs < 1e7f) || rr.c2 >= 1e37f)
+              reach = __all_sync(kFullMask, mabs * p.cap_in <= 0.6f) && rr.c4 >= 1.2e-38f &&
+                              rr.c4 < 1e37f
+                          ? kMid : kFar;
             top = fminf(top, rr.cap2);
           }
           if constexpr ((RULE & kBias) != 0)
-            top += far_bias ? fmaxf(0.f, -rr.slope2 * fmaxf(fabsf(at), fabsf(at + (HK - 1))))
+            top += far ? fmaxf(0.f, -rr.slope2 * fmaxf(fabsf(at), fabsf(at + (HK - 1))))
                             : fmaxf(rr.slope2 * at, rr.slope2 * fminf(at + (HK - 1), 0.f));
           auto half = [&](int h, uint32_t (&v)[32]) {
             tmem_ld32(tS + 32 * h, v);
@@ -834,8 +868,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int h = 0; h < HK / 32; ++h) {
               uint32_t v[32];
               half(h, v);
-              mx = fmaxf(mx, rule_pass<32, RULE, true>(v, rr, 0.f, at + 32.f * h, small,
-                                                       far_bias));
+              mx = fmaxf(mx, rule_pass<32, RULE, true>(v, rr, 0.f, at + 32.f * h, reach,
+                                                       far));
             }
             if (mx != -INFINITY) {
               if (m_used == -INFINITY) {
@@ -871,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           for (int h = 0; h < HK / 32; ++h) {
             uint32_t v[32];
             half(h, v);
-            psum += rule_pass<32, RULE, false>(v, rr, m, at + 32.f * h, small, far_bias);
+            psum += rule_pass<32, RULE, false>(v, rr, m, at + 32.f * h, reach, far);
             // P over the half's own columns: hi parts, then lo (as below)
             store_p(tS + 32 * h, tS + 32 * h + 16, v);
           }

@@ -225,7 +225,9 @@ def test_biased_windows_past_every_context(window):
 
 
 def test_biased_prefill_large_scores():
-    for cap, gain in ((5.0, 64.0), (1000.0, 64.0), (0.01, 1.0), (2.0, 4.0)):
+    # (and scores of up to a sixth and half of their cap)
+    for cap, gain in ((5.0, 64.0), (1000.0, 64.0), (0.01, 1.0), (2.0, 4.0), (30.0, 1.0),
+                      (10.0, 1.0)):
         case = _case(9, [(40, 30), (0, 150)], 8, 2, gain=gain)
         got, ref = _prefill(case, 0.1, softcap=cap)
         assert_close(got, ref, f"cap {cap} gain {gain}")
