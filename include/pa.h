@@ -525,27 +525,7 @@ pa_status pa_decode_step_fp8(void* out, const void* q, const void* key, const vo
                              float* ws_m, float* ws_l, unsigned* counters, int max_partitions,
                              const int32_t* order, int flags, pa_stream_t stream);
 
-/*
- * partition_size PA_SPLIT_EVEN (pa_decode_step_int4): one launch in which every
- * warp of the GPU takes the same share of the whole batch's context, whatever the
- * lengths; no partition size, no work order.  Faster than partitions for a few
- * long contexts (from about a million (token, KV head) pairs on, 32K tokens in one).
- *   ws_out  : pa_even_workspace_bytes(...) bytes, its size the same for every
- *             batch; ws_m, ws_l, max_partitions and order are ignored.
- *   counters: device uint32 [pa_even_counters(num_seqs, num_kv_heads)], all zero
- *             before the first call; every call leaves them zero.
- * num_q_heads / num_kv_heads 2 or 4, num_seqs <= PA_EVEN_MAX_SEQS and num_seqs *
- * num_kv_heads * max_blocks_per_seq < 2^31 (else PA_ERR_UNSUPPORTED_SHAPE).
- * Concurrent calls must not share counters or workspace.  Both functions ask for
- * the current device; 0 on invalid arguments or another group.
- */
-#define PA_SPLIT_EVEN (-1)
-#define PA_EVEN_MAX_SEQS 4096
-size_t pa_even_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim);
-size_t pa_even_counters(int num_seqs, int num_kv_heads);
-
-/* The fused decode step over a 4-bit cache: pa_decode_step's arguments, or
- * PA_SPLIT_EVEN. */
+/* The fused decode step over a 4-bit cache: pa_decode_step's arguments. */
 pa_status pa_decode_step_int4(void* out, const void* q, const void* key, const void* value,
                               const int64_t* slot_mapping, uint8_t* k_cache, uint8_t* v_cache,
                               const int32_t* block_tables, int max_blocks_per_seq,

@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpa.so")
 
-SOURCES = ["api.cu", "decode.cu", "decode_int4.cu", "decode_biased.cu", "decode_int4_even.cu",
+SOURCES = ["api.cu", "decode.cu", "decode_int4.cu", "decode_biased.cu",
            "splitk_reduce.cu", "reshape_and_cache.cu", "rope_append.cu", "copy_blocks.cu", "noalloc.cu",
            "prefill.cu", "prefill_biased.cu", "allocator.cpp", "sha256.cpp", "scheduler.cpp", "splitk_plan.cpp"]
 HEADERS = [os.path.join(ROOT, "include", "pa.h"), os.path.join(CSRC, "internal.h"),

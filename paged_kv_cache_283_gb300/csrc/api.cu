@@ -500,9 +500,8 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
                                   block_size, num_blocks, scale);
   if (s != PA_OK) return s;
   const bool write = key != nullptr || value != nullptr || slot_mapping != nullptr;
-  const bool even = partition_size == PA_SPLIT_EVEN && kv == 3;
-  const bool split = partition_size != 0 && !even;
-  if ((partition_size < 0 && !even) || (split && (partition_size % block_size != 0 || max_partitions <= 0 ||
+  const bool split = partition_size != 0;
+  if (partition_size < 0 || (split && (partition_size % block_size != 0 || max_partitions <= 0 ||
                                        max_partitions > 65535)))
     return PA_ERR_INVALID_ARG;
   if (num_seqs == 0) return keep ? nothing_to_do(keep) : PA_OK;
@@ -512,10 +511,6 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
   if (split && (!ok_ptr(ws_out, 16) || !ok_ptr(ws_m, 4) || !ok_ptr(ws_l, 4) ||
                 !ok_ptr(counters, 4)))
     return PA_ERR_INVALID_ARG;
-  if (even && (!ok_ptr(ws_out, 16) || !ok_ptr(counters, 4))) return PA_ERR_INVALID_ARG;
-  if (even && (num_seqs > PA_EVEN_MAX_SEQS || num_q_heads / num_kv_heads > 4 ||
-               static_cast<int64_t>(num_seqs) * num_kv_heads * max_blocks_per_seq > 0x7fffffff))
-    return PA_ERR_UNSUPPORTED_SHAPE;
   if ((kv == 1 || kv == 2) && (!ok_ptr(k_scales, 16) || !ok_ptr(v_scales, 16))) return PA_ERR_INVALID_ARG;
   if ((flags & ~PA_STEP_EARLY_READ) != 0) return PA_ERR_INVALID_ARG;
   if (order != nullptr) {
@@ -549,10 +544,7 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
   // launch (pa_splitk_reduce's kernel) over all SMs instead.
   constexpr int kMergeInKernelParts = 16;
   const bool merge_apart = split && max_partitions > kMergeInKernelParts;
-  if (even) {
-    p.ws_o = ws_out;
-    p.counters = counters;
-  } else if (split) {
+  if (split) {
     p.ws_o = ws_out;
     p.ws_m = ws_m;
     p.ws_l = ws_l;
@@ -573,7 +565,6 @@ pa_status decode_step_impl(void* out, const void* q, const void* key, const void
   const int window = p.rule.window;
   return launch_or_keep(
       [=](cudaStream_t st) {
-        if (even) return launch_decode_int4_even(p, head_dim, group, st);
         cudaError_t e = kv == 3 ? launch_decode_int4(p, head_dim, group, split, st)
                         : ruled ? launch_decode_biased(p, head_dim, group, split, st)
                                 : launch_decode(p, head_dim, group, split, st);
@@ -745,21 +736,6 @@ pa_status pa_decode_step_int4(void* out, const void* q, const void* key, const v
                           block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
                           num_kv_heads, head_dim, block_size, num_blocks, scale, partition_size,
                           ws_out, ws_m, ws_l, counters, max_partitions, order, flags, 3, stream);
-}
-
-size_t pa_even_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim) {
-  if (pa_decode_supported(num_q_heads, num_kv_heads, head_dim, 16) != PA_OK) return 0;
-  return sizeof(float) * even_floats_int4(head_dim, num_q_heads / num_kv_heads);
-}
-
-size_t pa_even_counters(int num_seqs, int num_kv_heads) {
-  if (num_seqs < 0 || num_kv_heads <= 0) return 0;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  // two for each group of 16 warps, of which an SM holds less than one
-  return static_cast<size_t>(num_seqs) * num_kv_heads + 2 * static_cast<size_t>(sms) + 2;
 }
 
 pa_status pa_decode_int4(void* out, const void* q, const uint8_t* k_cache, const uint8_t* v_cache,

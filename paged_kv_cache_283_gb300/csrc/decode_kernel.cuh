@@ -87,25 +87,22 @@ struct Pipe<128, SPLIT, Q> {
   static constexpr int NW = SPLIT ? PA_SPLIT_WARPS_D128 : PA_WHOLE_WARPS_D128;
   static constexpr int S = Q == 1 ? 3 : Q >= 2 ? 2 : (SPLIT ? PA_SPLIT_STAGES_D128 : PA_WHOLE_STAGES_D128);
 };
-// Blocks per pipeline stage (and tile step): a 4-bit block is small, and two
-// at a time halve the per-step costs that do not grow with the tokens.
-template <int Q, int G>
-constexpr int kStepBlocks = Q == 3 ? 2 : 1;
 // Small bf16 CTAs share an SM three at a time (<= 168 registers); groups of 8
 // heads need more registers than that and get one CTA's worth.  The 1-byte
 // kernels need fewer registers and more warps to hide their latencies: four
 // 4-warp INT8 CTAs per SM (<= 128 registers, 3 stages of 4.2 KiB per warp at
 // head_dim 128), five FP8 ones (<= 102 registers, 2 stages: measured faster
 // than 4 x 3 on the batch-64 and 32-layer steps; INT8 spills at that budget);
-// 8-warp CTAs two per SM.
-template <int NW, int G, int Q>
+// 8-warp CTAs two per SM.  4-bit ones: see launch_decode_int4.
+template <int D, int NW, int G, int Q, int SB>
 constexpr int min_blocks() {
-  if constexpr (Q == 3) return NW <= 4 ? (G <= 4 ? 4 : 3) : 2;
+  if constexpr (Q == 3) return NW <= 4 ? (D == 128 && SB == 4 ? 3 : 4) : 2;
   else if constexpr (Q != 0) return NW <= 4 ? (G <= 4 ? (Q == 2 ? 5 : 4) : 3) : 2;
   else return (NW <= 4 && G <= 4) ? 3 : 1;  // bf16
 }
 
-template <int D, int G, int NW, int S, int Q>
+// SB: blocks per pipeline stage and step (a 4-bit cache's; else 1)
+template <int D, int G, int NW, int S, int Q, int SB>
 struct SmemLayout {
   using Geo = Geometry<D, G>;
   static constexpr bool I8 = Q != 0;
@@ -114,7 +111,7 @@ struct SmemLayout {
   static constexpr int KT =      // bytes of one K (or V) tile
       Q == 3 ? int4_tile_bytes(D) : I8 ? Geo::BS * D : Geo::TILE;
   static constexpr int STAGE =
-      Q == 3 ? kStepBlocks<Q, G> * 2 * KT : I8 ? 2 * KT + 2 * Geo::BS * 4 : 2 * KT;
+      Q == 3 ? SB * 2 * KT : I8 ? 2 * KT + 2 * Geo::BS * 4 : 2 * KT;
   static constexpr int TILES = S * STAGE;
   // bf16: softmax weights of one tile and the heads' rescale factors (the
   // 1-byte caches keep both in registers)
@@ -292,15 +289,14 @@ __device__ __forceinline__ void load_q_bf16(const DecodeParams& p, int b, int kv
 // tile step (tile_step_1b: QK and PV on the tensor cores, weights in
 // registers); INT8 quantises q and its QK is exact in integers (f16 MMAs on
 // the codes), FP8 takes QK in E4M3 on two exact parts of q.
-// Q 3: a 4-bit cache (Warp4::step, two blocks per step).  RULE: the scores are
+// Q 3: a 4-bit cache (Warp4::step, SB blocks per step).  RULE: the scores are
 // changed (ScoreRule) and a window may hide the context's start.
-template <int D, int G, int NW, int S, bool SPLIT, int Q, bool RULE = false>
-__global__ void __launch_bounds__(NW * 32, (min_blocks<NW, G, Q>()))
+template <int D, int G, int NW, int S, bool SPLIT, int Q, bool RULE = false, int SB = 1>
+__global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
     paged_decode_kernel(const DecodeParams p) {
   constexpr bool I8 = Q != 0;   // 1-byte codes + scales
   using Geo = Geometry<D, G>;
-  using Lay = SmemLayout<D, G, NW, S, Q>;
-  constexpr int SB = kStepBlocks<Q, G>;
+  using Lay = SmemLayout<D, G, NW, S, Q, SB>;
   constexpr int BS = Geo::BS, L = Geo::L, P = Geo::P, R = Geo::R;
   extern __shared__ __align__(128) unsigned char smem[];
 
@@ -1029,12 +1025,12 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done_mask) {
   return e;
 }
 
-template <int D, int G, bool SPLIT, int Q, bool RULE>
+template <int D, int G, bool SPLIT, int Q, bool RULE, int SB = 1>
 cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
-  constexpr int NW = Pipe<D, SPLIT, Q>::NW, S = Pipe<D, SPLIT, Q>::S;
-  using Lay = SmemLayout<D, G, NW, S, Q>;
+  constexpr int NW = Pipe<D, SPLIT, Q>::NW, S = D == 64 && SB == 4 ? 2 : Pipe<D, SPLIT, Q>::S;
+  using Lay = SmemLayout<D, G, NW, S, Q, SB>;
   static std::atomic<uint64_t> smem_set{0};
-  auto kernel = paged_decode_kernel<D, G, NW, S, SPLIT, Q, RULE>;
+  auto kernel = paged_decode_kernel<D, G, NW, S, SPLIT, Q, RULE, SB>;
   cudaError_t e = allow_smem(kernel, Lay::TOTAL, smem_set);
   if (e != cudaSuccess) return e;
   const dim3 grid =

@@ -177,12 +177,6 @@ cudaError_t launch_decode_int4(const DecodeParams& p, int head_dim, int group, b
                                cudaStream_t stream);
 cudaError_t launch_decode_biased(const DecodeParams& p, int head_dim, int group, bool split,
                                  cudaStream_t stream);
-// The 4-bit decode with the work cut evenly among the GPU's warps
-// (decode_int4_even.cu; groups of 2 and 4), and the floats of workspace that takes
-// on the current device.
-cudaError_t launch_decode_int4_even(const DecodeParams& p, int head_dim, int group,
-                                    cudaStream_t stream);
-size_t even_floats_int4(int head_dim, int group);
 cudaError_t launch_splitk_reduce(const ReduceParams& p, int head_dim, cudaStream_t stream);
 // prefill.cu: the split-K partials of a decode batch's queries over a shared
 // prefix, partitions [0, splits) of split_blocks blocks each (head_dim 128);

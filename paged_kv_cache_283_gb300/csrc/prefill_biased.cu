@@ -1,5 +1,9 @@
 // Paged prefill on the tensor cores with changed scores and masks: the variants
-// of the kernel (prefill_kernel.cuh) that pa_prefill_biased launches.
+// of the kernel (prefill_kernel.cuh) that pa_prefill_biased launches.  A variant
+// for each pair of cap and bias: the softmax threads' code is what bounds the
+// kernel, and with both as run-time flags of one variant the 16 x 512-token step
+// below took 974 us.  16 x 512 new tokens after up to 3450 (32 query / 8 KV heads,
+// scores below a fifth of the cap): no change 328 us, cap 375, bias 347, both 410.
 
 #include "prefill_kernel.cuh"
 

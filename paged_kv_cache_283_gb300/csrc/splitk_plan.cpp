@@ -13,7 +13,7 @@
 //   + kMergeUs         (a sequence with several partitions: publishing and
 //                       merging the partial results)
 // and a batch whose sequences need more than 16 partitions merges in a second
-// launch (kApartUs).  The constants were fitted to pa_decode_step timings of
+// launch (apart).  The constants were fitted to pa_decode_step timings of
 // the Llama-3.1-8B-shaped batch-64 and 32-layer batch-256 steps on a GB300
 // (bf16 cache), once for each dispatch order: grid order at partition 384 ..
 // 1536, longest first (pa_splitk_order) at 768 .. 2048 (refitted to 7 µs a
@@ -28,15 +28,16 @@
 // measured best for them too (batch 64: 1024; 32 layers: 2048).
 //
 // The 4-bit cache and the bf16 cache with changed scores have costs of their
-// own, fitted to 40 and 33 batches of 1 to 256 sequences and 16 to 49,796 tokens
-// (the sizes' mean time over the best size's: 1.023 and 1.006; with the constants
-// above 1.031 and 1.033, and 54.2 instead of 48.7 us for 64 windows of 1024
+// own, fitted to 65 and 33 batches of 1 to 500 sequences and 16 to 131,072 tokens
+// (the sizes' mean time over the best size's: 1.008 and 1.006; with the constants
+// above 1.059 and 1.033, and 54.2 instead of 48.7 us for 64 windows of 1024
 // tokens, which 768 splits and 1280 does not).
 
 #include <stdint.h>
 
 #include <algorithm>
 #include <functional>
+#include <iterator>
 #include <queue>
 #include <vector>
 
@@ -49,21 +50,28 @@ struct Costs {
   double token;  // per token and KV head, head_dim 128
   double cta;
   double merge;
+  double apart;  // the merge as its own launch
 };
 // kv_kind: 0 bf16, 1 INT8, 2 FP8, 4 4-bit, 5 bf16 with changed scores
 Costs costs_of(int kv_kind, bool ordered) {
-  if (kv_kind == 4) return {0.006, 2.0, 1.0};
-  if (kv_kind == 5) return {0.022, 4.0, 1.0};
-  if (ordered) return {kv_kind == 0 ? 0.022 : 0.0167, 7.0, 3.0};
-  return {kv_kind == 0 ? 0.025 : 0.019, 4.0, 2.0};
+  if (kv_kind == 4) return {0.0045, 2.0, 1.0, 5.0};
+  if (kv_kind == 5) return {0.022, 4.0, 1.0, 3.0};
+  if (ordered) return {kv_kind == 0 ? 0.022 : 0.0167, 7.0, 3.0, 3.0};
+  return {kv_kind == 0 ? 0.025 : 0.019, 4.0, 2.0, 3.0};
 }
-constexpr double kApartUs = 3.0;
+// Of a 4-bit token's cost where three CTAs share an SM, not four.
+constexpr double kFewerCtas4 = 0.65;
 constexpr int kMergeInKernelParts = 16;  // as pa_decode_step
 constexpr int kCandidates[] = {256, 384, 512, 640, 768, 1024, 1280, 1536, 1792, 2048, 4096};
+// A 4-bit cache's launches are short, and how full their last wave is shows.
+constexpr int kCandidates4[] = {256,  384,  512,  640,  768,  1024, 1280, 1536, 1792, 2048,
+                                2304, 2560, 2816, 3328, 3584, 4096, 5120, 8192};
 
 // CTAs per SM of the split-K kernels (their __launch_bounds__ minimum).
-int ctas_per_sm(int group, int kv_kind) {
+int ctas_per_sm(int group, int kv_kind, int head_dim, int part) {
   if (kv_kind == 0 || kv_kind == 5) return group <= 4 ? 3 : 1;
+  if (kv_kind == 4)  // launch_decode_int4's choice of the step
+    return head_dim == 64 || (group <= 4 && part < 4096) ? 4 : 3;
   return group <= 4 ? 4 : 3;
 }
 
@@ -102,7 +110,7 @@ double makespan(const int32_t* ctx, int num_seqs, int hkv, int part, int slots, 
     end = std::max(end, free_at.top());
     free_at.pop();
   }
-  return end + (apart ? kApartUs : 0.0);
+  return end + (apart ? k.apart : 0.0);
 }
 
 }  // namespace
@@ -116,20 +124,26 @@ extern "C" int pa_splitk_partition_size(const int32_t* context_lens, int num_seq
       num_sms <= 0)
     return 0;
   const int group = num_q_heads / num_kv_heads;
-  const int slots = num_sms * ctas_per_sm(group, kv_kind);
+  const auto slots = [&](int part) {
+    return num_sms * ctas_per_sm(group, kv_kind, head_dim, part);
+  };
   const Costs k = costs_of(kv_kind, ordered != 0);
   const double token_us = k.token * head_dim / 128.0;
   int max_ctx = 0;
   for (int b = 0; b < num_seqs; ++b) max_ctx = std::max(max_ctx, context_lens[b]);
-  if (!ordered && (kv_kind == 1 || kv_kind == 2) && static_cast<int64_t>(num_seqs) * num_kv_heads < slots &&
+  if (!ordered && (kv_kind == 1 || kv_kind == 2) && static_cast<int64_t>(num_seqs) * num_kv_heads < slots(512) &&
       (static_cast<int64_t>(max_ctx) + 511) / 512 <= 65535)
     return 512;
   int best = 0;
   double best_t = 0.0;
-  for (int part : kCandidates) {
+  const int* first = kv_kind == 4 ? std::begin(kCandidates4) : std::begin(kCandidates);
+  const int* last = kv_kind == 4 ? std::end(kCandidates4) : std::end(kCandidates);
+  for (const int* at = first; at != last; ++at) {
+    const int part = *at;
     if ((static_cast<int64_t>(max_ctx) + part - 1) / part > 65535) continue;  // grid z
-    const double t =
-        makespan(context_lens, num_seqs, num_kv_heads, part, slots, k, token_us, ordered != 0);
+    const double f = kv_kind == 4 && slots(part) < 4 * num_sms ? kFewerCtas4 : 1.0;
+    const double t = makespan(context_lens, num_seqs, num_kv_heads, part, slots(part), k,
+                              f * token_us, ordered != 0);
     // ties go to the larger partition: fewer CTAs, less workspace
     if (best == 0 || t <= best_t + 1e-9) {
       best = part;

@@ -29,8 +29,6 @@ PA_DEVERR_ORDER = 0x10
 PA_DEVERR_PREFIX = 0x20
 PA_DEVERR_POSITION = 0x40
 PA_STEP_EARLY_READ = 0x1
-PA_SPLIT_EVEN = -1
-PA_EVEN_MAX_SEQS = 4096
 
 # Every function include/pa.h declares: name -> (restype, argtypes).
 _vp, _i, _u, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_float, ctypes.c_size_t
@@ -83,8 +81,6 @@ SIGNATURES = {
     "pa_decode_step_biased": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i,
                                    _i, _i, _i, _f, _f, _vp, _i, _i, _vp, _vp, _vp, _vp, _i, _vp,
                                    _i, _vp]),
-    "pa_even_workspace_bytes": (_sz, [_i, _i, _i]),
-    "pa_even_counters": (_sz, [_i, _i]),
     "pa_rope_reshape_and_cache": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
                                        _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
     "pa_rope_reshape_and_cache_int8": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
@@ -684,27 +680,6 @@ def step_counters(num_seqs, num_kv_heads, device="cuda"):
     return torch.zeros(num_seqs * num_kv_heads, dtype=torch.int32, device=device)
 
 
-def even_workspace(num_q_heads, num_kv_heads, head_dim, device="cuda"):
-    """(workspace float tensor, None, None) for a 4-bit pa_decode_step with
-    partition_size PA_SPLIT_EVEN: its size does not depend on the batch."""
-    torch = _torch()
-    device = torch.device(device)
-    with torch.cuda.device(device):
-        n = lib().pa_even_workspace_bytes(num_q_heads, num_kv_heads, head_dim)
-    if n == 0:
-        raise ValueError("even_workspace: unsupported shape")
-    return torch.empty(n // 4, dtype=torch.float32, device=device), None, None
-
-
-def even_counters(num_seqs, num_kv_heads, device="cuda"):
-    """Zeroed counters for a pa_decode_step with partition_size PA_SPLIT_EVEN."""
-    torch = _torch()
-    device = torch.device(device)
-    with torch.cuda.device(device):
-        n = lib().pa_even_counters(num_seqs, num_kv_heads)
-    return torch.zeros(n, dtype=torch.int32, device=device)
-
-
 # Past this many partitions per sequence a split-K pa_decode_step merges in a
 # second launch, the items are nearly all full partitions and the
 # longest-first order has nothing to balance (long contexts measured slower
@@ -760,34 +735,6 @@ def plan_decode_step(context_lens, num_q_heads, num_kv_heads, head_dim, kv="bf16
     if longest and maxp <= ORDER_MAX_PARTITIONS and ctx.shape[0] * maxp <= 65535:
         arr = splitk_order(ctx, partition_size, maxp)
     return StepPlan(partition_size, maxp, arr, chosen)
-
-
-# A 4-bit step is cut evenly among the warps from this many (token, KV head) pairs
-# on, if a context is this long.  With fewer pairs a warp's share (a dozen 64-token
-# steps at the border) does not outweigh its partial's way through the workspace;
-# without a long context partitions, some of them whole contexts, balance as well
-# and one CTA's four warps share a unit's beginning and end.  Evenly cut and in the
-# best partitions, us (contexts x their tokens; 8 KV heads, D = 128, G = 4):
-#   2 x 131059         54.8  63.7      64 x 128 to 2016        22.0  20.1
-#   4 x 58643 and less 46.8  49.4      32 x 15340 and less     37.3  33.6
-#   8 x 8K to 50K      47.6  53.7      16 x 29521 and less     60.4  58.4
-#   4 x 65536          56.8  59.7      64 x 15763 and less    113.5 113.4
-#   8 x 131072        193.0 196.6     256 x 4068 and less      98.3  92.9
-# (32 x 15340: G = 2).  Groups of 8 have no such kernel: their
-# state leaves it two CTAs an SM, and it was not faster.
-EVEN_MIN_PAIRS = 1000000
-EVEN_MIN_CONTEXT = 32768
-
-
-def int4_split_evenly(context_lens, num_q_heads, num_kv_heads):
-    """Whether a 4-bit step over these host context lengths is better cut evenly
-    among the GPU's warps (PA_SPLIT_EVEN) than in partitions.  A performance
-    choice only: both give the same attention whatever the lengths."""
-    import numpy as np
-    ctx = np.asarray(context_lens, dtype=np.int64)
-    return num_q_heads // num_kv_heads in (2, 4) and \
-        0 < ctx.shape[0] <= PA_EVEN_MAX_SEQS and int(ctx.max()) >= EVEN_MIN_CONTEXT and \
-        int(ctx.sum()) * num_kv_heads >= EVEN_MIN_PAIRS
 
 
 def recover_step_counters(counters):
@@ -847,20 +794,7 @@ def _step_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, key,
         kvs = (_dev(key, torch.bfloat16, "key", 3), _dev(value, torch.bfloat16, "value", 3),
                _dev(slot_mapping, torch.int64, "slot_mapping", 1))
     ps = int(partition_size)
-    if ps == PA_SPLIT_EVEN:
-        if not four:
-            raise ValueError("pa_decode_step: PA_SPLIT_EVEN needs a 4-bit cache")
-        if workspace is None or counters is None:
-            raise ValueError("pa_decode_step: PA_SPLIT_EVEN needs a workspace and counters")
-        if order is not None:
-            raise ValueError("pa_decode_step: PA_SPLIT_EVEN takes no order")
-        need = lib().pa_even_workspace_bytes(hq, hkv, d)
-        if need == 0 or workspace[0].numel() * 4 < need or \
-                counters.numel() < lib().pa_even_counters(B, hkv):
-            raise ValueError("pa_decode_step: even_workspace / even_counters of this shape")
-        wsa = (_dev(workspace[0], torch.float32, "workspace", 1), none, none,
-               _dev(counters, torch.int32, "counters", 1), 0)
-    elif ps > 0:
+    if ps > 0:
         if workspace is None or counters is None:
             raise ValueError("pa_decode_step: split-K needs a workspace and counters")
         ws_o, ws_m, ws_l = workspace
@@ -900,8 +834,6 @@ def pa_decode_step(out, q, k_cache, v_cache, block_tables, context_lens, scale, 
     """Cache write of each sequence's new token (key / value [B, Hkv, D] at
     slot_mapping [B], which must be the slot of position context_lens[b] - 1)
     and the decode, in one launch.  partition_size 0: whole-sequence CTAs;
-    PA_SPLIT_EVEN (4-bit cache, groups of 2 and 4): cut evenly among the GPU's
-    warps (workspace = even_workspace(...), counters = even_counters(...));
     > 0: split-K merged in the same launch (workspace = splitk_workspace(...),
     counters = step_counters(...)).  The cache dtype picks bf16 / INT8 (int8)
     / FP8 (uint8 codes, with k_scales / v_scales) / 4-bit (uint8 [NB, Hkv, 9 *
@@ -1214,10 +1146,8 @@ class DecodeStep:
     After a launch that raised PA_DEVERR_ORDER or PA_DEVERR_WAIT_TIMEOUT,
     call recover() before the next one.  softcap, alibi_slopes and window change
     the scores (pa_decode_step_biased); with a window the plan, the workspace
-    and the order cover the window only.  Over a 4-bit cache, where neither a
-    workspace nor counters or an order are passed, the choice may be to cut the
-    work evenly among the GPU's warps (int4_split_evenly).  key, value and
-    slot_mapping None: attention only.
+    and the order cover the window only.  key, value and slot_mapping None:
+    attention only.
 
     Every argument is checked and marshalled once, here; each call then makes
     two or three bare C calls, which keeps the host ahead of the GPU when a
@@ -1245,16 +1175,7 @@ class DecodeStep:
             B, hq, d = q.shape
             hkv = k_cache.shape[1]
             made = workspace is None or counters is None  # on the stream that is current now
-            if self.split and four and order is None and workspace is None and (
-                    partition_size == PA_SPLIT_EVEN or (
-                        partition_size is None and counters is None and
-                        host_context_lens is not None and
-                        int4_split_evenly(host_context_lens, hq, hkv))):
-                partition_size = PA_SPLIT_EVEN
-                workspace = even_workspace(hq, hkv, d, q.device)
-                if counters is None:
-                    counters = even_counters(B, hkv, q.device)
-            elif self.split and host_context_lens is not None and partition_size is None:
+            if self.split and host_context_lens is not None and partition_size is None:
                 # chosen for these contexts (plan_decode_step): the partition
                 # size for a longest-first launch, and that order.  The
                 # workspace and the order cover the block tables' capacity

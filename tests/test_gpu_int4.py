@@ -88,17 +88,6 @@ def _all_ways(case, scale, parts=(512,), what=""):
                               counters=counters, early_read=early)
             _gate(out, ref, V, f"{what} step {part}")
         assert not counters.any()
-    even = hq // dk.shape[1] <= 4
-    if even:
-        ws, counters = pa.even_workspace(hq, dk.shape[1], d), pa.even_counters(B, dk.shape[1])
-        ws[0].fill_(float("nan"))
-    for early in (False, True) if even else ():
-        out.fill_(float("nan"))
-        torch.cuda.synchronize()
-        pa.pa_decode_step(out, dq, dk, dv, t, c, scale, partition_size=pa.PA_SPLIT_EVEN,
-                          workspace=ws, counters=counters, early_read=early)
-        _gate(out, ref, V, f"{what} even")
-        assert not counters.any()
     assert pa.pa_get_device_error() == 0
 
 
@@ -128,13 +117,12 @@ def test_int4_decode(hq, hkv, d):
     _all_ways(case, d ** -0.5, (16, 48, 256, 512), f"hq={hq} hkv={hkv} d={d}")
 
 
-@pytest.mark.parametrize("ctx,hq,hkv", [
-    ([5000], 4, 1), ([40000], 8, 2), ([20000, 7, 0, 30000], 4, 1), ([2047] * 40, 8, 2),
-    (list(range(0, 1300, 13)), 4, 2), ([33] * 700, 4, 1)])
-def test_int4_even_split_shares(ctx, hq, hkv):
-    # units over many warps and groups of warps, warps over many units
-    case = _case(len(ctx), ctx, hq, hkv, 64 if hq == 4 else 128)
-    _all_ways(case, 0.088, (), f"{len(ctx)} sequences")
+@pytest.mark.parametrize("ctx,hq,hkv,d", [
+    ([9000, 4096, 4097, 63, 0, 1], 8, 2, 128), ([5000, 8191, 7], 4, 2, 128),
+    ([20000, 64, 65], 8, 1, 128), ([33] * 300, 4, 1, 64), ([9000, 4160, 0], 4, 2, 64)])
+def test_int4_decode_long_partitions(ctx, hq, hkv, d):
+    # (partitions of 4096 tokens on take 64 at a time)
+    _all_ways(_case(len(ctx), ctx, hq, hkv, d), 0.088, (1024, 4096, 8192), f"{len(ctx)} sequences")
 
 
 def test_int4_decode_more_than_sixteen_partitions():
@@ -197,7 +185,7 @@ def test_int4_bad_block_ids_and_lengths():
 
 
 @pytest.mark.parametrize("d", [128, 64])
-@pytest.mark.parametrize("part", [0, 16, 48, 256, pa.PA_SPLIT_EVEN])
+@pytest.mark.parametrize("part", [0, 16, 48, 256, 4096])
 def test_int4_step_writes_and_attends(d, part):
     rng, ctx, tables, pools, q = _case(8 + d, [1, 16, 17, 33, 400], 8, 2, d)
     B = len(ctx)
@@ -209,9 +197,7 @@ def test_int4_step_writes_and_attends(d, part):
     out = torch.empty(B, 8, d, dtype=torch.bfloat16, device="cuda")
     pa.pa_clear_device_error()
     kw = {}
-    if part == pa.PA_SPLIT_EVEN:
-        kw = dict(workspace=pa.even_workspace(8, 2, d), counters=pa.even_counters(B, 2))
-    elif part:
+    if part:
         kw = dict(workspace=pa.splitk_workspace(B, 8, d, 400, part),
                   counters=pa.step_counters(B, 2))
     pa.pa_decode_step(out, dev_bf16(q), dk, dv, _dev(tables, np.int32), _dev(ctx, np.int32), 0.1,
@@ -248,44 +234,18 @@ def test_int4_decode_step_handle_plans_and_replays():
         _gate(out, ref, V, f"replay {less}")
 
 
-def test_int4_handle_picks_the_even_split_for_long_batches():
-    assert not pa.int4_split_evenly([2048] * 10, 32, 8)
-    assert pa.int4_split_evenly([40000] * 4, 32, 8) and not pa.int4_split_evenly(
-        [40000] * 4, 64, 8)
-    rng, ctx, tables, pools, q = _case(15, [70000, 60000, 5], 32, 8, 64)
-    dk, dv = (torch.from_numpy(p).cuda() for p in pools)
-    out = torch.full((3, 32, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
-    step = pa.DecodeStep(None, None, dk, dv, None, dev_bf16(q), _dev(tables, np.int32),
-                         _dev(ctx, np.int32), out, 0.125, partition_size=None,
-                         host_context_lens=ctx)
-    assert step.partition_size == pa.PA_SPLIT_EVEN
-    pa.pa_clear_device_error()
-    for _ in range(2):
-        step()
-    ref, V = _ref((rng, ctx, tables, pools, q), 0.125)
-    _gate(out, ref, V, "even split of long contexts")
-    assert pa.pa_get_device_error() == 0 and not step.counters.any()
-
-
-def test_int4_handle_with_its_own_counters_and_another_stream():
-    rng, ctx, tables, pools, q = _case(16, [50000, 60000, 70000], 32, 8, 64)
-    assert pa.int4_split_evenly(ctx, 32, 8)
+def test_int4_handle_made_on_one_stream_and_run_on_another():
+    # its counters are zeros before the first call, whatever the stream that makes
+    # it is doing
+    rng, ctx, tables, pools, q = _case(16, [5000, 6000, 17000], 32, 8, 64)
     dk, dv = (torch.from_numpy(p).cuda() for p in pools)
     dq, t, c = dev_bf16(q), _dev(tables, np.int32), _dev(ctx, np.int32)
     ref, V = _ref((rng, ctx, tables, pools, q), 0.125)
-    # partitions' counters are given: the lengths do not change that choice
-    out = torch.full((3, 32, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
-    step = pa.DecodeStep(None, None, dk, dv, None, dq, t, c, out, 0.125, partition_size=None,
-                         host_context_lens=ctx, counters=pa.step_counters(3, 8))
-    assert step.partition_size != pa.PA_SPLIT_EVEN
-    step()
-    _gate(out, ref, V, "counters given")
-    # a handle made behind other work on one stream and run on another: its
-    # counters are zeros before that
+    out = torch.empty(3, 32, 64, dtype=torch.bfloat16, device="cuda")
     other = torch.cuda.Stream()
-    for ps in (None, 4096):
+    for ps in (None, 2048):
         out.fill_(float("nan"))
-        dirty = [torch.full((n,), -1, dtype=torch.int32, device="cuda") for n in (24, 512)]
+        dirty = torch.full((24,), -1, dtype=torch.int32, device="cuda")
         torch.cuda.synchronize()
         del dirty                               # (the handle's counters may take its place)
         work = torch.randn(4096, 4096, device="cuda")
@@ -295,7 +255,7 @@ def test_int4_handle_with_its_own_counters_and_another_stream():
                              host_context_lens=ctx, stream=other)
         step()
         other.synchronize()
-        _gate(out, ref, V, f"another stream {ps}")
+        _gate(out, ref, V, f"partition {ps}")
         torch.cuda.synchronize()
 
 
@@ -344,14 +304,8 @@ def test_int4_binding_refusals():
             pa.pa_decode_int4(**{**ok, **bad})
     with pytest.raises(ValueError):
         pa.pa_decode_step(**ok, softcap=30.0)       # rules need a bf16 cache
-    with pytest.raises(ValueError):                 # no counters; too small; groups of 8
-        pa.pa_decode_step(**ok, partition_size=pa.PA_SPLIT_EVEN)
-    with pytest.raises(ValueError):
-        pa.pa_decode_step(**ok, partition_size=pa.PA_SPLIT_EVEN,
-                          workspace=(torch.empty(4, device="cuda"), None, None),
-                          counters=pa.even_counters(2, 2))
-    with pytest.raises(ValueError):
-        pa.even_workspace(16, 2, 128)
+    with pytest.raises(ValueError):                 # no workspace
+        pa.pa_decode_step(**ok, partition_size=256)
     with pytest.raises(ValueError):
         pa.pa_decode_step(**ok, k_scales=torch.zeros(3, 2, 16, device="cuda"))
     with pytest.raises(ValueError):

@@ -260,14 +260,7 @@ def test_int4_host_checks(lib):
     assert step(order=F, part=0) == bad
     assert step(order=F, seqs=300, maxp=300) == shape
     assert step(seqs=0) == pa.PA_OK
-    even = pa.PA_SPLIT_EVEN
-    assert step(part=even, ws=None) == bad and step(part=even, counters=None) == bad
-    assert step(part=even, seqs=5000) == shape and step(part=-2) == bad
-    assert lib.pa_decode_step_int4(F, F, None, None, None, F, F, F, 4, F, 2, 64, 8, 128, 16, 10,
-                                   0.1, even, F, F, F, F, 4, None, 0, None) == shape  # groups of 8
-    assert lib.pa_decode_step(F, F, None, None, None, F, F, F, 4, F, 2, 32, 8, 128, 16, 10, 0.1,
-                              even, F, F, F, F, 4, None, 0, None) == bad  # 4-bit only
-    assert lib.pa_even_workspace_bytes(32, 8, 96) == 0 and lib.pa_even_counters(-1, 8) == 0
+    assert step(part=-1) == bad
 
 
 def test_biased_host_checks(lib):
