@@ -600,7 +600,7 @@ def step_launch(workload_idx, w, kv="bf16", step="fused", attn="auto", partition
             "plan": plan, "early_read": fused and early_read == "on"}
 
 
-def recorded_traffic(kernel, workload_name, partition, sources=("decode.cu", "decode_tile.cuh")):
+def recorded_traffic(kernel, workload_name, partition, sources=("decode_kernel.cuh", "decode_tile.cuh")):
     """DRAM bytes per launch from the committed ncu summaries, or None when the
     kernel source (the files ``sources``) or the launch shape changed since the
     counters were taken.  ``profiles/decode_traffic.txt`` holds one
@@ -769,8 +769,8 @@ def run_gpu(args):
                 "frac": round(achieved / (hbm_peak if hbm_peak else 6800.0), 4),
                 "traffic": args.traffic if args.traffic is not None else recorded_traffic(
                     kkey, w.name, args.partition,
-                    ("decode.cu", "decode_tile.cuh", "prefill.cu") if lp["shared_prefix"]
-                    else ("decode.cu", "decode_tile.cuh")),
+                    ("decode_kernel.cuh", "decode_tile.cuh", "prefill_kernel.cuh") if lp["shared_prefix"]
+                    else ("decode_kernel.cuh", "decode_tile.cuh")),
                 "kernel": kname,
                 "peak_source": "measured (MEASURED_PEAKS.json hbm_gbs)" if hbm_peak
                 else "fallback 6.8 TB/s",
@@ -1194,7 +1194,7 @@ def run_prefill(args):
         "roofline": {"bound": "tensor", "achieved": round(tflops, 2),
                      "peak": peak if peak else 1900.0, "unit": "TFLOP/s",
                      "frac": round(tflops / (peak if peak else 1900.0), 4),
-                     "traffic": recorded_traffic("pa_prefill", w.name, 0, ("prefill.cu",)),
+                     "traffic": recorded_traffic("pa_prefill", w.name, 0, ("prefill_kernel.cuh",)),
                      "kernel": "pa_prefill",
                      "peak_source": "measured (MEASURED_PEAKS.json bf16_tflops, burst)"
                      if peak else "fallback 1.9 PFLOP/s",

@@ -34,6 +34,10 @@ Modules:
                  per-row quantisation, the FP8 cache write and decode.
 * ``quant``      the INT8 KV scheme: per-row quantisation, the INT8 cache
                  write and the INT8 decode.
+* ``rope``       the rotary embedding of q and k.
+* ``int4``       the 4-bit KV scheme: groups of 64 dims with an offset and a
+                 scale, and the decode over the values they stand for.
+* ``biased``     attention with capped, biased, windowed and prefix-opened scores.
 * ``cache``      the cache write (scatter of new K/V through a slot mapping).
 * ``allocator``  a pure-Python block allocator model (FIFO free list,
                  refcounts, fork / copy-on-write, free).
