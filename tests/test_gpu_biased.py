@@ -381,3 +381,66 @@ def test_prompt_then_decode_steps():
         assert np.all(np.abs(bf16_to_f64(out) - ref) <=
                       2.0 ** -8 * np.abs(ref) + 2.0 ** -11 * 10 + 2.0 ** -13 * 5)
     assert pa.pa_get_device_error() == 0
+
+
+def test_two_layers_at_once_on_two_streams():
+    """Two chains of append, 4-bit step and capped step, each with buffers of its
+    own and captured into a graph, run at once on two streams: the results of
+    each are those of running it alone."""
+    hq, hkv, d, B, n = 8, 2, 128, 12, 700
+    table = pa.rope_table(1024, d, 10000.0)
+    ctx = [n - 31 * b for b in range(B)]
+    chains = []
+    for seed in (21, 22):
+        rng = np.random.default_rng(seed)
+        nb = 44 * B
+        tables = _dev(rng.permutation(nb).reshape(B, 44), np.int32)
+        c = _dev(ctx, np.int32)
+        pos = c - 1
+        slots = (tables.gather(1, (pos // 16).long()[:, None])[:, 0] * 16 + pos % 16).long()
+        kc, vc = (dev_bf16(normal_bf16(rng, (nb, hkv, 16, d))) for _ in "kv")
+        pools = []
+        for src in (kc, vc):
+            pools.append(src.clone())
+        k4, v4 = pa.int4_pool(nb, hkv, d), pa.int4_pool(nb, hkv, d)
+        every = torch.arange(nb * 16, device="cuda")
+        rows = [p.permute(0, 2, 1, 3).reshape(nb * 16, hkv, d).contiguous() for p in pools]
+        pa.pa_reshape_and_cache_int4(*rows, k4, v4, every)
+        qkv = dev_bf16(normal_bf16(rng, (B, hq + 2 * hkv, d)))
+        q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+        q_out = torch.empty(B, hq, d, dtype=torch.bfloat16, device="cuda")
+        outs = [torch.empty_like(q_out) for _ in range(2)]
+        calls = [pa.RopeAppend(q_out, q, k, v, kc, vc, slots, pos, table),
+                 pa.RopeAppend(q_out, q, k, v, k4, v4, slots, pos, table),
+                 pa.DecodeStep(None, None, k4, v4, None, q_out, tables, c, outs[0], 0.088,
+                               partition_size=64),
+                 pa.DecodeStep(None, None, kc, vc, None, q_out, tables, c, outs[1], 0.088,
+                               partition_size=128, softcap=20.0, window=300)]
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        for call in calls:
+            call()
+        torch.cuda.synchronize()
+        want = [o.clone() for o in outs]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(stream), torch.cuda.graph(graph, stream=stream):
+            for call in calls:
+                call()
+        chains.append((calls, stream, graph, outs, want))
+    for replay in (False, True):
+        for _, _, _, outs, _ in chains:
+            for o in outs:
+                o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for calls, stream, graph, _, _ in chains:
+                with torch.cuda.stream(stream):
+                    if replay:
+                        graph.replay()
+                    else:
+                        for call in calls:
+                            call()
+        torch.cuda.synchronize()
+        for _, _, _, outs, want in chains:
+            assert all(torch.equal(o, w) for o, w in zip(outs, want)), f"replay {replay}"
+    assert pa.pa_get_device_error() == 0

@@ -198,10 +198,11 @@ def test_rope_in_place_and_handle_under_a_graph():
 
 
 def test_rope_far_offsets():
-    # a pool of more than 2^31 elements: the last block's offset passes 32 bits
-    nb, hkv, d = 70000, 8, 128
+    # a pool of more than 2^31 elements (2^32 bytes): the last block's offset does
+    # not fit 32 bits
+    nb, hkv, d = 140000, 8, 128
     pools = [torch.zeros(nb, hkv, 16, d, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
-    assert pools[0].numel() > 1 << 30 and pools[0].numel() * 2 > 1 << 31
+    assert pools[0].numel() > 1 << 31
     rng, qkv, q, k, v = _inputs(12, 2, 8, hkv, d, False)
     slots = torch.tensor([nb * 16 - 1, 5], device="cuda")
     pos = torch.zeros(2, dtype=torch.int32, device="cuda")
