@@ -10,6 +10,7 @@ Tensors: bf16 data is passed as ``torch.bfloat16`` tensors; block tables and
 context lengths as ``torch.int32``; slot mappings as ``torch.int64``.
 """
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -182,21 +183,23 @@ def _torch():
 
 
 _raw_stream = None  # torch's (device index) -> current stream handle
+_raw_device = None  # and () -> current device index
 
 
 def _stream(stream):
     """The stream's handle.  Without one, the current device's current stream,
     asked of torch directly where it offers that: building its Stream object
     takes 3 us, as long as the rest of a small call."""
-    global _raw_stream
+    global _raw_stream, _raw_device
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
-    torch = _torch()
     if _raw_stream is None:
+        torch = _torch()
         torch.cuda.current_stream()  # initialises CUDA, or raises
+        _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream().cuda_stream)
-    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+    return _raw_stream(_raw_device())
 
 
 def _dev(t, dtype, name, ndim=None):
@@ -264,12 +267,7 @@ class _Prepared:
         fn = getattr(lib(), prepare)
         _check(fn(ctypes.byref(h), *args), prepare)
         self._h = h
-        self._run = lib().pa_run
-
-    def __call__(self, stream, where):
-        st = self._run(self._h, stream)
-        if st != PA_OK:
-            _check(st, where)
+        self.run = functools.partial(lib().pa_run, h)  # (stream) -> status
 
     def __del__(self):
         try:
@@ -453,7 +451,9 @@ class RopeAppend:
 
     def __call__(self, stream=None):
         s = self._stream if stream is None and self._stream is not None else _stream(stream)
-        self._call(s, "RopeAppend: pa_rope_reshape_and_cache")
+        st = self._call.run(s)
+        if st != PA_OK:
+            _check(st, "RopeAppend: pa_rope_reshape_and_cache")
 
 
 def _decode_common(q, k_cache, v_cache, block_tables, context_lens):
@@ -1115,7 +1115,9 @@ class PrefillStep:
 
     def __call__(self, stream=None):
         s = self._stream if stream is None and self._stream is not None else _stream(stream)
-        self._call(s, "PrefillStep: prefill")
+        st = self._call.run(s)
+        if st != PA_OK:
+            _check(st, "PrefillStep: prefill")
 
 
 def pa_plan_step(budget, num_decodes, prefill_remaining):
@@ -1301,10 +1303,7 @@ class DecodeStep:
     def __call__(self, stream=None):
         s = self._stream if stream is None and self._stream is not None else _stream(stream)
         if self.fused:
-            if self._call is not None:
-                self._call(s, "DecodeStep: pa_decode_step")
-                return
-            st = self._fn(*self._args, s)
+            st = self._call.run(s) if self._call is not None else self._fn(*self._args, s)
             if st != PA_OK:
                 _check(st, "DecodeStep: pa_decode_step")
             return
