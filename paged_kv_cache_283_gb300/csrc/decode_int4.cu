@@ -27,7 +27,9 @@ namespace {
 //                  8 x 131,072              194.1     188.2  (5120)
 // So groups of 8 take four, smaller ones from kLongPartition on: there one wave of
 // three CTAs an SM holds the launch, and its CTAs run long.  One block at a time
-// with four CTAs: 22.0 us for the 64, 145 for the 256.  D = 64 has the registers
+// with four CTAs: 22.0 us for the 64, 145 for the 256.  Eight warps a CTA, two CTAs
+// an SM, are faster only for whole contexts in one wave (the 64: 17.0; 500: 128),
+// which the launch cannot know from lengths in device memory.  D = 64 has the registers
 // for four blocks and four CTAs: 64 x 15,763 66.7 us against 74.3 with two,
 // 256 x 4094 68.1 against 76.7, 32 x 595 5.3 and 5.3.
 constexpr int kLongPartition = 4096 / kBlockSize;  // blocks
