@@ -665,11 +665,11 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
   const int my_i0 = (sub * R) % P;
   RuleLane rule;
   if constexpr (RULE) {
+    static_assert(Q == 0, "changed scores: bf16 only");
     rule.cap2 = p.rule.softcap * 1.4426950408889634f;
     rule.inv_cap2 = rule.cap2 > 0.f ? 1.f / rule.cap2 : 0.f;
     if (p.rule.slopes != nullptr)
-      rule.slope2 = 1.4426950408889634f *
-                    __ldg(p.rule.slopes + kvh * G + (I8 ? QCols<G>::head(lane >> 2) : my_head));
+      rule.slope2 = 1.4426950408889634f * __ldg(p.rule.slopes + kvh * G + my_head);
     rule.last = ctx - 1;
     rule.first = lo_tok;
   }
@@ -717,7 +717,6 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
         tile_step<D, G, false>(kt, vt, ps, alpha_s, q2, acc, m_run, l_run, nvalid, lane, sub,
                                rg, my_head, my_i0);
     } else if constexpr (Q == 3) {
-      static_assert(!RULE, "changed scores: bf16 only");
       if (nvalid == SB * BS)
         w4.template step<SB, true>(stage, nvalid, lane);
       else

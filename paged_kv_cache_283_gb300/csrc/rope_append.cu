@@ -228,8 +228,13 @@ __device__ __forceinline__ void store_quantised(const RopeAppendParams& p, bool 
 // takes its rows s, s + row_slots, ..., U of them at most, loaded together and
 // before the position and the slot are known (their round trips overlap).  All
 // L lanes of a row follow the same path.
+//
+// Four CTAs of 256 threads an SM (64 registers): a quantising thread would take 92,
+// and its row's chain of steps wants warps beside it.  8192 tokens of 32 + 16 rows,
+// with 92, 80, 64 and 48 registers: 4-bit 55.6, 51.1, 44.2, 55.3 us (26.7 at the
+// copy rate), INT8 49.8, 49.9, 43.9, 56.4, FP8 46.9, 47.0, 41.5, 55.0.
 template <int D, int Q, int U>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendParams p) {
+__global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const RopeAppendParams p) {
   constexpr int L = D / 16;
   griddep_wait();  // the producer of q / key / value is complete
   griddep_launch_dependents();
@@ -348,12 +353,12 @@ cudaError_t launch_t(const RopeAppendParams& p, cudaStream_t stream) {
   // trips and a row to a thread is the shortest; past that a thread takes up to U
   // rows, which share its cosines and sines and overlap their loads.  In us, one
   // row and U (D = 128; bf16 with 32 + 16 rows a token, 4-bit with 16 + 8):
-  //   bf16   64 tokens,   25K threads   1.8   2.1      128,  49K  2.1  2.1
-  //         256,          98K           2.7   2.3     8192, 3.1M 44.8 34.2
-  //   4-bit 400,          77K           3.6   3.8      512,  98K  4.1  3.9
-  //        1024,         197K           6.4   5.2     8192, 1.6M 35.3 29.7
-  // U: 8192 bf16 tokens take 36.6 us with 2 rows, 34.6 with 3, 34.7 with 4, 37.8
-  // with 6.
+  //   bf16   64 tokens,   25K threads   1.9   2.1      128,  49K  1.9  2.1
+  //         256,          98K           2.5   2.3     8192, 3.1M 49.3 34.5
+  //   4-bit 400,          77K           3.6   4.0      512,  98K  4.1  4.0
+  //        1024,         197K           6.4   4.8     8192, 1.6M 35.2 24.2
+  // U: 8192 bf16 tokens take 36.6 us with 2 rows, 34.7 with 3, 34.8 with 4, 35.8
+  // with 6; into a 4-bit cache 44.2 with 3, 59.3 with 4.
   const bool one = static_cast<int64_t>(p.num_tokens) * rows * L <= kOneRowThreads;
   RopeAppendParams r = p;
   r.row_slots = one ? rows : (rows + U - 1) / U;
