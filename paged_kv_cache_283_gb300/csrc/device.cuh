@@ -119,21 +119,6 @@ __device__ __forceinline__ void bulk_copy_g2s(void* dst, const void* src, unsign
       : "memory");
 }
 
-// The same, and arrive.expect_tx, on 32-bit shared-memory addresses.
-__device__ __forceinline__ void mbar_expect_u32(uint32_t bar, unsigned bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_copy_u32(uint32_t dst, const void* src, unsigned bytes,
-                                              uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-      "[%0], [%1], %2, [%3], %4;" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
-      : "memory");
-}
-
 // Programmatic dependent launch.  Every kernel of this library is launched
 // with programmatic stream serialisation, so it may be scheduled while the
 // previous kernel in the stream is still running; it executes griddep_wait()
