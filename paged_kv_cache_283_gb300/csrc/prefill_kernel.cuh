@@ -313,13 +313,14 @@ __device__ __forceinline__ float max_abs(const uint32_t (&v)[HK]) {
 // degree 2 while every |z| of the warp is at most 0.2 (kNear: 1.1e-7 of the
 // result, x = s (c0 + c1 s^2 + c2 s^4) - m, three packed operations a pair beside
 // the one that x takes anyway) and of degree 4 up to 0.6 (kMid: 8e-8; five).
-// Elsewhere (kFar), and for maxima, 1 - 2 / (1 + e^2z), two more special-function
-// operations a score, to 2e-7 of the cap.  A masked score, -inf, stays one: the
-// last coefficients are positive.  16 x 512 new tokens after up to 3450 (32 query
-// / 8 KV heads; uncapped 328 us): every score near
-// 375, mid 403, far 537.  Packed multiply-adds have the rate of two single ones,
-// so mid without near makes the small scores 395; near and far alone 366 and 522,
-// which leaves scores of a fifth of the cap at 522.
+// Elsewhere (kFar), and for maxima under a bias, 1 - 2 / (1 + e^2z), two more
+// special-function operations a score, to 2e-7 of the cap.  A masked score, -inf,
+// stays one: the last coefficients are positive.  16 x 512 new tokens after up to
+// 3450 (32 query / 8 KV heads; uncapped 328 us): every score near 372, mid 403, far
+// 507.  Packed multiply-adds have the rate of two single ones, so mid without near
+// makes the small scores 395; near and far alone 366 and 522, which leaves scores
+// past a fifth of the cap at 522 (both with maxima taken score by score, 375, 403
+// and 537 in the form above).
 //
 // The bias, slope (j - p) where no key after the query is visible, runs along
 // the keys in four chains of additions (a packed multiply-add would want its
@@ -868,9 +869,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int h = 0; h < HK / 32; ++h) {
               uint32_t v[32];
               half(h, v);
-              mx = fmaxf(mx, rule_pass<32, RULE, true>(v, rr, 0.f, at + 32.f * h, reach,
-                                                       far));
+              if constexpr ((RULE & kBias) != 0) {
+                mx = fmaxf(mx, rule_pass<32, RULE, true>(v, rr, 0.f, at + 32.f * h, reach,
+                                                         far));
+              } else {  // the cap keeps the order: the largest raw score's
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(v[j]));
+                mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+              }
             }
+            if constexpr ((RULE & kBias) == 0)
+              if (mx != -INFINITY)
+                mx = (RULE & kCap) ? rr.cap2 * tanhf(mx * p.cap_in) : mx * sl2;
             if (mx != -INFINITY) {
               if (m_used == -INFINITY) {
                 m_used = mx;
