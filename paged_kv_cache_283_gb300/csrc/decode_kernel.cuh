@@ -668,8 +668,6 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
     static_assert(Q == 0, "changed scores: bf16 only");
     rule.cap2 = p.rule.softcap * 1.4426950408889634f;
     rule.inv_cap2 = rule.cap2 > 0.f ? 1.f / rule.cap2 : 0.f;
-    if (p.rule.slopes != nullptr)
-      rule.slope2 = 1.4426950408889634f * __ldg(p.rule.slopes + kvh * G + my_head);
     rule.last = ctx - 1;
     rule.first = lo_tok;
   }
@@ -679,6 +677,10 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
   if (p.early_read) {
     griddep_wait();
     load_q();
+  }
+  if constexpr (RULE) {  // (after the wait: the promise of early reads has no slopes in it)
+    if (p.rule.slopes != nullptr)
+      rule.slope2 = 1.4426950408889634f * load_after_wait(p.rule.slopes + kvh * G + my_head);
   }
   // this warp patches its tile of the sequence's last block (the only
   // block with ctx - j * BS <= BS)

@@ -140,6 +140,15 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A load that stays where it stands: of what the preceding kernel may still be writing
+// before griddep_wait() (the compiler takes __ldg's memory as constant for the whole
+// kernel and may load it before the wait).
+__device__ __forceinline__ float load_after_wait(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // Launches `kernel<<<grid, block, smem, stream>>>(args...)` with
 // programmatic stream serialisation allowed (see above).
 template <typename... KArgs, typename... Args>
