@@ -647,7 +647,10 @@ pa_status pa_prefill(void* out, const void* q, const void* k_cache, const void* 
  * j > p - window; its scores are
  *   s_j = softcap * tanh(x_j / softcap) - alibi_slopes[h] * |p - j|,
  *   x_j = scale * dot(q_p, K_j)
- * (softcap 0: x_j itself; alibi_slopes NULL: no second term).  prefix_lens:
+ * (softcap 0: x_j itself; alibi_slopes NULL: no second term).  The tanh is taken to
+ * 1e-7 of itself while the visible scores of a query's 32 neighbouring rows (tokens
+ * and heads) in 64 keys lie within 0.6 of the cap, else to 2e-7 of 1, so that s_j is
+ * off by 2e-7 of the cap; what hidden places hold changes nothing.  prefix_lens:
  * device int32 [num_seqs] (or NULL), leading positions that every query of the
  * sequence sees (a bidirectional prefix; their K and V are in the cache before
  * the call).  A prefix outside [0, context_lens[b]] sets PA_DEVERR_PREFIX and

@@ -839,6 +839,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           for (int h = 0; h < HK / 32; ++h)
             tmem_ld32(tS + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * h));
           tmem_wait_ld();
+          if constexpr ((RULE & kCap) != 0) {
+            // the curve goes by the visible scores alone: hidden places, and slots
+            // that no copy filled, may hold anything
+            if (masked) {
+#pragma unroll
+              for (int h = 0; h < HK; h += 32) {
+                const int top_bit = lim - h, low_bit = low - h;
+                const uint32_t seen =
+                    (top_bit >= 31 ? ~0u : top_bit < 0 ? 0u : (2u << top_bit) - 1u) &
+                    (low_bit <= 0 ? ~0u : low_bit > 31 ? 0u : ~0u << low_bit);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!(seen >> j & 1u)) sv[h + j] = 0u;
+              }
+            }
+          }
           const float mabs = max_abs<HK>(sv);
           int reach = kNear;
           float top = mabs * sl2;
