@@ -707,6 +707,14 @@ pa_status pa_run(const pa_prepared* prepared, pa_stream_t stream);
 void pa_prepared_destroy(pa_prepared* prepared);
 
 /*
+ * Orders `stream` behind a recorded event (a cudaEvent_t), so that buffers made on
+ * another stream can be used on it.  While `stream` is being captured, when its
+ * graph could not hold the wait, the host waits for the event instead.
+ * PA_ERR_INVALID_ARG for a NULL event.
+ */
+pa_status pa_await_event(void* event, pa_stream_t stream);
+
+/*
  * Split-K partition size for a decode batch (host): the size, from {256, 384,
  * 512, 640, 768, 1024, 1280, 1536, 1792, 2048, 4096} tokens, that minimises a
  * model of the split-K launch's time -- its CTAs handed in grid order to the first free

@@ -990,4 +990,24 @@ pa_status pa_run(const pa_prepared* prepared, pa_stream_t stream) {
 
 void pa_prepared_destroy(pa_prepared* prepared) { delete prepared; }
 
+pa_status pa_await_event(void* event, pa_stream_t stream) {
+  if (!event) return PA_ERR_INVALID_ARG;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaEvent_t ev = static_cast<cudaEvent_t>(event);
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(s, &capturing);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (capturing == cudaStreamCaptureStatusNone) {
+    e = cudaStreamWaitEvent(s, ev, 0);
+  } else {  // (an event from outside a capture may only be waited for by the host)
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return cuda_fail(e);
+    e = cudaEventSynchronize(ev);
+    const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e == cudaSuccess) e = back;
+  }
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
 }  // extern "C"

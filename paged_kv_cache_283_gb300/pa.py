@@ -110,6 +110,7 @@ SIGNATURES = {
              _i, _i, _f, _f, _vp, _i, _vp]),
     "pa_run": (_i, [_vp, _vp]),
     "pa_prepared_destroy": (None, [_vp]),
+    "pa_await_event": (_i, [_vp, _vp]),
     "pa_plan_step": (_i, [_i, _i, _vp, _i, _vp, _pint]),
     "pa_alloc_create": (_i, [_i, _i, _vp, ctypes.POINTER(_vp)]),
     "pa_alloc_destroy": (None, [_vp]),
@@ -1165,6 +1166,7 @@ class DecodeStep:
                  host_context_lens=None, softcap=0.0, alibi_slopes=None, window=0):
         torch = _torch()
         self.fused = bool(fused)
+        self._ready = None  # the event behind the counters and workspace made here
         four = k_cache.dtype == torch.uint8 and k_cache.dim() == 3
         block = 16 if four else k_cache.shape[2]
         if not self.fused and (four or softcap or alibi_slopes is not None or window):
@@ -1213,8 +1215,9 @@ class DecodeStep:
                 if counters is None:
                     counters = step_counters(B, hkv, q.device)
                 if made and not torch.cuda.is_current_stream_capturing():
-                    # the first call may go to another stream
-                    torch.cuda.current_stream(q.device).synchronize()
+                    # the first call may go to another stream, or into a graph that
+                    # is replayed on one: it awaits what was enqueued here
+                    self._ready = torch.cuda.current_stream(q.device).record_event()
             self.workspace, self.counters = workspace, counters
             self._fn, self._args = _step_args(
                 out, q, k_cache, v_cache, block_tables, context_lens, scale, key, value,
@@ -1300,9 +1303,16 @@ class DecodeStep:
             return recover_step_counters(self.counters)
         return pa_get_device_error()
 
+    def _await_made(self, stream):
+        """Before the first call: `stream` goes behind what the constructor enqueued."""
+        _check(lib().pa_await_event(self._ready.cuda_event, stream), "DecodeStep: pa_await_event")
+        self._ready = None
+
     def __call__(self, stream=None):
         s = self._stream if stream is None and self._stream is not None else _stream(stream)
         if self.fused:
+            if self._ready is not None:
+                self._await_made(s)
             st = self._call.run(s) if self._call is not None else self._fn(*self._args, s)
             if st != PA_OK:
                 _check(st, "DecodeStep: pa_decode_step")
