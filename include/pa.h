@@ -297,7 +297,9 @@ pa_status pa_decode_splitk_fp8(float* ws_out, float* ws_m, float* ws_l,
  * one head and one token: num_kv_heads 1, block_size 1, head_dim Hkv * 9 * D / 2.
  * Decode keeps q unquantised (scaled by a power of two it is exact in f16) and
  * takes QK and PV on the tensor cores over the codes, with fp32 accumulation;
- * the softmax weights times a token's V scale enter PV as one f16 (11 bits).
+ * the softmax weights times a token's V scale enter PV as one f16 each: 11 bits for
+ * products down to 2^-21 of the largest in a head's and warp's share of the context,
+ * fewer below, none below 2^-32.
  * pa_reshape_and_cache_int4: head_dim 64 or 128, block_size 16; slots as
  * pa_reshape_and_cache.  The decodes' shapes, checks and results otherwise as
  * the bf16 calls'.

@@ -4,8 +4,8 @@
 // them: a step of 32 tokens for 4 heads is 352 instructions (Warp4), a third of
 // them the unpacking of codes, and short batches are bounded by a launch's head
 // and tail.  Measured, in us, with the time at the copy rate: 64 contexts of 128
-// to 2016 tokens (32 query / 8 KV heads, D = 128) 19.8 (11.7); 256 of up to 4094
-// with groups of 8 111 (91); 8 of up to 49,796 42.4 (33.0).
+// to 2016 tokens (32 query / 8 KV heads, D = 128) 19.9 (11.7); 256 of up to 4094
+// with groups of 8 113.9 (91); 8 of up to 49,796 41.6 (33.0).
 
 #include "decode_kernel.cuh"
 

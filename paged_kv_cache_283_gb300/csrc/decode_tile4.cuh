@@ -22,10 +22,20 @@
 //   s = sum_g sc_g c_g + lo_g qs_g.
 //
 // PV: out^T = V^T W, V's codes as f16 subnormals in the same way (undone once at
-// the end).  W holds p * sc_g, one f16 each (11 bits: an output's error is about
-// 2^-12 of its size, against the 2^-9 of its bf16 rounding); the offsets' share,
-// sum p * lo_g, is summed in fp32 beside it.  W's columns: for G <= 4, 2 h + g;
-// for G = 8, heads tig and tig + 4 at 2 tig and 2 tig + 1, one operand per group.
+// the end).  W holds p * sc, one f16 each, in units of a power of two per head that
+// follows the head's largest product: where one passes f16's range, the unit rises
+// until it lies in [2^7, 2^8), and where the softmax reference rises, the unit falls
+// with the products so far.  So a product keeps 11 bits (the output's error is about
+// 2^-12 of its size, against the 2^-9 of its bf16 rounding) down to 2^-21 of the
+// head's largest in the warp's tokens, and only below 2^-32 of it is it lost; a
+// scale counts by its weight, however large.  (A unit that followed the largest
+// scale alone, whatever its weight, put outputs off by 0.56 with one light token of
+// 2^20 times the others' scale, and lost 17 % of a long context.  This one costs
+// nothing for groups of 4, 64 contexts 19.8 and 19.9 us, and 3 % for groups of 8, 256
+// contexts 110.7 and 113.9.)  The accumulators are fp32, to which the MMA truncates:
+// some 2^-25 of a head's sum for every 16 tokens of a warp.  The offsets' share, sum
+// p * lo, is summed in fp32 beside them.  W's columns: for G <= 4, 2 h + g; for G = 8,
+// heads tig and tig + 4 at 2 tig and 2 tig + 1, one operand per group.
 // A lane computes its tokens' row of W; a matrix transpose of 8 x 8 halves
 // (movmatrix) makes the operand.  So the lane that weighs head tig also holds
 // the columns of head tig of the result, and its own rescale factor.
@@ -60,7 +70,7 @@ struct Warp4 {
   float m[H], l[H];        // softmax reference (base 2), the lane's share of the sum
   float z[H][NG];          // the lane's share of sum p * lo
   float acc[D / 16][4];
-  float vbound, vinv;      // the warp's bound on the V scales it has weighed
+  float vb[H];             // unit of the heads' PV weights and sums
 
   static __device__ __forceinline__ int head(int tig, int h) { return (tig + 4 * h) % G; }
   // whether no other lane of the row holds the same results
@@ -124,13 +134,12 @@ struct Warp4 {
       }
       m[h] = -INFINITY;
       l[h] = 0.f;
+      vb[h] = kUnitFloor;
     }
 #pragma unroll
     for (int c = 0; c < D / 16; ++c)
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[c][k] = 0.f;
-    vbound = 0x1p-126f;
-    vinv = 0x1p126f;
   }
 
   static __device__ __forceinline__ float hi16(uint32_t w) {
@@ -151,6 +160,17 @@ struct Warp4 {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
+  }
+
+  // The least unit: p * reciprocal(unit) stays finite for p up to 2^8 (lazy_max), and
+  // what is below 2^-32 of a scale of 2^-126 is below any bf16.
+  static constexpr float kUnitFloor = 0x1p-118f;
+  // 1 / x of a power of two, and the largest power of two up to x (0 below 2^-126)
+  static __device__ __forceinline__ float reciprocal(float x) {
+    return __uint_as_float((254u << 23) - __float_as_uint(x));
+  }
+  static __device__ __forceinline__ float power_of_2(float x) {
+    return __uint_as_float(__float_as_uint(x) & 0x7F800000u);
   }
 
   // One step: NB blocks, K tile then V tile each, of which the first nvalid
@@ -229,8 +249,8 @@ struct Warp4 {
       alpha[h] = 1.f;
       if (m_new != m[h]) {
         alpha[h] = ex2_fast(m[h] - m_new);
+        moved |= m[h] != -INFINITY;  // (the sums before the first step are zeros)
         m[h] = m_new;
-        moved = true;
       }
       const float2 neg = make_float2(-m[h], -m[h]);
       float2 sum = make_float2(0.f, 0.f);
@@ -242,65 +262,107 @@ struct Warp4 {
       }
       l[h] = fmaf(l[h], alpha[h], sum.x + sum.y);
     }
-    // V's parameters, and whether a scale passes the warp's bound (the words
-    // order as their scales do: scales are not negative)
-    uint32_t w0[NB][NG], w1[NB][NG];
-    uint32_t top = 0;
-#pragma unroll
-    for (int u = 0; u < NB; ++u) {
-      const unsigned char* vt = stage + u * 2 * KT + KT;
-      load_params(vt, gid, w0[u]);
-      load_params(vt, gid + 8, w1[u]);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        if constexpr (!FULL) {
-          if (!(16 * u + gid < nvalid)) w0[u][g] = 0u;
-          if (!(16 * u + gid + 8 < nvalid)) w1[u][g] = 0u;
-        }
-        top = __vimax3_u32(top, w0[u][g], w1[u][g]);
-      }
-    }
-    float r = 1.f;
-    if (__any_sync(kFullMask, (top & 0xffff0000u) > __float_as_uint(vbound))) {
-      float vm = hi16(top);
-      vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 4));
-      vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 8));
-      vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, 16));
-      r = raise_v_bound(vm, vbound, vinv);
-      moved = true;
-    }
+    // a risen reference lowers what was summed by alpha; its power of two goes into
+    // the unit, so that weights to come keep their range
     if (__any_sync(kFullMask, moved)) {
+      float f[H];
 #pragma unroll
-      for (int h = 0; h < H; ++h)
+      for (int h = 0; h < H; ++h) {
+        const float now = alpha[h] * vb[h];
+        vb[h] = fmaxf(power_of_2(now), kUnitFloor);
+        f[h] = now * reciprocal(vb[h]);
 #pragma unroll
         for (int g = 0; g < NG; ++g) z[h][g] *= alpha[h];
-      const float fa = alpha[0] * r, fb = alpha[H - 1] * r;
-      scale_acc<D>(acc, fa, fb);  // columns 2 tig and 2 tig + 1 are the lane's heads
+      }
+      scale_acc<D>(acc, f[0], f[H - 1]);  // columns 2 tig and 2 tig + 1 are the lane's heads
     }
-    uint32_t b0[NB][NW], b1[NB][NW];
+    // V's parameters of the lane's tokens of block u (hidden ones count nothing)
+    auto load_v = [&](int u, uint32_t(&w0)[NG], uint32_t(&w1)[NG]) {
+      const unsigned char* vt = stage + u * 2 * KT + KT;
+      load_params(vt, gid, w0);
+      load_params(vt, gid + 8, w1);
+      if constexpr (!FULL) {
 #pragma unroll
-    for (int u = 0; u < NB; ++u) {
+        for (int g = 0; g < NG; ++g) {
+          if (!(16 * u + gid < nvalid)) w0[g] = 0u;
+          if (!(16 * u + gid + 8 < nvalid)) w1[g] = 0u;
+        }
+      }
+    };
+    // the lane's rows of W: tokens gid (b0) and gid + 8 (b1), before the transpose;
+    // returns their largest halves
+    uint32_t b0[NB][NW], b1[NB][NW];
+    auto weigh = [&](int u, const uint32_t(&w0)[NG], const uint32_t(&w1)[NG], uint32_t top) {
       float2 y[H];
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        y[h] = __fmul2_rn(s[u][h], make_float2(vinv, vinv));
+        const float inv = reciprocal(vb[h]);
+        y[h] = __fmul2_rn(s[u][h], make_float2(inv, inv));
+      }
+#pragma unroll
+      for (int n = 0; n < NW; ++n) {
+        // columns 2 tig and 2 tig + 1: two heads' (G = 8), else one head's two groups
+        // (one group: the odd columns are not read)
+        const int ga = G == 8 ? n : 0, gb = G == 8 ? n : NG - 1;
+        b0[u][n] = f16x2_rn(y[0].x * hi16(w0[ga]), y[H - 1].x * hi16(w0[gb]));
+        b1[u][n] = f16x2_rn(y[0].y * hi16(w1[ga]), y[H - 1].y * hi16(w1[gb]));
+        top = __vimax3_u16x2(top, b0[u][n], b1[u][n]);
+      }
+      return top;
+    };
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      uint32_t w0[NG], w1[NG];
+      load_v(u, w0, w1);
+#pragma unroll
+      for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int g = 0; g < NG; ++g)
-          z[h][g] = fmaf(s[u][h].x, lo16(w0[u][g]), fmaf(s[u][h].y, lo16(w1[u][g]), z[h][g]));
-      }
-      if constexpr (G == 8) {
+          z[h][g] = fmaf(s[u][h].x, lo16(w0[g]), fmaf(s[u][h].y, lo16(w1[g]), z[h][g]));
+      top = weigh(u, w0, w1, top);
+    }
+    // a half of 0x7C00 or more is a product past f16's range (65,504 units): the unit
+    // rises, and the step's products are taken again
+    if (__any_sync(kFullMask, ((top + 0x04000400u) & 0x80008000u) != 0)) {
+      float f[H], w[H];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          b0[u][g] = transpose(f16x2_rn(y[0].x * hi16(w0[u][g]), y[H - 1].x * hi16(w0[u][g])));
-          b1[u][g] = transpose(f16x2_rn(y[0].y * hi16(w1[u][g]), y[H - 1].y * hi16(w1[u][g])));
-        }
-      } else {  // column 2 h + g (one group: the odd columns are not read)
-        b0[u][0] =
-            transpose(f16x2_rn(y[0].x * hi16(w0[u][0]), y[0].x * hi16(w0[u][NG - 1])));
-        b1[u][0] =
-            transpose(f16x2_rn(y[0].y * hi16(w1[u][0]), y[0].y * hi16(w1[u][NG - 1])));
+      for (int h = 0; h < H; ++h) w[h] = 0.f;
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        uint32_t w0[NG], w1[NG];
+        load_v(u, w0, w1);
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int g = 0; g < NG; ++g)  // (times 2^-16: finite for any p and scale)
+            w[h] = fmaxf(w[h], fmaxf(s[u][h].x * 0x1p-16f * hi16(w0[g]),
+                                     s[u][h].y * 0x1p-16f * hi16(w1[g])));
+      }
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        w[h] = fmaxf(w[h], __shfl_xor_sync(kFullMask, w[h], 4));
+        w[h] = fmaxf(w[h], __shfl_xor_sync(kFullMask, w[h], 8));
+        w[h] = fmaxf(w[h], __shfl_xor_sync(kFullMask, w[h], 16));
+        const float nb = fmaxf(vb[h], power_of_2(w[h]) * 0x1p9f);
+        f[h] = vb[h] * reciprocal(nb);
+        vb[h] = nb;
+      }
+      scale_acc<D>(acc, f[0], f[H - 1]);
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        uint32_t w0[NG], w1[NG];
+        load_v(u, w0, w1);
+        weigh(u, w0, w1, 0u);
       }
     }
+#pragma unroll
+    for (int u = 0; u < NB; ++u)
+#pragma unroll
+      for (int n = 0; n < NW; ++n) {
+        b0[u][n] = transpose(b0[u][n]);
+        b1[u][n] = transpose(b1[u][n]);
+      }
 #pragma unroll
     for (int u = 0; u < NB; ++u) {
       const unsigned char* base = stage + u * 2 * KT + KT + lane * (D / 4);
@@ -323,7 +385,6 @@ struct Warp4 {
   // The warp's sums: v[(2 c + j) * H + h] = sum p v of head(tig, h), dim 16 c +
   // gid + 8 j; ml[h] = (m, l).  All 32 lanes must call it.
   __device__ __forceinline__ void finish(int lane, float (&v)[V], float2 (&ml)[H]) {
-    const float up = vbound * 0x1p20f;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
 #pragma unroll
@@ -337,8 +398,9 @@ struct Warp4 {
       for (int c = 0; c < D / 16; ++c) {
         const int g = c / 4;
         const int col = G == 8 ? h : g;  // 2 tig or 2 tig + 1
-        v[2 * c * H + h] = fmaf(acc[c][col] * 16.f, up, z[h][g]);
-        v[(2 * c + 1) * H + h] = fmaf(acc[c][2 + col], up, z[h][g]);
+        // (the codes' 2^-24 and 2^-20 first: a unit may be near the largest float)
+        v[2 * c * H + h] = fmaf(acc[c][col] * 0x1p24f, vb[h], z[h][g]);
+        v[(2 * c + 1) * H + h] = fmaf(acc[c][2 + col] * 0x1p20f, vb[h], z[h][g]);
       }
     }
   }
