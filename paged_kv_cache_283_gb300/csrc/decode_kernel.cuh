@@ -310,7 +310,9 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
   // partitions (the merge) and before exiting.
   const bool after_prefix = SPLIT && p.first_partition > 0;
   if (!p.early_read && !after_prefix) griddep_wait();
-  griddep_launch_dependents();
+  // With early reads only after the wait: the next launch may read early in turn, what
+  // the launch before this one's predecessor wrote among it.
+  if (!p.early_read) griddep_launch_dependents();
   const int kvh = blockIdx.x;
   // (sequence, partition): the grid's, or the order array's entry for this
   // CTA (its grid is then (Hkv, B * max_partitions, 1)); an entry out of
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
     const int item = __ldg(p.order + blockIdx.y);
     if (item < 0 || item >= p.num_seqs * (p.max_partitions - p.first_partition)) {
       if (threadIdx.x == 0) raise_error(p.err, PA_DEVERR_ORDER);
-      if (after_prefix) griddep_wait();
+      if (p.early_read || after_prefix) griddep_wait();
       return;
     }
     b = item % p.num_seqs;
@@ -676,6 +678,7 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
   for (int i = 0; i < npro; ++i) issue(i, i);
   if (p.early_read) {
     griddep_wait();
+    griddep_launch_dependents();
     load_q();
   }
   if constexpr (RULE) {  // (after the wait: the promise of early reads has no slopes in it)

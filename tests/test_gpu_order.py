@@ -185,3 +185,32 @@ def test_a_prefill_reads_after_the_launch_before(rule):
     fn = pa.pa_prefill_biased if rule else pa.pa_prefill
     _check(lambda **x: fn(out, k_cache=pools[0], v_cache=pools[1], max_query_len=40, scale=0.088,
                           **x, **kw), [out], late, inputs)
+
+
+@pytest.mark.parametrize("kind,rule", [("bf16", False), ("bf16", True), ("int8", False),
+                                       ("fp8", False), ("int4", False)])
+def test_early_reads_find_what_the_launch_before_the_last_wrote(kind, rule):
+    """A step with early reads may read lengths, tables and pools while the launch just
+    before it runs, which is itself such a step over other buffers; what the launch
+    before that one writes is complete by then."""
+    torch.manual_seed(4)
+    B, hq, hkv, d = 2, 8, 2, 128
+    (k0, v0), s0 = _pools(kind, 8, hkv, d)
+    (k1, v1), s1 = _pools(kind, 26, hkv, d)
+    ctx = torch.tensor([200, 100], dtype=torch.int32, device="cuda")
+    tables = torch.randperm(26, device="cuda").to(torch.int32).view(2, 13)
+    small = torch.tensor([[0], [1]], dtype=torch.int32, device="cuda")
+    short = torch.tensor([5, 9], dtype=torch.int32, device="cuda")
+    q = _normal(B, hq, d)
+    kw = dict(scale=0.088, partition_size=0, early_read=True)
+    if rule:
+        kw["window"] = 150
+    between, out = torch.empty_like(q), torch.empty_like(q)
+
+    def call(context_lens, block_tables):
+        pa.pa_decode_step(between, q, k0, v0, small, short, **kw, **s0)
+        pa.pa_decode_step(out, q, k1, v1, block_tables, context_lens, **kw, **s1)
+
+    _check(call, [between, out], dict(context_lens=(ctx, ctx - 60),
+                                      block_tables=(tables, tables.flip(0).contiguous())),
+           dict(context_lens=ctx, block_tables=tables))
