@@ -334,7 +334,9 @@ pa_status pa_decode_splitk_int4(float* ws_out, float* ws_m, float* ws_l, int max
  * stored in a bf16 or 4-bit cache are those of pa_reshape_and_cache (_int4) on
  * the rotated k and v; INT8 and FP8 rows take their scale as max|x| times the
  * float nearest 1 / 127 or 1 / 448 (one rounding step from the plain writes'
- * quotient at most), and their codes from it by the plain writes' rule.
+ * quotient at most), and their codes from it by the plain writes' rule: of normal
+ * values, a row in a hundred (INT8) or in twenty (FP8) has a code on the other side
+ * of a border than the plain write or the fused step would give it.
  *   q, key, value : [num_tokens] rows of heads * head_dim bf16, stride elements
  *     apart (a multiple of 8, at least the row): slices of one fused projection
  *     need no copy.  q_out [num_tokens, num_q_heads, head_dim], contiguous; it
@@ -718,7 +720,8 @@ pa_status pa_await_event(void* event, pa_stream_t stream);
 
 /*
  * Split-K partition size for a decode batch (host): the size, from {256, 384,
- * 512, 640, 768, 1024, 1280, 1536, 1792, 2048, 4096} tokens, that minimises a
+ * 512, 640, 768, 1024, 1280, 1536, 1792, 2048, 4096} tokens (a 4-bit cache: also
+ * 2304, 2560, 2816, 3328, 3584, 5120 and 8192), that minimises a
  * model of the split-K launch's time -- its CTAs handed in grid order to the first free
  * CTA slot (num_sms x the kernel's CTAs per SM), each costing a time per
  * token, a fixed start-up and, for sequences of several partitions, a merge
@@ -728,7 +731,8 @@ pa_status pa_await_event(void* event, pa_stream_t stream);
  * [num_seqs]; kv_kind 0 = bf16 cache, 1 = INT8, 2 = FP8, 4 = 4-bit,
  * 5 = bf16 with changed scores (pa_decode_step_biased); num_sms the device's
  * multiprocessor count; ordered != 0 models the launch with the
- * longest-first order of pa_splitk_order, 0 the plain grid order.  Returns 0
+ * longest-first order of pa_splitk_order, 0 the plain grid order (kinds 0 to 2
+ * with costs of its own; 4 and 5 with those of the ordered launch).  Returns 0
  * on invalid arguments.  The result is a
  * performance choice only: any partition size gives the same attention.
  */

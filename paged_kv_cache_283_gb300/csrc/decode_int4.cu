@@ -25,15 +25,13 @@ namespace {
 //                  8 x 49,796                54.0      42.4  (4096-token partitions)
 //                 12 x 46,911, 4 KV heads    46.7      42.2  (4096)
 //                  8 x 131,072              194.1     188.2  (5120)
-// So groups of 8 take four, smaller ones from kLongPartition on: there one wave of
+// So groups of 8 take four, smaller ones from kLongPartition4 tokens on: there one wave of
 // three CTAs an SM holds the launch, and its CTAs run long.  One block at a time
 // with four CTAs: 22.0 us for the 64, 145 for the 256.  Eight warps a CTA, two CTAs
 // an SM, are faster only for whole contexts in one wave (the 64: 17.0; 500: 128),
 // which the launch cannot know from lengths in device memory.  D = 64 has the registers
 // for four blocks and four CTAs: 64 x 15,763 66.7 us against 74.3 with two,
 // 256 x 4094 68.1 against 76.7, 32 x 595 5.3 and 5.3.
-constexpr int kLongPartition = 4096 / kBlockSize;  // blocks
-
 template <int D, int G>
 cudaError_t launch_g(const DecodeParams& p, bool split, cudaStream_t stream) {
   if constexpr (D == 64) {
@@ -42,7 +40,7 @@ cudaError_t launch_g(const DecodeParams& p, bool split, cudaStream_t stream) {
   } else {
     if (!split) return launch_decode_t<D, G, false, 3, false, 2>(p, stream);
     if constexpr (G < 8)
-      if (p.partition_blocks < kLongPartition)
+      if (p.partition_blocks < kLongPartition4 / kBlockSize)
         return launch_decode_t<D, G, true, 3, false, 2>(p, stream);
     return launch_decode_t<D, G, true, 3, false, 4>(p, stream);
   }

@@ -80,7 +80,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 template <int D, bool SPLIT, int Q>
 struct Pipe {  // head_dim 64: 2 KiB tiles, deeper rings
   static constexpr int NW = 4;
-  static constexpr int S = Q == 3 ? 4 : Q != 0 ? 6 : 4;
+  // (4-bit: stages of four blocks; a third made 256 contexts of up to 4094 tokens 69.0
+  // us, not 68.1)
+  static constexpr int S = Q == 3 ? 2 : Q != 0 ? 6 : 4;
 };
 template <bool SPLIT, int Q>
 struct Pipe<128, SPLIT, Q> {
@@ -1031,10 +1033,7 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done_mask) {
 
 template <int D, int G, bool SPLIT, int Q, bool RULE, int SB = 1>
 cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
-  constexpr int NW = Pipe<D, SPLIT, Q>::NW;
-  // (64-dim stages of four 4-bit blocks: two of them; a third made 256 contexts of
-  // up to 4094 tokens 69.0 us, not 68.1)
-  constexpr int S = D == 64 && SB == 4 ? 2 : Pipe<D, SPLIT, Q>::S;
+  constexpr int NW = Pipe<D, SPLIT, Q>::NW, S = Pipe<D, SPLIT, Q>::S;
   using Lay = SmemLayout<D, G, NW, S, Q, SB>;
   static std::atomic<uint64_t> smem_set{0};
   auto kernel = paged_decode_kernel<D, G, NW, S, SPLIT, Q, RULE, SB>;

@@ -40,6 +40,11 @@ inline ScoreRule within_capacity(ScoreRule r, int64_t capacity) {
 // Whether a rule's values make sense beside the score scale (api.cu).
 bool score_rule_ok(const ScoreRule& r, float scale);
 
+// The 4-bit split-K step of 128-dim heads in groups of up to 4 takes four blocks at a
+// time, three CTAs an SM, from partitions of this many tokens on (launch_decode_int4;
+// the partition chooser counts with it).
+constexpr int kLongPartition4 = 4096;
+
 // Arguments of the decode kernels (plain and split-K).  Pointers are device
 // pointers, already validated on the host.
 struct DecodeParams {

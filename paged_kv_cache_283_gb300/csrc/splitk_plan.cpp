@@ -42,6 +42,7 @@
 #include <vector>
 
 #include "../../include/pa.h"
+#include "internal.h"
 
 namespace {
 
@@ -52,7 +53,8 @@ struct Costs {
   double merge;
   double apart;  // the merge as its own launch
 };
-// kv_kind: 0 bf16, 1 INT8, 2 FP8, 4 4-bit, 5 bf16 with changed scores
+// kv_kind: 0 bf16, 1 INT8, 2 FP8, 4 4-bit, 5 bf16 with changed scores (one set of
+// costs for both orders, fitted longest first, as DecodeStep launches them)
 Costs costs_of(int kv_kind, bool ordered) {
   if (kv_kind == 4) return {0.0045, 2.0, 1.0, 5.0};
   if (kv_kind == 5) return {0.022, 4.0, 1.0, 3.0};
@@ -71,7 +73,7 @@ constexpr int kCandidates4[] = {256,  384,  512,  640,  768,  1024, 1280, 1536, 
 int ctas_per_sm(int group, int kv_kind, int head_dim, int part) {
   if (kv_kind == 0 || kv_kind == 5) return group <= 4 ? 3 : 1;
   if (kv_kind == 4)  // launch_decode_int4's choice of the step
-    return head_dim == 64 || (group <= 4 && part < 4096) ? 4 : 3;
+    return head_dim == 64 || (group <= 4 && part < pa::kLongPartition4) ? 4 : 3;
   return group <= 4 ? 4 : 3;
 }
 
