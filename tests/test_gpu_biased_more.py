@@ -113,3 +113,71 @@ def test_biased_step_window_of_many_partitions(d, hq, hkv):
         assert pa.pa_get_device_error() == 0
         assert_close(bf16_to_f64(out), ref, f"partitions of {part}")
         assert not counters.any()
+
+
+@pytest.mark.parametrize("prefix", [False, True])
+def test_slopes_of_either_sign(prefix):
+    # far keys heavier than near ones: the reference maximum climbs chunk by chunk
+    rng = np.random.default_rng(45)
+    slopes = (0.05 * rng.standard_normal(16)).astype(np.float32)
+    case = _case(46, MIXED, 16, 4)
+    ctx, n, tables, kc, vc, q = case
+    pre = [5, 20, 0, 53, 400, 64, 1033, 1] if prefix else None
+    for cap in (0.0, 4.0):
+        out = _fill(case, [dev_bf16(kc), dev_bf16(vc)], 0.088, pre, softcap=cap,
+                    alibi_slopes=_dev(slopes, np.float32))
+        assert_close(bf16_to_f64(out), OB.batch(q, kc, vc, tables, ctx, n, 0.088, softcap=cap,
+                                                slopes=slopes, prefix_lens=pre), f"cap {cap}")
+    ends = np.cumsum(n) - 1
+    last = q[ends]
+    step = pa.DecodeStep(None, None, dev_bf16(kc), dev_bf16(vc), None, dev_bf16(last),
+                         _dev(tables, np.int32), _dev(ctx, np.int32),
+                         torch.empty(len(n), 16, 128, dtype=torch.bfloat16, device="cuda"), 0.088,
+                         partition_size=64, alibi_slopes=_dev(slopes, np.float32))
+    step()
+    assert_close(bf16_to_f64(step._keep[8]),
+                 OB.batch(last, kc, vc, tables, ctx, np.ones_like(n), 0.088, slopes=slopes),
+                 "step")
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("part", [0, 64])
+def test_prepared_steps_of_the_plain_caches(kind, part):
+    # pa_prepare_decode_step without a rule launches what the direct call launches
+    torch.manual_seed(kind)
+    B, hq, hkv, d, nb = 3, 8, 2, 128, 30
+    ctx = torch.tensor([200, 1, 77], dtype=torch.int32, device="cuda")
+    tables = torch.randperm(nb, device="cuda")[:39].to(torch.int32)
+    tables = torch.cat([tables, tables[:9]]).view(3, 13)
+    tables[1, 0], tables[2, :5] = 29, torch.arange(20, 25, device="cuda")
+    tables[0] = torch.arange(13, device="cuda")
+    dtype = (torch.bfloat16, torch.int8, torch.uint8)[kind]
+    pools = [torch.randint(0, 100, (nb, hkv, 16, d), device="cuda").to(dtype) for _ in "kv"]
+    scales = [torch.rand(nb, hkv, 16, device="cuda") * 1e-2 for _ in "kv"] if kind else []
+    q, key, value = (torch.randn(B, h, d, device="cuda").to(torch.bfloat16)
+                     for h in (hq, hkv, hkv))
+    last = ctx - 1
+    slots = tables.gather(1, (last // 16).long()[:, None])[:, 0].long() * 16 + last % 16
+    ws = pa.splitk_workspace(B, hq, d, 208, part) if part else None
+    counters = pa.step_counters(B, hkv) if part else None
+    outs = []
+    for prepared in (False, True):
+        mine = [p.clone() for p in pools + scales]
+        out = torch.empty_like(q)
+        kw = dict(k_scales=mine[2], v_scales=mine[3]) if kind else {}
+        call = (out, q, mine[0], mine[1], tables, ctx, 0.088, key, value, slots, part, ws,
+                counters, kw.get("k_scales"), kw.get("v_scales"))
+        fn, a = pa._step_args(*call)
+        if prepared:
+            at = 7 if not kind else 9           # the pools, and the scales of these kinds
+            a = a[:7] + (a[7:9] if kind else (None, None)) + a[at:]
+            a = a[:19] + (0.0, None, 0) + a[19:]
+            h = pa._Prepared("pa_prepare_decode_step", kind, *a)
+            h.run(torch.cuda.current_stream().cuda_stream)
+        else:
+            pa._check(fn(*a, torch.cuda.current_stream().cuda_stream), "step")
+        torch.cuda.synchronize()
+        outs.append([out, *mine])
+    assert pa.pa_get_device_error() == 0
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
