@@ -32,18 +32,19 @@ namespace {
 // which the launch cannot know from lengths in device memory.  D = 64 has the registers
 // for four blocks and four CTAs: 64 x 15,763 66.7 us against 74.3 with two,
 // 256 x 4094 68.1 against 76.7, 32 x 595 5.3 and 5.3.
+// Partitions of up to this many tokens keep each of their warps below kSettleSteps
+// steps of four blocks.
+constexpr int kShortPartition = kSettleSteps * 4 * 4 * kBlockSize;
+
 template <int D, int G>
 cudaError_t launch_g(const DecodeParams& p, bool split, cudaStream_t stream) {
-  if constexpr (D == 64) {
-    return split ? launch_decode_t<D, G, true, 3, false, 4>(p, stream)
-                 : launch_decode_t<D, G, false, 3, false, 4>(p, stream);
-  } else {
-    if (!split) return launch_decode_t<D, G, false, 3, false, 2>(p, stream);
-    if constexpr (G < 8)
-      if (p.partition_blocks < kLongPartition4 / kBlockSize)
-        return launch_decode_t<D, G, true, 3, false, 2>(p, stream);
-    return launch_decode_t<D, G, true, 3, false, 4>(p, stream);
-  }
+  if (!split) return launch_decode_t<D, G, false, 3, false, D == 64 ? 4 : 2, true>(p, stream);
+  if (p.partition_blocks > kShortPartition / kBlockSize)
+    return launch_decode_t<D, G, true, 3, false, 4, true>(p, stream);
+  if constexpr (D == 128 && G < 8)
+    if (p.partition_blocks < kLongPartition4 / kBlockSize)
+      return launch_decode_t<D, G, true, 3, false, 2>(p, stream);
+  return launch_decode_t<D, G, true, 3, false, 4>(p, stream);
 }
 
 template <int D>

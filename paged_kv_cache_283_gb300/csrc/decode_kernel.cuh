@@ -293,7 +293,9 @@ __device__ __forceinline__ void load_q_bf16(const DecodeParams& p, int b, int kv
 // the codes), FP8 takes QK in E4M3 on two exact parts of q.
 // Q 3: a 4-bit cache (Warp4::step, SB blocks per step).  RULE: the scores are
 // changed (ScoreRule) and a window may hide the context's start.
-template <int D, int G, int NW, int S, bool SPLIT, int Q, bool RULE = false, int SB = 1>
+// LONG: a 4-bit launch of partitions (or whole contexts) that may be long.
+template <int D, int G, int NW, int S, bool SPLIT, int Q, bool RULE = false, int SB = 1,
+          bool LONG = false>
 __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
     paged_decode_kernel(const DecodeParams p) {
   constexpr bool I8 = Q != 0;   // 1-byte codes + scales
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
   // factor (tile_step_1b)
   uint32_t qa[D / 8];
   float qf = 0.f;
-  Warp4<D, G> w4;  // 4-bit cache: q, softmax state and sums
+  Warp4<D, G, LONG> w4;  // 4-bit cache: q, softmax state and sums
   float qoff = 0.f;  // int8 cache: 128 * the sum of head(gid)'s q codes (tile_step_1b)
   // q of the group into this lane's registers (or, for the int8 cache,
   // quantised through shared memory): the inputs a preceding kernel may
@@ -728,6 +730,8 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
         w4.template step<SB, true>(stage, nvalid, lane);
       else
         w4.template step<SB, false>(stage, nvalid, lane);
+      if constexpr (LONG)
+        if (i % kSettleSteps == kSettleSteps - 1) w4.settle();
     } else {
       const float* ksc = reinterpret_cast<const float*>(stage + 2 * Lay::KT);
       const float* vsc = ksc + BS;
@@ -800,7 +804,7 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
       }
     }
   } else if constexpr (Q == 3) {
-    using W4 = Warp4<D, G>;
+    using W4 = Warp4<D, G, LONG>;
     float v4[W4::V];
     float2 ml[W4::H];
     w4.finish(lane, v4, ml);
@@ -1031,12 +1035,12 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done_mask) {
   return e;
 }
 
-template <int D, int G, bool SPLIT, int Q, bool RULE, int SB = 1>
+template <int D, int G, bool SPLIT, int Q, bool RULE, int SB = 1, bool LONG = false>
 cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t stream) {
   constexpr int NW = Pipe<D, SPLIT, Q>::NW, S = Pipe<D, SPLIT, Q>::S;
   using Lay = SmemLayout<D, G, NW, S, Q, SB>;
   static std::atomic<uint64_t> smem_set{0};
-  auto kernel = paged_decode_kernel<D, G, NW, S, SPLIT, Q, RULE, SB>;
+  auto kernel = paged_decode_kernel<D, G, NW, S, SPLIT, Q, RULE, SB, LONG>;
   cudaError_t e = allow_smem(kernel, Lay::TOTAL, smem_set);
   if (e != cudaSuccess) return e;
   const dim3 grid =

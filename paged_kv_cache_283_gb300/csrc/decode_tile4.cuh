@@ -33,8 +33,8 @@
 // 2^20 times the others' scale, and lost 17 % of a long context.  This one costs
 // nothing for groups of 4, 64 contexts 19.8 and 19.9 us, and 3 % for groups of 8, 256
 // contexts 110.7 and 113.9.)  The accumulators are fp32, to which the MMA truncates:
-// some 2^-25 of a head's sum for every 16 tokens of a warp.  The offsets' share, sum
-// p * lo, is summed in fp32 beside them.  W's columns: for G <= 4, 2 h + g; for G = 8,
+// some 2^-25 of a head's sum for every 16 tokens of a warp (settle).  The offsets' share,
+// sum p * lo, is summed in fp32 beside them.  W's columns: for G <= 4, 2 h + g; for G = 8,
 // heads tig and tig + 4 at 2 tig and 2 tig + 1, one operand per group.
 // A lane computes its tokens' row of W; a matrix transpose of 8 x 8 halves
 // (movmatrix) makes the operand.  So the lane that weighs head tig also holds
@@ -54,7 +54,10 @@
 
 namespace pa {
 
-template <int D, int G>
+// LONG: a warp may take more than kSettleSteps steps (settle).
+constexpr int kSettleSteps = 32;
+
+template <int D, int G, bool LONG>
 struct Warp4 {
   static constexpr int NG = D / kInt4Group;
   static constexpr int H = G == 8 ? 2 : 1;      // heads per lane: tig (+ 4)
@@ -71,6 +74,7 @@ struct Warp4 {
   float z[H][NG];          // the lane's share of sum p * lo
   float acc[D / 16][4];
   float vb[H];             // unit of the heads' PV weights and sums
+  float taken[2];          // what settle() took from columns 2 tig, 2 tig + 1 (of 2^20 codes)
 
   static __device__ __forceinline__ int head(int tig, int h) { return (tig + 4 * h) % G; }
   // whether no other lane of the row holds the same results
@@ -140,6 +144,37 @@ struct Warp4 {
     for (int c = 0; c < D / 16; ++c)
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[c][k] = 0.f;
+    taken[0] = taken[1] = 0.f;
+  }
+
+  // Every kSettleSteps steps: the sums of a column's weights times codes (0 to 15) grow
+  // with its weights, all alike; their mean is taken out of them, so that what the MMA
+  // truncates stays small.  (Without, whole contexts of 131,072 tokens were off by 2.9 %
+  // of their outputs' norm at D = 128 and 8.9 % at D = 64, now 0.18 and 0.21 %; compiled
+  // into the short launches it costs them 1 to 3 %.)
+  __device__ __forceinline__ void settle() {
+    static_assert(LONG, "the means would be lost");
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float a = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) a += fmaf(acc[c][k], 16.f, acc[c][2 + k]);
+      a *= 8.f / D;
+      taken[k] += a;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        acc[c][k] = fmaf(a, -0.0625f, acc[c][k]);
+        acc[c][2 + k] -= a;
+      }
+    }
+  }
+  // factors of the columns 2 tig and 2 tig + 1
+  __device__ __forceinline__ void rescale(float fa, float fb) {
+    scale_acc<D>(acc, fa, fb);
+    if constexpr (LONG) {
+      taken[0] *= fa;
+      taken[1] *= fb;
+    }
   }
 
   static __device__ __forceinline__ float hi16(uint32_t w) {
@@ -274,7 +309,7 @@ struct Warp4 {
 #pragma unroll
         for (int g = 0; g < NG; ++g) z[h][g] *= alpha[h];
       }
-      scale_acc<D>(acc, f[0], f[H - 1]);  // columns 2 tig and 2 tig + 1 are the lane's heads
+      rescale(f[0], f[H - 1]);  // the columns are the lane's heads
     }
     // V's parameters of the lane's tokens of block u (hidden ones count nothing)
     auto load_v = [&](int u, uint32_t(&w0)[NG], uint32_t(&w1)[NG]) {
@@ -348,7 +383,7 @@ struct Warp4 {
         f[h] = vb[h] * reciprocal(nb);
         vb[h] = nb;
       }
-      scale_acc<D>(acc, f[0], f[H - 1]);
+      rescale(f[0], f[H - 1]);
 #pragma unroll
       for (int u = 0; u < NB; ++u) {
         uint32_t w0[NG], w1[NG];
@@ -399,8 +434,13 @@ struct Warp4 {
         const int g = c / 4;
         const int col = G == 8 ? h : g;  // 2 tig or 2 tig + 1
         // (the codes' 2^-24 and 2^-20 first: a unit may be near the largest float)
-        v[2 * c * H + h] = fmaf(acc[c][col] * 0x1p24f, vb[h], z[h][g]);
-        v[(2 * c + 1) * H + h] = fmaf(acc[c][2 + col] * 0x1p20f, vb[h], z[h][g]);
+        float a = acc[c][col] * 16.f, b = acc[c][2 + col];
+        if constexpr (LONG) {
+          a += taken[col];
+          b += taken[col];
+        }
+        v[2 * c * H + h] = fmaf(a * 0x1p20f, vb[h], z[h][g]);
+        v[(2 * c + 1) * H + h] = fmaf(b * 0x1p20f, vb[h], z[h][g]);
       }
     }
   }

@@ -205,3 +205,22 @@ def test_int4_long_contexts_by_norm(ctx, hq, hkv, d):
     for how, got in _ways(q, pools, tables, ctx, 0.088, (1024, 4096)):
         off = np.linalg.norm(got - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
         assert (off <= 7.8e-3).all(), f"{how}: off by {off.max():.2e} of the output"
+
+
+@pytest.mark.parametrize("d,hq,hkv,n", [(128, 4, 1, 100000), (64, 2, 1, 100000),
+                                        (128, 8, 1, 40000)])
+def test_int4_whole_long_contexts_by_norm(d, hq, hkv, n):
+    """One warp's sums over thousands of tokens: 7.8e-3 of each output's norm, as above
+    (the MMA's truncation in runs of 32 steps of 64 tokens at most, so 1e-5 again, of
+    outputs of 0.005: 2e-3 instead of 5e-4), together 9.3e-3."""
+    rng = np.random.default_rng(n + d)
+    nb = -(-n // 16)
+    pools = [pack(*_normal(rng, nb, hkv, d), v) for v in (False, True)]
+    q = normal_bf16(rng, (1, hq, d))
+    tables = rng.permutation(nb)[None]
+    scale = d ** -0.5
+    ref = O4.decode(bf16_bits_to_f64(q), pool_values(pools[0], d, False),
+                    pool_values(pools[1], d, True), tables, [n], scale)
+    for how, got in _ways(q, pools, tables, [n], scale, (8192, 16384, 131072)):
+        off = np.linalg.norm(got - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+        assert (off <= 9.3e-3).all(), f"{how}: off by {off.max():.2e} of the output"
