@@ -1178,6 +1178,10 @@ class DecodeStep:
             self.split = bool(split)
             B, hq, d = q.shape
             hkv = k_cache.shape[1]
+            if window < 0:
+                raise ValueError("DecodeStep: window must not be negative")
+            # what a step with a window reads at most: the window, from a block's start
+            cover = min(int(window) + block - 1, block_tables.shape[1] * block)
             made = workspace is None or counters is None  # on the stream that is current now
             if self.split and host_context_lens is not None and partition_size is None:
                 # chosen for these contexts (plan_decode_step): the partition
@@ -1191,10 +1195,10 @@ class DecodeStep:
                         "bf16-biased" if ruled else "bf16")
                 if max_context_len is None:
                     max_context_len = block_tables.shape[1] * block
-                if window:  # what a step reads: the window, from a block's start
+                if window:
                     import numpy as np
-                    host_context_lens = np.minimum(host_context_lens, int(window) + block - 1)
-                    max_context_len = min(int(max_context_len), int(window) + block - 1)
+                    host_context_lens = np.minimum(host_context_lens, cover)
+                    max_context_len = min(int(max_context_len), cover)
                 plan = plan_decode_step(
                     host_context_lens, hq, hkv, d, kind,
                     torch.cuda.get_device_properties(q.device).multi_processor_count,
@@ -1210,7 +1214,7 @@ class DecodeStep:
                     mc = (int(max_context_len) if max_context_len is not None
                           else block_tables.shape[1] * block)
                     if window:
-                        mc = min(mc, int(window) + block - 1)
+                        mc = min(mc, cover)
                     workspace = splitk_workspace(B, hq, d, mc, partition_size, q.device)
                 if counters is None:
                     counters = step_counters(B, hkv, q.device)

@@ -181,3 +181,29 @@ def test_prepared_steps_of_the_plain_caches(kind, part):
     assert pa.pa_get_device_error() == 0
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("window", [1, 300, 2 ** 31 - 1])
+@pytest.mark.parametrize("as_lens", [list, lambda x: np.asarray(x, dtype=np.int32),
+                                     lambda x: np.asarray(x, dtype=np.int64)])
+def test_handles_plan_for_any_window(window, as_lens):
+    case = _case(47, [(c - 1, 1) for c in (500, 17, 900)], 8, 2, 128, window)
+    ctx, n, tables, kc, vc, q = case
+    out = torch.empty(3, 8, 128, dtype=torch.bfloat16, device="cuda")
+    step = pa.DecodeStep(None, None, dev_bf16(kc), dev_bf16(vc), None, dev_bf16(q),
+                         _dev(tables, np.int32), _dev(ctx, np.int32), out, 0.088,
+                         partition_size=None, host_context_lens=as_lens(ctx), window=window)
+    step()
+    assert_close(bf16_to_f64(out), OB.batch(q, kc, vc, tables, ctx, n, 0.088, window=window),
+                 f"window {window}")
+
+
+def test_handles_refuse_a_negative_window():
+    ctx, n, tables, kc, vc, q = _case(48, [(9, 1)], 8, 2)
+    for window in (-1, -100):
+        for ps in (None, 64):
+            with pytest.raises(ValueError, match="window"):
+                pa.DecodeStep(None, None, dev_bf16(kc), dev_bf16(vc), None, dev_bf16(q),
+                              _dev(tables, np.int32), _dev(ctx, np.int32), torch.empty_like(
+                                  dev_bf16(q)), 0.1, partition_size=ps, host_context_lens=[10],
+                              window=window)
