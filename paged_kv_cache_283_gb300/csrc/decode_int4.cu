@@ -1,9 +1,10 @@
 // The paged decode kernel (decode_kernel.cuh) over a 4-bit cache.
 //
-// At 4.5 bits a value the bytes come in faster than a warp's instructions take
-// them: a step of 32 tokens for 4 heads is 352 instructions (Warp4), a third of
-// them the unpacking of codes, and short batches are bounded by a launch's head
-// and tail.  Measured, in us, with the time at the copy rate: 64 contexts of 128
+// At 4.5 bits a value the bytes come in faster than a warp's steps take them: one of
+// 32 tokens for 4 heads is some 350 instructions (Warp4), a third of them the
+// unpacking of codes, in dependent chains (scores, maximum, weights, products) that
+// three or four warps a scheduler do not hide: issue slots 43 to 52 % used, the tensor
+// pipe 18 to 27 %.  Short batches are bounded by a launch's head and tail.  Measured, in us, with the time at the copy rate: 64 contexts of 128
 // to 2016 tokens (32 query / 8 KV heads, D = 128) 19.9 (11.7); 256 of up to 4094
 // with groups of 8 113.9 (91); 8 of up to 49,796 41.6 (33.0).
 

@@ -317,7 +317,7 @@ __device__ __forceinline__ float max_abs(const uint32_t (&v)[HK]) {
 // special-function operations a score, to 2e-7 of the cap.  A masked score, -inf,
 // stays one: the last coefficients are positive.  16 x 512 new tokens after up to
 // 3450 (32 query / 8 KV heads; uncapped 328 us): every score near 372, mid 403, far
-// 507.  Packed multiply-adds have the rate of two single ones, so mid without near
+// 507 (on another GPU near 385, far 523).  Packed multiply-adds have the rate of two single ones, so mid without near
 // makes the small scores 395; near and far alone 366 and 522, which leaves scores
 // past a fifth of the cap at 522 (both with maxima taken score by score, 375, 403
 // and 537 in the form above).
@@ -840,19 +840,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             tmem_ld32(tS + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * h));
           tmem_wait_ld();
           if constexpr ((RULE & kCap) != 0) {
-            // the curve goes by the visible scores alone: hidden places, and slots
-            // that no copy filled, may hold anything
-            if (masked) {
+            // The curve goes by the visible scores alone: hidden places, and slots that
+            // no copy filled, may hold anything.  (Costs the step with a cap alone
+            // nothing, the one with a bias too 5 %: 412 -> 430 us.)
+            if (masked) {  // visible: low <= j <= lim
+              const bool none = lim < low;
+              const uint32_t first = none ? 1u : static_cast<uint32_t>(-low);
+              const uint32_t span = none ? 0u : static_cast<uint32_t>(lim - low);
 #pragma unroll
-              for (int h = 0; h < HK; h += 32) {
-                const int top_bit = lim - h, low_bit = low - h;
-                const uint32_t seen =
-                    (top_bit >= 31 ? ~0u : top_bit < 0 ? 0u : (2u << top_bit) - 1u) &
-                    (low_bit <= 0 ? ~0u : low_bit > 31 ? 0u : ~0u << low_bit);
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!(seen >> j & 1u)) sv[h + j] = 0u;
-              }
+              for (int j = 0; j < HK; ++j)
+                if (first + j > span) sv[j] = 0u;
             }
           }
           const float mabs = max_abs<HK>(sv);
