@@ -16,6 +16,10 @@
  *   pa_rope_reshape_and_cache*  rotary embedding of q and k and the cache write
  *   pa_prefill             causal attention of chunks of new tokens (prefill)
  *   *_biased               decode and prefill with capped / biased / windowed scores
+ *   pa_cross_attention     attention to paged source states (encoder-decoder)
+ *   pa_read_cache          positions of a cache of any type read back as bf16
+ *   pa_beam_select         beam search's selection over beams and vocabulary
+ *   pa_reorder_states      states of the beams moved to where their parents went
  *   pa_alloc_*             fixed-size block allocator with reference counts,
  *                          copy-on-write and automatic prefix caching (host
  *                          only, never on the GPU path)
@@ -105,6 +109,8 @@ typedef enum {
 #define PA_DEVERR_ORDER 0x10u       /* a work-order entry outside [0, num_seqs * max_partitions) */
 #define PA_DEVERR_PREFIX 0x20u      /* a sequence does not hold the prefix it was given */
 #define PA_DEVERR_POSITION 0x40u    /* a position outside the cosine / sine table */
+#define PA_DEVERR_PARENT 0x80u      /* a parent outside its group of beams */
+#define PA_DEVERR_LOGITS 0x100u     /* a NaN or +inf logit or beam score */
 
 /* Static description of a status code; never NULL. */
 const char* pa_status_string(pa_status status);
@@ -674,6 +680,148 @@ pa_status pa_prefill_biased(void* out, const void* q, const void* k_cache, const
                             pa_stream_t stream);
 
 /*
+ * Cross attention: the queries of each sequence attend to all of its source's
+ * states, an encoder's K and V that lie in a paged cache (written by
+ * pa_reshape_and_cache like a context's).  With S = source_lens[b]
+ *   out[t, h] = sum_{j < S} softmax_j(scale * dot(q[t, h], K_j)) V_j
+ * whatever the query's position; S has nothing to do with the number of queries.
+ * S = 0 gives zeros.  One call takes decoder prompts, single steps or a step of
+ * several beams: the beams of one source are its sequence's queries, and each
+ * K / V tile is read once for all of them (for 128 (query, head) pairs of a KV
+ * head at a time).
+ *   q               : [T, Hq, head_dim] bf16, tokens q_stride elements apart (a
+ *                     multiple of 8, >= Hq * head_dim); out [T, Hq, head_dim],
+ *                     not overlapping q; T = total_query_tokens.
+ *   query_start_loc : [num_seqs + 1] int32 (device), sequence b's rows are
+ *                     query_start_loc[b] .. query_start_loc[b+1] - 1.  Rows of
+ *                     no sequence are not written.
+ *   max_query_len   : host bound on every sequence's rows (further ones are not
+ *                     computed).
+ *   source_lens     : [num_seqs] int32 (device).
+ *   ws_out, ws_ml   : workspace, fp32 [ws_ctas * 2 * R * head_dim] and
+ *                     [ws_ctas * 2 * R * 2], R = pa_cross_attention_rows(
+ *                     max_query_len, Hq / Hkv).
+ *   counters        : [ws_ctas], zero before the first call; each call leaves
+ *                     them zero.  Calls that may run at the same time (two
+ *                     streams, two replayed graphs) must not share workspace or
+ *                     counters.
+ *   ws_ctas         : how many CTAs the call may use, >= 1; pa_cross_attention_ctas(
+ *                     num_sms) fills the GPU.
+ * Runs on the tensor cores (bf16 in, fp32 accumulate; the softmax weights enter
+ * the PV product rounded to bf16, their sum is taken before).  V of a source
+ * position must be finite; what the cache holds past the source changes nothing.
+ * head_dim 64 or 128, block_size 16, Hq / Hkv in {1, 2, 4, 8} (else
+ * PA_ERR_UNSUPPORTED_SHAPE), scale > 0.  Device-side checks: 0 <= S <=
+ * max_blocks_per_seq * 16 and rows within T (else PA_DEVERR_CONTEXT_LEN and the
+ * sequence is skipped); bad block ids as pa_decode.  Asynchronous on `stream`.
+ */
+int pa_cross_attention_supported(int head_dim, int group, int block_size);
+int pa_cross_attention_ctas(int num_sms);
+int pa_cross_attention_rows(int max_query_len, int group);
+pa_status pa_cross_attention(void* out, const void* q, int64_t q_stride, const void* k_cache,
+                             const void* v_cache, const int32_t* block_tables,
+                             int max_blocks_per_seq, const int32_t* source_lens,
+                             const int32_t* query_start_loc, int max_query_len, int num_seqs,
+                             int total_query_tokens, int num_q_heads, int num_kv_heads,
+                             int head_dim, int block_size, int num_blocks, float scale,
+                             float* ws_out, float* ws_ml, unsigned* counters, int ws_ctas,
+                             pa_stream_t stream);
+
+/*
+ * Reads positions of a cache back as bf16: the inverse of the cache writes.  Row
+ * r = row_start_loc[b] + i of sequence b (r < row_start_loc[b + 1]) is its
+ * position first_positions[b] + i (first_positions NULL: i): K to row r of k_out,
+ * V to row r of v_out.  INT8 and FP8 values are code * scale, 4-bit ones offset +
+ * scale * code, in fp32, rounded once to bf16.  What a quantised prompt's next
+ * chunk needs: its prefix read into a bf16 cache, over which pa_prefill runs.
+ *   kv_kind         : 0 = bf16 cache, 1 = INT8, 2 = FP8 (with k_scales,
+ *                     v_scales), 4 = 4-bit; pools as the cache writes'.
+ *   block_tables    : [num_seqs, max_blocks_per_seq] int32 (device); first_positions
+ *                     [num_seqs] int32, row_start_loc [num_seqs + 1] int32 (device).
+ *   max_rows        : host bound on every sequence's rows (further ones are not
+ *                     read, PA_DEVERR_CONTEXT_LEN); total_rows: rows of the outputs.
+ *   slot_mapping    : NULL: k_out, v_out are [total_rows, Hkv, head_dim] bf16, rows
+ *                     out_stride elements apart (a multiple of 8, >= Hkv *
+ *                     head_dim).  Else int64 [total_rows] (device) and k_out, v_out
+ *                     are bf16 pools [num_out_blocks, Hkv, 16, head_dim]: row r goes
+ *                     to slot slot_mapping[r] (negative: nowhere; past the pool:
+ *                     PA_DEVERR_SLOT, nowhere).  Distinct rows, distinct slots.
+ * The outputs must not overlap the pools.  head_dim 64 or 128, block_size 16 (else
+ * PA_ERR_UNSUPPORTED_SHAPE); num_seqs <= 65535.  Device-side checks: row ranges
+ * within total_rows and positions within the table's capacity (else
+ * PA_DEVERR_CONTEXT_LEN and the sequence is skipped); bad block ids as pa_decode.
+ * Asynchronous on `stream`.
+ */
+pa_status pa_read_cache(int kv_kind, void* k_out, void* v_out, int64_t out_stride,
+                        const void* k_cache, const void* v_cache, const float* k_scales,
+                        const float* v_scales, const int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* first_positions,
+                        const int32_t* row_start_loc, int max_rows, int num_seqs, int total_rows,
+                        const int64_t* slot_mapping, int num_out_blocks, int num_kv_heads,
+                        int head_dim, int block_size, int num_blocks, pa_stream_t stream);
+
+/*
+ * Beam search's selection.  Each of num_searches searches has num_beams beams;
+ * beam w of search b is row r = b * num_beams + w of logits and scores.  Its
+ * continuations' totals are
+ *   scores[r] + logits[r, v] - log sum_u exp(logits[r, u]),  0 <= v < vocab
+ * and a finished beam (finished[r] != 0) has one continuation, eos_token, with
+ * total scores[r].  Totals are compared in 64 bits.  The num_keep largest of a
+ * search, largest first (equal ones: the lower beam first, of one beam the larger
+ * logit, then the lower token), go to
+ *   scores_out  [num_searches, num_keep] fp32,
+ *   parents_out [num_searches, num_keep] int32: the row r that it continues,
+ *   tokens_out  [num_searches, num_keep] int32,
+ *   finished_out (may be NULL) uint8: the beam was finished, or the token is
+ *               eos_token.
+ * A logit of -inf is no continuation; a row of
+ * nothing else, or a beam whose score is -inf, has none.  A NaN or +inf logit, or
+ * such a score, sets PA_DEVERR_LOGITS and counts as -inf.  Where a search has fewer
+ * continuations than num_keep, the rest get score -inf, parent and token -1, not
+ * finished.
+ *   flags: 0, or PA_BEAM_IN_PLACE (num_keep == num_beams): entry i of a search is
+ *     its place i, and a beam that goes on keeps its place: the best continuation
+ *     of beam w stands at place w, every other one, in order, at the first place
+ *     left, and those missing after them.  Then pa_reorder_states with these
+ *     parents moves the forks only.
+ *   logits : [num_searches * num_beams] rows of vocab elements, row_stride elements
+ *     apart (>= vocab), dtype 0 = bf16, 1 = fp16, 2 = fp32; aligned to their type.
+ *   finished: uint8 (may be NULL: none is); eos_token: a token, or -1: none ends
+ *     (no beam may be finished then).
+ *   ws: workspace of pa_beam_select_workspace_bytes(...) bytes (0: unsupported),
+ *     16-byte aligned; counters: [num_searches], zero before the first call; each
+ *     call leaves them zero.  Calls that may run at the same time must not share
+ *     them.
+ * scores_out may be scores and finished_out finished (num_keep == num_beams).
+ * num_beams <= 32, num_keep <= 64, vocab <= 2^27, num_searches * num_beams <= 65535
+ * (else PA_ERR_UNSUPPORTED_SHAPE).  Asynchronous on `stream`.
+ */
+#define PA_BEAM_IN_PLACE 0x1
+size_t pa_beam_select_workspace_bytes(int num_searches, int num_beams, int num_keep, int vocab,
+                                      int dtype);
+pa_status pa_beam_select(float* scores_out, int32_t* parents_out, int32_t* tokens_out,
+                         uint8_t* finished_out, const void* logits, int64_t row_stride, int dtype,
+                         const float* scores, const uint8_t* finished, int eos_token,
+                         int num_searches, int num_beams, int num_keep, int vocab, void* ws,
+                         unsigned* counters, int flags, pa_stream_t stream);
+
+/*
+ * Moves states to where the beams' parents went, in place: row i of every tensor
+ * becomes what row parents[i] was before the call.  states: host array of
+ * num_tensors device pointers, each num_groups * num_beams rows of row_bytes bytes,
+ * row_stride bytes apart (>= row_bytes); parents: [num_groups * num_beams] int32
+ * (device), row numbers.  A row's parent lies in its own group of num_beams rows
+ * (rows g * num_beams ..; else PA_DEVERR_PARENT and the row is left); a negative
+ * parent, or its own, leaves the row as it is.  Rows may be of any type: block
+ * tables, recurrent states, token histories.  Only changed rows and their parents
+ * are touched.  num_beams <= 32, num_groups <= 65535 (else
+ * PA_ERR_UNSUPPORTED_SHAPE).  Asynchronous on `stream`; up to 64 tensors a launch.
+ */
+pa_status pa_reorder_states(void* const* states, int num_tensors, const int32_t* parents,
+                            int num_groups, int num_beams, int64_t row_bytes, int64_t row_stride,
+                            pa_stream_t stream);
+
+/*
  * Prepared calls: a call on fixed device buffers checked once and launched many
  * times.  pa_prepare_* takes the arguments of the call without the stream, checks
  * them as the call does, and on PA_OK leaves an object in *prepared (on an error
@@ -707,6 +855,29 @@ pa_status pa_prepare_prefill(
     const int32_t* query_start_loc, int max_query_len, int num_seqs, int total_query_tokens,
     int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
     float softcap, const float* alibi_slopes, int window, const int32_t* prefix_lens);
+pa_status pa_prepare_cross_attention(
+    pa_prepared** prepared, void* out, const void* q, int64_t q_stride, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* source_lens, const int32_t* query_start_loc, int max_query_len, int num_seqs,
+    int total_query_tokens, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+    int num_blocks, float scale, float* ws_out, float* ws_ml, unsigned* counters, int ws_ctas);
+pa_status pa_prepare_read_cache(pa_prepared** prepared, int kv_kind, void* k_out, void* v_out,
+                                int64_t out_stride, const void* k_cache, const void* v_cache,
+                                const float* k_scales, const float* v_scales,
+                                const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* first_positions, const int32_t* row_start_loc,
+                                int max_rows, int num_seqs, int total_rows,
+                                const int64_t* slot_mapping, int num_out_blocks,
+                                int num_kv_heads, int head_dim, int block_size, int num_blocks);
+pa_status pa_prepare_beam_select(pa_prepared** prepared, float* scores_out, int32_t* parents_out,
+                                 int32_t* tokens_out, uint8_t* finished_out, const void* logits,
+                                 int64_t row_stride, int dtype, const float* scores,
+                                 const uint8_t* finished, int eos_token, int num_searches,
+                                 int num_beams, int num_keep, int vocab, void* ws,
+                                 unsigned* counters, int flags);
+pa_status pa_prepare_reorder_states(pa_prepared** prepared, void* const* states, int num_tensors,
+                                    const int32_t* parents, int num_groups, int num_beams,
+                                    int64_t row_bytes, int64_t row_stride);
 pa_status pa_run(const pa_prepared* prepared, pa_stream_t stream);
 void pa_prepared_destroy(pa_prepared* prepared);
 
@@ -809,6 +980,14 @@ pa_status pa_alloc_reserve(pa_alloc* a, int seq_id, int num_tokens,
 /* child_id becomes a copy of parent_id sharing all its blocks (+1 reference
  * each).  PA_ERR_INVALID_ARG if parent is unknown or child exists. */
 pa_status pa_alloc_fork(pa_alloc* a, int parent_id, int child_id);
+
+/* A beam search's step: the n distinct sequences seq_ids[i] become copies of what
+ * seq_ids[parents[i]] were before the call (parents[i] in [0, n); negative: seq_ids[i]
+ * keeps its own), sharing their parent's blocks.  A block that no sequence holds any
+ * more returns to the free tail, in the order of the sequences that held it and their
+ * logical order (cached-but-evictable blocks as pa_alloc_free_seq's).  A later append
+ * into a shared, partly filled block copies it on write. */
+pa_status pa_alloc_reorder(pa_alloc* a, const int* seq_ids, const int32_t* parents, int n);
 
 /* Drops the sequence; blocks whose count reaches 0 return to the free tail. */
 pa_status pa_alloc_free_seq(pa_alloc* a, int seq_id);

@@ -157,6 +157,26 @@ class BlockAllocatorModel:
         for blk in self.tables[child]:
             self.ref[blk] += 1
 
+    def reorder(self, seqs, parents):
+        """The sequences become copies of their parents (entries of ``seqs``;
+        negative: unchanged), all at once."""
+        seqs = list(seqs)
+        if len(set(seqs)) != len(seqs):
+            raise InvalidArg("a sequence appears twice")
+        for s, p in zip(seqs, parents):
+            self._check(s)
+            if p >= len(seqs):
+                raise InvalidArg(f"no parent {p}")
+        new = {s: (list(self.tables[seqs[p]]), self.lens[seqs[p]])
+               for s, p in zip(seqs, parents) if p >= 0 and seqs[p] != s}
+        for table, _ in new.values():
+            for blk in table:
+                self.ref[blk] += 1
+        for s, (table, n) in new.items():
+            for blk in self.tables[s]:
+                self._release(blk)
+            self.tables[s], self.lens[s] = table, n
+
     def free_seq(self, seq):
         """Drop the sequence; blocks whose count reaches zero go to the free tail."""
         self._check(seq)

@@ -21,9 +21,11 @@ LIB = os.path.join(HERE, "libpa.so")
 
 SOURCES = ["api.cu", "decode.cu", "decode_int4.cu", "decode_biased.cu",
            "splitk_reduce.cu", "reshape_and_cache.cu", "rope_append.cu", "copy_blocks.cu", "noalloc.cu",
+           "cross_attention.cu", "read_cache.cu", "reorder_states.cu", "beam_select.cu",
            "prefill.cu", "prefill_biased.cu", "allocator.cpp", "sha256.cpp", "scheduler.cpp", "splitk_plan.cpp"]
 HEADERS = [os.path.join(ROOT, "include", "pa.h"), os.path.join(CSRC, "internal.h"),
-           os.path.join(CSRC, "device.cuh"), os.path.join(CSRC, "decode_tile.cuh"),
+           os.path.join(CSRC, "device.cuh"), os.path.join(CSRC, "tensor.cuh"),
+           os.path.join(CSRC, "decode_tile.cuh"),
            os.path.join(CSRC, "decode_tile4.cuh"),
            os.path.join(CSRC, "decode_kernel.cuh"), os.path.join(CSRC, "prefill_kernel.cuh"),
            os.path.join(CSRC, "int4_row.cuh"),

@@ -30,6 +30,7 @@
 #include <string>
 #include <unordered_map>
 #include <unordered_set>
+#include <utility>
 #include <vector>
 
 #include "../../include/pa.h"
@@ -252,6 +253,32 @@ pa_status pa_alloc_fork(pa_alloc* a, int parent_id, int child_id) {
   Sequence c = *p;
   for (int32_t b : c.table) a->refs[b] += 1;
   a->seqs.emplace(child_id, std::move(c));
+  return PA_OK;
+}
+
+pa_status pa_alloc_reorder(pa_alloc* a, const int* seq_ids, const int32_t* parents, int n) {
+  if (!a || n < 0 || (n > 0 && (!seq_ids || !parents))) return PA_ERR_INVALID_ARG;
+  try {
+    std::unordered_set<int> distinct;
+    std::vector<Sequence*> ptrs(n);
+    for (int i = 0; i < n; ++i) {
+      if (!distinct.insert(seq_ids[i]).second || parents[i] >= n) return PA_ERR_INVALID_ARG;
+      ptrs[i] = a->find(seq_ids[i]);
+      if (!ptrs[i]) return PA_ERR_INVALID_ARG;
+    }
+    std::vector<std::pair<int, Sequence>> changed;  // what they become
+    for (int i = 0; i < n; ++i)
+      if (parents[i] >= 0 && parents[i] != i) changed.emplace_back(i, *ptrs[parents[i]]);
+    // the new holders first, so that no block that goes on is given back between
+    for (const auto& c : changed)
+      for (int32_t b : c.second.table) a->refs[b] += 1;
+    for (auto& c : changed) {
+      for (int32_t b : ptrs[c.first]->table) a->release(b);
+      *ptrs[c.first] = std::move(c.second);
+    }
+  } catch (const std::bad_alloc&) {
+    return PA_ERR_INVALID_ARG;
+  }
   return PA_OK;
 }
 

@@ -1,0 +1,1015 @@
+// Cross attention over paged source states on the 5th-generation tensor cores,
+// sm_103a: decoder queries (prompts, or the beams of a step) against an
+// encoder's K and V, which lie in a paged cache like a context's.
+//
+//   out[t, h] = sum_j softmax_j(scale q[t, h] . K_j) V_j,  0 <= j < source_lens[b]
+//
+// Every query of a sequence sees the whole source, whatever its position, and
+// the source's length has nothing to do with the number of queries.
+//
+// Design:
+//  * A tile is 128 query rows, (token, head) pairs of one GQA group, so the
+//    beams of a source and the heads of a group share each K / V tile: a step of
+//    W beams reads its source once per KV head, not W times.  S = Q K^T and
+//    O += P V are tcgen05.mma with S, P and O in tensor memory; K and V arrive
+//    per 16-token block by TMA (the block table is a gather of 16-row boxes), 64
+//    keys a chunk.
+//  * The batch's work, all (sequence, KV head, tile) units' chunks of keys one after
+//    another, is cut evenly among persistent CTAs (two an SM: 4 softmax warps, a
+//    row a thread, a warp each for the MMAs of Q K^T and of P V and for the copies
+//    of K and of V: a warp's waits take it longer than what it waits to issue), each taking one run of chunks
+//    whatever units it begins and ends in: ragged sources, few long ones and many
+//    short ones all keep every SM busy to the end.  The lengths are read on the
+//    device, so a captured call follows them.  The warps walk their CTA's run on
+//    their own, the copy warps ahead of the others, so that the next unit's first
+//    tiles are on their way while the last one's are used.
+//  * A unit that several CTAs share is joined by the last of them to arrive: each
+//    leaves its rows' (m, l, o) in the workspace, where a CTA has two places, one
+//    for the unit it begins in and one for the unit it ends in.
+//  * The softmax takes a chunk's weights against the row's reference maximum
+//    first; only where their sum says that the reference could be 2^8 too low
+//    are the chunk's maxima taken and O rescaled in tensor memory.
+//  * The weights enter P V as bf16, rounded to nearest, their sum is taken
+//    before the rounding, in fp32.  Each weight is then off by up to 2^-9 of
+//    itself, as if its score were off by 2^-9 -- less than what the rounding of
+//    q and K to bf16 moves scores by -- and an output by at most 2^-9 of the
+//    weighted mean of |V|, which its own rounding to bf16 doubles.
+//  * Warps whose rows are all past the tile's queries (a step of few beams) do
+//    no work but keep the barriers' counts.
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "../../include/pa.h"
+#include "device.cuh"
+#include "internal.h"
+#include "tensor.cuh"
+
+namespace pa {
+
+struct CrossParams {
+  __nv_bfloat16* out;           // [T, Hq, D]
+  const int32_t* block_tables;
+  const int32_t* source_lens;
+  const int32_t* query_start;
+  float* ws_o;                  // [CTAs, 2, ws_rows, D]
+  float2* ws_ml;                // [CTAs, 2, ws_rows]: reference maximum (base 2), sum
+  unsigned* counters;           // [CTAs]
+  unsigned* err;
+  int max_blocks_per_seq;
+  int num_seqs;
+  int num_q_heads;
+  int num_kv_heads;
+  int num_blocks;
+  int total_q;
+  int max_query_len;
+  int group;
+  int tile_tokens;              // 128 / group
+  int ws_rows;                  // rows of a tile that can hold queries
+  float scale_log2;
+};
+
+namespace {
+
+constexpr int kRows = 128;    // query rows per tile = MMA M
+constexpr int kKeys = 64;     // keys per chunk = MMA N of S = Q K^T
+constexpr int kBS = 16;       // tokens per cache block
+constexpr int kChunkBlocks = kKeys / kBS;
+constexpr int kSoftmaxThreads = 128;
+constexpr int kThreads = kSoftmaxThreads + 128;
+constexpr int kScoreWarp = 4, kMixWarp = 5, kCopyWarp = 6;  // Q K^T, P V, copies of K and of V
+constexpr int kMinChunks = 4;  // of a unit's part, on average: less is not worth a join
+constexpr int kMaxParts = 64;  // CTAs that share a unit, on average at most
+constexpr uint32_t kTO = 2 * kKeys;     // O's first column, after two S buffers
+constexpr uint32_t kTmemCols = 256;
+#ifndef PA_CROSS_P_PARTS
+#define PA_CROSS_P_PARTS 2
+#endif
+constexpr int kPParts = PA_CROSS_P_PARTS;
+
+template <int D>
+struct Shape {
+  static constexpr int kHalves = D / 64;                // 64-column halves of a row
+  static constexpr int kQHalf = kRows * 128;            // bytes of a half of Q
+  static constexpr int kKVHalf = kKeys * 128;           // of a K or V chunk
+  static constexpr int kBox = kBS * 128;                // of a block
+  static constexpr int kStage = kHalves * kKVHalf;
+  static constexpr int kStages = D == 128 ? 2 : 4;      // chunks in the K and V rings
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + kHalves * kQHalf;
+  static constexpr int kV = kK + kStages * kStage;
+  static constexpr int kBar = kV + kStages * kStage;
+  static constexpr int kSmem = kBar + 256 + 1024;       // + alignment
+  static constexpr uint32_t kIdescQK = idesc_bf16(kRows, kKeys, 0, 0);
+  static constexpr uint32_t kIdescPV = idesc_bf16(kRows, D, 0, 1);
+  static_assert(kTO + D <= kTmemCols, "tensor memory");
+  static_assert(2 * kSmem <= 232448, "two CTAs an SM");
+};
+
+// A sequence's lengths, read and checked on the device.
+struct Seq {
+  int q0, n;     // its rows; 0 for one that is skipped
+  int src;       // source length
+  int chunks;    // of keys
+  int tiles;     // of queries
+  bool bad;
+};
+__device__ __forceinline__ Seq read_seq(const CrossParams& p, int b) {
+  Seq s;
+  s.q0 = __ldg(p.query_start + b);
+  const int q1 = __ldg(p.query_start + b + 1);
+  s.src = __ldg(p.source_lens + b);
+  s.bad = s.q0 < 0 || q1 < s.q0 || q1 > p.total_q || s.src < 0 ||
+          s.src > p.max_blocks_per_seq * kBS;
+  s.n = s.bad ? 0 : min(q1 - s.q0, p.max_query_len);
+  s.chunks = s.bad ? 0 : (s.src + kKeys - 1) / kKeys;
+  s.tiles = (s.n + p.tile_tokens - 1) / p.tile_tokens;
+  return s;
+}
+
+// a / b of non-negative numbers, most of which fit 32 bits (a 64-bit division
+// takes ten times as long).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// The list of units is ordered in pairs (tile, sequence), the tile the slower
+// (kTileMajor), each with its KV heads: runs that begin at different tiles then
+// pass the same keys at the same time, and a source larger than L2 is read from
+// memory once for all its tiles, not once for each (16 x 512 queries on sources
+// of 94 MB ... see the launch).  With more pairs than a CTA looks through in a few
+// microseconds the pairs are the sequences, each with its heads and their tiles.
+constexpr int kMostPairs = 64 * kThreads;
+
+struct Order {
+  int num_seqs;
+  int pairs;
+  bool tile_major;
+  __device__ int seq(int pair) const { return tile_major ? pair % num_seqs : pair; }
+  __device__ int tile0(int pair) const { return tile_major ? pair / num_seqs : 0; }
+  // tiles of a pair, from tile0 on
+  __device__ int span(int pair, const Seq& s) const {
+    return tile_major ? s.tiles > tile0(pair) : s.tiles;
+  }
+  __device__ int64_t work(const CrossParams& p, int pair, const Seq& s) const {
+    return static_cast<int64_t>(s.chunks) * span(pair, s) * p.num_kv_heads;
+  }
+};
+
+// What all CTAs agree on, and where this one's run begins.
+struct Run {
+  Order order;
+  int ctas;          // that take part
+  int64_t total;     // chunks of all units
+  int64_t most;      // a run has this many chunks, from CTA `rest` on one less
+  int rest;
+  int pair;          // of the first chunk,
+  int kvh, inner;    // its unit (tile0 + inner),
+  int first;         // and its place in the unit's keys
+  int64_t left;      // chunks of this run
+  int64_t unit;      // position of the first unit's first chunk
+};
+
+// CTA whose run holds chunk `at`.
+__device__ __forceinline__ int owner(const Run& r, int64_t at) {
+  const int64_t longer = r.rest * r.most;
+  if (at < longer) return static_cast<int>(quotient(at, r.most));
+  return r.rest + static_cast<int>(quotient(at - longer, r.most - 1));
+}
+
+// A part of a unit: chunks [first, first + count) of its keys.
+struct Part {
+  int b, kvh, i0;
+  Seq seq;
+  int first, count;
+  int64_t unit;      // position of the unit's first chunk
+};
+
+struct Walk {
+  const Order& order;  // (in shared memory)
+  int64_t left, unit;
+  int pair, kvh, inner, first, span;
+  Seq seq;
+  __device__ Walk(const CrossParams& p, const Run& r)
+      : order(r.order), left(r.left), unit(r.unit), pair(r.pair), kvh(r.kvh), inner(r.inner),
+        first(r.first), span(0) {
+    if (left > 0) enter(p);
+  }
+  __device__ void enter(const CrossParams& p) {
+    seq = read_seq(p, order.seq(pair));
+    span = order.span(pair, seq);
+  }
+  __device__ bool next(const CrossParams& p, Part& t) {
+    if (left <= 0) return false;
+    while (span == 0 || seq.chunks == 0 || kvh == p.num_kv_heads) {
+      kvh = inner = 0;
+      if (++pair >= order.pairs) {  // (the run ends within the units)
+        left = 0;
+        return false;
+      }
+      enter(p);
+    }
+    t.b = order.seq(pair);
+    t.kvh = kvh;
+    t.i0 = (order.tile0(pair) + inner) * p.tile_tokens;
+    t.seq = seq;
+    t.unit = unit;
+    t.first = first;
+    t.count = static_cast<int>(min(static_cast<int64_t>(seq.chunks - first), left));
+    left -= t.count;
+    unit += seq.chunks;
+    first = 0;
+    if (++inner == span) {
+      inner = 0;
+      ++kvh;
+    }
+    return true;
+  }
+};
+
+// The even cut: sums of the pairs' work by the whole CTA, each thread taking a run
+// of pairs; the thread whose run holds the CTA's first chunk finds it.
+__device__ void cut(const CrossParams& p, Run* out, int64_t* warp_sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kThreads / 32;
+  int* warp_ints = reinterpret_cast<int*>(warp_sums + kWarps);
+  // tiles of the longest sequence (the host knows a bound)
+  int tiles = 1;
+  if (p.max_query_len > p.tile_tokens) {
+    for (int b = tid; b < p.num_seqs; b += kThreads) tiles = max(tiles, read_seq(p, b).tiles);
+    tiles = __reduce_max_sync(kFullMask, tiles);
+    if (lane == 0) warp_ints[warp] = tiles;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) tiles = max(tiles, warp_ints[w]);
+    __syncthreads();
+  }
+  Order order;
+  order.num_seqs = p.num_seqs;
+  order.tile_major = static_cast<int64_t>(tiles) * p.num_seqs <= kMostPairs;
+  order.pairs = order.tile_major ? tiles * p.num_seqs : p.num_seqs;
+  const int per = (order.pairs + kThreads - 1) / kThreads;
+  const int a0 = min(tid * per, order.pairs), a1 = min(a0 + per, order.pairs);
+  int64_t sum = 0;
+  int units = 0;  // counted as far as it matters
+  for (int a = a0; a < a1; ++a) {
+    const Seq s = read_seq(p, order.seq(a));
+    const int64_t w = order.work(p, a, s);
+    sum += w;
+    if (w > 0)
+      units = static_cast<int>(min(static_cast<int64_t>(order.span(a, s)) * p.num_kv_heads + units,
+                                   static_cast<int64_t>(1 << 20)));
+  }
+  int64_t incl = sum;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int64_t o = __shfl_up_sync(kFullMask, incl, k);
+    if (lane >= k) incl += o;
+  }
+  units = __reduce_add_sync(kFullMask, units);
+  if (lane == 31) {
+    warp_sums[warp] = incl;
+    warp_ints[warp] = units;
+  }
+  __syncthreads();
+  int64_t total = 0, before = 0;
+  units = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_sums[w];
+    total += warp_sums[w];
+    units += warp_ints[w];
+  }
+  // a CTA for each unit, or for each kMinChunks chunks where those are more
+  int ctas = static_cast<int>(max(static_cast<int64_t>(units),
+                                  min(total / kMinChunks, static_cast<int64_t>(units) * kMaxParts)));
+  ctas = max(1, min(static_cast<int>(min(total, static_cast<int64_t>(gridDim.x))), ctas));
+  const int c = blockIdx.x;
+  const int64_t least = quotient(total, ctas);
+  const int rest = static_cast<int>(total - least * ctas);
+  const int64_t begin = c * least + min(c, rest);
+  const int64_t left = c < ctas ? least + (c < rest) : 0;
+  before += incl - sum;
+  if (left > 0 ? before <= begin && begin < before + sum : tid == 0) {
+    Run r{order, ctas, total, least + 1, rest, a0, 0, 0, 0, left, before};
+    if (left > 0) {
+      Seq s;
+      for (;; ++r.pair) {
+        s = read_seq(p, order.seq(r.pair));
+        const int64_t w = order.work(p, r.pair, s);
+        if (begin < r.unit + w || r.pair + 1 >= a1) break;
+        r.unit += w;
+      }
+      const int u = static_cast<int>(quotient(begin - r.unit, s.chunks));
+      const int span = order.span(r.pair, s);
+      r.unit += static_cast<int64_t>(u) * s.chunks;
+      r.first = static_cast<int>(begin - r.unit);
+      r.kvh = u / span;
+      r.inner = u - r.kvh * span;
+    }
+    *out = r;
+  }
+  __syncthreads();
+}
+
+// The rows of a unit from its parts' (m, l, o): part k lies in the place of CTA
+// c0 + k, the first one in that of the unit its CTA ends in.  A thread takes 4
+// dims of a row at a time, four such pieces and two parts of each in flight.
+template <int D>
+__device__ __noinline__ void join(const CrossParams& p, const Part& it, int c0, int parts) {
+  constexpr int kPieces = 4, kCols = D / 4;
+  const int shift = 31 - __clz(p.group);
+  const int rows = min(kRows, (it.seq.n - it.i0) << shift);
+  auto at = [&](int k, int row) {
+    return (static_cast<int64_t>(c0 + k) * 2 + (k == 0)) * p.ws_rows + row;
+  };
+  for (int q0 = threadIdx.x; q0 < rows * kCols; q0 += kPieces * kSoftmaxThreads) {
+    float m[kPieces], l[kPieces];
+    float4 acc[kPieces];
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      m[j] = -INFINITY;
+      l[j] = 0.f;
+      acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int k0 = 0; k0 < parts; k0 += 2) {
+      float2 ml[kPieces][2];
+      float4 o[kPieces][2];
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int q = q0 + j * kSoftmaxThreads;
+          ml[j][e] = make_float2(-INFINITY, 0.f);
+          o[j][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (q < rows * kCols && k0 + e < parts) {
+            const int64_t r = at(k0 + e, q / kCols);
+            ml[j][e] = __ldcg(p.ws_ml + r);
+            o[j][e] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + r * D) + q % kCols);
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const float top = fmaxf(m[j], fmaxf(ml[j][0].x, ml[j][1].x));
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float a = ex2(m[j] - ref), b = ex2(ml[j][0].x - ref), c = ex2(ml[j][1].x - ref);
+        m[j] = top;
+        l[j] = fmaf(l[j], a, fmaf(ml[j][0].y, b, ml[j][1].y * c));
+        acc[j].x = fmaf(acc[j].x, a, fmaf(o[j][0].x, b, o[j][1].x * c));
+        acc[j].y = fmaf(acc[j].y, a, fmaf(o[j][0].y, b, o[j][1].y * c));
+        acc[j].z = fmaf(acc[j].z, a, fmaf(o[j][0].z, b, o[j][1].z * c));
+        acc[j].w = fmaf(acc[j].w, a, fmaf(o[j][0].w, b, o[j][1].w * c));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int q = q0 + j * kSoftmaxThreads, r = q / kCols;
+      if (q >= rows * kCols) continue;
+      const float z = l[j] > 0.f ? 1.f / l[j] : 0.f;
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[j].x * z, acc[j].y * z);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[j].z * z, acc[j].w * z);
+      const int64_t row = static_cast<int64_t>(it.seq.q0 + it.i0 + (r >> shift)) * p.num_q_heads +
+                          it.kvh * p.group + (r & (p.group - 1));
+      reinterpret_cast<uint2*>(p.out + row * D)[q % kCols] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                     *reinterpret_cast<const uint32_t*>(&hi));
+    }
+  }
+}
+
+// grid: persistent.  Barriers (each wait names one use of one slot):
+//   k_full / v_full [stage]: copies landed; k_free / v_free [stage]: the MMA that
+//   read the stage is done; s_done [2]: scores of a chunk ready; p_ready [2]:
+//   its weights written (an arrival a softmax warp); pv_done [2]: PV read them;
+//   q_full / q_free: a unit's Q landed / its last scores taken; o_free: O read.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    cross_attention_kernel(const __grid_constant__ CUtensorMap tq,
+                           const __grid_constant__ CUtensorMap tk,
+                           const __grid_constant__ CUtensorMap tv, const CrossParams p) {
+  using S = Shape<D>;
+  constexpr int kStages = S::kStages;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBar);
+  uint64_t* k_full = bars;
+  uint64_t* v_full = bars + kStages;
+  uint64_t* k_free = bars + 2 * kStages;
+  uint64_t* v_free = bars + 3 * kStages;
+  uint64_t* s_done = bars + 4 * kStages;
+  uint64_t* pv_done = s_done + 2;
+  uint64_t* p_ready = s_done + 4;
+  uint64_t* q_full = s_done + 6;
+  uint64_t* q_free = s_done + 7;
+  uint64_t* o_free = s_done + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kBar + 240);
+  unsigned* last_slot = reinterpret_cast<unsigned*>(sm + S::kBar + 244);
+  static_assert((4 * kStages + 9) * 8 <= 240, "barriers");
+
+  if (tid == 0) {
+    for (int i = 0; i < 4 * kStages + 9; ++i) mbar_init(bars + i, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(p_ready + i, kSoftmaxThreads / 32);
+    mbar_init(o_free, kSoftmaxThreads / 32);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  __shared__ Run run_slot;
+  __shared__ int64_t warp_sums[2 * (kThreads / 32)];
+  tc_fence_before();
+  cut(p, &run_slot, warp_sums);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Run& run = run_slot;
+
+  if (warp >= kCopyWarp) {
+    // ------------------------------------------------------------ copies
+    // One warp for Q and the K ring, one for the V ring.  Block ids run kAhead
+    // chunks ahead of the copies, across units.
+    const bool vwarp = warp == kCopyWarp + 1;
+    struct Ahead {
+      int id;       // lane j: the raw table entry of block j (checked at use)
+      int blocks;   // of the chunk; 0: no chunk
+      int kvh, q_row;  // q_row: of the chunk's Q if it opens a part, else -1
+    };
+    constexpr int kAhead = 4;
+    Walk walk(p, run);
+    Part it;
+    bool some = walk.next(p, it);
+    int c = 0;  // chunk of `it` that is fetched next
+    auto fetch = [&]() -> Ahead {
+      Ahead a{0, 0, 0, -1};
+      if (!some) return a;
+      const int block = (it.first + c) * kChunkBlocks;
+      a.blocks = min(kChunkBlocks, (it.seq.src + kBS - 1) / kBS - block);
+      a.kvh = it.kvh;
+      if (c == 0) a.q_row = it.seq.q0 + it.i0;
+      if (lane < a.blocks)
+        a.id = __ldg(p.block_tables + static_cast<int64_t>(it.b) * p.max_blocks_per_seq + block +
+                     lane);
+      if (++c == it.count) {
+        some = walk.next(p, it);
+        c = 0;
+      }
+      return a;
+    };
+    const uint32_t leader = elect_lane();
+    auto wait = [&](uint64_t* bar, int use) {
+      return __all_sync(kFullMask, mbar_wait_bounded(bar, use & 1, p.err)) != 0;
+    };
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(vwarp ? &tv : &tk))
+                   : "memory");
+      if (!vwarp)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tq)) : "memory");
+    }
+    Ahead ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ahead[i] = fetch();
+    bool ok = true;
+    int g = 0, items = 0;
+    for (; ahead[0].blocks > 0; ++g) {
+      Ahead a = ahead[0];
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+      ahead[kAhead - 1] = fetch();
+      if (lane < a.blocks && (a.id < 0 || a.id >= p.num_blocks)) {
+        raise_error(p.err, PA_DEVERR_BLOCK_ID);  // never dereferenced: block 0 is read instead
+        a.id = 0;
+      }
+      const int row = (a.id * p.num_kv_heads + a.kvh) * kBS;
+      const int st = g % kStages;
+      if (g >= kStages) ok = wait(vwarp ? &v_free[st] : &k_free[st], g / kStages - 1);
+      if (!ok) break;
+      uint64_t* bar = vwarp ? &v_full[st] : &k_full[st];
+      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(a.blocks * S::kHalves * S::kBox), leader);
+      if (vwarp) {
+        unsigned char* dst = sm + S::kV + st * S::kStage;
+#pragma unroll
+        for (int j = 0; j < kChunkBlocks; ++j) {
+          const int y = __shfl_sync(kFullMask, row, j);
+          if (j < a.blocks)
+            tma_3d(dst + j * S::kHalves * S::kBox, &tv, 0, y, 0, bar, leader);
+        }
+      } else {
+        unsigned char* dst = sm + S::kK + st * S::kStage;
+#pragma unroll
+        for (int j = 0; j < kChunkBlocks; ++j) {
+          const int y = __shfl_sync(kFullMask, row, j);
+          if (j < a.blocks) {
+#pragma unroll
+            for (int h = 0; h < S::kHalves; ++h)
+              tma_2d(dst + h * S::kKVHalf + j * S::kBox, &tk, 64 * h, y, bar, leader);
+          }
+        }
+        if (a.q_row >= 0) {
+          if (items > 0) ok = wait(q_free, items - 1);
+          if (!ok) {
+            ++g;
+            break;
+          }
+          mbar_arrive_expect_tx(q_full, S::kHalves * S::kQHalf, leader);
+#pragma unroll
+          for (int h = 0; h < S::kHalves; ++h)
+            tma_3d(sm + S::kQ + h * S::kQHalf, &tq, 64 * h, a.kvh * p.group, a.q_row, q_full,
+                   leader);
+          ++items;
+        }
+      }
+    }
+    // Copies this warp issued land before the CTA's shared memory is given up
+    // (an earlier use of a stage completed before its last copy was issued).
+    if (lane == 0) {
+      for (int st = 0; st < kStages && st < g; ++st) {
+        const int last = g - 1 - (g - 1 - st) % kStages;  // the last chunk in this stage
+        mbar_wait_bounded(vwarp ? &v_full[st] : &k_full[st], (last / kStages) & 1, p.err);
+      }
+      if (!vwarp && items > 0) mbar_wait_bounded(q_full, (items - 1) & 1, p.err);
+    }
+  } else if (warp == kScoreWarp) {
+    // ------------------------------------------------------------ scores
+    // (the whole warp in step: see umma_bf16)
+    const uint32_t leader = elect_lane();
+    auto wait = [&](uint64_t* bar, int use) {
+      return __all_sync(kFullMask, mbar_wait_bounded(bar, use & 1, p.err)) != 0;
+    };
+    const uint64_t qdesc = sw128_desc(smem_u32(sm + S::kQ), 16, 1024);
+    const uint32_t sK = smem_u32(sm + S::kK);
+    Walk walk(p, run);
+    Part it;
+    bool ok = true;
+    int g = 0;
+    for (int items = 0; ok && walk.next(p, it); ++items) {
+      ok = wait(q_full, items);
+      for (int c = 0; c < it.count && ok; ++c) {
+        const int sb = g & 1, st = g % kStages;
+        ok = wait(&k_full[st], g / kStages);
+        // PV of two chunks ago has read the weights in this S buffer
+        if (ok && g >= 2) ok = wait(&pv_done[sb], (g - 2) >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t kdesc = sw128_desc(sK + st * S::kStage, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t qoff = ((kk >> 2) * S::kQHalf + (kk & 3) * 32) >> 4;
+          const uint32_t koff = ((kk >> 2) * S::kKVHalf + (kk & 3) * 32) >> 4;
+          umma_bf16(tmem + sb * kKeys, qdesc + qoff, kdesc + koff, S::kIdescQK, kk > 0, leader);
+        }
+        umma_commit(&s_done[sb], leader);
+        umma_commit(&k_free[st], leader);
+        if (c + 1 == it.count) umma_commit(q_free, leader);
+        ++g;
+      }
+    }
+    // The MMAs issued complete before tensor and shared memory are given up.
+    if (g > 0) wait(&s_done[(g - 1) & 1], (g - 1) >> 1);
+  } else if (warp == kMixWarp) {
+    // ------------------------------------------------------------ O += P V
+    const uint32_t leader = elect_lane();
+    auto wait = [&](uint64_t* bar, int use) {
+      return __all_sync(kFullMask, mbar_wait_bounded(bar, use & 1, p.err)) != 0;
+    };
+    const uint32_t sV = smem_u32(sm + S::kV);
+    Walk walk(p, run);
+    Part it;
+    bool ok = true;
+    int g = 0;
+    for (int items = 0; ok && walk.next(p, it); ++items) {
+      for (int c = 0; c < it.count && ok; ++c) {
+        const int sb = g & 1, st = g % kStages;
+        // the part before has been read out of O
+        if (c == 0 && items > 0) ok = wait(o_free, items - 1);
+        ok = ok && wait(&v_full[st], g / kStages) && wait(&p_ready[sb], g >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vdesc = sw128_desc(sV + st * S::kStage, S::kBox, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kChunkBlocks; ++kk) {
+          const uint64_t v = vdesc + kk * (S::kHalves * S::kBox >> 4);
+          umma_bf16_ts(tmem + kTO, tmem + sb * kKeys + 8 * kk, v, S::kIdescPV,
+                       (c > 0 || kk > 0) ? 1u : 0u, leader);
+          if constexpr (kPParts == 2)
+            umma_bf16_ts(tmem + kTO, tmem + sb * kKeys + kKeys / 2 + 8 * kk, v, S::kIdescPV, 1u,
+                         leader);
+        }
+        umma_commit(&pv_done[sb], leader);
+        umma_commit(&v_free[st], leader);
+        ++g;
+      }
+    }
+    if (g > 0) wait(&pv_done[(g - 1) & 1], (g - 1) >> 1);
+  } else {
+    // ------------------------------------------------------------ softmax
+    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tO = tmem + lane_base + kTO;
+    const int shift = 31 - __clz(p.group);
+    const int tok = tid >> shift, head = tid & (p.group - 1);  // row: token, head of the group
+    const float sl2 = p.scale_log2;
+    const float2 sl2x2 = make_float2(sl2, sl2);
+    bool ok = true;  // sticky: this thread's waits all succeeded
+    int g = 0;
+    Walk walk(p, run);
+    Part it;
+    while (walk.next(p, it)) {
+      const int qi = it.i0 + tok;
+      const bool row_ok = qi < it.seq.n;
+      const bool warp_ok = it.i0 + ((warp * 32) >> shift) < it.seq.n;  // some row of the warp is
+      const int64_t orow = static_cast<int64_t>(it.seq.q0 + (row_ok ? qi : 0)) * p.num_q_heads +
+                           it.kvh * p.group + head;
+      float m_used = -INFINITY;  // reference maximum of the exponentials (base 2)
+      float l_sum = 0.f;
+      for (int c = 0; c < it.count; ++c, ++g) {
+        const int sb = g & 1;
+        const uint32_t tS = tmem + lane_base + sb * kKeys;
+        const int valid = it.seq.src - (it.first + c) * kKeys;  // keys of this chunk
+        bool lok = ok && mbar_wait_bounded(&s_done[sb], (g >> 1) & 1, p.err);
+        lok = __all_sync(kFullMask, lok);
+        if (lok && warp_ok) {
+          tc_fence_after();
+          uint32_t sv[kKeys];
+          auto scores = [&]() {
+#pragma unroll
+            for (int h = 0; h < kKeys / 32; ++h)
+              tmem_ld32(tS + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * h));
+            tmem_wait_ld();
+            if (valid < kKeys) {
+#pragma unroll
+              for (int j = 0; j < kKeys; ++j)
+                if (j >= valid) sv[j] = __float_as_uint(-INFINITY);
+            }
+          };
+          float psum = 0.f;
+          auto weights = [&]() {
+            const bool live = m_used != -INFINITY;
+            const float2 neg2 = make_float2(live ? -m_used : 0.f, live ? -m_used : 0.f);
+            float2 ps4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                             make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int j = 0; j < kKeys; j += 2) {
+              const float2 x = __ffma2_rn(
+                  make_float2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), sl2x2, neg2);
+              const float2 e = make_float2(ex2(x.x), ex2(x.y));
+              ps4[(j >> 1) & 3] = __fadd2_rn(ps4[(j >> 1) & 3], e);
+              sv[j] = __float_as_uint(e.x);
+              sv[j + 1] = __float_as_uint(e.y);
+            }
+            const float2 pa = __fadd2_rn(__fadd2_rn(ps4[0], ps4[2]), __fadd2_rn(ps4[1], ps4[3]));
+            psum = pa.x + pa.y;
+          };
+          scores();
+          if (c > 0) weights();
+          // A weight above 2^8 makes a sum above 2^7: only then, and in a
+          // part's first chunk, are the maxima taken.
+          const bool want = m_used == -INFINITY || !(psum <= 128.f);
+          float alpha = 1.f;
+          if (__any_sync(kFullMask, want && row_ok)) {
+            if (c > 0) scores();
+            float m8[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m8[k] = __uint_as_float(sv[k]);
+#pragma unroll
+            for (int j = 8; j < kKeys; ++j) m8[j & 7] = fmaxf(m8[j & 7], __uint_as_float(sv[j]));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m8[k] = fmaxf(m8[k], m8[k + 4]);
+            const float mx = fmaxf(fmaxf(m8[0], m8[2]), fmaxf(m8[1], m8[3])) * sl2;
+            if (mx != -INFINITY) {
+              if (m_used == -INFINITY) {
+                m_used = mx;
+              } else if (mx > m_used + 8.f) {
+                alpha = ex2(m_used - mx);
+                m_used = mx;
+              }
+            }
+            weights();
+          }
+          l_sum = l_sum * alpha + psum;
+          // O is rescaled before this chunk's PV: PV of the chunk before must be
+          // done with it (the part's first PV overwrites O)
+          if (c > 0 && __any_sync(kFullMask, alpha != 1.f)) {
+            lok = mbar_wait_bounded(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err);
+            lok = __all_sync(kFullMask, lok);
+            if (lok) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int q4 = 0; q4 < D / 16; ++q4) {
+                uint32_t o[16];
+                tmem_ld16(tO + 16 * q4, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                tmem_st16(tO + 16 * q4, o);
+              }
+            }
+          }
+          // P over the scores' own columns: bf16 pairs, hi parts, then lo
+#pragma unroll
+          for (int h = 0; h < kKeys / 32; ++h) {
+            uint32_t(&v)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * h);
+            if constexpr (kPParts == 2) {
+              store_p(tS + 16 * h, tS + kKeys / 2 + 16 * h, v);
+            } else {
+              uint32_t w[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[2 * k]),
+                                                               __uint_as_float(v[2 * k + 1]));
+                w[k] = *reinterpret_cast<const uint32_t*>(&x);
+              }
+              tmem_st16(tS + 16 * h, w);
+            }
+          }
+          tmem_wait_st();
+        }
+        // V of keys past the source's end may hold anything (a partly filled
+        // block, blocks not loaded): P is 0 there, but 0 * NaN is not.
+        if (lok && valid < kKeys) {
+          const int st = g % kStages;
+          lok = mbar_wait_bounded(&v_full[st], (g / kStages) & 1, p.err);
+          if (lok && tid >= valid && tid < kKeys) {
+            const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int hh = 0; hh < S::kHalves; ++hh) {
+              uint4* row = reinterpret_cast<uint4*>(
+                  sm + S::kV + st * S::kStage + ((tid / kBS) * S::kHalves + hh) * S::kBox +
+                  (tid % kBS) * 128);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) row[k] = z;
+            }
+          }
+        }
+        ok = ok && lok;
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[sb]);
+      }
+      // the rows' result, once the part's last PV is done
+      bool lok = ok && mbar_wait_bounded(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err);
+      lok = __all_sync(kFullMask, lok);
+      ok = ok && lok;
+      tc_fence_after();
+      const bool shared = it.count < it.seq.chunks;  // with other CTAs
+      // (a part that opens its unit is its CTA's last, any other its first)
+      const int64_t place = (static_cast<int64_t>(blockIdx.x) * 2 + (it.first == 0)) * p.ws_rows;
+      const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
+      if (warp_ok && lok) {
+#pragma unroll 1
+        for (int q4 = 0; q4 < D / 16; ++q4) {
+          uint32_t o[16];
+          tmem_ld16(tO + 16 * q4, o);
+          tmem_wait_ld();
+          if (!row_ok) continue;
+          if (shared) {
+            uint4* w = reinterpret_cast<uint4*>(p.ws_o + (place + tid) * D + 16 * q4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 h2 =
+                    __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]) * inv,
+                                          __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                w[e] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              *reinterpret_cast<uint4*>(p.out + orow * D + 16 * q4 + 8 * k) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      tc_fence_before();
+      if (lane == 0) mbar_arrive(o_free);
+      if (shared) {
+        if (row_ok && lok) p.ws_ml[place + tid] = make_float2(m_used, l_sum);
+        // the last CTA of the unit joins its parts (counted at its first CTA)
+        const int c0 = owner(run, it.unit);
+        const int parts = owner(run, it.unit + it.seq.chunks - 1) - c0 + 1;
+        __threadfence();
+        asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+        if (tid == 0) *last_slot = atomicAdd(p.counters + c0, 1u);
+        asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+        if (*last_slot + 1 == static_cast<unsigned>(parts)) {
+          __threadfence();
+          join<D>(p, it, c0, parts);
+          if (tid == 0) p.counters[c0] = 0;
+        }
+      }
+    }
+    // sequences without a source, and bad ones
+    for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
+      const Seq s = read_seq(p, b);
+      if (s.bad) {
+        if (tid == 0) raise_error(p.err, PA_DEVERR_CONTEXT_LEN);
+      } else if (s.src == 0) {
+        const int64_t row = static_cast<int64_t>(p.num_q_heads) * D / 8;
+        uint4* dst = reinterpret_cast<uint4*>(p.out) + s.q0 * row;
+        for (int64_t i = tid; i < s.n * row; i += kSoftmaxThreads) dst[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                   const CrossParams& p, int ctas, cudaStream_t stream) {
+  static std::atomic<uint64_t> smem_set{0};
+  auto kernel = cross_attention_kernel<D>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(smem_set.load() & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shape<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    smem_set.fetch_or(bit);
+  }
+  return launch_pdl(kernel, dim3(ctas), dim3(kThreads), Shape<D>::kSmem, stream, tq, tk, tv, p);
+}
+
+// The K pool as [num_blocks * Hkv * 16 rows][D] bf16, boxes of 16 rows x 64
+// columns; the V pool as [D / 64 halves][rows][64], boxes of a block's 16 rows in
+// every half; q as [T][Hq][D], tokens q_stride elements apart, boxes of 128 / group
+// tokens x group heads x 64 columns; 128-byte swizzle.
+bool encode_rows(CUtensorMap* map, const void* base, int head_dim, int64_t rows) {
+  const auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(head_dim) * 2};
+  const cuuint32_t box[2] = {64, kBS};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+bool encode_blocks(CUtensorMap* map, const void* base, int head_dim, int64_t rows) {
+  const auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t halves = static_cast<cuuint64_t>(head_dim / 64);
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), halves};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, 128};
+  const cuuint32_t box[3] = {64, kBS, static_cast<cuuint32_t>(halves)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+bool encode_queries(CUtensorMap* map, const void* base, int head_dim, int num_q_heads, int total_q,
+                    int64_t q_stride, int group) {
+  const auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim),
+                              static_cast<cuuint64_t>(num_q_heads),
+                              static_cast<cuuint64_t>(total_q)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
+                                 static_cast<cuuint64_t>(q_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group),
+                             static_cast<cuuint32_t>(kRows / group)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// Rows of a workspace place: what a tile of up to max_query_len queries holds.
+int cross_rows(int max_query_len, int group) {
+  return max_query_len < kRows / group ? max_query_len * group : kRows;
+}
+
+pa_status cross_impl(void* out, const void* q, int64_t q_stride, const void* k_cache,
+                     const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+                     const int32_t* source_lens, const int32_t* query_start_loc,
+                     int max_query_len, int num_seqs, int total_query_tokens, int num_q_heads,
+                     int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+                     float* ws_out, float* ws_ml, unsigned* counters, int ws_ctas,
+                     pa_stream_t stream, pa_prepared** keep) {
+  if (num_seqs < 0 || max_query_len < 0 || total_query_tokens < 0 || num_q_heads <= 0 ||
+      num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || max_blocks_per_seq <= 0 ||
+      num_blocks <= 0 || !(scale > 0.f) || ws_ctas < 1)
+    return PA_ERR_INVALID_ARG;
+  const int group = num_q_heads / num_kv_heads;
+  if (!pa_cross_attention_supported(head_dim, group, block_size)) return PA_ERR_UNSUPPORTED_SHAPE;
+  if (num_seqs == 0 || max_query_len == 0 || total_query_tokens == 0)
+    return keep ? nothing_to_do(keep) : PA_OK;
+  if (!aligned_ptr(out, 16) || !aligned_ptr(q, 16) || !aligned_ptr(k_cache, 16) ||
+      !aligned_ptr(v_cache, 16) || !aligned_ptr(block_tables, 4) || !aligned_ptr(source_lens, 4) ||
+      !aligned_ptr(query_start_loc, 4))
+    return PA_ERR_INVALID_ARG;
+  if (q_stride < static_cast<int64_t>(num_q_heads) * head_dim || q_stride % 8 != 0 ||
+      q_stride >= (1ll << 39))
+    return PA_ERR_INVALID_ARG;
+  if (!aligned_ptr(ws_out, 16) || !aligned_ptr(ws_ml, 16) || !aligned_ptr(counters, 4))
+    return PA_ERR_INVALID_ARG;
+  const int64_t rows = static_cast<int64_t>(num_blocks) * num_kv_heads * kBS;
+  if (rows > 0x7fffffffll || static_cast<int64_t>(max_blocks_per_seq) * kBS > 0x7fffffffll)
+    return PA_ERR_INVALID_ARG;
+  CrossParams p{};
+  p.group = group;
+  p.tile_tokens = kRows / group;
+  p.max_query_len = max_query_len < total_query_tokens ? max_query_len : total_query_tokens;
+  CUtensorMap tq, tk, tv;
+  if (!encode_queries(&tq, q, head_dim, num_q_heads, total_query_tokens, q_stride, group) ||
+      !encode_rows(&tk, k_cache, head_dim, rows) || !encode_blocks(&tv, v_cache, head_dim, rows))
+    return cuda_fail(cudaErrorInvalidValue);  // tensor-map encoding refused the buffers
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.block_tables = block_tables;
+  p.source_lens = source_lens;
+  p.query_start = query_start_loc;
+  p.ws_o = ws_out;
+  p.ws_ml = reinterpret_cast<float2*>(ws_ml);
+  p.counters = counters;
+  p.err = device_error_word();
+  if (!p.err) return cuda_fail(cudaGetLastError());
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.num_blocks = num_blocks;
+  p.total_q = total_query_tokens;
+  p.ws_rows = cross_rows(p.max_query_len, group);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  // no more CTAs than the longest sources that the tables hold could feed
+  const int64_t most = static_cast<int64_t>((max_blocks_per_seq + kChunkBlocks - 1) / kChunkBlocks) *
+                       ((p.max_query_len + p.tile_tokens - 1) / p.tile_tokens) * num_seqs;
+  int ctas = ws_ctas;
+  if (most < ws_ctas)  // (then no product below passes 64 bits)
+    ctas = static_cast<int>(std::min<int64_t>(ws_ctas, most * num_kv_heads));
+  return launch_or_keep(
+      [=](cudaStream_t s) {
+        return head_dim == 64 ? launch<64>(tq, tk, tv, p, ctas, s)
+                              : launch<128>(tq, tk, tv, p, ctas, s);
+      },
+      keep, stream);
+}
+
+}  // namespace
+
+}  // namespace pa
+
+extern "C" int pa_cross_attention_supported(int head_dim, int group, int block_size) {
+  return (head_dim == 64 || head_dim == 128) && block_size == 16 &&
+         (group == 1 || group == 2 || group == 4 || group == 8);
+}
+
+extern "C" int pa_cross_attention_ctas(int num_sms) { return num_sms > 0 ? 2 * num_sms : 0; }
+
+extern "C" int pa_cross_attention_rows(int max_query_len, int group) {
+  return max_query_len > 0 && group > 0 ? pa::cross_rows(max_query_len, group) : 0;
+}
+
+extern "C" pa_status pa_cross_attention(
+    void* out, const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* source_lens,
+    const int32_t* query_start_loc, int max_query_len, int num_seqs, int total_query_tokens,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    float* ws_out, float* ws_ml, unsigned* counters, int ws_ctas, pa_stream_t stream) {
+  return pa::cross_impl(out, q, q_stride, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                        source_lens, query_start_loc, max_query_len, num_seqs,
+                        total_query_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                        num_blocks, scale, ws_out, ws_ml, counters, ws_ctas, stream, nullptr);
+}
+
+extern "C" pa_status pa_prepare_cross_attention(
+    pa_prepared** prepared, void* out, const void* q, int64_t q_stride, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* source_lens, const int32_t* query_start_loc, int max_query_len, int num_seqs,
+    int total_query_tokens, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+    int num_blocks, float scale, float* ws_out, float* ws_ml, unsigned* counters, int ws_ctas) {
+  if (!prepared) return PA_ERR_INVALID_ARG;
+  *prepared = nullptr;
+  return pa::cross_impl(out, q, q_stride, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                        source_lens, query_start_loc, max_query_len, num_seqs,
+                        total_query_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                        num_blocks, scale, ws_out, ws_ml, counters, ws_ctas, nullptr, prepared);
+}

@@ -2,6 +2,8 @@
 // translation units.  Not installed; not part of the ABI.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -160,6 +162,69 @@ struct RopeAppendParams {
   int row_slots;                  // thread groups per token (set by the launcher)
 };
 
+inline bool aligned_ptr(const void* p, uintptr_t a) {
+  return p != nullptr && reinterpret_cast<uintptr_t>(p) % a == 0;
+}
+
+// Positions of a cache read back (read_cache.cu).
+struct ReadCacheParams {
+  __nv_bfloat16* k_out;           // rows of Hkv * D at out_stride, or (slots) a bf16 pool
+  __nv_bfloat16* v_out;
+  const void* k_cache;            // kind 0 bf16, 1 INT8, 2 FP8, 3 4-bit tiles
+  const void* v_cache;
+  const float* k_scales;
+  const float* v_scales;
+  const int32_t* block_tables;
+  const int32_t* first;           // [B] first position read (null: 0)
+  const int32_t* row_start;       // [B + 1]
+  const int64_t* slots;           // [T] slots of the bf16 pool (null: rows)
+  unsigned* err;
+  int64_t out_stride;
+  int64_t num_out_slots;
+  int64_t total_rows;
+  int kind;
+  int max_rows;
+  int max_blocks_per_seq;
+  int num_kv_heads;
+  int num_blocks;
+};
+
+// States reordered in place (reorder_states.cu), up to kReorderMaxTensors a launch.
+constexpr int kReorderMaxTensors = 64;
+constexpr int kReorderMaxBeams = 32;
+struct ReorderParams {
+  void* states[kReorderMaxTensors];
+  const int32_t* parents;  // [groups * beams]
+  unsigned* err;
+  int64_t row_bytes;
+  int64_t row_stride;      // bytes
+  int beams;
+  int chunk;               // bytes of a row that a CTA moves (set by the launcher)
+};
+
+// Beam search's selection (beam_select.cu).
+constexpr int kBeamMaxBeams = 32;
+constexpr int kBeamMaxKeep = 64;
+constexpr int kBeamMaxVocab = 1 << 27;
+struct BeamParams {
+  float* out_scores;       // [searches, keep]
+  int32_t* out_parents;
+  int32_t* out_tokens;
+  uint8_t* out_finished;   // may be null
+  const void* logits;      // [searches * beams] rows of vocab at row_stride
+  const float* scores;     // [searches * beams]
+  const uint8_t* finished; // may be null
+  uint64_t* ws_keys;       // [searches * beams, parts, keep]
+  float2* ws_sums;         // [searches * beams, parts]: maximum, sum of exp
+  unsigned* counters;      // [searches]
+  unsigned* err;
+  int64_t row_stride;      // elements
+  int searches, beams, vocab, keep, eos, in_place;
+  int parts;
+  int part_len;            // (set by the launcher)
+  int groups;              // (set by the launcher)
+};
+
 // Pools of up to kCopyMaxLayers layers go to one copy_blocks launch.
 constexpr int kCopyMaxLayers = 64;
 
@@ -197,8 +262,19 @@ cudaError_t launch_prefix_partials(const void* q, const void* k_cache, const voi
 cudaError_t launch_reshape_and_cache(const CacheWriteParams& p, cudaStream_t stream);
 cudaError_t launch_reshape_and_cache_int8(const CacheWriteParams& p, cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeAppendParams& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_read_cache(const ReadCacheParams& p, int head_dim, int num_seqs,
+                              cudaStream_t stream);
+// vec: bytes of one access, 1, 2, 4 or 16.
+cudaError_t launch_reorder_states(ReorderParams p, int groups, int tensors, int vec,
+                                  cudaStream_t stream);
+// Parts that a row of logits is cut into (dtype 0 bf16, 1 fp16, 2 fp32).
+int beam_parts(int rows, int vocab, int dtype);
+cudaError_t launch_beam_select(BeamParams p, int dtype, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const CopyBlocksParams& p, int num_pairs, int num_layers,
                                cudaStream_t stream);
+
+// The driver's tensor-map encoder (cuTensorMapEncodeTiled), or nullptr (prefill.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Address of the current device's error word (device memory), or nullptr.
 unsigned* device_error_word();

@@ -16,7 +16,6 @@
 #include "prefill_kernel.cuh"
 
 namespace pa {
-namespace {
 
 // ---- host side -------------------------------------------------------------
 
@@ -33,6 +32,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
+
+namespace {
 
 // K or V pool as a 2-D bf16 tensor [num_blocks * Hkv * 16 rows][128], boxes of
 // 16 rows x 64 columns, 128-byte swizzle.

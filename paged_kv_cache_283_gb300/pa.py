@@ -29,7 +29,10 @@ PA_DEVERR_WAIT_TIMEOUT = 0x8
 PA_DEVERR_ORDER = 0x10
 PA_DEVERR_PREFIX = 0x20
 PA_DEVERR_POSITION = 0x40
+PA_DEVERR_PARENT = 0x80
+PA_DEVERR_LOGITS = 0x100
 PA_STEP_EARLY_READ = 0x1
+PA_BEAM_IN_PLACE = 0x1
 
 # Every function include/pa.h declares: name -> (restype, argtypes).
 _vp, _i, _u, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_float, ctypes.c_size_t
@@ -108,6 +111,28 @@ SIGNATURES = {
     "pa_prepare_prefill": (
         _i, [ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i,
              _i, _i, _f, _f, _vp, _i, _vp]),
+    "pa_cross_attention_supported": (_i, [_i, _i, _i]),
+    "pa_cross_attention_ctas": (_i, [_i]),
+    "pa_cross_attention_rows": (_i, [_i, _i]),
+    "pa_cross_attention": (_i, [_vp, _vp, _i64, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
+                                _i, _i, _i, _f, _vp, _vp, _vp, _i, _vp]),
+    "pa_prepare_cross_attention": (
+        _i, [ctypes.POINTER(_vp), _vp, _vp, _i64, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i,
+             _i, _i, _i, _i, _f, _vp, _vp, _vp, _i]),
+    "pa_read_cache": (_i, [_i, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i,
+                           _vp, _i, _i, _i, _i, _i, _vp]),
+    "pa_prepare_read_cache": (
+        _i, [ctypes.POINTER(_vp), _i, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i,
+             _i, _i, _vp, _i, _i, _i, _i, _i]),
+    "pa_beam_select_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "pa_beam_select": (_i, [_vp, _vp, _vp, _vp, _vp, _i64, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp,
+                            _vp, _i, _vp]),
+    "pa_prepare_beam_select": (
+        _i, [ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _vp, _i64, _i, _vp, _vp, _i, _i, _i, _i,
+             _i, _vp, _vp, _i]),
+    "pa_reorder_states": (_i, [_vp, _i, _vp, _i, _i, _i64, _i64, _vp]),
+    "pa_prepare_reorder_states": (
+        _i, [ctypes.POINTER(_vp), _vp, _i, _vp, _i, _i, _i64, _i64]),
     "pa_run": (_i, [_vp, _vp]),
     "pa_prepared_destroy": (None, [_vp]),
     "pa_await_event": (_i, [_vp, _vp]),
@@ -119,6 +144,7 @@ SIGNATURES = {
     "pa_alloc_append_slots": (_i, [_vp, _vp, _i, _vp, _vp, _vp]),
     "pa_alloc_reserve": (_i, [_vp, _i, _i, _pi32, _pi32]),
     "pa_alloc_fork": (_i, [_vp, _i, _i]),
+    "pa_alloc_reorder": (_i, [_vp, _vp, _vp, _i]),
     "pa_alloc_free_seq": (_i, [_vp, _i]),
     "pa_alloc_block_table": (_i, [_vp, _i, _vp, _i, _pint]),
     "pa_alloc_block_tables": (_i, [_vp, _vp, _i, _vp, _i, _vp]),
@@ -1121,6 +1147,358 @@ class PrefillStep:
             _check(st, "PrefillStep: prefill")
 
 
+class _FixedCall:
+    """A prepared call on fixed device buffers (`prepare`: its pa_prepare_* function
+    and arguments); each call is one bare launch.  The buffers' contents may change
+    between calls, their shapes and addresses may not.  `made`: buffers made here on
+    the current stream, which the first call's stream awaits."""
+
+    def _fix(self, what, prepare, args, stream, keep, made=False):
+        torch = _torch()
+        self._what = what
+        self._call = _Prepared(prepare, *args)
+        self._stream = None if stream is None else ctypes.c_void_p(stream.cuda_stream)
+        self._keep = keep
+        self._ready = None
+        if made and not torch.cuda.is_current_stream_capturing():
+            self._ready = torch.cuda.current_stream().record_event()
+
+    def __call__(self, stream=None):
+        s = self._stream if stream is None and self._stream is not None else _stream(stream)
+        if self._ready is not None:
+            _check(lib().pa_await_event(self._ready.cuda_event, s), self._what)
+            self._ready = None
+        st = self._call.run(s)
+        if st != PA_OK:
+            _check(st, self._what)
+
+
+def pa_cross_attention_supported(head_dim, group, block_size=16):
+    return bool(lib().pa_cross_attention_supported(head_dim, group, block_size))
+
+
+def cross_attention_workspace(max_query_len, num_q_heads, num_kv_heads, head_dim, device=None):
+    """(ws_out, ws_ml, counters) for pa_cross_attention on a device: fp32 [CTAs, 2, rows,
+    head_dim] and [CTAs, 2, rows, 2], and zeroed int32 [CTAs]."""
+    torch = _torch()
+    device = torch.device("cuda" if device is None else device)
+    ctas = lib().pa_cross_attention_ctas(
+        torch.cuda.get_device_properties(device).multi_processor_count)
+    rows = max(1, lib().pa_cross_attention_rows(int(max_query_len), num_q_heads // num_kv_heads))
+    return (torch.empty(ctas, 2, rows, head_dim, dtype=torch.float32, device=device),
+            torch.empty(ctas, 2, rows, 2, dtype=torch.float32, device=device),
+            torch.zeros(ctas, dtype=torch.int32, device=device))
+
+
+def _cross_args(out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc,
+                max_query_len, scale, workspace):
+    """Checked and marshalled arguments of pa_cross_attention (without the stream)."""
+    torch = _torch()
+    what = "pa_cross_attention"
+    ws_o, ws_ml, counters = workspace
+    _one_device(what, out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc, ws_o,
+                ws_ml, counters)
+    pq, stride = _heads(q, "q")
+    T, hq, d = q.shape
+    if out.shape != q.shape:
+        raise ValueError(f"{what}: out must match q")
+    pk = _dev(k_cache, torch.bfloat16, "k_cache", 4)
+    nb, hkv, bs, d2 = k_cache.shape
+    if v_cache.shape != k_cache.shape or d2 != d or hq % hkv:
+        raise ValueError(f"{what}: cache shapes")
+    pt = _dev(block_tables, torch.int32, "block_tables", 2)
+    B, mb = block_tables.shape
+    if source_lens.shape != (B,) or query_start_loc.shape != (B + 1,):
+        raise ValueError(f"{what}: source_lens / query_start_loc shapes")
+    max_query_len = int(max_query_len)
+    rows = lib().pa_cross_attention_rows(max_query_len, hq // hkv)
+    ctas = counters.shape[0]
+    if ws_o.dim() != 4 or ws_o.shape[:2] != (ctas, 2) or ws_o.shape[2] < rows or \
+            ws_o.shape[3] != d or ws_ml.shape != (*ws_o.shape[:3], 2):
+        raise ValueError(f"{what}: workspace shapes")
+    return (_dev(out, torch.bfloat16, "out", 3), pq, stride, pk,
+            _dev(v_cache, torch.bfloat16, "v_cache", 4), pt, mb,
+            _dev(source_lens, torch.int32, "source_lens", 1),
+            _dev(query_start_loc, torch.int32, "query_start_loc", 1), max_query_len, B, T, hq,
+            hkv, d, bs, nb, float(scale), _dev(ws_o, torch.float32, "ws_out", 4),
+            _dev(ws_ml, torch.float32, "ws_ml", 4), _dev(counters, torch.int32, "counters", 1),
+            ctas)
+
+
+def pa_cross_attention(out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc,
+                       max_query_len, scale, workspace, stream=None):
+    """Attention of each sequence's queries to all of its source's states in a paged
+    bf16 cache (pa.h): decoder prompts, or the beams of a step (a source's beams are
+    its sequence's queries and share the reading of it).
+
+    q [T, Hq, D] bf16, tokens strided or not, out [T, Hq, D]; source_lens [B],
+    query_start_loc [B + 1] int32 (device); max_query_len: host bound on every
+    sequence's queries; workspace = cross_attention_workspace(...)."""
+    args = _cross_args(out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc,
+                       max_query_len, scale, workspace)
+    _check(lib().pa_cross_attention(*args, _stream(stream)), "pa_cross_attention")
+
+
+class CrossAttention(_FixedCall):
+    """pa_cross_attention of one layer on fixed device buffers, its arguments checked
+    and marshalled once.  Without a workspace it makes its own (of two such handles'
+    calls, each may then run beside the other's; one handle's may not)."""
+
+    def __init__(self, out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc,
+                 max_query_len, scale, workspace=None, stream=None):
+        made = workspace is None
+        if made:
+            workspace = cross_attention_workspace(max_query_len, q.shape[1], k_cache.shape[1],
+                                                  q.shape[2], q.device)
+        self.workspace = workspace
+        args = _cross_args(out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc,
+                           max_query_len, scale, workspace)
+        self._fix("CrossAttention: pa_cross_attention", "pa_prepare_cross_attention", args,
+                  stream, [out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc,
+                           workspace], made)
+
+
+def _read_args(k_out, v_out, k_cache, v_cache, block_tables, row_start_loc, max_rows,
+               first_positions, k_scales, v_scales, slot_mapping):
+    """Checked and marshalled arguments of pa_read_cache (without the stream)."""
+    torch = _torch()
+    what = "pa_read_cache"
+    _one_device(what, k_out, v_out, k_cache, v_cache, block_tables, row_start_loc,
+                first_positions, k_scales, v_scales, slot_mapping)
+    none = ctypes.c_void_p(None)
+    bs, scales = 16, (none, none)
+    if k_cache.dim() == 3:       # 4-bit
+        kind = 4
+        pk, nb, hkv, d = _pool4(k_cache, "k_cache")
+        pools = (pk, _pool4(v_cache, "v_cache", hkv, d)[0])
+    elif k_cache.dtype == torch.bfloat16:
+        kind = 0
+        pools = (_dev(k_cache, torch.bfloat16, "k_cache", 4),
+                 _dev(v_cache, torch.bfloat16, "v_cache", 4))
+        nb, hkv, bs, d = k_cache.shape
+    else:
+        kind = 2 if k_cache.dtype == torch.uint8 else 1
+        if k_scales is None or v_scales is None:
+            raise ValueError(f"{what}: a 1-byte cache needs k_scales and v_scales")
+        ptrs, (nb, hkv, bs, d) = _int8_pools(k_cache, v_cache, k_scales, v_scales, kind == 2)
+        pools, scales = ptrs[:2], ptrs[2:]
+    if kind in (0, 4) and (k_scales is not None or v_scales is not None):
+        raise ValueError(f"{what}: only a 1-byte cache has scales")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError(f"{what}: k_cache and v_cache must have one shape")
+    pt = _dev(block_tables, torch.int32, "block_tables", 2)
+    B, mb = block_tables.shape
+    if row_start_loc.shape != (B + 1,) or (
+            first_positions is not None and first_positions.shape != (B,)):
+        raise ValueError(f"{what}: row_start_loc must be [B + 1], first_positions [B]")
+    if v_out.shape != k_out.shape:
+        raise ValueError(f"{what}: k_out and v_out must have one shape")
+    if slot_mapping is None:
+        if k_out.dim() != 3 or k_out.shape[1:] != (hkv, d):
+            raise ValueError(f"{what}: k_out and v_out must be [T, Hkv, D]")
+        ko, stride = _heads(k_out, "k_out")
+        vo, vstride = _heads(v_out, "v_out")
+        if vstride != stride:
+            raise ValueError(f"{what}: k_out and v_out must have one stride")
+        T, slots, nob = k_out.shape[0], none, 0
+    else:
+        if k_out.dim() != 4 or k_out.shape[1:] != (hkv, bs, d):
+            raise ValueError(f"{what}: with slots, k_out and v_out are pools [NB, Hkv, 16, D]")
+        ko = _dev(k_out, torch.bfloat16, "k_out", 4)
+        vo = _dev(v_out, torch.bfloat16, "v_out", 4)
+        slots = _dev(slot_mapping, torch.int64, "slot_mapping", 1)
+        T, stride, nob = slot_mapping.shape[0], 0, k_out.shape[0]
+    return (kind, ko, vo, stride, *pools, *scales, pt, mb,
+            none if first_positions is None else
+            _dev(first_positions, torch.int32, "first_positions", 1),
+            _dev(row_start_loc, torch.int32, "row_start_loc", 1), int(max_rows), B, T, slots, nob,
+            hkv, d, bs, nb)
+
+
+def pa_read_cache(k_out, v_out, k_cache, v_cache, block_tables, row_start_loc, max_rows,
+                  first_positions=None, k_scales=None, v_scales=None, slot_mapping=None,
+                  stream=None):
+    """Reads positions of a cache of any type back as bf16 (pa.h): sequence b's rows
+    row_start_loc[b] .. row_start_loc[b + 1] - 1 are its positions from
+    first_positions[b] (or 0) on.
+
+    Without slot_mapping k_out / v_out are [T, Hkv, D] (rows strided or not); with
+    one ([T] int64) they are bf16 pools [NB, Hkv, 16, D] and row r goes to its slot.
+    The pools' type says which cache is read: bf16, int8 or uint8 (FP8 codes)
+    [NB, Hkv, 16, D] with scales, or 4-bit [NB, Hkv, 9 * D] uint8."""
+    args = _read_args(k_out, v_out, k_cache, v_cache, block_tables, row_start_loc, max_rows,
+                      first_positions, k_scales, v_scales, slot_mapping)
+    _check(lib().pa_read_cache(*args, _stream(stream)), "pa_read_cache")
+
+
+class ReadCache(_FixedCall):
+    """pa_read_cache on fixed device buffers, its arguments checked and marshalled
+    once."""
+
+    def __init__(self, k_out, v_out, k_cache, v_cache, block_tables, row_start_loc, max_rows,
+                 first_positions=None, k_scales=None, v_scales=None, slot_mapping=None,
+                 stream=None):
+        args = _read_args(k_out, v_out, k_cache, v_cache, block_tables, row_start_loc, max_rows,
+                          first_positions, k_scales, v_scales, slot_mapping)
+        self._fix("ReadCache: pa_read_cache", "pa_prepare_read_cache", args, stream,
+                  [k_out, v_out, k_cache, v_cache, block_tables, row_start_loc, first_positions,
+                   k_scales, v_scales, slot_mapping])
+
+
+def _beam_dtype(logits):
+    torch = _torch()
+    kinds = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    if logits.dtype not in kinds:
+        raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
+    return kinds[logits.dtype]
+
+
+def beam_select_workspace(logits, num_beams, num_keep):
+    """(workspace, counters) for pa_beam_select on these logits: bytes, and zeroed
+    int32 [num_searches]."""
+    torch = _torch()
+    rows, vocab = logits.shape
+    n = lib().pa_beam_select_workspace_bytes(rows // num_beams, num_beams, num_keep, vocab,
+                                             _beam_dtype(logits))
+    return (torch.empty(max(16, n), dtype=torch.uint8, device=logits.device),
+            torch.zeros(rows // num_beams, dtype=torch.int32, device=logits.device))
+
+
+def _flags(t, name):
+    """Pointer of a contiguous bool or uint8 tensor of flags."""
+    torch = _torch()
+    return _dev(t, torch.bool if t.dtype == torch.bool else torch.uint8, name)
+
+
+def _beam_args(scores_out, parents_out, tokens_out, logits, scores, num_beams, finished,
+               eos_token, finished_out, in_place, workspace):
+    """Checked and marshalled arguments of pa_beam_select (without the stream)."""
+    torch = _torch()
+    what = "pa_beam_select"
+    ws, counters = workspace
+    _one_device(what, scores_out, parents_out, tokens_out, logits, scores, finished, finished_out,
+                ws, counters)
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 2:
+        raise ValueError(f"{what}: logits must be a CUDA tensor [searches * beams, vocab]")
+    kind = _beam_dtype(logits)
+    rows, vocab = logits.shape
+    num_beams = int(num_beams)
+    if num_beams <= 0 or rows % num_beams:
+        raise ValueError(f"{what}: the logits' rows must be a multiple of num_beams")
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError(f"{what}: a row of logits must be contiguous")
+    stride = logits.stride(0) if rows > 1 else vocab
+    if stride < vocab:
+        raise ValueError(f"{what}: rows of logits must not overlap")
+    n = rows // num_beams
+    if scores_out.dim() != 2 or scores_out.shape[0] != n:
+        raise ValueError(f"{what}: outputs must be [searches, num_keep]")
+    keep = scores_out.shape[1]
+    if parents_out.shape != (n, keep) or tokens_out.shape != (n, keep) or (
+            finished_out is not None and finished_out.shape != (n, keep)):
+        raise ValueError(f"{what}: outputs must be [searches, num_keep]")
+    if scores.numel() != rows or (finished is not None and finished.numel() != rows):
+        raise ValueError(f"{what}: one score, and one finished flag, per beam")
+    if counters.shape != (n,):
+        raise ValueError(f"{what}: counters must be [searches]")
+    need = lib().pa_beam_select_workspace_bytes(n, num_beams, keep, vocab, kind)
+    if ws.numel() * ws.element_size() < need:
+        raise ValueError(f"{what}: the workspace needs {need} bytes")
+    none = ctypes.c_void_p(None)
+    return (_dev(scores_out, torch.float32, "scores_out", 2),
+            _dev(parents_out, torch.int32, "parents_out", 2),
+            _dev(tokens_out, torch.int32, "tokens_out", 2),
+            none if finished_out is None else _flags(finished_out, "finished_out"),
+            ctypes.c_void_p(logits.data_ptr()), stride, kind,
+            _dev(scores, torch.float32, "scores"),
+            none if finished is None else _flags(finished, "finished"), int(eos_token), n,
+            num_beams, keep, vocab, _dev(ws, ws.dtype, "workspace"),
+            _dev(counters, torch.int32, "counters", 1), PA_BEAM_IN_PLACE if in_place else 0)
+
+
+def pa_beam_select(scores_out, parents_out, tokens_out, logits, scores, num_beams, workspace,
+                   finished=None, eos_token=-1, finished_out=None, in_place=False, stream=None):
+    """Beam search's selection (pa.h): of the continuations of each search's num_beams
+    beams, those with the largest scores[r] + log_softmax(logits[r])[v].
+
+    logits [searches * num_beams, vocab] bf16, fp16 or fp32 (rows strided or not);
+    scores and finished (bool) hold one entry per row; outputs [searches, num_keep]:
+    scores fp32, parents (rows of the beams they continue) and tokens int32,
+    finished_out bool.  in_place (num_keep = num_beams): beams that go on keep their
+    places.  workspace = beam_select_workspace(...)."""
+    args = _beam_args(scores_out, parents_out, tokens_out, logits, scores, num_beams, finished,
+                      eos_token, finished_out, in_place, workspace)
+    _check(lib().pa_beam_select(*args, _stream(stream)), "pa_beam_select")
+
+
+class BeamSelect(_FixedCall):
+    """pa_beam_select on fixed device buffers, its arguments checked and marshalled
+    once.  Without a workspace it makes its own."""
+
+    def __init__(self, scores_out, parents_out, tokens_out, logits, scores, num_beams,
+                 finished=None, eos_token=-1, finished_out=None, in_place=False, workspace=None,
+                 stream=None):
+        made = workspace is None
+        if made:
+            workspace = beam_select_workspace(logits, num_beams, scores_out.shape[1])
+        self.workspace = workspace
+        args = _beam_args(scores_out, parents_out, tokens_out, logits, scores, num_beams,
+                          finished, eos_token, finished_out, in_place, workspace)
+        self._fix("BeamSelect: pa_beam_select", "pa_prepare_beam_select", args, stream,
+                  [scores_out, parents_out, tokens_out, logits, scores, finished, finished_out,
+                   workspace], made)
+
+
+def _reorder_args(states, parents, num_beams):
+    """Checked and marshalled arguments of pa_reorder_states (without the stream)."""
+    torch = _torch()
+    what = "pa_reorder_states"
+    states = [states] if isinstance(states, torch.Tensor) else list(states)
+    _one_device(what, parents, *states)
+    par = _dev(parents, torch.int32, "parents")
+    rows, num_beams = parents.numel(), int(num_beams)
+    if num_beams <= 0 or rows % num_beams:
+        raise ValueError(f"{what}: the rows must be a multiple of num_beams")
+    shape = None
+    for t in states:
+        if not t.is_cuda:
+            raise ValueError(f"{what}: states must be CUDA tensors")
+        if t.dim() == 0 or t.shape[0] != rows:
+            raise ValueError(f"{what}: states must have a row per beam")
+        if rows and not t[0].is_contiguous():
+            raise ValueError(f"{what}: a row of a state must be contiguous")
+        size = t.element_size()
+        row = (t.numel() // rows if rows else 0) * size
+        stride = t.stride(0) * size if rows > 1 else row
+        if shape is None:
+            shape = (row, stride)
+        if (row, stride) != shape:
+            raise ValueError(f"{what}: all states must have rows of one size and stride")
+        if stride < row:
+            raise ValueError(f"{what}: rows of a state must not overlap")
+    ptrs = (ctypes.c_void_p * max(1, len(states)))(*[t.data_ptr() for t in states])
+    row, stride = shape or (0, 0)
+    return (ptrs, len(states), par, rows // num_beams, num_beams, row, stride)
+
+
+def pa_reorder_states(states, parents, num_beams, stream=None):
+    """Row i of every state (a tensor [searches * num_beams, ...] of any type, or a
+    list of such with rows of one size) becomes what row parents[i] was, in place;
+    parents int32 (pa_beam_select's), within the groups of num_beams rows; negative:
+    the row stays."""
+    _check(lib().pa_reorder_states(*_reorder_args(states, parents, num_beams), _stream(stream)),
+           "pa_reorder_states")
+
+
+class ReorderStates(_FixedCall):
+    """pa_reorder_states on fixed device buffers, its arguments checked and
+    marshalled once."""
+
+    def __init__(self, states, parents, num_beams, stream=None):
+        self._fix("ReorderStates: pa_reorder_states", "pa_prepare_reorder_states",
+                  _reorder_args(states, parents, num_beams), stream, [states, parents])
+
+
 def pa_plan_step(budget, num_decodes, prefill_remaining):
     """(decodes scheduled, numpy int32 tokens per queued prefill) for one step."""
     import numpy as np
@@ -1410,6 +1788,17 @@ class BlockAllocator:
 
     def fork(self, parent, child):
         _check(lib().pa_alloc_fork(self._h, parent, child), "pa_alloc_fork")
+
+    def reorder(self, seqs, parents):
+        """The sequences become copies of their parents (entries of `seqs`; negative:
+        unchanged), sharing their blocks: a beam search's step."""
+        np = self._np
+        ids = np.ascontiguousarray(seqs, dtype=np.intc)
+        par = np.ascontiguousarray(parents, dtype=np.int32)
+        if par.shape != ids.shape or ids.ndim != 1:
+            raise ValueError("reorder: one parent per sequence")
+        _check(lib().pa_alloc_reorder(self._h, ids.ctypes.data_as(_vp), par.ctypes.data_as(_vp),
+                                      ids.shape[0]), "pa_alloc_reorder")
 
     def free_seq(self, seq):
         _check(lib().pa_alloc_free_seq(self._h, seq), "pa_alloc_free_seq")
