@@ -34,6 +34,11 @@
 //    itself, as if its score were off by 2^-9 -- less than what the rounding of
 //    q and K to bf16 moves scores by -- and an output by at most 2^-9 of the
 //    weighted mean of |V|, which its own rounding to bf16 doubles.
+//  * Few rows (beams of one step): a softmax thread's way through its row of 64
+//    scores takes longer than the copies of their keys.  With 32 rows or fewer
+//    the tile holds four copies of them, each of which takes a quarter of every
+//    chunk's keys (zero weights for the others) and so a quarter of the time, and
+//    ends with a share of the row's (m, l, O); with 64, two copies.
 //  * Warps whose rows are all past the tile's queries (a step of few beams) do
 //    no work but keep the barriers' counts.
 
@@ -84,14 +89,11 @@ constexpr int kChunkBlocks = kKeys / kBS;
 constexpr int kSoftmaxThreads = 128;
 constexpr int kThreads = kSoftmaxThreads + 128;
 constexpr int kScoreWarp = 4, kMixWarp = 5, kCopyWarp = 6;  // Q K^T, P V, copies of K and of V
+constexpr int kSumFloats = 4 * 32 * 20;  // room for 16 columns of every row's copies
 constexpr int kMinChunks = 4;  // of a unit's part, on average: less is not worth a join
 constexpr int kMaxParts = 64;  // CTAs that share a unit, on average at most
 constexpr uint32_t kTO = 2 * kKeys;     // O's first column, after two S buffers
 constexpr uint32_t kTmemCols = 256;
-#ifndef PA_CROSS_P_PARTS
-#define PA_CROSS_P_PARTS 2
-#endif
-constexpr int kPParts = PA_CROSS_P_PARTS;
 
 template <int D>
 struct Shape {
@@ -105,11 +107,14 @@ struct Shape {
   static constexpr int kK = kQ + kHalves * kQHalf;
   static constexpr int kV = kK + kStages * kStage;
   static constexpr int kBar = kV + kStages * kStage;
-  static constexpr int kSmem = kBar + 256 + 1024;       // + alignment
+  static constexpr int kSums = kBar + 256;               // the copies' sums (few rows)
+  static constexpr int smem(int copies) {                // + alignment
+    return kSums + (copies > 1 ? kSumFloats * 4 + kRows * 8 : 0) + 1024;
+  }
   static constexpr uint32_t kIdescQK = idesc_bf16(kRows, kKeys, 0, 0);
   static constexpr uint32_t kIdescPV = idesc_bf16(kRows, D, 0, 1);
   static_assert(kTO + D <= kTmemCols, "tensor memory");
-  static_assert(2 * kSmem <= 232448, "two CTAs an SM");
+  static_assert(2 * (smem(4) + 2048) <= 232448, "two CTAs an SM");
 };
 
 // A sequence's lengths, read and checked on the device.
@@ -388,7 +393,7 @@ __device__ __noinline__ void join(const CrossParams& p, const Part& it, int c0, 
 //   read the stage is done; s_done [2]: scores of a chunk ready; p_ready [2]:
 //   its weights written (an arrival a softmax warp); pv_done [2]: PV read them;
 //   q_full / q_free: a unit's Q landed / its last scores taken; o_free: O read.
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 2)
     cross_attention_kernel(const __grid_constant__ CUtensorMap tq,
                            const __grid_constant__ CUtensorMap tk,
@@ -415,6 +420,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kBar + 240);
   unsigned* last_slot = reinterpret_cast<unsigned*>(sm + S::kBar + 244);
   static_assert((4 * kStages + 9) * 8 <= 240, "barriers");
+  float* sums = reinterpret_cast<float*>(sm + S::kSums);                         // R > 1
+  float2* stats = reinterpret_cast<float2*>(sm + S::kSums + kSumFloats * 4);  // [128]
 
   if (tid == 0) {
     for (int i = 0; i < 4 * kStages + 9; ++i) mbar_init(bars + i, 1);
@@ -526,8 +533,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           mbar_arrive_expect_tx(q_full, S::kHalves * S::kQHalf, leader);
 #pragma unroll
           for (int h = 0; h < S::kHalves; ++h)
-            tma_3d(sm + S::kQ + h * S::kQHalf, &tq, 64 * h, a.kvh * p.group, a.q_row, q_full,
-                   leader);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              tma_3d(sm + S::kQ + h * S::kQHalf + r * (S::kQHalf / R), &tq, 64 * h,
+                     a.kvh * p.group, a.q_row, q_full, leader);
           ++items;
         }
       }
@@ -603,9 +612,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           const uint64_t v = vdesc + kk * (S::kHalves * S::kBox >> 4);
           umma_bf16_ts(tmem + kTO, tmem + sb * kKeys + 8 * kk, v, S::kIdescPV,
                        (c > 0 || kk > 0) ? 1u : 0u, leader);
-          if constexpr (kPParts == 2)
-            umma_bf16_ts(tmem + kTO, tmem + sb * kKeys + kKeys / 2 + 8 * kk, v, S::kIdescPV, 1u,
-                         leader);
+          umma_bf16_ts(tmem + kTO, tmem + sb * kKeys + kKeys / 2 + 8 * kk, v, S::kIdescPV, 1u,
+                       leader);
         }
         umma_commit(&pv_done[sb], leader);
         umma_commit(&v_free[st], leader);
@@ -615,10 +623,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (g > 0) wait(&pv_done[(g - 1) & 1], (g - 1) >> 1);
   } else {
     // ------------------------------------------------------------ softmax
+    constexpr int kTileRows = kRows / R, kCols = kKeys / R;  // rows; columns of S a thread takes
+    const int copy = warp / (4 / R);                         // of the rows: its columns of S
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t tO = tmem + lane_base + kTO;
+    const int row = tid & (kTileRows - 1);
     const int shift = 31 - __clz(p.group);
-    const int tok = tid >> shift, head = tid & (p.group - 1);  // row: token, head of the group
+    const int tok = row >> shift, head = row & (p.group - 1);  // row: token, head of the group
     const float sl2 = p.scale_log2;
     const float2 sl2x2 = make_float2(sl2, sl2);
     bool ok = true;  // sticky: this thread's waits all succeeded
@@ -628,7 +639,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     while (walk.next(p, it)) {
       const int qi = it.i0 + tok;
       const bool row_ok = qi < it.seq.n;
-      const bool warp_ok = it.i0 + ((warp * 32) >> shift) < it.seq.n;  // some row of the warp is
+      // some row of the warp is
+      const bool warp_ok = it.i0 + (((warp * 32) & (kTileRows - 1)) >> shift) < it.seq.n;
       const int64_t orow = static_cast<int64_t>(it.seq.q0 + (row_ok ? qi : 0)) * p.num_q_heads +
                            it.kvh * p.group + head;
       float m_used = -INFINITY;  // reference maximum of the exponentials (base 2)
@@ -636,20 +648,26 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int c = 0; c < it.count; ++c, ++g) {
         const int sb = g & 1;
         const uint32_t tS = tmem + lane_base + sb * kKeys;
-        const int valid = it.seq.src - (it.first + c) * kKeys;  // keys of this chunk
+        const int keys = it.seq.src - (it.first + c) * kKeys;  // of this chunk
+        const int valid = keys - copy * kCols;                 // of this thread's columns
         bool lok = ok && mbar_wait_bounded(&s_done[sb], (g >> 1) & 1, p.err);
         lok = __all_sync(kFullMask, lok);
         if (lok && warp_ok) {
           tc_fence_after();
-          uint32_t sv[kKeys];
+          uint32_t sv[kCols];
           auto scores = [&]() {
+            if constexpr (kCols >= 32) {
 #pragma unroll
-            for (int h = 0; h < kKeys / 32; ++h)
-              tmem_ld32(tS + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * h));
+              for (int h = 0; h < kCols / 32; ++h)
+                tmem_ld32(tS + copy * kCols + 32 * h,
+                          *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * h));
+            } else {
+              tmem_ld16(tS + copy * kCols, *reinterpret_cast<uint32_t(*)[16]>(sv));
+            }
             tmem_wait_ld();
-            if (valid < kKeys) {
+            if (valid < kCols) {
 #pragma unroll
-              for (int j = 0; j < kKeys; ++j)
+              for (int j = 0; j < kCols; ++j)
                 if (j >= valid) sv[j] = __float_as_uint(-INFINITY);
             }
           };
@@ -660,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             float2 ps4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                              make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int j = 0; j < kKeys; j += 2) {
+            for (int j = 0; j < kCols; j += 2) {
               const float2 x = __ffma2_rn(
                   make_float2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), sl2x2, neg2);
               const float2 e = make_float2(ex2(x.x), ex2(x.y));
@@ -673,17 +691,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           };
           scores();
           if (c > 0) weights();
-          // A weight above 2^8 makes a sum above 2^7: only then, and in a
-          // part's first chunk, are the maxima taken.
-          const bool want = m_used == -INFINITY || !(psum <= 128.f);
+          // A weight above 2^8 makes a sum above 2^7: only then, and while a row has
+          // seen nothing (a part's first chunk; copies whose columns lie past the
+          // source's end have weights of 0), are the maxima taken.
+          const bool want = (m_used == -INFINITY && valid > 0) || !(psum <= 128.f);
           float alpha = 1.f;
-          if (__any_sync(kFullMask, want && row_ok)) {
+          if (__any_sync(kFullMask, want && row_ok) || c == 0) {
             if (c > 0) scores();
             float m8[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) m8[k] = __uint_as_float(sv[k]);
 #pragma unroll
-            for (int j = 8; j < kKeys; ++j) m8[j & 7] = fmaxf(m8[j & 7], __uint_as_float(sv[j]));
+            for (int j = 8; j < kCols; ++j) m8[j & 7] = fmaxf(m8[j & 7], __uint_as_float(sv[j]));
 #pragma unroll
             for (int k = 0; k < 4; ++k) m8[k] = fmaxf(m8[k], m8[k + 4]);
             const float mx = fmaxf(fmaxf(m8[0], m8[2]), fmaxf(m8[1], m8[3])) * sl2;
@@ -716,44 +735,64 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
             }
           }
-          // P over the scores' own columns: bf16 pairs, hi parts, then lo
+          // P over the scores' columns: bf16 pairs, hi parts, then lo; a copy of
+          // the rows has weights in its own columns and zeros in the others
+          if constexpr (R == 1) {
 #pragma unroll
-          for (int h = 0; h < kKeys / 32; ++h) {
-            uint32_t(&v)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * h);
-            if constexpr (kPParts == 2) {
-              store_p(tS + 16 * h, tS + kKeys / 2 + 16 * h, v);
-            } else {
-              uint32_t w[16];
+            for (int h = 0; h < kKeys / 32; ++h)
+              store_p(tS + 16 * h, tS + kKeys / 2 + 16 * h,
+                      *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * h));
+          } else {
+            uint32_t wh[kCols / 2], wl[kCols / 2];
+            uint32_t none[kCols / 2];
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[2 * k]),
-                                                               __uint_as_float(v[2 * k + 1]));
-                w[k] = *reinterpret_cast<const uint32_t*>(&x);
+            for (int k = 0; k < kCols / 2; ++k) {
+              split_p(sv[2 * k], sv[2 * k + 1], wh[k], wl[k]);
+              none[k] = 0;
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const uint32_t th = tS + r * (kCols / 2), tl = th + kKeys / 2;
+              if constexpr (R == 2) {
+                if (r == copy) {
+                  tmem_st16(th, wh);
+                  tmem_st16(tl, wl);
+                } else {
+                  tmem_st16(th, none);
+                  tmem_st16(tl, none);
+                }
+              } else {
+                if (r == copy) {
+                  tmem_st8(th, wh);
+                  tmem_st8(tl, wl);
+                } else {
+                  tmem_st8(th, none);
+                  tmem_st8(tl, none);
+                }
               }
-              tmem_st16(tS + 16 * h, w);
             }
           }
           tmem_wait_st();
         }
         // V of keys past the source's end may hold anything (a partly filled
         // block, blocks not loaded): P is 0 there, but 0 * NaN is not.
-        if (lok && valid < kKeys) {
+        if (lok && keys < kKeys) {
           const int st = g % kStages;
           lok = mbar_wait_bounded(&v_full[st], (g / kStages) & 1, p.err);
-          if (lok && tid >= valid && tid < kKeys) {
+          if (lok && tid >= keys && tid < kKeys) {
             const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int hh = 0; hh < S::kHalves; ++hh) {
-              uint4* row = reinterpret_cast<uint4*>(
+              uint4* dst = reinterpret_cast<uint4*>(
                   sm + S::kV + st * S::kStage + ((tid / kBS) * S::kHalves + hh) * S::kBox +
                   (tid % kBS) * 128);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) row[k] = z;
+              for (int k = 0; k < 8; ++k) dst[k] = z;
             }
           }
+          fence_proxy_async();
         }
         ok = ok && lok;
-        fence_proxy_async();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_ready[sb]);
@@ -766,41 +805,97 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool shared = it.count < it.seq.chunks;  // with other CTAs
       // (a part that opens its unit is its CTA's last, any other its first)
       const int64_t place = (static_cast<int64_t>(blockIdx.x) * 2 + (it.first == 0)) * p.ws_rows;
-      const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
-      if (warp_ok && lok) {
+      // The copies' shares of a row: against their common maximum, summed through
+      // shared memory, some columns at a time.
+      float factor = 1.f, total = l_sum;
+      if constexpr (R > 1) {
+        stats[tid] = make_float2(m_used, l_sum);
+        asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+        float top = m_used;
+#pragma unroll
+        for (int r = 0; r < R; ++r) top = fmaxf(top, stats[r * kTileRows + row].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        total = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float2 e = stats[r * kTileRows + row];
+          total = fmaf(e.y, ex2(e.x - ref), total);
+        }
+        factor = ex2(m_used - ref);
+        m_used = top;
+      }
+      const float inv = shared ? factor : total > 0.f ? factor / total : 0.f;
+      auto put = [&](int col, const float4& v) {  // four columns of this thread's row
+        if (shared) {
+          *reinterpret_cast<float4*>(p.ws_o + (place + row) * D + col) = v;
+        } else {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y);
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z, v.w);
+          *reinterpret_cast<uint2*>(p.out + orow * D + col) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                         *reinterpret_cast<const uint32_t*>(&hi));
+        }
+      };
+      if constexpr (R == 1) {
+        if (warp_ok && lok) {
 #pragma unroll 1
-        for (int q4 = 0; q4 < D / 16; ++q4) {
-          uint32_t o[16];
-          tmem_ld16(tO + 16 * q4, o);
-          tmem_wait_ld();
-          if (!row_ok) continue;
-          if (shared) {
-            uint4* w = reinterpret_cast<uint4*>(p.ws_o + (place + tid) * D + 16 * q4);
+          for (int q4 = 0; q4 < D / 16; ++q4) {
+            uint32_t o[16];
+            tmem_ld16(tO + 16 * q4, o);
+            tmem_wait_ld();
+            if (!row_ok) continue;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              w[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          } else {
+              put(16 * q4 + 4 * k,
+                  make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
+                              __uint_as_float(o[4 * k + 2]) * inv,
+                              __uint_as_float(o[4 * k + 3]) * inv));
+          }
+        }
+      } else {
+        // columns of a round: what the buffer holds of the rows that there are
+        const int rows = min(kTileRows, (it.seq.n - it.i0) << shift);
+        int round = 16;
+        while (round < D && rows * R * (2 * round + 4) <= kSumFloats) round *= 2;
+        const int pitch = round + 4;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += round) {
+          if (warp_ok && lok) {
+#pragma unroll 1
+            for (int q4 = 0; q4 < round / 16; ++q4) {
+              uint32_t o[16];
+              tmem_ld16(tO + c0 + 16 * q4, o);
+              tmem_wait_ld();
+              if (!row_ok) continue;
+              float4* dst = reinterpret_cast<float4*>(sums + (copy * rows + row) * pitch + 16 * q4);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 h2 =
-                    __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]) * inv,
-                                          __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-                w[e] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
-              *reinterpret_cast<uint4*>(p.out + orow * D + 16 * q4 + 8 * k) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
+              for (int k = 0; k < 4; ++k)
+                dst[k] = make_float4(
+                    __uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
+                    __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
             }
           }
+          asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+          if (row_ok && lok) {
+            for (int k = copy; k < round / 4; k += R) {
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int r = 0; r < R; ++r) {
+                const float4 x = *reinterpret_cast<const float4*>(sums + (r * rows + row) * pitch +
+                                                                  4 * k);
+                v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+              }
+              put(c0 + 4 * k, v);
+            }
+          }
+          asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
         }
       }
       __syncwarp();
       tc_fence_before();
       if (lane == 0) mbar_arrive(o_free);
       if (shared) {
-        if (row_ok && lok) p.ws_ml[place + tid] = make_float2(m_used, l_sum);
+        if (row_ok && lok && copy == 0) p.ws_ml[place + row] = make_float2(m_used, total);
         // the last CTA of the unit joins its parts (counted at its first CTA)
         const int c0 = owner(run, it.unit);
         const int parts = owner(run, it.unit + it.seq.chunks - 1) - c0 + 1;
@@ -837,27 +932,37 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <int D>
+template <int D, int R>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const CrossParams& p, int ctas, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
-  auto kernel = cross_attention_kernel<D>;
+  auto kernel = cross_attention_kernel<D, R>;
+  constexpr int smem = Shape<D>::smem(R);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(smem_set.load() & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Shape<D>::kSmem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     smem_set.fetch_or(bit);
   }
-  return launch_pdl(kernel, dim3(ctas), dim3(kThreads), Shape<D>::kSmem, stream, tq, tk, tv, p);
+  return launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem, stream, tq, tk, tv, p);
+}
+
+template <int D>
+cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                     const CrossParams& p, int copies, int ctas, cudaStream_t stream) {
+  switch (copies) {
+    case 4: return launch<D, 4>(tq, tk, tv, p, ctas, stream);
+    case 2: return launch<D, 2>(tq, tk, tv, p, ctas, stream);
+    default: return launch<D, 1>(tq, tk, tv, p, ctas, stream);
+  }
 }
 
 // The K pool as [num_blocks * Hkv * 16 rows][D] bf16, boxes of 16 rows x 64
 // columns; the V pool as [D / 64 halves][rows][64], boxes of a block's 16 rows in
-// every half; q as [T][Hq][D], tokens q_stride elements apart, boxes of 128 / group
+// every half; q as [T][Hq][D], tokens q_stride elements apart, boxes of rows / group
 // tokens x group heads x 64 columns; 128-byte swizzle.
 bool encode_rows(CUtensorMap* map, const void* base, int head_dim, int64_t rows) {
   const auto enc = tensor_map_encoder();
@@ -885,7 +990,7 @@ bool encode_blocks(CUtensorMap* map, const void* base, int head_dim, int64_t row
          CUDA_SUCCESS;
 }
 bool encode_queries(CUtensorMap* map, const void* base, int head_dim, int num_q_heads, int total_q,
-                    int64_t q_stride, int group) {
+                    int64_t q_stride, int group, int rows) {
   const auto enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim),
@@ -894,7 +999,7 @@ bool encode_queries(CUtensorMap* map, const void* base, int head_dim, int num_q_
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
                                  static_cast<cuuint64_t>(q_stride) * 2};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group),
-                             static_cast<cuuint32_t>(kRows / group)};
+                             static_cast<cuuint32_t>(rows / group)};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -936,10 +1041,14 @@ pa_status cross_impl(void* out, const void* q, int64_t q_stride, const void* k_c
     return PA_ERR_INVALID_ARG;
   CrossParams p{};
   p.group = group;
-  p.tile_tokens = kRows / group;
   p.max_query_len = max_query_len < total_query_tokens ? max_query_len : total_query_tokens;
+  // Copies of the rows in a tile: 4 where a sequence has 32 rows at most, 2 where 64.
+  const int rows_each = cross_rows(p.max_query_len, group);
+  const int copies = rows_each <= 32 ? 4 : rows_each <= 64 ? 2 : 1;
+  p.tile_tokens = kRows / copies / group;
   CUtensorMap tq, tk, tv;
-  if (!encode_queries(&tq, q, head_dim, num_q_heads, total_query_tokens, q_stride, group) ||
+  if (!encode_queries(&tq, q, head_dim, num_q_heads, total_query_tokens, q_stride, group,
+                      kRows / copies) ||
       !encode_rows(&tk, k_cache, head_dim, rows) || !encode_blocks(&tv, v_cache, head_dim, rows))
     return cuda_fail(cudaErrorInvalidValue);  // tensor-map encoding refused the buffers
   p.out = static_cast<__nv_bfloat16*>(out);
@@ -967,8 +1076,8 @@ pa_status cross_impl(void* out, const void* q, int64_t q_stride, const void* k_c
     ctas = static_cast<int>(std::min<int64_t>(ws_ctas, most * num_kv_heads));
   return launch_or_keep(
       [=](cudaStream_t s) {
-        return head_dim == 64 ? launch<64>(tq, tk, tv, p, ctas, s)
-                              : launch<128>(tq, tk, tv, p, ctas, s);
+        return head_dim == 64 ? launch_d<64>(tq, tk, tv, p, copies, ctas, s)
+                              : launch_d<128>(tq, tk, tv, p, copies, ctas, s);
       },
       keep, stream);
 }

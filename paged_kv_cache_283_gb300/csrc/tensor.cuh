@@ -131,6 +131,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
       "r"(v[15]));
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
+}
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -185,22 +190,24 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, unsigned by
       : "memory");
 }
 
-// 32 weights as hi + lo bf16 parts, pairs packed, 16 columns each at th and tl
-// of this thread's TMEM lane: hi = p truncated to bf16 (its upper 16 bits), lo
-// = bf16(p - hi) (p - hi is exact and below 2^-7 p, so hi + lo keeps p to
+// Two weights as hi + lo bf16 parts, packed: hi = p truncated to bf16 (its upper 16
+// bits), lo = bf16(p - hi) (p - hi is exact and below 2^-7 p, so hi + lo keeps p to
 // ~2^-16).
+__device__ __forceinline__ void split_p(uint32_t ua, uint32_t ue, uint32_t& hi, uint32_t& lo) {
+  hi = __byte_perm(ua, ue, 0x7632);
+  const float2 r2 = __fadd2_rn(
+      make_float2(__uint_as_float(ua), __uint_as_float(ue)),
+      make_float2(-__uint_as_float(ua & 0xFFFF0000u), -__uint_as_float(ue & 0xFFFF0000u)));
+  const __nv_bfloat162 l = __floats2bfloat162_rn(r2.x, r2.y);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// 32 weights as hi + lo parts (split_p), 16 columns each at th and tl of this
+// thread's TMEM lane.
 __device__ __forceinline__ void store_p(uint32_t th, uint32_t tl, const uint32_t (&v)[32]) {
   uint32_t wh[16], wl[16];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const uint32_t ua = v[2 * k], ue = v[2 * k + 1];
-    wh[k] = __byte_perm(ua, ue, 0x7632);
-    const float2 r2 = __fadd2_rn(
-        make_float2(__uint_as_float(ua), __uint_as_float(ue)),
-        make_float2(-__uint_as_float(ua & 0xFFFF0000u), -__uint_as_float(ue & 0xFFFF0000u)));
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(r2.x, r2.y);
-    wl[k] = *reinterpret_cast<const uint32_t*>(&lo);
-  }
+  for (int k = 0; k < 16; ++k) split_p(v[2 * k], v[2 * k + 1], wh[k], wl[k]);
   tmem_st16(th, wh);
   tmem_st16(tl, wl);
 }
