@@ -75,37 +75,97 @@ __device__ __forceinline__ double unordered64(uint64_t o) {
   return __longlong_as_double(o & 0x8000000000000000ull ? o ^ 0x8000000000000000ull : ~o);
 }
 
+// Eight logits in 32-bit words: unpacked in pairs, and, two in a word where they
+// are 16-bit, compared without unpacking.
 template <typename T>
-struct Words;  // eight logits in 32-bit words
+struct Words;
 template <>
 struct Words<float> {
   static constexpr int N = 8;
-  __device__ static float get(const uint32_t (&w)[8], int i) { return __uint_as_float(w[i]); }
-  __device__ static void set(uint32_t (&w)[8], int i, float x) { w[i] = __float_as_uint(x); }
+  static constexpr float kLowest = -FLT_MAX;
+  using Top = float;
+  __device__ static float2 pair(const uint32_t (&w)[8], int i) {
+    return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+  __device__ static void lowest(uint32_t (&w)[8], int i) { w[i] = 0xff800000u; }
+  // the larger of top and the eight, NaN passed over
+  __device__ static void raise(float& top, const uint32_t (&w)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; k += 2)
+      top = fmaxf(top, fmaxf(__uint_as_float(w[k]), __uint_as_float(w[k + 1])));
+  }
+  __device__ static float none() { return -INFINITY; }
+  __device__ static float value(float top) { return top; }
+  // bit i: logit i is at least `bound`
+  __device__ static uint32_t reach(const uint32_t (&w)[8], float bound) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bits |= __uint_as_float(w[k]) >= bound ? 1u << k : 0u;
+    return bits;
+  }
+};
+template <typename T2>
+struct Halves {
+  static constexpr int N = 4;
+  using Top = T2;
+  __device__ static T2 word(uint32_t w) { return *reinterpret_cast<const T2*>(&w); }
+  __device__ static void lowest(uint32_t (&w)[4], int i, uint32_t bits) {
+    w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | bits << 16 : (w[i / 2] & 0xffff0000u) | bits;
+  }
+  __device__ static void raise(T2& top, const uint32_t (&w)[4]) {
+    top = __hmax2(top, __hmax2(__hmax2(word(w[0]), word(w[1])), __hmax2(word(w[2]), word(w[3]))));
+  }
+  __device__ static uint32_t reach2(const uint32_t (&w)[4], T2 bound) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t m = __hge2_mask(word(w[k]), bound);  // 0xffff in each half that reaches
+      bits |= m & (0x00010001u << k);
+    }
+    // low halves are bits 0 .. 3 (logits 0, 2, 4, 6), high ones bits 16 .. 19
+    return bits;
+  }
 };
 template <>
-struct Words<__nv_bfloat16> {
-  static constexpr int N = 4;
-  __device__ static float get(const uint32_t (&w)[4], int i) {
-    return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+struct Words<__nv_bfloat16> : Halves<__nv_bfloat162> {
+  static constexpr float kLowest = -3.38953139e38f;
+  __device__ static float2 pair(const uint32_t (&w)[4], int i) { return bf16x2_to_float2(w[i]); }
+  __device__ static void lowest(uint32_t (&w)[4], int i) {
+    Halves<__nv_bfloat162>::lowest(w, i, 0xff80u);
   }
-  __device__ static void set(uint32_t (&w)[4], int i, float x) {
-    const uint32_t u = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-    w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | (u << 16) : (w[i / 2] & 0xffff0000u) | u;
+  __device__ static __nv_bfloat162 none() { return word(0xff80ff80u); }
+  __device__ static float value(__nv_bfloat162 t) {
+    return fmaxf(__low2float(t), __high2float(t));
+  }
+  __device__ static uint32_t reach(const uint32_t (&w)[4], float bound) {
+    return reach2(w, __float2bfloat162_rn(bound));
   }
 };
 template <>
-struct Words<__half> {
-  static constexpr int N = 4;
-  __device__ static float get(const uint32_t (&w)[4], int i) {
-    const __half2 h = *reinterpret_cast<const __half2*>(&w[i / 2]);
-    return i & 1 ? __high2float(h) : __low2float(h);
+struct Words<__half> : Halves<__half2> {
+  static constexpr float kLowest = -65504.f;
+  __device__ static float2 pair(const uint32_t (&w)[4], int i) { return __half22float2(word(w[i])); }
+  __device__ static void lowest(uint32_t (&w)[4], int i) {
+    Halves<__half2>::lowest(w, i, 0xfc00u);
   }
-  __device__ static void set(uint32_t (&w)[4], int i, float x) {
-    const uint32_t u = __half_as_ushort(__float2half_rn(x));
-    w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | (u << 16) : (w[i / 2] & 0xffff0000u) | u;
+  __device__ static __half2 none() { return word(0xfc00fc00u); }
+  __device__ static float value(__half2 t) { return fmaxf(__low2float(t), __high2float(t)); }
+  __device__ static uint32_t reach(const uint32_t (&w)[4], float bound) {
+    return reach2(w, __float2half2_rn(bound));
   }
 };
+// The logit of a bit of reach().
+template <typename T>
+__device__ __forceinline__ int logit_of(int bit) {
+  return sizeof(T) == 4 ? bit : 2 * (bit & 15) + (bit >> 4);
+}
+
+// A logit as it counts: NaN and +inf are hidden.
+template <typename T>
+__device__ __forceinline__ float visible(T x) {
+  const float f = static_cast<float>(x);
+  return f < INFINITY ? f : -INFINITY;
+}
 
 struct Shared {
   uint64_t v[kRoom];
@@ -113,22 +173,30 @@ struct Shared {
   Key best[kWarps];
   Key last;
   float group_max[64];
-  uint64_t group_key[64];
+  uint64_t group_key[64], warp_key[kWarps][32];
   float m[kWarps], s[kWarps];
+  uint64_t out_v[kBeamMaxKeep];  // the K found, first to last
+  uint64_t out_i[kBeamMaxKeep];
+  double lse[kBeamMaxBeams];
+  int place[kBeamMaxKeep];
   uint64_t bound;
   int count;
   unsigned arrived;
 };
+__device__ __forceinline__ Shared& shared() {
+  __shared__ Shared sh;
+  return sh;
+}
 
-// The K largest of the CTA's keys, one by one: each thread offers through
-// scan(prev) its largest key after `prev`.  For few threads' many equal values.
-template <typename Scan, typename Emit>
-__device__ void one_by_one(Shared& sh, int k, Scan&& scan, Emit&& emit) {
+// The K first of the CTA's keys, one by one, to sh.out_*: each thread offers
+// through scan(prev, first) its first key after `prev`.  For many equal values.
+template <typename Scan>
+__device__ __forceinline__ void one_by_one(int k, Scan&& scan) {
+  Shared& sh = shared();
   Key prev{~0ull, 0};
-  bool first = true;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int r = 0; r < k; ++r) {
-    Key best = scan(prev, first);
+    Key best = scan(prev, r == 0);
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) {
       Key o;
@@ -142,52 +210,152 @@ __device__ void one_by_one(Shared& sh, int k, Scan&& scan, Emit&& emit) {
       for (int w = 1; w < kWarps; ++w)
         if (before(sh.best[w], best)) best = sh.best[w];
       sh.last = best;
-      emit(r, best);
+      sh.out_v[r] = best.v;
+      sh.out_i[r] = best.i;
     }
     __syncthreads();
     prev = sh.last;
-    first = false;
     if (prev.i == kNone) {  // no more
-      for (int q = r + 1 + threadIdx.x; q < k; q += kThreads) emit(q, nothing());
+      for (int q = r + 1 + threadIdx.x; q < k; q += kThreads) {
+        sh.out_v[q] = 0;
+        sh.out_i[q] = kNone;
+      }
       break;
     }
   }
   __syncthreads();
 }
 
-// The K first of sh.v / sh.i[0 .. count), count <= kRoom, to emit(rank, key).
-template <typename Emit>
-__device__ void best_of_room(Shared& sh, int count, int k, Emit&& emit) {
-  if (count <= kRank) {
+__device__ __noinline__ void one_by_one_of_room(int count, int k) {
+  Shared& sh = shared();
+  one_by_one(k, [&](const Key& prev, bool first) {
+    Key best = nothing();
     for (int c = threadIdx.x; c < count; c += kThreads) {
-      const Key mine{sh.v[c], sh.i[c]};
-      int rank = 0;
-      for (int o = 0; o < count; ++o) rank += before(Key{sh.v[o], sh.i[o]}, mine);
-      if (rank < k) emit(rank, mine);
+      const Key x{sh.v[c], sh.i[c]};
+      if ((first || before(prev, x)) && before(x, best)) best = x;
     }
-    for (int r = count + threadIdx.x; r < k; r += kThreads) emit(r, nothing());
+    return best;
+  });
+}
+
+template <typename T>
+__device__ __noinline__ void one_by_one_of_row(const T* row, int begin, int end, int k) {
+  one_by_one(k, [&](const Key& prev, bool first) {
+    Key best = nothing();
+    for (int e = begin + threadIdx.x; e < end; e += kThreads) {
+      const float x = visible(row[e]);
+      const Key key{ordered(x), static_cast<uint64_t>(e)};
+      if (x > -INFINITY && (first || before(prev, key)) && before(key, best)) best = key;
+    }
+    return best;
+  });
+}
+
+// The K first of sh.v / sh.i[0 .. count), count <= kRoom, to sh.out_*.  Each is
+// compared with every other: four neighbouring lanes a candidate, a quarter of
+// them each.
+__device__ __forceinline__ void best_of_room(int count, int k) {
+  Shared& sh = shared();
+  if (count <= kRank) {
+    const int seg = threadIdx.x & 3;
+    for (int c0 = 0; c0 < count; c0 += kThreads / 4) {
+      const int c = c0 + static_cast<int>(threadIdx.x >> 2);
+      const Key mine = c < count ? Key{sh.v[c], sh.i[c]} : nothing();
+      int rank = 0;
+#pragma unroll 4
+      for (int o = seg; o < count; o += 4) rank += before(Key{sh.v[o], sh.i[o]}, mine);
+      rank += __shfl_xor_sync(kFullMask, rank, 1);
+      rank += __shfl_xor_sync(kFullMask, rank, 2);
+      if (seg == 0 && c < count && rank < k) {
+        sh.out_v[rank] = mine.v;
+        sh.out_i[rank] = mine.i;
+      }
+    }
+    for (int r = count + threadIdx.x; r < k; r += kThreads) {
+      sh.out_v[r] = 0;
+      sh.out_i[r] = kNone;
+    }
     __syncthreads();
   } else {
-    one_by_one(
-        sh, k,
-        [&](const Key& prev, bool first) {
-          Key best = nothing();
-          for (int c = threadIdx.x; c < count; c += kThreads) {
-            const Key x{sh.v[c], sh.i[c]};
-            if ((first || before(prev, x)) && before(x, best)) best = x;
-          }
-          return best;
-        },
-        emit);
+    one_by_one_of_room(count, k);
   }
 }
 
+// The K-th largest (rank K - 1) of the groups' values, by the first warps.
+__device__ __forceinline__ uint64_t bits_of(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ uint64_t bits_of(uint64_t x) { return x; }
+template <typename V>
+__device__ __forceinline__ void kth_of_groups(const V* value, int groups, int k, uint64_t* out) {
+  if (threadIdx.x < static_cast<unsigned>(groups)) {
+    const V x = value[threadIdx.x];
+    int rank = 0;
+#pragma unroll 8
+    for (int g = 0; g < groups; ++g) {
+      const V o = value[g];
+      rank += o > x || (o == x && g < static_cast<int>(threadIdx.x));
+    }
+    if (rank == k - 1) *out = bits_of(x);
+  }
+}
+
+// A part's find (beam w, `key` of the workspace) as a candidate of its search.
+__device__ __forceinline__ Key candidate(const BeamParams& p, int search, int w, bool first,
+                                         uint64_t key) {
+  const int64_t row = static_cast<int64_t>(search) * p.beams + w;
+  const float score = p.scores[row];
+  if (!isfinite(score)) return nothing();
+  const uint64_t beam = static_cast<uint64_t>(w) << 59;
+  if (p.finished && p.finished[row])  // its one continuation
+    return first ? Key{ordered(static_cast<double>(score)), beam | static_cast<uint32_t>(p.eos)}
+                 : nothing();
+  if (key == 0) return nothing();
+  const uint32_t o = static_cast<uint32_t>(key >> 32);
+  const double total =
+      static_cast<double>(score) + (static_cast<double>(unordered(o)) - shared().lse[w]);
+  return Key{ordered(total), beam | static_cast<uint64_t>(~o) << 27 |
+                                 static_cast<uint32_t>(~static_cast<uint32_t>(key))};
+}
+__device__ __forceinline__ Key candidate(const BeamParams& p, int search, int c, uint64_t key) {
+  const int w = c / (p.parts * p.keep);
+  return candidate(p, search, w, c == w * p.parts * p.keep, key);
+}
+
+__device__ __noinline__ void one_by_one_of_parts(const BeamParams* p, int search) {
+  const int total = p->beams * p->parts * p->keep;
+  const uint64_t* parts = p->ws_keys + static_cast<int64_t>(search) * total;
+  one_by_one(p->keep, [&](const Key& prev, bool first) {
+    Key best = nothing();
+    for (int c = threadIdx.x; c < total; c += kThreads) {
+      const Key x = candidate(*p, search, c, __ldcg(parts + c));
+      if ((first || before(prev, x)) && before(x, best)) best = x;
+    }
+    return best;
+  });
+}
+
 // Joins the parts of a search: the last CTA's work.
-__device__ void merge(const BeamParams& p, Shared& sh, int search) {
-  __shared__ double lse[kBeamMaxBeams];
-  __shared__ uint64_t out_v[kBeamMaxKeep];
-  __shared__ uint64_t out_i[kBeamMaxKeep];
+__device__ __forceinline__ void merge(const BeamParams& p, int search) {
+  Shared& sh = shared();
   const int tid = threadIdx.x, W = p.beams, K = p.keep;
+  const int total = W * p.parts * K;
+  const uint64_t* parts = p.ws_keys + static_cast<int64_t>(search) * total;
+  // Thread t takes candidates t, t + 256, .. of the parts' firsts, then their seconds
+  // and so on, and group g of `groups` the threads t = g mod groups: every group has
+  // firsts of every beam, and the bound below is a good one.
+  const int lists = W * p.parts;
+  auto place = [&](int c) {
+    const int r = c / lists;
+    return (c - r * lists) * K + r;
+  };
+  constexpr int kHeld = 2;  // candidates of a thread that stay in registers
+  uint64_t raw[kHeld];
+  int at[kHeld];
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) {
+    const int c = tid + q * kThreads;
+    at[q] = place(c);
+    raw[q] = c < total ? __ldcg(parts + at[q]) : 0;
+  }
   for (int w = tid >> 5; w < W; w += kWarps) {  // each row's log-sum from its parts
     const float2* ms = p.ws_sums + (static_cast<int64_t>(search) * W + w) * p.parts;
     float top = -INFINITY;
@@ -197,58 +365,49 @@ __device__ void merge(const BeamParams& p, Shared& sh, int search) {
     double s = 0.0;
     for (int c = tid & 31; c < p.parts; c += 32) {
       const float2 part = __ldcg(ms + c);
-      if (part.y > 0.f)
-        s += static_cast<double>(part.y) * exp(static_cast<double>(part.x) - top);
+      if (part.y > 0.f) s += part.y * ex2((part.x - top) * kLog2e);
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(kFullMask, s, m);
-    if ((tid & 31) == 0) lse[w] = s > 0.0 ? static_cast<double>(top) + log(s) : 0.0;
+    if ((tid & 31) == 0) sh.lse[w] = s > 0.0 ? static_cast<double>(top) + log(s) : 0.0;
   }
   if (tid == 0) sh.count = 0;
   __syncthreads();
-  const int per_row = p.parts * K, total = W * per_row;
-  auto candidate = [&](int c) -> Key {
-    const int w = c / per_row;
-    const int64_t row = static_cast<int64_t>(search) * W + w;
-    const float score = p.scores[row];
-    if (!isfinite(score)) return nothing();
-    const uint64_t beam = static_cast<uint64_t>(w) << 59;
-    if (p.finished && p.finished[row])  // its one continuation
-      return c % per_row == 0
-                 ? Key{ordered(static_cast<double>(score)), beam | static_cast<uint32_t>(p.eos)}
-                 : nothing();
-    const uint64_t key = __ldcg(p.ws_keys + row * per_row + c % per_row);
-    if (key == 0) return nothing();
-    const uint32_t o = static_cast<uint32_t>(key >> 32);
-    const double total = static_cast<double>(score) + (static_cast<double>(unordered(o)) - lse[w]);
-    return Key{ordered(total), beam | static_cast<uint64_t>(~o) << 27 |
-                                   static_cast<uint32_t>(~static_cast<uint32_t>(key))};
-  };
   // the K-th largest of the groups' maxima bounds the K-th largest of all
-  Key mine = nothing();
-  for (int c = tid; c < total; c += kThreads) {
-    const Key x = candidate(c);
-    if (before(x, mine)) mine = x;
+  auto nth = [&](int c) {
+    const int a = place(c);
+    return candidate(p, search, a, __ldcg(parts + a));
+  };
+  Key held[kHeld];
+  uint64_t gm = 0;
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) {
+    held[q] = tid + q * kThreads < total ? candidate(p, search, at[q], raw[q]) : nothing();
+    gm = held[q].v > gm ? held[q].v : gm;
   }
-  uint64_t gm = mine.v;
-  const int lanes = kThreads / p.groups;
-  for (int m = 1; m < lanes; m <<= 1) {
+  for (int c = tid + kHeld * kThreads; c < total; c += kThreads) {
+    const Key x = nth(c);
+    gm = x.v > gm ? x.v : gm;
+  }
+  for (int m = p.groups; m < 32; m <<= 1) {
     const uint64_t o = __shfl_xor_sync(kFullMask, gm, m);
     gm = o > gm ? o : gm;
   }
-  if (tid % lanes == 0) sh.group_key[tid / lanes] = gm;
+  sh.warp_key[tid >> 5][tid & 31] = gm;
   __syncthreads();
-  if (tid < p.groups) {
-    const uint64_t x = sh.group_key[tid];
-    int rank = 0;
-    for (int g = 0; g < p.groups; ++g)
-      rank += sh.group_key[g] > x || (sh.group_key[g] == x && g < tid);
-    if (rank == K - 1) sh.bound = x;
+  if (tid < p.groups) {  // (64 groups: of every second warp)
+    uint64_t x = 0;
+    for (int w = tid >> 5; w < kWarps; w += p.groups > 32 ? 2 : 1) {
+      const uint64_t o = sh.warp_key[w][tid & 31];
+      x = o > x ? o : x;
+    }
+    sh.group_key[tid] = x;
   }
   __syncthreads();
+  kth_of_groups(sh.group_key, p.groups, K, &sh.bound);
+  __syncthreads();
   const uint64_t bound = sh.bound;
-  for (int c = tid; c < total; c += kThreads) {
-    const Key x = candidate(c);
+  auto take = [&](const Key& x) {
     if (x.i != kNone && x.v >= bound) {
       const int at = atomicAdd(&sh.count, 1);
       if (at < kRoom) {
@@ -256,65 +415,48 @@ __device__ void merge(const BeamParams& p, Shared& sh, int search) {
         sh.i[at] = x.i;
       }
     }
-  }
-  __syncthreads();
-  auto emit = [&](int r, const Key& k) {
-    out_v[r] = k.v;
-    out_i[r] = k.i;
   };
-  if (sh.count <= kRoom) {
-    best_of_room(sh, sh.count, K, emit);
-  } else {
-    one_by_one(
-        sh, K,
-        [&](const Key& prev, bool first) {
-          Key best = nothing();
-          for (int c = tid; c < total; c += kThreads) {
-            const Key x = candidate(c);
-            if ((first || before(prev, x)) && before(x, best)) best = x;
-          }
-          return best;
-        },
-        emit);
-  }
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) take(held[q]);
+  for (int c = tid + kHeld * kThreads; c < total; c += kThreads)
+    take(nth(c));
   __syncthreads();
+  const int count = sh.count;
+  if (count <= kRoom)
+    best_of_room(count, K);
+  else
+    one_by_one_of_parts(&p, search);
   // Places: by rank; or (in_place, K = W) the first child of a beam keeps its
   // parent's place and the others take the free ones in order.
-  __shared__ int place[kBeamMaxKeep];
-  if (tid == 0) {
+  if (p.in_place && tid == 0) {
     unsigned taken = 0, homes = 0;
-    if (p.in_place) {
-      for (int r = 0; r < K; ++r) {
-        if (out_i[r] == kNone) continue;
-        const unsigned w = static_cast<unsigned>(out_i[r] >> 59);
-        if (!(taken >> w & 1u)) {
-          taken |= 1u << w;
-          homes |= 1u << r;
-          place[r] = static_cast<int>(w);
-        }
+    for (int r = 0; r < K; ++r) {
+      if (sh.out_i[r] == kNone) continue;
+      const unsigned w = static_cast<unsigned>(sh.out_i[r] >> 59);
+      if (!(taken >> w & 1u)) {
+        taken |= 1u << w;
+        homes |= 1u << r;
+        sh.place[r] = static_cast<int>(w);
       }
-      int next = 0;
-      for (int r = 0; r < K; ++r) {
-        if (homes >> r & 1u) continue;
-        while (taken >> next & 1u) ++next;
-        place[r] = next++;
-      }
-    } else {
-      for (int r = 0; r < K; ++r) place[r] = r;
+    }
+    int next = 0;
+    for (int r = 0; r < K; ++r) {
+      if (homes >> r & 1u) continue;
+      while (taken >> next & 1u) ++next;
+      sh.place[r] = next++;
     }
   }
-  __syncthreads();
   // (K <= kThreads; the outputs may be the inputs' buffers: read, then written)
   static_assert(kBeamMaxKeep <= kThreads, "a thread per output");
-  const bool some = tid < K && out_i[tid] != kNone;
-  const int w = some ? static_cast<int>(out_i[tid] >> 59) : 0;
-  const int token = some ? static_cast<int>(out_i[tid] & kTokenMask) : -1;
+  const bool some = tid < K && sh.out_i[tid] != kNone;
+  const int w = some ? static_cast<int>(sh.out_i[tid] >> 59) : 0;
+  const int token = some ? static_cast<int>(sh.out_i[tid] & kTokenMask) : -1;
   const int64_t row = static_cast<int64_t>(search) * W + w;
   const bool done = some && (token == p.eos || (p.finished && p.finished[row] != 0));
   __syncthreads();
   if (tid < K) {
-    const int64_t at = static_cast<int64_t>(search) * K + place[tid];
-    p.out_scores[at] = some ? static_cast<float>(unordered64(out_v[tid])) : -INFINITY;
+    const int64_t at = static_cast<int64_t>(search) * K + (p.in_place ? sh.place[tid] : tid);
+    p.out_scores[at] = some ? static_cast<float>(unordered64(sh.out_v[tid])) : -INFINITY;
     p.out_parents[at] = some ? static_cast<int32_t>(row) : -1;
     p.out_tokens[at] = token;
     if (p.out_finished) p.out_finished[at] = done;
@@ -361,35 +503,35 @@ __device__ __forceinline__ void load8(const T* row, int64_t e, int64_t end, uint
 #pragma unroll
     for (int k = 0; k < N; ++k) w[k] = __funnelshift_r(u[k], u[k + 1], sh);
   } else {
+    T v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float x = -INFINITY;
-      if (e + k < end) x = static_cast<float>(row[e + k]);
-      Words<T>::set(w, k, x);
-    }
+    for (int k = 0; k < 8; ++k)
+      if (e + k < end) v[k] = row[e + k];
+#pragma unroll
+    for (int k = 0; k < N; ++k) w[k] = reinterpret_cast<const uint32_t*>(v)[k];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (e + k >= end) Words<T>::lowest(w, k);
   }
 }
 
 // grid (parts, rows).  V: pieces of eight logits a thread.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kThreads, 4)
+    beam_select_kernel(const __grid_constant__ BeamParams p) {
   using W = Words<T>;
-  __shared__ Shared sh;
+  Shared& sh = shared();
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = p.keep;
   const int64_t row = blockIdx.y;
   const int part = blockIdx.x, search = static_cast<int>(row / p.beams);
   uint64_t* keys = p.ws_keys + (row * p.parts + part) * K;
-  auto emit = [&](int r, const Key& k) {
-    keys[r] = k.i == kNone ? 0 : (k.v << 32) | ~static_cast<uint32_t>(k.i);
-  };
   const float score = p.scores[row];
   if (part == 0 && tid == 0 && !isfinite(score) && score != -INFINITY)
     raise_error(p.err, PA_DEVERR_LOGITS);
   if (isfinite(score) && !(p.finished && p.finished[row])) {
-    const int64_t begin = static_cast<int64_t>(part) * p.part_len;
-    const int64_t end = min(begin + p.part_len, static_cast<int64_t>(p.vocab));
+    const int begin = part * p.part_len, end = min(begin + p.part_len, p.vocab);
     const T* logits = static_cast<const T*>(p.logits);
     const T* mine = logits + row * p.row_stride;
     const uintptr_t lo = reinterpret_cast<uintptr_t>(logits);
@@ -399,50 +541,29 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamParams 
 #pragma unroll
     for (int j = 0; j < V; ++j)
       load8<T>(mine, begin + (j * kThreads + tid) * 8, end, lo, hi, w[j]);
-    float tm = -INFINITY;  // the thread's maximum (NaN is passed over)
-    auto maximum = [&]() {
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    // the thread's maximum, and the warp's
+    typename W::Top top = W::none();
 #pragma unroll
-      for (int j = 0; j < V; ++j)
+    for (int j = 0; j < V; ++j) W::raise(top, w[j]);
+    float tm = W::value(top), wm = tm;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m4[i & 3] = fmaxf(m4[i & 3], W::get(w[j], i));
-      tm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-    };
-    maximum();
-    // sum of exp(x - m), m the warp's maximum; NaN where a logit is NaN or +inf
-    float wm, ws;
-    auto sum = [&]() {
-      wm = tm;
+    for (int m = 16; m >= 1; m >>= 1) wm = fmaxf(wm, __shfl_xor_sync(kFullMask, wm, m));
+    // the warp's sum of exp(x - its maximum); NaN where a logit is NaN or +inf
+    const float ref = wm == -INFINITY ? 0.f : -wm;
+    const float2 ref2 = make_float2(ref, ref), unit = make_float2(kLog2e, kLog2e);
+    float2 s4[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) wm = fmaxf(wm, __shfl_xor_sync(kFullMask, wm, m));
-      const float ref = wm == -INFINITY ? 0.f : -wm;
-      const float2 ref2 = make_float2(ref, ref), unit = make_float2(kLog2e, kLog2e);
-      float2 s4[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+    for (int j = 0; j < V; ++j)
 #pragma unroll
-      for (int j = 0; j < V; ++j)
+      for (int i = 0; i < 4; ++i) {
+        const float2 d = __fmul2_rn(__fadd2_rn(W::pair(w[j], i), ref2), unit);
+        s4[i] = __fadd2_rn(s4[i], make_float2(ex2(d.x), ex2(d.y)));
+      }
+    const float2 a2 = __fadd2_rn(__fadd2_rn(s4[0], s4[1]), __fadd2_rn(s4[2], s4[3]));
+    float ws = a2.x + a2.y;
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float2 d = __fmul2_rn(
-              __fadd2_rn(make_float2(W::get(w[j], i), W::get(w[j], i + 1)), ref2), unit);
-          s4[i >> 1] = __fadd2_rn(s4[i >> 1], make_float2(ex2(d.x), ex2(d.y)));
-        }
-      const float2 a = __fadd2_rn(__fadd2_rn(s4[0], s4[1]), __fadd2_rn(s4[2], s4[3]));
-      ws = a.x + a.y;
-#pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) ws += __shfl_xor_sync(kFullMask, ws, m);
-    };
-    sum();
-    if (!(ws < INFINITY)) {  // (the whole warp) a NaN or +inf: no token of the row's
-      if (lane == 0) raise_error(p.err, PA_DEVERR_LOGITS);
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (!(W::get(w[j], i) < INFINITY)) W::set(w[j], i, -INFINITY);
-      maximum();
-      sum();
-    }
-    // the groups' maxima, and their K-th largest
+    for (int m = 16; m >= 1; m >>= 1) ws += __shfl_xor_sync(kFullMask, ws, m);
+    // the groups' maxima
     const int lanes = kThreads / p.groups;
     float gm = tm;
     for (int m = 1; m < lanes; m <<= 1) gm = fmaxf(gm, __shfl_xor_sync(kFullMask, gm, m));
@@ -452,15 +573,59 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamParams 
       sh.s[warp] = ws;
     }
     if (tid == 0) sh.count = 0;
-    __syncthreads();
-    if (tid < p.groups) {
-      const float x = sh.group_max[tid];
-      int rank = 0;
-      for (int g = 0; g < p.groups; ++g) {
-        const float o = sh.group_max[g];
-        rank += o > x || (o == x && g < tid);
+    if (__syncthreads_or(!(ws < INFINITY))) {
+      // A NaN or +inf is no token: the part once more from memory, which hides them.
+      if (tid == 0) raise_error(p.err, PA_DEVERR_LOGITS);
+      tm = -INFINITY;
+      for (int e = begin + tid; e < end; e += kThreads) tm = fmaxf(tm, visible(mine[e]));
+      wm = tm;
+      for (int m = 16; m >= 1; m >>= 1) wm = fmaxf(wm, __shfl_xor_sync(kFullMask, wm, m));
+      ws = 0.f;
+      if (wm > -INFINITY)
+        for (int e = begin + tid; e < end; e += kThreads)
+          ws += ex2((visible(mine[e]) - wm) * kLog2e);
+      for (int m = 16; m >= 1; m >>= 1) ws += __shfl_xor_sync(kFullMask, ws, m);
+      if (lane == 0) {
+        sh.m[warp] = wm;
+        sh.s[warp] = ws;
       }
-      if (rank == K - 1) sh.bound = __float_as_uint(x);
+      if (tid == 0) sh.count = kRoom + 1;  // (the largest one by one)
+      __syncthreads();
+    } else {
+      // the K-th largest of the groups' maxima, and the logits that reach it
+      kth_of_groups(sh.group_max, p.groups, K, &sh.bound);
+      __syncthreads();
+      // (at least the type's lowest number: what is hidden reaches nothing)
+      const float bound =
+          fmaxf(__uint_as_float(static_cast<uint32_t>(sh.bound)), Words<T>::kLowest);
+      if (tm >= bound) {
+        uint32_t bits[V];
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          bits[j] = W::reach(w[j], bound);
+          n += __popc(bits[j]);
+        }
+        int at = atomicAdd(&sh.count, n);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          while (bits[j]) {
+            const int i = logit_of<T>(__ffs(bits[j]) - 1);
+            bits[j] &= bits[j] - 1;
+            float2 two = W::pair(w[j], 0);
+#pragma unroll
+            for (int k = 1; k < 4; ++k)
+              if (i >> 1 == k) two = W::pair(w[j], k);
+            const float x = i & 1 ? two.y : two.x;
+            if (at < kRoom) {
+              sh.v[at] = ordered(x);
+              sh.i[at] = static_cast<uint64_t>(begin + (j * kThreads + tid) * 8 + i);
+            }
+            ++at;
+          }
+        }
+      }
+      __syncthreads();
     }
     if (tid == kThreads - 1) {
       float m = sh.m[0];
@@ -470,54 +635,26 @@ __global__ void __launch_bounds__(kThreads) beam_select_kernel(const BeamParams 
         for (int q = 0; q < kWarps; ++q) s += sh.s[q] * ex2((sh.m[q] - m) * kLog2e);
       p.ws_sums[row * p.parts + part] = make_float2(m, s);
     }
-    __syncthreads();
-    const float bound = __uint_as_float(static_cast<uint32_t>(sh.bound));
-    if (tm >= bound) {
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x = W::get(w[j], i);
-          if (x >= bound && x > -INFINITY) {
-            const int at = atomicAdd(&sh.count, 1);
-            if (at < kRoom) {
-              sh.v[at] = ordered(x);
-              sh.i[at] = static_cast<uint64_t>(begin + (j * kThreads + tid) * 8 + i);
-            }
-          }
-        }
-    }
-    __syncthreads();
-    if (sh.count <= kRoom) {
-      best_of_room(sh, sh.count, K, emit);
-    } else {
-      one_by_one(
-          sh, K,
-          [&](const Key& prev, bool first) {
-            Key best = nothing();
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float x = W::get(w[j], i);
-                const Key k{ordered(x),
-                            static_cast<uint64_t>(begin + (j * kThreads + tid) * 8 + i)};
-                if (x > -INFINITY && (first || before(prev, k)) && before(k, best)) best = k;
-              }
-            return best;
-          },
-          emit);
-    }
+    const int count = sh.count;
+    if (count <= kRoom)
+      best_of_room(count, K);
+    else
+      one_by_one_of_row(mine, begin, end, K);
+    if (tid < K)
+      keys[tid] = sh.out_i[tid] == kNone
+                      ? 0
+                      : (sh.out_v[tid] << 32) | ~static_cast<uint32_t>(sh.out_i[tid]);
   }
   // the last CTA of the search joins
-  __threadfence();
   __syncthreads();
-  if (tid == 0)
+  if (tid == 0) {
+    __threadfence();
     sh.arrived = atomicAdd(p.counters + search, 1u);
+    __threadfence();
+  }
   __syncthreads();
   if (sh.arrived + 1 != static_cast<unsigned>(p.parts) * p.beams) return;
-  __threadfence();
-  merge(p, sh, search);
+  merge(p, search);
   if (tid == 0) p.counters[search] = 0;
 }
 
