@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtas = 4;      // an SM
 constexpr int kRoom = 1024;   // candidates that a CTA can hold
 constexpr int kRank = 192;    // up to this many are ranked by counting
 constexpr float kLog2e = 1.4426950408889634f;
@@ -167,6 +168,40 @@ __device__ __forceinline__ float visible(T x) {
   return f < INFINITY ? f : -INFINITY;
 }
 
+// 2^(-i / 64)
+__constant__ double kPowers[64] = {
+    1.0, 0.9892280131939755, 0.9785720620877001, 0.9680308967461472,
+    0.9576032806985737, 0.9472879907934828, 0.93708381705515, 0.9269895625416927,
+    0.9170040432046712, 0.9071260877501994, 0.8973545375015536, 0.8876882462632606,
+    0.8781260801866497, 0.8686669176368531, 0.859309649061239, 0.8500531768592617,
+    0.8408964152537145, 0.8318382901633682, 0.8228777390769825, 0.8140137109286739,
+    0.8052451659746271, 0.7965710756711335, 0.7879904225539432, 0.7795022001189185,
+    0.7711054127039704, 0.7627990753722692, 0.7545822137967114, 0.7464538641456324,
+    0.7384130729697497, 0.7304588970903235, 0.7225904034885233, 0.714806669195985,
+    0.7071067811865476, 0.6994898362691556, 0.691954940981916, 0.6845012114872953,
+    0.6771277734684463, 0.6698337620266515, 0.6626183215798707, 0.6554806057623822,
+    0.6484197773255048, 0.6414350080393891, 0.6345254785958666, 0.6276903785123455,
+    0.620928906036742, 0.614240268053435, 0.6076236799902345, 0.6010783657263515,
+    0.5946035575013605, 0.5881984958251406, 0.5818624293887887, 0.5755946149764913,
+    0.5693943173783458, 0.5632608093041209, 0.5571933712979462, 0.5511912916539204,
+    0.5452538663326288, 0.5393803988785599, 0.5335702003384118, 0.5278225891802786,
+    0.5221368912137069, 0.5165124395106142, 0.5109485743270583, 0.5054446430258502};
+
+// ln(s) of 1 <= s < 2^60 to 1e-11, in a tenth of the time of 64-bit arithmetic all
+// through: j / 64 is the binary logarithm to half a 64th, t = s 2^(-j / 64) - 1 is
+// within 0.0055 of 0, and ln(1 + t) = t - t^2 / 2 + ..., the terms after t in fp32.
+__device__ __forceinline__ double log64(double s) {
+  float l;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(l) : "f"(static_cast<float>(s)));
+  const int j = __float2int_rn(64.f * l);
+  const double scaled = __longlong_as_double(__double_as_longlong(s) -
+                                             (static_cast<int64_t>(j >> 6) << 52));  // s 2^-(j / 64)
+  const double t = scaled * kPowers[j & 63] - 1.0;
+  const float f = static_cast<float>(t);
+  const float rest = f * f * fmaf(f, fmaf(f, fmaf(f, 0.2f, -0.25f), 1.f / 3.f), -0.5f);
+  return fma(static_cast<double>(j), 0.010830424696249145, t + static_cast<double>(rest));
+}
+
 struct Shared {
   uint64_t v[kRoom];
   uint64_t i[kRoom];
@@ -177,7 +212,8 @@ struct Shared {
   float m[kWarps], s[kWarps];
   uint64_t out_v[kBeamMaxKeep];  // the K found, first to last
   uint64_t out_i[kBeamMaxKeep];
-  double lse[kBeamMaxBeams];
+  double lse[kBeamMaxBeams], score[kBeamMaxBeams];
+  int state[kBeamMaxBeams];  // of a beam: 0 ended in nothing, 1 goes on, 2 finished
   int place[kBeamMaxKeep];
   uint64_t bound;
   int count;
@@ -263,7 +299,10 @@ __device__ __forceinline__ void best_of_room(int count, int k) {
       const Key mine = c < count ? Key{sh.v[c], sh.i[c]} : nothing();
       int rank = 0;
 #pragma unroll 4
-      for (int o = seg; o < count; o += 4) rank += before(Key{sh.v[o], sh.i[o]}, mine);
+      for (int o = seg; o < count; o += 4) {
+        const uint64_t v = sh.v[o], i = sh.i[o];
+        rank += (v > mine.v) | ((v == mine.v) & (i < mine.i));
+      }
       rank += __shfl_xor_sync(kFullMask, rank, 1);
       rank += __shfl_xor_sync(kFullMask, rank, 2);
       if (seg == 0 && c < count && rank < k) {
@@ -299,25 +338,21 @@ __device__ __forceinline__ void kth_of_groups(const V* value, int groups, int k,
 }
 
 // A part's find (beam w, `key` of the workspace) as a candidate of its search.
-__device__ __forceinline__ Key candidate(const BeamParams& p, int search, int w, bool first,
-                                         uint64_t key) {
-  const int64_t row = static_cast<int64_t>(search) * p.beams + w;
-  const float score = p.scores[row];
-  if (!isfinite(score)) return nothing();
+__device__ __forceinline__ Key candidate(const BeamParams& p, int w, bool first, uint64_t key) {
+  const Shared& sh = shared();
+  const int state = sh.state[w];
   const uint64_t beam = static_cast<uint64_t>(w) << 59;
-  if (p.finished && p.finished[row])  // its one continuation
-    return first ? Key{ordered(static_cast<double>(score)), beam | static_cast<uint32_t>(p.eos)}
-                 : nothing();
-  if (key == 0) return nothing();
+  if (state == 2)  // its one continuation
+    return first ? Key{ordered(sh.score[w]), beam | static_cast<uint32_t>(p.eos)} : nothing();
+  if (state == 0 || key == 0) return nothing();
   const uint32_t o = static_cast<uint32_t>(key >> 32);
-  const double total =
-      static_cast<double>(score) + (static_cast<double>(unordered(o)) - shared().lse[w]);
+  const double total = sh.score[w] + (static_cast<double>(unordered(o)) - sh.lse[w]);
   return Key{ordered(total), beam | static_cast<uint64_t>(~o) << 27 |
                                  static_cast<uint32_t>(~static_cast<uint32_t>(key))};
 }
-__device__ __forceinline__ Key candidate(const BeamParams& p, int search, int c, uint64_t key) {
+__device__ __forceinline__ Key candidate(const BeamParams& p, int c, uint64_t key) {
   const int w = c / (p.parts * p.keep);
-  return candidate(p, search, w, c == w * p.parts * p.keep, key);
+  return candidate(p, w, c == w * p.parts * p.keep, key);
 }
 
 __device__ __noinline__ void one_by_one_of_parts(const BeamParams* p, int search) {
@@ -326,7 +361,7 @@ __device__ __noinline__ void one_by_one_of_parts(const BeamParams* p, int search
   one_by_one(p->keep, [&](const Key& prev, bool first) {
     Key best = nothing();
     for (int c = threadIdx.x; c < total; c += kThreads) {
-      const Key x = candidate(*p, search, c, __ldcg(parts + c));
+      const Key x = candidate(*p, c, __ldcg(parts + c));
       if ((first || before(prev, x)) && before(x, best)) best = x;
     }
     return best;
@@ -357,32 +392,40 @@ __device__ __forceinline__ void merge(const BeamParams& p, int search) {
     raw[q] = c < total ? __ldcg(parts + at[q]) : 0;
   }
   for (int w = tid >> 5; w < W; w += kWarps) {  // each row's log-sum from its parts
-    const float2* ms = p.ws_sums + (static_cast<int64_t>(search) * W + w) * p.parts;
-    float top = -INFINITY;
-    for (int c = tid & 31; c < p.parts; c += 32) top = fmaxf(top, __ldcg(ms + c).x);
+    const int64_t row = static_cast<int64_t>(search) * W + w;
+    const float2* ms = p.ws_sums + row * p.parts;
+    const float score = p.scores[row];
+    const bool finished = p.finished && p.finished[row];
+    const float2 mine = (tid & 31) < p.parts ? __ldcg(ms + (tid & 31)) : make_float2(-INFINITY, 0.f);
+    float top = mine.x;
+    for (int c = (tid & 31) + 32; c < p.parts; c += 32) top = fmaxf(top, __ldcg(ms + c).x);
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, m));
-    double s = 0.0;
-    for (int c = tid & 31; c < p.parts; c += 32) {
+    double s = mine.y > 0.f ? mine.y * ex2((mine.x - top) * kLog2e) : 0.f;
+    for (int c = (tid & 31) + 32; c < p.parts; c += 32) {
       const float2 part = __ldcg(ms + c);
       if (part.y > 0.f) s += part.y * ex2((part.x - top) * kLog2e);
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(kFullMask, s, m);
-    if ((tid & 31) == 0) sh.lse[w] = s > 0.0 ? static_cast<double>(top) + log(s) : 0.0;
+    if ((tid & 31) == 0) {
+      sh.lse[w] = s > 0.0 ? static_cast<double>(top) + log64(s) : 0.0;
+      sh.score[w] = score;
+      sh.state[w] = !isfinite(score) ? 0 : finished ? 2 : 1;
+    }
   }
   if (tid == 0) sh.count = 0;
   __syncthreads();
   // the K-th largest of the groups' maxima bounds the K-th largest of all
   auto nth = [&](int c) {
     const int a = place(c);
-    return candidate(p, search, a, __ldcg(parts + a));
+    return candidate(p, a, __ldcg(parts + a));
   };
   Key held[kHeld];
   uint64_t gm = 0;
 #pragma unroll
   for (int q = 0; q < kHeld; ++q) {
-    held[q] = tid + q * kThreads < total ? candidate(p, search, at[q], raw[q]) : nothing();
+    held[q] = tid + q * kThreads < total ? candidate(p, at[q], raw[q]) : nothing();
     gm = held[q].v > gm ? held[q].v : gm;
   }
   for (int c = tid + kHeld * kThreads; c < total; c += kThreads) {
@@ -463,24 +506,41 @@ __device__ __forceinline__ void merge(const BeamParams& p, int search) {
   }
 }
 
-// Eight logits of a row from element e on, as words; those past the row's end
-// are -inf.  lo / hi: the addresses that the logits' tensor spans.
+// Eight logits as words, from a 16-byte boundary.
 template <typename T>
-__device__ __forceinline__ void load8(const T* row, int64_t e, int64_t end, uintptr_t lo,
-                                      uintptr_t hi, uint32_t (&w)[Words<T>::N]) {
+__device__ __forceinline__ void load8_aligned(const T* at, uint32_t (&w)[Words<T>::N]) {
+#pragma unroll
+  for (int k = 0; k < Words<T>::N / 4; ++k) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(at) + k);
+    w[4 * k] = q.x;
+    w[4 * k + 1] = q.y;
+    w[4 * k + 2] = q.z;
+    w[4 * k + 3] = q.w;
+  }
+}
+// Those of a row from element e on, one by one; past its end they are -inf.
+template <typename T>
+__device__ __forceinline__ void load8_each(const T* row, int e, int end,
+                                           uint32_t (&w)[Words<T>::N]) {
+  T v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (e + k < end) v[k] = row[e + k];
+#pragma unroll
+  for (int k = 0; k < Words<T>::N; ++k) w[k] = reinterpret_cast<const uint32_t*>(v)[k];
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (e + k >= end) Words<T>::lowest(w, k);
+}
+// Those of a row off a 16-byte boundary: aligned words, shifted, where they lie within
+// the addresses [lo, hi) that the logits span.
+template <typename T>
+__device__ __forceinline__ void load8_shifted(const T* row, int e, int end, uintptr_t lo,
+                                              uintptr_t hi, uint32_t (&w)[Words<T>::N]) {
   constexpr int N = Words<T>::N;
   const uintptr_t addr = reinterpret_cast<uintptr_t>(row + e);
   const unsigned off = addr & 15u;  // the same for the whole row
-  if (e + 8 <= end && off == 0) {
-#pragma unroll
-    for (int k = 0; k < N / 4; ++k) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(addr) + k);
-      w[4 * k] = q.x;
-      w[4 * k + 1] = q.y;
-      w[4 * k + 2] = q.z;
-      w[4 * k + 3] = q.w;
-    }
-  } else if (e + 8 <= end && addr - off >= lo && addr - off + 4 * N + 16 <= hi) {
+  if (e + 8 <= end && addr - off >= lo && addr - off + 4 * N + 16 <= hi) {
     uint32_t u[N + 4];
     const uint4* a = reinterpret_cast<const uint4*>(addr - off);
 #pragma unroll
@@ -503,21 +563,13 @@ __device__ __forceinline__ void load8(const T* row, int64_t e, int64_t end, uint
 #pragma unroll
     for (int k = 0; k < N; ++k) w[k] = __funnelshift_r(u[k], u[k + 1], sh);
   } else {
-    T v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (e + k < end) v[k] = row[e + k];
-#pragma unroll
-    for (int k = 0; k < N; ++k) w[k] = reinterpret_cast<const uint32_t*>(v)[k];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (e + k >= end) Words<T>::lowest(w, k);
+    load8_each<T>(row, e, end, w);
   }
 }
 
 // grid (parts, rows).  V: pieces of eight logits a thread.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kCtas)
     beam_select_kernel(const __grid_constant__ BeamParams p) {
   using W = Words<T>;
   Shared& sh = shared();
@@ -526,7 +578,6 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = p.keep;
   const int64_t row = blockIdx.y;
   const int part = blockIdx.x, search = static_cast<int>(row / p.beams);
-  uint64_t* keys = p.ws_keys + (row * p.parts + part) * K;
   const float score = p.scores[row];
   if (part == 0 && tid == 0 && !isfinite(score) && score != -INFINITY)
     raise_error(p.err, PA_DEVERR_LOGITS);
@@ -534,13 +585,24 @@ __global__ void __launch_bounds__(kThreads, 4)
     const int begin = part * p.part_len, end = min(begin + p.part_len, p.vocab);
     const T* logits = static_cast<const T*>(p.logits);
     const T* mine = logits + row * p.row_stride;
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(logits);
-    const uintptr_t hi = reinterpret_cast<uintptr_t>(
-        logits + (static_cast<int64_t>(gridDim.y) - 1) * p.row_stride + p.vocab);
     uint32_t w[V][W::N];
+    if ((reinterpret_cast<uintptr_t>(mine) & 15) == 0) {  // (begin is a multiple of 8)
+      const T* at = mine + begin + tid * 8;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      load8<T>(mine, begin + (j * kThreads + tid) * 8, end, lo, hi, w[j]);
+      for (int j = 0; j < V; ++j) {
+        if (begin + (j * kThreads + tid) * 8 + 8 <= end)
+          load8_aligned<T>(at + j * kThreads * 8, w[j]);
+        else
+          load8_each<T>(mine, begin + (j * kThreads + tid) * 8, end, w[j]);
+      }
+    } else {
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(logits);
+      const uintptr_t hi = reinterpret_cast<uintptr_t>(
+          logits + (static_cast<int64_t>(gridDim.y) - 1) * p.row_stride + p.vocab);
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        load8_shifted<T>(mine, begin + (j * kThreads + tid) * 8, end, lo, hi, w[j]);
+    }
     // the thread's maximum, and the warp's
     typename W::Top top = W::none();
 #pragma unroll
@@ -608,22 +670,11 @@ __global__ void __launch_bounds__(kThreads, 4)
         }
         int at = atomicAdd(&sh.count, n);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          while (bits[j]) {
-            const int i = logit_of<T>(__ffs(bits[j]) - 1);
-            bits[j] &= bits[j] - 1;
-            float2 two = W::pair(w[j], 0);
-#pragma unroll
-            for (int k = 1; k < 4; ++k)
-              if (i >> 1 == k) two = W::pair(w[j], k);
-            const float x = i & 1 ? two.y : two.x;
-            if (at < kRoom) {
-              sh.v[at] = ordered(x);
-              sh.i[at] = static_cast<uint64_t>(begin + (j * kThreads + tid) * 8 + i);
-            }
-            ++at;
-          }
-        }
+        for (int j = 0; j < V; ++j)
+          for (; bits[j] != 0; bits[j] &= bits[j] - 1, ++at)
+            if (at < kRoom)
+              sh.i[at] = static_cast<uint64_t>(begin + (j * kThreads + tid) * 8 +
+                                               logit_of<T>(__ffs(bits[j]) - 1));
       }
       __syncthreads();
     }
@@ -636,22 +687,26 @@ __global__ void __launch_bounds__(kThreads, 4)
       p.ws_sums[row * p.parts + part] = make_float2(m, s);
     }
     const int count = sh.count;
-    if (count <= kRoom)
+    if (count <= kRoom) {  // (their values once more: they are in the nearest cache)
+      for (int c = tid; c < count; c += kThreads)
+        sh.v[c] = ordered(static_cast<float>(mine[sh.i[c]]));
+      __syncthreads();
       best_of_room(count, K);
-    else
+    } else {
       one_by_one_of_row(mine, begin, end, K);
+    }
     if (tid < K)
-      keys[tid] = sh.out_i[tid] == kNone
-                      ? 0
-                      : (sh.out_v[tid] << 32) | ~static_cast<uint32_t>(sh.out_i[tid]);
+      p.ws_keys[(row * p.parts + part) * K + tid] =
+          sh.out_i[tid] == kNone ? 0
+                                 : (sh.out_v[tid] << 32) | ~static_cast<uint32_t>(sh.out_i[tid]);
   }
   // the last CTA of the search joins
   __syncthreads();
-  if (tid == 0) {
-    __threadfence();
-    sh.arrived = atomicAdd(p.counters + search, 1u);
-    __threadfence();
-  }
+  if (tid == 0)
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                 : "=r"(sh.arrived)
+                 : "l"(p.counters + search)
+                 : "memory");
   __syncthreads();
   if (sh.arrived + 1 != static_cast<unsigned>(p.parts) * p.beams) return;
   merge(p, search);
