@@ -327,14 +327,15 @@ __device__ void cut(const CrossParams& p, Run* out, int64_t* warp_sums) {
 // c0 + k, the first one in that of the unit its CTA ends in.  A thread takes 4
 // dims of a row at a time, four such pieces and two parts of each in flight.
 template <int D>
-__device__ __noinline__ void join(const CrossParams& p, const Part& it, int c0, int parts) {
+__device__ __forceinline__ void join(const CrossParams& p, const Part& it, int c0, int parts) {
   constexpr int kPieces = 4, kCols = D / 4;
   const int shift = 31 - __clz(p.group);
   const int rows = min(kRows, (it.seq.n - it.i0) << shift);
   auto at = [&](int k, int row) {
     return (static_cast<int64_t>(c0 + k) * 2 + (k == 0)) * p.ws_rows + row;
   };
-  for (int q0 = threadIdx.x; q0 < rows * kCols; q0 += kPieces * kSoftmaxThreads) {
+  const int pieces = rows * kCols;
+  for (int q0 = threadIdx.x; q0 < pieces; q0 += kPieces * kSoftmaxThreads) {
     float m[kPieces], l[kPieces];
     float4 acc[kPieces];
 #pragma unroll
@@ -346,19 +347,21 @@ __device__ __noinline__ void join(const CrossParams& p, const Part& it, int c0, 
     for (int k0 = 0; k0 < parts; k0 += 2) {
       float2 ml[kPieces][2];
       float4 o[kPieces][2];
+      // (loads without conditions, so that none waits for another: past the end the
+      // last piece or part again, without weight)
 #pragma unroll
       for (int j = 0; j < kPieces; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int q = q0 + j * kSoftmaxThreads;
-          ml[j][e] = make_float2(-INFINITY, 0.f);
-          o[j][e] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (q < rows * kCols && k0 + e < parts) {
-            const int64_t r = at(k0 + e, q / kCols);
-            ml[j][e] = __ldcg(p.ws_ml + r);
-            o[j][e] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + r * D) + q % kCols);
-          }
+          const int q = min(q0 + j * kSoftmaxThreads, pieces - 1);
+          const int64_t r = at(min(k0 + e, parts - 1), q / kCols);
+          ml[j][e] = __ldcg(p.ws_ml + r);
+          o[j][e] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + r * D) + q % kCols);
         }
+      if (k0 + 1 >= parts) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) ml[j][1] = make_float2(-INFINITY, 0.f);
+      }
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         const float top = fmaxf(m[j], fmaxf(ml[j][0].x, ml[j][1].x));
@@ -375,7 +378,7 @@ __device__ __noinline__ void join(const CrossParams& p, const Part& it, int c0, 
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
       const int q = q0 + j * kSoftmaxThreads, r = q / kCols;
-      if (q >= rows * kCols) continue;
+      if (q >= pieces) continue;
       const float z = l[j] > 0.f ? 1.f / l[j] : 0.f;
       const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[j].x * z, acc[j].y * z);
       const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[j].z * z, acc[j].w * z);
@@ -666,6 +669,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             tmem_wait_ld();
             if (valid < kCols) {
+              asm volatile("");  // (a branch: as selects they would cost every chunk)
 #pragma unroll
               for (int j = 0; j < kCols; ++j)
                 if (j >= valid) sv[j] = __float_as_uint(-INFINITY);
@@ -825,7 +829,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         m_used = top;
       }
       const float inv = shared ? factor : total > 0.f ? factor / total : 0.f;
-      auto put = [&](int col, const float4& v) {  // four columns of this thread's row
+      // four columns of this thread's row
+      auto put = [&](int col, const float4& v) {
         if (shared) {
           *reinterpret_cast<float4*>(p.ws_o + (place + row) * D + col) = v;
         } else {
@@ -844,12 +849,24 @@ __global__ void __launch_bounds__(kThreads, 2)
             tmem_ld16(tO + 16 * q4, o);
             tmem_wait_ld();
             if (!row_ok) continue;
+            if (shared) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              put(16 * q4 + 4 * k,
-                  make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
-                              __uint_as_float(o[4 * k + 2]) * inv,
-                              __uint_as_float(o[4 * k + 3]) * inv));
+              for (int k = 0; k < 4; ++k)
+                put(16 * q4 + 4 * k,
+                    make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3])));
+            } else {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(
+                    __uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                w[e] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 16 * q4);
+              dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         }
       } else {
@@ -899,12 +916,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         // the last CTA of the unit joins its parts (counted at its first CTA)
         const int c0 = owner(run, it.unit);
         const int parts = owner(run, it.unit + it.seq.chunks - 1) - c0 + 1;
-        __threadfence();
         asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
-        if (tid == 0) *last_slot = atomicAdd(p.counters + c0, 1u);
+        if (tid == 0)
+          asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                       : "=r"(*last_slot)
+                       : "l"(p.counters + c0)
+                       : "memory");
         asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
         if (*last_slot + 1 == static_cast<unsigned>(parts)) {
-          __threadfence();
           join<D>(p, it, c0, parts);
           if (tid == 0) p.counters[c0] = 0;
         }
