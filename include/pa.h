@@ -705,10 +705,10 @@ pa_status pa_prefill_biased(void* out, const void* q, const void* k_cache, const
  *                     them zero.  Calls that may run at the same time (two
  *                     streams, two replayed graphs) must not share workspace or
  *                     counters.
- *   ws_ctas         : how many CTAs the call may use, >= 1; pa_cross_attention_ctas(
+ *   ws_ctas         : how many CTAs the call may use, 1 to 2^20; pa_cross_attention_ctas(
  *                     num_sms) fills the GPU.
  * Runs on the tensor cores (bf16 in, fp32 accumulate; the softmax weights enter
- * the PV product rounded to bf16, their sum is taken before).  V of a source
+ * the PV product as two bf16 parts, which keep 2^-16 of them).  V of a source
  * position must be finite; what the cache holds past the source changes nothing.
  * head_dim 64 or 128, block_size 16, Hq / Hkv in {1, 2, 4, 8} (else
  * PA_ERR_UNSUPPORTED_SHAPE), scale > 0.  Device-side checks: 0 <= S <=

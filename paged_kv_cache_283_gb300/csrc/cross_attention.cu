@@ -15,25 +15,28 @@
 //    per 16-token block by TMA (the block table is a gather of 16-row boxes), 64
 //    keys a chunk.
 //  * The batch's work, all (sequence, KV head, tile) units' chunks of keys one after
-//    another, is cut evenly among persistent CTAs (two an SM: 4 softmax warps, a
-//    row a thread, a warp each for the MMAs of Q K^T and of P V and for the copies
-//    of K and of V: a warp's waits take it longer than what it waits to issue), each taking one run of chunks
-//    whatever units it begins and ends in: ragged sources, few long ones and many
-//    short ones all keep every SM busy to the end.  The lengths are read on the
-//    device, so a captured call follows them.  The warps walk their CTA's run on
-//    their own, the copy warps ahead of the others, so that the next unit's first
-//    tiles are on their way while the last one's are used.
+//    another, is cut evenly among persistent CTAs (two an SM), each taking one run
+//    of chunks whatever units it begins and ends in: ragged sources, few long ones
+//    and many short ones all keep every SM busy to the end.  A unit's beginning and end
+//    count as kUnitCost chunks (64 x 4 beams of sources of 128 to 2048 keys 75 ->
+//    62 us, 16 x 512 prompts 466 -> 445, against counting the chunks alone).  The
+//    lengths are read on the device, so a captured call follows them.
+//  * A CTA is 4 softmax warps, a row a thread, and a warp each for the MMAs of
+//    Q K^T and of P V and for the copies of K and of V: a warp's waits take it
+//    longer than what it waits to issue.  The warps walk their CTA's run on their
+//    own, the copy warps ahead of the others, so that the next unit's first tiles
+//    are on their way while the last one's are used.
 //  * A unit that several CTAs share is joined by the last of them to arrive: each
 //    leaves its rows' (m, l, o) in the workspace, where a CTA has two places, one
 //    for the unit it begins in and one for the unit it ends in.
 //  * The softmax takes a chunk's weights against the row's reference maximum
 //    first; only where their sum says that the reference could be 2^8 too low
 //    are the chunk's maxima taken and O rescaled in tensor memory.
-//  * The weights enter P V as bf16, rounded to nearest, their sum is taken
-//    before the rounding, in fp32.  Each weight is then off by up to 2^-9 of
-//    itself, as if its score were off by 2^-9 -- less than what the rounding of
-//    q and K to bf16 moves scores by -- and an output by at most 2^-9 of the
-//    weighted mean of |V|, which its own rounding to bf16 doubles.
+//  * The weights enter P V as two bf16 parts, hi + lo, which keep 2^-16 of them;
+//    their sum is taken before, in fp32.  One part would be off by up to 2^-9 of
+//    the weighted mean of |V|, far more than the rounding of an output whose terms
+//    cancel.  It would save a fourth of the time of long prompts (16 x 512 queries
+//    of 512 to 4096 keys: 343 us against 470, both measured then).
 //  * Few rows (beams of one step): a softmax thread's way through its row of 64
 //    scores takes longer than the copies of their keys.  With 32 rows or fewer
 //    the tile holds four copies of them, each of which takes a quarter of every
@@ -91,6 +94,8 @@ constexpr int kThreads = kSoftmaxThreads + 128;
 constexpr int kScoreWarp = 4, kMixWarp = 5, kCopyWarp = 6;  // Q K^T, P V, copies of K and of V
 constexpr int kSumFloats = 4 * 32 * 20;  // room for 16 columns of every row's copies
 constexpr int kMinChunks = 4;  // of a unit's part, on average: less is not worth a join
+constexpr int kAhead = 4;      // chunks that block ids run ahead of their copies
+constexpr int kUnitCost = 2;   // of a unit's beginning and end, in chunks
 constexpr int kMaxParts = 64;  // CTAs that share a unit, on average at most
 constexpr uint32_t kTO = 2 * kKeys;     // O's first column, after two S buffers
 constexpr uint32_t kTmemCols = 256;
@@ -149,9 +154,9 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 // The list of units is ordered in pairs (tile, sequence), the tile the slower
 // (kTileMajor), each with its KV heads: runs that begin at different tiles then
 // pass the same keys at the same time, and a source larger than L2 is read from
-// memory once for all its tiles, not once for each (16 x 512 queries on sources
-// of 94 MB ... see the launch).  With more pairs than a CTA looks through in a few
-// microseconds the pairs are the sequences, each with its heads and their tiles.
+// memory once for all its tiles, not once for each (16 x 512 queries: 0.31 GB read
+// in place of 1.2).  With more pairs than a CTA looks through in a few microseconds
+// the pairs are the sequences, each with its heads and their tiles.
 constexpr int kMostPairs = 64 * kThreads;
 
 struct Order {
@@ -165,47 +170,53 @@ struct Order {
     return tile_major ? s.tiles > tile0(pair) : s.tiles;
   }
   __device__ int64_t work(const CrossParams& p, int pair, const Seq& s) const {
-    return static_cast<int64_t>(s.chunks) * span(pair, s) * p.num_kv_heads;
+    return s.chunks == 0 ? 0
+                         : static_cast<int64_t>(s.chunks + kUnitCost) * span(pair, s) *
+                               p.num_kv_heads;
   }
 };
 
-// What all CTAs agree on, and where this one's run begins.
-struct Run {
+// What all CTAs agree on: a unit takes kUnitCost + chunks positions of the list, its
+// chunk c the position kUnitCost + c of them; CTA c's run has `least` positions, the
+// first `rest` CTAs' one more.
+struct Plan {
   Order order;
-  int ctas;          // that take part
-  int64_t total;     // chunks of all units
-  int64_t most;      // a run has this many chunks, from CTA `rest` on one less
+  int ctas;           // that take part
+  int64_t least;
   int rest;
-  int pair;          // of the first chunk,
-  int kvh, inner;    // its unit (tile0 + inner),
-  int first;         // and its place in the unit's keys
-  int64_t left;      // chunks of this run
-  int64_t unit;      // position of the first unit's first chunk
+  __device__ int64_t begin(int c) const { return c * least + min(c, rest); }
+  __device__ int64_t length(int c) const { return c < ctas ? least + (c < rest) : 0; }
+  __device__ int owner(int64_t at) const {
+    const int64_t longer = rest * (least + 1);
+    if (at < longer) return static_cast<int>(quotient(at, least + 1));
+    return rest + static_cast<int>(quotient(at - longer, least));
+  }
 };
 
-// CTA whose run holds chunk `at`.
-__device__ __forceinline__ int owner(const Run& r, int64_t at) {
-  const int64_t longer = r.rest * r.most;
-  if (at < longer) return static_cast<int>(quotient(at, r.most));
-  return r.rest + static_cast<int>(quotient(at - longer, r.most - 1));
-}
+// A CTA's run of positions, and the unit that it begins in.
+struct Run {
+  int64_t left;       // positions
+  int64_t unit;       // the unit's first position
+  int pair, kvh, inner;
+  int offset;         // in the unit
+};
 
 // A part of a unit: chunks [first, first + count) of its keys.
 struct Part {
   int b, kvh, i0;
   Seq seq;
   int first, count;
-  int64_t unit;      // position of the unit's first chunk
+  int64_t unit;      // the unit's first position
 };
 
 struct Walk {
   const Order& order;  // (in shared memory)
   int64_t left, unit;
-  int pair, kvh, inner, first, span;
+  int pair, kvh, inner, offset, span;
   Seq seq;
-  __device__ Walk(const CrossParams& p, const Run& r)
-      : order(r.order), left(r.left), unit(r.unit), pair(r.pair), kvh(r.kvh), inner(r.inner),
-        first(r.first), span(0) {
+  __device__ Walk(const CrossParams& p, const Order& o, const Run& r)
+      : order(o), left(r.left), unit(r.unit), pair(r.pair), kvh(r.kvh), inner(r.inner),
+        offset(r.offset), span(0) {
     if (left > 0) enter(p);
   }
   __device__ void enter(const CrossParams& p) {
@@ -213,36 +224,40 @@ struct Walk {
     span = order.span(pair, seq);
   }
   __device__ bool next(const CrossParams& p, Part& t) {
-    if (left <= 0) return false;
-    while (span == 0 || seq.chunks == 0 || kvh == p.num_kv_heads) {
-      kvh = inner = 0;
-      if (++pair >= order.pairs) {  // (the run ends within the units)
-        left = 0;
-        return false;
+    while (left > 0) {
+      while (span == 0 || seq.chunks == 0 || kvh == p.num_kv_heads) {
+        kvh = inner = 0;
+        if (++pair >= order.pairs) {  // (the run ends within the units)
+          left = 0;
+          return false;
+        }
+        enter(p);
       }
-      enter(p);
+      const int size = seq.chunks + kUnitCost;
+      const int taken = static_cast<int>(min(static_cast<int64_t>(size - offset), left));
+      t.first = max(0, offset - kUnitCost);
+      t.count = max(0, offset + taken - kUnitCost) - t.first;
+      t.b = order.seq(pair);
+      t.kvh = kvh;
+      t.i0 = (order.tile0(pair) + inner) * p.tile_tokens;
+      t.seq = seq;
+      t.unit = unit;
+      left -= taken;
+      unit += size;
+      offset = 0;
+      if (++inner == span) {
+        inner = 0;
+        ++kvh;
+      }
+      if (t.count > 0) return true;  // (a run may end before its last unit's first chunk)
     }
-    t.b = order.seq(pair);
-    t.kvh = kvh;
-    t.i0 = (order.tile0(pair) + inner) * p.tile_tokens;
-    t.seq = seq;
-    t.unit = unit;
-    t.first = first;
-    t.count = static_cast<int>(min(static_cast<int64_t>(seq.chunks - first), left));
-    left -= t.count;
-    unit += seq.chunks;
-    first = 0;
-    if (++inner == span) {
-      inner = 0;
-      ++kvh;
-    }
-    return true;
+    return false;
   }
 };
 
 // The even cut: sums of the pairs' work by the whole CTA, each thread taking a run
-// of pairs; the thread whose run holds the CTA's first chunk finds it.
-__device__ void cut(const CrossParams& p, Run* out, int64_t* warp_sums) {
+// of pairs; the thread whose pairs hold the CTA's first position finds it.
+__device__ void cut(const CrossParams& p, Plan* plan, Run* out, int64_t* warp_sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kThreads / 32;
   int* warp_ints = reinterpret_cast<int*>(warp_sums + kWarps);
@@ -291,18 +306,22 @@ __device__ void cut(const CrossParams& p, Run* out, int64_t* warp_sums) {
     total += warp_sums[w];
     units += warp_ints[w];
   }
-  // a CTA for each unit, or for each kMinChunks chunks where those are more
-  int ctas = static_cast<int>(max(static_cast<int64_t>(units),
-                                  min(total / kMinChunks, static_cast<int64_t>(units) * kMaxParts)));
-  ctas = max(1, min(static_cast<int>(min(total, static_cast<int64_t>(gridDim.x))), ctas));
-  const int c = blockIdx.x;
-  const int64_t least = quotient(total, ctas);
-  const int rest = static_cast<int>(total - least * ctas);
-  const int64_t begin = c * least + min(c, rest);
-  const int64_t left = c < ctas ? least + (c < rest) : 0;
   before += incl - sum;
+  // a CTA for each unit, or for each kMinChunks chunks where those are more
+  const int64_t chunks = total - static_cast<int64_t>(units) * kUnitCost;
+  int ctas = static_cast<int>(
+      max(static_cast<int64_t>(units),
+          min(chunks / kMinChunks, static_cast<int64_t>(units) * kMaxParts)));
+  ctas = max(1, min(static_cast<int>(min(total, static_cast<int64_t>(gridDim.x))), ctas));
+  Plan n;
+  n.order = order;
+  n.ctas = ctas;
+  n.least = quotient(total, ctas);
+  n.rest = static_cast<int>(total - n.least * ctas);
+  if (tid == 0) *plan = n;
+  const int64_t begin = n.begin(blockIdx.x), left = n.length(blockIdx.x);
   if (left > 0 ? before <= begin && begin < before + sum : tid == 0) {
-    Run r{order, ctas, total, least + 1, rest, a0, 0, 0, 0, left, before};
+    Run r{left, before, a0, 0, 0, 0};
     if (left > 0) {
       Seq s;
       for (;; ++r.pair) {
@@ -311,10 +330,11 @@ __device__ void cut(const CrossParams& p, Run* out, int64_t* warp_sums) {
         if (begin < r.unit + w || r.pair + 1 >= a1) break;
         r.unit += w;
       }
-      const int u = static_cast<int>(quotient(begin - r.unit, s.chunks));
-      const int span = order.span(r.pair, s);
-      r.unit += static_cast<int64_t>(u) * s.chunks;
-      r.first = static_cast<int>(begin - r.unit);
+      const int size = s.chunks + kUnitCost;
+      const int u = static_cast<int>(quotient(begin - r.unit, size));
+      const int span = max(1, order.span(r.pair, s));
+      r.unit += static_cast<int64_t>(u) * size;
+      r.offset = static_cast<int>(begin - r.unit);
       r.kvh = u / span;
       r.inner = u - r.kvh * span;
     }
@@ -420,14 +440,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* q_full = s_done + 6;
   uint64_t* q_free = s_done + 7;
   uint64_t* o_free = s_done + 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kBar + 240);
-  unsigned* last_slot = reinterpret_cast<unsigned*>(sm + S::kBar + 244);
-  static_assert((4 * kStages + 9) * 8 <= 240, "barriers");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kBar + 248);
+  unsigned* last_slot = reinterpret_cast<unsigned*>(sm + S::kBar + 252);
+  constexpr int kBarriers = 4 * kStages + 9;
+  static_assert(kBarriers * 8 <= 248, "barriers");
   float* sums = reinterpret_cast<float*>(sm + S::kSums);                         // R > 1
   float2* stats = reinterpret_cast<float2*>(sm + S::kSums + kSumFloats * 4);  // [128]
 
   if (tid == 0) {
-    for (int i = 0; i < 4 * kStages + 9; ++i) mbar_init(bars + i, 1);
+    for (int i = 0; i < kBarriers; ++i) mbar_init(bars + i, 1);
     for (int i = 0; i < 2; ++i) mbar_init(p_ready + i, kSoftmaxThreads / 32);
     mbar_init(o_free, kSoftmaxThreads / 32);
     fence_mbar_init();
@@ -439,26 +460,25 @@ __global__ void __launch_bounds__(kThreads, 2)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  __shared__ Run run_slot;
+  __shared__ Plan plan;
+  __shared__ Run run;
   __shared__ int64_t warp_sums[2 * (kThreads / 32)];
   tc_fence_before();
-  cut(p, &run_slot, warp_sums);
+  cut(p, &plan, &run, warp_sums);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Run& run = run_slot;
+  const bool vwarp = warp == kCopyWarp + 1;
 
   if (warp >= kCopyWarp) {
     // ------------------------------------------------------------ copies
     // One warp for Q and the K ring, one for the V ring.  Block ids run kAhead
     // chunks ahead of the copies, across units.
-    const bool vwarp = warp == kCopyWarp + 1;
     struct Ahead {
       int id;       // lane j: the raw table entry of block j (checked at use)
       int blocks;   // of the chunk; 0: no chunk
       int kvh, q_row;  // q_row: of the chunk's Q if it opens a part, else -1
     };
-    constexpr int kAhead = 4;
-    Walk walk(p, run);
+    Walk walk(p, plan.order, run);
     Part it;
     bool some = walk.next(p, it);
     int c = 0;  // chunk of `it` that is fetched next
@@ -562,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     const uint64_t qdesc = sw128_desc(smem_u32(sm + S::kQ), 16, 1024);
     const uint32_t sK = smem_u32(sm + S::kK);
-    Walk walk(p, run);
+    Walk walk(p, plan.order, run);
     Part it;
     bool ok = true;
     int g = 0;
@@ -597,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       return __all_sync(kFullMask, mbar_wait_bounded(bar, use & 1, p.err)) != 0;
     };
     const uint32_t sV = smem_u32(sm + S::kV);
-    Walk walk(p, run);
+    Walk walk(p, plan.order, run);
     Part it;
     bool ok = true;
     int g = 0;
@@ -637,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float2 sl2x2 = make_float2(sl2, sl2);
     bool ok = true;  // sticky: this thread's waits all succeeded
     int g = 0;
-    Walk walk(p, run);
+    Walk walk(p, plan.order, run);
     Part it;
     while (walk.next(p, it)) {
       const int qi = it.i0 + tok;
@@ -669,7 +689,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             tmem_wait_ld();
             if (valid < kCols) {
-              asm volatile("");  // (a branch: as selects they would cost every chunk)
 #pragma unroll
               for (int j = 0; j < kCols; ++j)
                 if (j >= valid) sv[j] = __float_as_uint(-INFINITY);
@@ -914,8 +933,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (shared) {
         if (row_ok && lok && copy == 0) p.ws_ml[place + row] = make_float2(m_used, total);
         // the last CTA of the unit joins its parts (counted at its first CTA)
-        const int c0 = owner(run, it.unit);
-        const int parts = owner(run, it.unit + it.seq.chunks - 1) - c0 + 1;
+        const int64_t at = it.unit + kUnitCost;
+        const int c0 = plan.owner(at);
+        const int shares = plan.owner(at + it.seq.chunks - 1) - c0 + 1;
         asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
         if (tid == 0)
           asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
@@ -923,8 +943,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                        : "l"(p.counters + c0)
                        : "memory");
         asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
-        if (*last_slot + 1 == static_cast<unsigned>(parts)) {
-          join<D>(p, it, c0, parts);
+        if (*last_slot + 1 == static_cast<unsigned>(shares)) {
+          join<D>(p, it, c0, shares);
           if (tid == 0) p.counters[c0] = 0;
         }
       }
@@ -1040,7 +1060,8 @@ pa_status cross_impl(void* out, const void* q, int64_t q_stride, const void* k_c
                      pa_stream_t stream, pa_prepared** keep) {
   if (num_seqs < 0 || max_query_len < 0 || total_query_tokens < 0 || num_q_heads <= 0 ||
       num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || max_blocks_per_seq <= 0 ||
-      num_blocks <= 0 || !(scale > 0.f) || ws_ctas < 1)
+      num_blocks <= 0 || !(scale > 0.f) || ws_ctas < 1 ||
+      ws_ctas > (1 << 20))
     return PA_ERR_INVALID_ARG;
   const int group = num_q_heads / num_kv_heads;
   if (!pa_cross_attention_supported(head_dim, group, block_size)) return PA_ERR_UNSUPPORTED_SHAPE;

@@ -1177,17 +1177,23 @@ def pa_cross_attention_supported(head_dim, group, block_size=16):
     return bool(lib().pa_cross_attention_supported(head_dim, group, block_size))
 
 
-def cross_attention_workspace(max_query_len, num_q_heads, num_kv_heads, head_dim, device=None):
-    """(ws_out, ws_ml, counters) for pa_cross_attention on a device: fp32 [CTAs, 2, rows,
-    head_dim] and [CTAs, 2, rows, 2], and zeroed int32 [CTAs]."""
-    torch = _torch()
-    device = torch.device("cuda" if device is None else device)
-    ctas = lib().pa_cross_attention_ctas(
-        torch.cuda.get_device_properties(device).multi_processor_count)
-    rows = max(1, lib().pa_cross_attention_rows(int(max_query_len), num_q_heads // num_kv_heads))
-    return (torch.empty(ctas, 2, rows, head_dim, dtype=torch.float32, device=device),
-            torch.empty(ctas, 2, rows, 2, dtype=torch.float32, device=device),
-            torch.zeros(ctas, dtype=torch.int32, device=device))
+class CrossWorkspace:
+    """Workspace of pa_cross_attention: ws_out fp32 [ctas, 2, rows, head_dim], ws_ml fp32
+    [ctas, 2, rows, 2] and zeroed counters int32 [ctas], for sequences of up to
+    max_query_len queries.  ctas: the CTAs a call may use (default: what fills the GPU)."""
+
+    def __init__(self, max_query_len, num_q_heads, num_kv_heads, head_dim, device=None,
+                 ctas=None):
+        torch = _torch()
+        device = torch.device("cuda" if device is None else device)
+        self.ctas = int(ctas) if ctas is not None else lib().pa_cross_attention_ctas(
+            torch.cuda.get_device_properties(device).multi_processor_count)
+        group = num_q_heads // num_kv_heads
+        self.rows = max(1, lib().pa_cross_attention_rows(int(max_query_len), group))
+        self.ws_out = torch.empty(self.ctas, 2, self.rows, head_dim, dtype=torch.float32,
+                                  device=device)
+        self.ws_ml = torch.empty(self.ctas, 2, self.rows, 2, dtype=torch.float32, device=device)
+        self.counters = torch.zeros(self.ctas, dtype=torch.int32, device=device)
 
 
 def _cross_args(out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc,
@@ -1195,7 +1201,7 @@ def _cross_args(out, q, k_cache, v_cache, block_tables, source_lens, query_start
     """Checked and marshalled arguments of pa_cross_attention (without the stream)."""
     torch = _torch()
     what = "pa_cross_attention"
-    ws_o, ws_ml, counters = workspace
+    ws_o, ws_ml, counters = workspace.ws_out, workspace.ws_ml, workspace.counters
     _one_device(what, out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc, ws_o,
                 ws_ml, counters)
     pq, stride = _heads(q, "q")
@@ -1212,17 +1218,16 @@ def _cross_args(out, q, k_cache, v_cache, block_tables, source_lens, query_start
         raise ValueError(f"{what}: source_lens / query_start_loc shapes")
     max_query_len = int(max_query_len)
     rows = lib().pa_cross_attention_rows(max_query_len, hq // hkv)
-    ctas = counters.shape[0]
-    if ws_o.dim() != 4 or ws_o.shape[:2] != (ctas, 2) or ws_o.shape[2] < rows or \
-            ws_o.shape[3] != d or ws_ml.shape != (*ws_o.shape[:3], 2):
-        raise ValueError(f"{what}: workspace shapes")
+    need = workspace.ctas * 2 * rows
+    if ws_o.numel() < need * d or ws_ml.numel() < need * 2 or counters.numel() < workspace.ctas:
+        raise ValueError(f"{what}: the workspace was made for fewer rows")
     return (_dev(out, torch.bfloat16, "out", 3), pq, stride, pk,
             _dev(v_cache, torch.bfloat16, "v_cache", 4), pt, mb,
             _dev(source_lens, torch.int32, "source_lens", 1),
             _dev(query_start_loc, torch.int32, "query_start_loc", 1), max_query_len, B, T, hq,
             hkv, d, bs, nb, float(scale), _dev(ws_o, torch.float32, "ws_out", 4),
             _dev(ws_ml, torch.float32, "ws_ml", 4), _dev(counters, torch.int32, "counters", 1),
-            ctas)
+            workspace.ctas)
 
 
 def pa_cross_attention(out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc,
@@ -1233,7 +1238,7 @@ def pa_cross_attention(out, q, k_cache, v_cache, block_tables, source_lens, quer
 
     q [T, Hq, D] bf16, tokens strided or not, out [T, Hq, D]; source_lens [B],
     query_start_loc [B + 1] int32 (device); max_query_len: host bound on every
-    sequence's queries; workspace = cross_attention_workspace(...)."""
+    sequence's queries; workspace = CrossWorkspace(...)."""
     args = _cross_args(out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc,
                        max_query_len, scale, workspace)
     _check(lib().pa_cross_attention(*args, _stream(stream)), "pa_cross_attention")
@@ -1248,8 +1253,8 @@ class CrossAttention(_FixedCall):
                  max_query_len, scale, workspace=None, stream=None):
         made = workspace is None
         if made:
-            workspace = cross_attention_workspace(max_query_len, q.shape[1], k_cache.shape[1],
-                                                  q.shape[2], q.device)
+            workspace = CrossWorkspace(max_query_len, q.shape[1], k_cache.shape[1], q.shape[2],
+                                       q.device)
         self.workspace = workspace
         args = _cross_args(out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc,
                            max_query_len, scale, workspace)

@@ -4,8 +4,8 @@ several CTAs' worth, queries from one to many tiles, strided queries, rows of no
 sequence, NaN past the sources, bad lengths and blocks.
 
 Tolerance per element, from the roundings: the output to bf16, 2^-8 of itself; each
-weight to bf16, 2^-8 of it, so 2^-8 of the weighted mean of |V|; the scores'
-accumulation in fp32 (D terms, truncated: D 2^-23 of sum |q K| each) which moves
+weight to two bf16 parts, 2^-16 of it, and its exponential, 2^-20, so their sum of
+the weighted mean of |V|; the scores' accumulation in fp32 (D terms, truncated: D 2^-23 of sum |q K| each) which moves
 every weight by twice that; the accumulation over n keys, n 2^-23 of the mean."""
 import numpy as np
 import pytest
@@ -64,7 +64,7 @@ class Case:
         kmax = np.nan_to_num(np.abs(bf16_bits_to_f64(self.k))).max()
         moved = 2 * self.d * 2.0 ** -23 * self.scale * q * kmax
         n = np.repeat(self.sources, self.counts)[:, None, None]
-        tol = 2.0 ** -8 * np.abs(ref) + mean * (2.0 ** -8 + moved + (n + 64) * 2.0 ** -23)
+        tol = 2.0 ** -8 * np.abs(ref) + mean * (2.0 ** -16 + 2.0 ** -20 + moved + (n + 64) * 2.0 ** -23)
         bad = np.abs(got - ref) > tol * 1.0001 + 1e-30
         assert not bad.any(), (what, np.argwhere(bad)[:4], got[bad][:4], ref[bad][:4])
         assert not got[n[:, 0, 0] == 0].any(), "no source: zeros"
@@ -73,11 +73,11 @@ class Case:
 def _call(c, gap_value=7.0, **kw):
     q, k, v, tables, sources, start = c.on_gpu()
     out = torch.full_like(q, gap_value)
-    ws = pa.cross_attention_workspace(max(1, int(c.counts.max())), c.hq, c.hkv, c.d)
+    ws = pa.CrossWorkspace(max(1, int(c.counts.max())), c.hq, c.hkv, c.d)
     pa.pa_cross_attention(out, q, k, v, tables, sources, start, max(1, int(c.counts.max())),
                           c.scale, ws, **kw)
     torch.cuda.synchronize()
-    assert not ws[2].any(), "counters are left at zero"
+    assert not ws.counters.any(), "counters are left at zero"
     assert bool((out[int(c.counts.sum()):] == gap_value).all()), "rows of no sequence are left"
     return out
 
@@ -125,14 +125,31 @@ def test_any_number_of_ctas(ctas, d):
     c = Case(90, [700, 0, 64, 1300, 3], [3, 4, 40, 1, 2], 8, 2, d)
     q, k, v, tables, sources, start = c.on_gpu()
     out = torch.full_like(q, float("nan"))
-    ws = (torch.full((ctas, 2, 128, d), float("nan"), device="cuda"),
-          torch.full((ctas, 2, 128, 2), float("nan"), device="cuda"),
-          torch.zeros(ctas, dtype=torch.int32, device="cuda"))
+    ws = pa.CrossWorkspace(40, 8, 2, d, ctas=ctas)
+    ws.ws_out.fill_(float("nan"))
+    ws.ws_ml.fill_(float("nan"))
     for _ in range(2):
         pa.pa_cross_attention(out, q, k, v, tables, sources, start, 40, c.scale, ws)
     torch.cuda.synchronize()
     c.check(out, f"{ctas} CTAs")
-    assert not ws[2].any() and pa.pa_get_device_error() == 0
+    assert not ws.counters.any() and pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("ctas", [1, 2, 5, 40, 304])
+@pytest.mark.parametrize("d,m", [(64, 5), (128, 4), (128, 13)])
+def test_any_number_of_ctas_for_few_rows(ctas, d, m):
+    pa.pa_clear_device_error()
+    c = Case(100 + m, [9000, 0, 64, 1300, 3, 2500], [m, 1, m, 1, 0, m], 8, 2, d)
+    q, k, v, tables, sources, start = c.on_gpu()
+    out = torch.full_like(q, float("nan"))
+    ws = pa.CrossWorkspace(m, 8, 2, d, ctas=ctas)
+    ws.ws_out.fill_(float("nan"))
+    ws.ws_ml.fill_(float("nan"))
+    for _ in range(3):
+        pa.pa_cross_attention(out, q, k, v, tables, sources, start, m, c.scale, ws)
+    torch.cuda.synchronize()
+    c.check(out, f"{ctas} CTAs")
+    assert not ws.counters.any() and pa.pa_get_device_error() == 0
 
 
 def test_many_sequences():
@@ -188,7 +205,7 @@ def test_strided_queries():
     wide = torch.full((q.shape[0], 11, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
     wide[:, 2:10] = q
     out = torch.zeros_like(q)
-    ws = pa.cross_attention_workspace(33, 8, 2, 128)
+    ws = pa.CrossWorkspace(33, 8, 2, 128)
     pa.pa_cross_attention(out, wide[:, 2:10], k, v, tables, sources, start, 33, c.scale, ws)
     c.check(out)
     with pytest.raises(ValueError):
@@ -202,7 +219,7 @@ def test_queries_past_the_bound_are_left():
     c = Case(96, [70, 90], [40, 4], 4, 1, 128)
     q, k, v, tables, sources, start = c.on_gpu()
     out = torch.full_like(q, 7.0)
-    ws = pa.cross_attention_workspace(33, 4, 1, 128)
+    ws = pa.CrossWorkspace(33, 4, 1, 128)
     pa.pa_cross_attention(out, q, k, v, tables, sources, start, 33, c.scale, ws)
     assert bool((out[33:40] == 7.0).all())
     out[33:40] = _call(c)[33:40]
@@ -212,7 +229,7 @@ def test_queries_past_the_bound_are_left():
 def test_bad_lengths_skip_their_sequence():
     c = Case(97, [70, 90, 33], [4, 5, 6], 4, 2, 64)
     q, k, v, tables, sources, start = c.on_gpu()
-    ws = pa.cross_attention_workspace(6, 4, 2, 64)
+    ws = pa.CrossWorkspace(6, 4, 2, 64)
     for bad_s, bad_at in ((-1, None), (tables.shape[1] * 16 + 1, None), (None, 16), (None, 3)):
         s, at = sources.clone(), start.clone()
         if bad_s is not None:
@@ -245,7 +262,7 @@ def test_bad_block_is_reported():
         t[0, 2] = bad
         out = torch.zeros_like(q)
         pa.pa_cross_attention(out, q, k, v, t, sources, start, 5, c.scale,
-                              pa.cross_attention_workspace(5, 4, 2, 64))
+                              pa.CrossWorkspace(5, 4, 2, 64))
         assert pa.pa_get_device_error() == pa.PA_DEVERR_BLOCK_ID
         out[:4] = good[:4]
         c.check(out)
@@ -305,15 +322,15 @@ def test_first_call_on_another_stream():
     call()
     torch.cuda.synchronize()
     c.check(out)
-    assert not call.workspace[2].any() and pa.pa_get_device_error() == 0
+    assert not call.workspace.counters.any() and pa.pa_get_device_error() == 0
 
 
 def test_refusals():
     c = Case(121, [70], [4], 4, 2, 64)
     q, k, v, tables, sources, start = c.on_gpu()
     out = torch.zeros_like(q)
-    ws = pa.cross_attention_workspace(4, 4, 2, 64)
-    small = pa.cross_attention_workspace(3, 4, 2, 64)
+    ws = pa.CrossWorkspace(4, 4, 2, 64)
+    small = pa.CrossWorkspace(3, 4, 2, 64)
 
     def call(out=out, q=q, k=k, v=v, tables=tables, sources=sources, start=start, n=4, ws=ws):
         pa.pa_cross_attention(out, q, k, v, tables, sources, start, n, c.scale, ws)
@@ -343,6 +360,6 @@ def test_offsets_past_32_bits():
     q = dev_bf16(c.q)
     out = torch.zeros_like(q)
     pa.pa_cross_attention(out, q, k, v, _dev(c.tables + nb - n), _dev(c.sources), _dev(c.start), 3,
-                          c.scale, pa.cross_attention_workspace(3, 8, 8, d))
+                          c.scale, pa.CrossWorkspace(3, 8, 8, d))
     c.check(out)
     assert pa.pa_get_device_error() == 0

@@ -38,7 +38,7 @@ def test_cross_attention_refusals(lib):
                     dict(stride=1032 - 4), dict(stride=1016), dict(mb=0), dict(n=-1), dict(T=-1),
                     dict(max_q=-1), dict(hkv=3), dict(hkv=0), dict(nb=0), dict(scale=0.0),
                     dict(scale=-1.0), dict(scale=float("nan")), dict(ws=None), dict(ml=MIS8),
-                    dict(counters=None), dict(ctas=0), dict(nb=1 << 27), dict(mb=1 << 28)):
+                    dict(counters=None), dict(ctas=0), dict(ctas=(1 << 20) + 1), dict(nb=1 << 27), dict(mb=1 << 28)):
             assert call(prepare=prepare, **bad) == BAD, bad
         for shape in (dict(d=96), dict(d=256), dict(bs=32), dict(hq=64), dict(hq=12)):
             assert call(prepare=prepare, stride=1 << 14, **shape) == SHAPE, shape
