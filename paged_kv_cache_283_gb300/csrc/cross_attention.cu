@@ -96,7 +96,7 @@ constexpr int kThreads = kSoftmaxThreads + 128;
 constexpr int kScoreWarp = 4, kMixWarp = 5, kCopyWarp = 6;  // Q K^T, P V, copies of K and of V
 constexpr int kSumFloats = 4 * 32 * 20;  // room for 16 columns of every row's copies
 constexpr int kMinChunks = 4;  // of a unit's part, on average: less is not worth a join
-constexpr int kAhead = 4;      // chunks that block ids run ahead of their copies
+constexpr int kAhead = 2;      // batches of block ids that run ahead of their copies
 constexpr int kUnitCost = 2;   // of a unit's beginning and end, in chunks
 constexpr int kMaxParts = 64;  // CTAs that share a unit, on average at most
 constexpr uint32_t kTO = 2 * kKeys;     // O's first column, after two S buffers
@@ -485,28 +485,31 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp >= kCopyWarp) {
     // ------------------------------------------------------------ copies
-    // One warp for Q and the K ring, one for the V ring.  Block ids run kAhead
-    // chunks ahead of the copies, across units.
-    struct Ahead {
-      int id;       // lane j: the raw table entry of block j (checked at use)
-      int blocks;   // of the chunk; 0: no chunk
-      int kvh, q_row;  // q_row: of the chunk's Q if it opens a part, else -1
+    // One warp for Q and the K ring, one for the V ring.  A part's block ids are
+    // fetched a lane each, 32 at a time, kAhead such batches ahead of their copies.
+    constexpr int kBatch = 32 / kChunkBlocks;  // chunks
+    struct Batch {
+      int id;          // lane j: the raw table entry of block j (checked at use)
+      int blocks;      // 0: no batch
+      int kvh, q_row;  // q_row: of the Q of a part that the batch opens, else -1
     };
     Walk walk(p, plan.order, run);
     Part it;
     bool some = walk.next(p, it);
     int c = 0;  // chunk of `it` that is fetched next
-    auto fetch = [&]() -> Ahead {
-      Ahead a{0, 0, 0, -1};
+    auto fetch = [&]() -> Batch {
+      Batch a{0, 0, 0, -1};
       if (!some) return a;
       const int block = (it.first + c) * kChunkBlocks;
-      a.blocks = min(kChunkBlocks, (it.seq.src + kBS - 1) / kBS - block);
+      const int chunks = min(kBatch, it.count - c);
+      a.blocks = min(chunks * kChunkBlocks, (it.seq.src + kBS - 1) / kBS - block);
       a.kvh = it.kvh;
       if (c == 0) a.q_row = it.seq.q0 + it.i0;
       if (lane < a.blocks)
         a.id = __ldg(p.block_tables + static_cast<int64_t>(it.b) * p.max_blocks_per_seq + block +
                      lane);
-      if (++c == it.count) {
+      c += chunks;
+      if (c == it.count) {
         some = walk.next(p, it);
         c = 0;
       }
@@ -522,51 +525,50 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!vwarp)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tq)) : "memory");
     }
-    Ahead ahead[kAhead];
+    Batch ahead[kAhead];
+#pragma unroll 1
+    for (int i = 0; i < kAhead; ++i) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) ahead[i] = fetch();
+      for (int k = 0; k + 1 < kAhead; ++k) ahead[k] = ahead[k + 1];
+      ahead[kAhead - 1] = fetch();
+    }
     bool ok = true;
     int g = 0, items = 0;
-    for (; ahead[0].blocks > 0; ++g) {
-      Ahead a = ahead[0];
+    while (ok && ahead[0].blocks > 0) {
+      Batch a = ahead[0];
 #pragma unroll
-      for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+      for (int k = 0; k + 1 < kAhead; ++k) ahead[k] = ahead[k + 1];
       ahead[kAhead - 1] = fetch();
       if (lane < a.blocks && (a.id < 0 || a.id >= p.num_blocks)) {
         raise_error(p.err, PA_DEVERR_BLOCK_ID);  // never dereferenced: block 0 is read instead
         a.id = 0;
       }
       const int row = (a.id * p.num_kv_heads + a.kvh) * kBS;
-      const int st = g % kStages;
-      if (g >= kStages) ok = wait(vwarp ? &v_free[st] : &k_free[st], g / kStages - 1);
-      if (!ok) break;
-      uint64_t* bar = vwarp ? &v_full[st] : &k_full[st];
-      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(a.blocks * S::kHalves * S::kBox), leader);
-      if (vwarp) {
-        unsigned char* dst = sm + S::kV + st * S::kStage;
+#pragma unroll 1
+      for (int at = 0; at < a.blocks; at += kChunkBlocks) {
+        const int blocks = min(kChunkBlocks, a.blocks - at);
+        const int st = g % kStages;
+        if (g >= kStages) ok = wait(vwarp ? &v_free[st] : &k_free[st], g / kStages - 1);
+        if (!ok) break;
+        uint64_t* bar = vwarp ? &v_full[st] : &k_full[st];
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(blocks * S::kHalves * S::kBox), leader);
+        ++g;
+        unsigned char* dst = sm + (vwarp ? S::kV : S::kK) + st * S::kStage;
 #pragma unroll
         for (int j = 0; j < kChunkBlocks; ++j) {
-          const int y = __shfl_sync(kFullMask, row, j);
-          if (j < a.blocks)
+          const int y = __shfl_sync(kFullMask, row, at + j);
+          if (j >= blocks) continue;
+          if (vwarp) {
             tma_3d(dst + j * S::kHalves * S::kBox, &tv, 0, y, 0, bar, leader);
-        }
-      } else {
-        unsigned char* dst = sm + S::kK + st * S::kStage;
-#pragma unroll
-        for (int j = 0; j < kChunkBlocks; ++j) {
-          const int y = __shfl_sync(kFullMask, row, j);
-          if (j < a.blocks) {
+          } else {
 #pragma unroll
             for (int h = 0; h < S::kHalves; ++h)
               tma_2d(dst + h * S::kKVHalf + j * S::kBox, &tk, 64 * h, y, bar, leader);
           }
         }
-        if (a.q_row >= 0) {
+        if (!vwarp && at == 0 && a.q_row >= 0) {
           if (items > 0) ok = wait(q_free, items - 1);
-          if (!ok) {
-            ++g;
-            break;
-          }
+          if (!ok) break;
           mbar_arrive_expect_tx(q_full, S::kHalves * S::kQHalf, leader);
 #pragma unroll
           for (int h = 0; h < S::kHalves; ++h)
