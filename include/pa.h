@@ -746,7 +746,7 @@ pa_status pa_cross_attention(void* out, const void* q, int64_t q_stride, const v
  *                     are bf16 pools [num_out_blocks, Hkv, 16, head_dim]: row r goes
  *                     to slot slot_mapping[r] (negative: nowhere; past the pool:
  *                     PA_DEVERR_SLOT, nowhere).  Distinct rows, distinct slots.
- * The outputs must not overlap the pools.  head_dim 64 or 128, block_size 16 (else
+ * The outputs must not overlap the pools or each other.  head_dim 64 or 128, block_size 16 (else
  * PA_ERR_UNSUPPORTED_SHAPE); num_seqs <= 65535.  Device-side checks: row ranges
  * within total_rows and positions within the table's capacity (else
  * PA_DEVERR_CONTEXT_LEN and the sequence is skipped); bad block ids as pa_decode.
@@ -792,7 +792,8 @@ pa_status pa_read_cache(int kv_kind, void* k_out, void* v_out, int64_t out_strid
  *     16-byte aligned; counters: [num_searches], zero before the first call; each
  *     call leaves them zero.  Calls that may run at the same time must not share
  *     them.
- * scores_out may be scores and finished_out finished (num_keep == num_beams).
+ * scores_out may be scores and finished_out finished (num_keep == num_beams); else
+ * they do not overlap.
  * num_beams <= 32, num_keep <= 64, vocab <= 2^27, num_searches * num_beams <= 65535
  * (else PA_ERR_UNSUPPORTED_SHAPE).  Asynchronous on `stream`.
  */
@@ -813,7 +814,8 @@ pa_status pa_beam_select(float* scores_out, int32_t* parents_out, int32_t* token
  * (device), row numbers.  A row's parent lies in its own group of num_beams rows
  * (rows g * num_beams ..; else PA_DEVERR_PARENT and the row is left); a negative
  * parent, or its own, leaves the row as it is.  Rows may be of any type: block
- * tables, recurrent states, token histories.  Only changed rows and their parents
+ * tables, recurrent states, token histories.  The tensors' rows share no bytes with
+ * one another or with parents.  Only changed rows and their parents
  * are touched.  num_beams <= 32, num_groups <= 65535 (else
  * PA_ERR_UNSUPPORTED_SHAPE).  Asynchronous on `stream`; up to 64 tensors a launch.
  */

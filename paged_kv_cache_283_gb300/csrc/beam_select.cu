@@ -788,9 +788,12 @@ pa_status beam_impl(float* scores_out, int32_t* parents_out, int32_t* tokens_out
     return PA_ERR_INVALID_ARG;
   // an output may be the input of its kind only where a search's entries take its
   // own beams' places: the searches end at different times
-  if (num_keep != num_beams &&
-      (scores_out == scores || (finished_out && finished_out == finished)))
-    return PA_ERR_INVALID_ARG;
+  const int64_t in = static_cast<int64_t>(num_searches) * num_beams;
+  const int64_t found = static_cast<int64_t>(num_searches) * num_keep;
+  auto clash = [&](const void* o, const void* i, int64_t size) {
+    return ranges_meet(o, found * size, i, in * size) && !(o == i && num_keep == num_beams);
+  };
+  if (clash(scores_out, scores, 4) || clash(finished_out, finished, 1)) return PA_ERR_INVALID_ARG;
   BeamParams p{};
   p.out_scores = scores_out;
   p.out_parents = parents_out;

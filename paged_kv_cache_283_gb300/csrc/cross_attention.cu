@@ -53,7 +53,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <algorithm>
 #include <atomic>
 
 #include "../../include/pa.h"
@@ -1058,6 +1057,11 @@ pa_status cross_impl(void* out, const void* q, int64_t q_stride, const void* k_c
   if (q_stride < static_cast<int64_t>(num_q_heads) * head_dim || q_stride % 8 != 0 ||
       q_stride >= (1ll << 39))
     return PA_ERR_INVALID_ARG;
+  // (tiles are read by one CTA after others have written theirs)
+  const int64_t row = 2ll * num_q_heads * head_dim;
+  if (ranges_meet(out, row * total_query_tokens, q,
+                  2 * q_stride * (total_query_tokens - 1ll) + row))
+    return PA_ERR_INVALID_ARG;
   if (!aligned_ptr(ws_out, 16) || !aligned_ptr(ws_ml, 16) || !aligned_ptr(counters, 4))
     return PA_ERR_INVALID_ARG;
   const int64_t rows = static_cast<int64_t>(num_blocks) * num_kv_heads * kBS;
@@ -1093,11 +1097,10 @@ pa_status cross_impl(void* out, const void* q, int64_t q_stride, const void* k_c
   p.ws_rows = cross_rows(p.max_query_len, group);
   p.scale_log2 = scale * 1.4426950408889634f;
   // no more CTAs than the longest sources that the tables hold could feed
-  const int64_t most = static_cast<int64_t>((max_blocks_per_seq + kChunkBlocks - 1) / kChunkBlocks) *
-                       ((p.max_query_len + p.tile_tokens - 1) / p.tile_tokens) * num_seqs;
-  int ctas = ws_ctas;
-  if (most < ws_ctas)  // (then no product below passes 64 bits)
-    ctas = static_cast<int>(std::min<int64_t>(ws_ctas, most * num_kv_heads));
+  const double most = static_cast<double>((max_blocks_per_seq + kChunkBlocks - 1) / kChunkBlocks) *
+                      ((p.max_query_len + p.tile_tokens - 1) / p.tile_tokens) * num_seqs *
+                      num_kv_heads;
+  const int ctas = most < ws_ctas ? static_cast<int>(most) : ws_ctas;
   return launch_or_keep(
       [=](cudaStream_t s) {
         return head_dim == 64 ? launch_d<64>(tq, tk, tv, p, copies, ctas, s)

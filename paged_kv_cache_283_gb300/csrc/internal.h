@@ -166,6 +166,12 @@ inline bool aligned_ptr(const void* p, uintptr_t a) {
   return p != nullptr && reinterpret_cast<uintptr_t>(p) % a == 0;
 }
 
+inline bool ranges_meet(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + static_cast<uintptr_t>(b_bytes) &&
+         y < x + static_cast<uintptr_t>(a_bytes);
+}
+
 // Positions of a cache read back (read_cache.cu).
 struct ReadCacheParams {
   __nv_bfloat16* k_out;           // rows of Hkv * D at out_stride, or (slots) a bf16 pool

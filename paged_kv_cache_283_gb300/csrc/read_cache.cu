@@ -341,11 +341,12 @@ pa_status read_impl(int kv_kind, void* k_out, void* v_out, int64_t out_stride,
   const int64_t pool = tile * num_blocks * num_kv_heads;
   const int64_t written = slot_mapping ? 2 * kBS * row * num_out_blocks
                                        : 2 * ((total_rows - 1) * out_stride + row);
-  const char* outs[2] = {static_cast<const char*>(k_out), static_cast<const char*>(v_out)};
-  const char* pools[2] = {static_cast<const char*>(k_cache), static_cast<const char*>(v_cache)};
-  for (const char* o : outs)
-    for (const char* c : pools)
-      if (o < c + pool && c < o + written) return PA_ERR_INVALID_ARG;
+  const void* outs[2] = {k_out, v_out};
+  const void* pools[2] = {k_cache, v_cache};
+  for (const void* o : outs)
+    for (const void* c : pools)
+      if (ranges_meet(o, written, c, pool)) return PA_ERR_INVALID_ARG;
+  if (k_out == v_out) return PA_ERR_INVALID_ARG;
   p.k_out = static_cast<__nv_bfloat16*>(k_out);
   p.v_out = static_cast<__nv_bfloat16*>(v_out);
   p.k_cache = k_cache;

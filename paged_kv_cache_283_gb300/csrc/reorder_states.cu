@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <new>
 #include <utility>
 #include <vector>
@@ -208,6 +209,30 @@ struct Launches {
   }
 };
 
+// Whether two tensors' rows, or a row and the parents, share bytes: each tensor is
+// moved by CTAs of its own, and none may change what another still reads.  (Rows of
+// two tensors may alternate, as views of one.)
+bool rows_meet(void* const* states, int num_tensors, const int32_t* parents, int64_t rows,
+               int64_t row_bytes, int64_t row_stride) {
+  const uintptr_t stride = static_cast<uintptr_t>(row_stride);
+  const uintptr_t extent = static_cast<uintptr_t>((rows - 1) * row_stride + row_bytes);
+  std::vector<uintptr_t> at(num_tensors);
+  for (int t = 0; t < num_tensors; ++t) {
+    at[t] = reinterpret_cast<uintptr_t>(states[t]);
+    if (ranges_meet(states[t], static_cast<int64_t>(extent), parents, 4 * rows)) return true;
+  }
+  std::sort(at.begin(), at.end());
+  for (int i = 0; i < num_tensors; ++i)
+    for (int j = i + 1; j < num_tensors && at[j] - at[i] < extent; ++j) {
+      const uintptr_t past = (at[j] - at[i]) % stride;  // into a row's stride
+      const bool last = (at[j] - at[i]) / stride == static_cast<uintptr_t>(rows - 1);
+      if (past < static_cast<uintptr_t>(row_bytes) ||
+          (!last && stride - past < static_cast<uintptr_t>(row_bytes)))
+        return true;
+    }
+  return false;
+}
+
 pa_status reorder_impl(void* const* states, int num_tensors, const int32_t* parents,
                        int num_groups, int num_beams, int64_t row_bytes, int64_t row_stride,
                        pa_stream_t stream, pa_prepared** keep) {
@@ -224,6 +249,13 @@ pa_status reorder_impl(void* const* states, int num_tensors, const int32_t* pare
   for (int t = 0; t < num_tensors; ++t) {
     if (!states[t]) return PA_ERR_INVALID_ARG;
     bits |= reinterpret_cast<uintptr_t>(states[t]);
+  }
+  try {
+    if (rows_meet(states, num_tensors, parents, static_cast<int64_t>(num_groups) * num_beams,
+                  row_bytes, row_stride))
+      return PA_ERR_INVALID_ARG;
+  } catch (const std::bad_alloc&) {
+    return PA_ERR_INVALID_ARG;
   }
   ReorderParams p{};
   p.parents = parents;

@@ -1210,7 +1210,7 @@ def _cross_args(out, q, k_cache, v_cache, block_tables, source_lens, query_start
         raise ValueError(f"{what}: out must match q")
     pk = _dev(k_cache, torch.bfloat16, "k_cache", 4)
     nb, hkv, bs, d2 = k_cache.shape
-    if v_cache.shape != k_cache.shape or d2 != d or hq % hkv:
+    if v_cache.shape != k_cache.shape or d2 != d or not hkv or hq % hkv:
         raise ValueError(f"{what}: cache shapes")
     pt = _dev(block_tables, torch.int32, "block_tables", 2)
     B, mb = block_tables.shape

@@ -336,6 +336,28 @@ def test_reorder_cycles_strides_and_many_tensors():
     assert pa.pa_get_device_error() == 0
 
 
+@pytest.mark.parametrize("beams", [4, 16])
+def test_reorder_views_of_one_tensor(beams):
+    """Rows of several states that alternate in one tensor."""
+    pa.pa_clear_device_error()
+    rng = np.random.default_rng(beams)
+    parents = np.arange(48) // beams * beams + rng.integers(0, beams, 48)
+    whole = torch.randn((48, 5, 36), device="cuda")
+    before = whole.clone()
+    views = [whole[:, i] for i in (3, 0, 4, 1)]
+    pa.pa_reorder_states(views, _dev(parents, np.int32), beams)
+    want = before[parents.tolist()]
+    want[:, 2] = before[:, 2]
+    assert torch.equal(whole, want) and pa.pa_get_device_error() == 0
+    for twice in ([whole[:, 1], whole[:, 1]], [whole[:, 1:3], whole[:, 2:4]]):
+        with pytest.raises(pa.PAError):
+            pa.pa_reorder_states(twice, _dev(parents, np.int32), beams)
+    own = _dev(parents, np.int32)
+    with pytest.raises(pa.PAError):
+        pa.pa_reorder_states(own.view(48, 1), own, beams)
+    assert torch.equal(whole, want)
+
+
 def test_reorder_bad_parents_leave_their_rows():
     x = torch.randn((6, 33), device="cuda")
     before = x.clone()

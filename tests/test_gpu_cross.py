@@ -214,6 +214,21 @@ def test_strided_queries():
     assert pa.pa_get_device_error() == 0
 
 
+@pytest.mark.parametrize("m", [5, 50, 300])
+@pytest.mark.parametrize("bad", [0x7FC0, 0x7F80])
+def test_a_bad_query_keeps_to_itself(m, bad):
+    """A query of NaN or infinities gives NaN and leaves its tile's others as they are."""
+    pa.pa_clear_device_error()
+    c = Case(98, [700, 130], [m, m], 2, 1, 64)
+    clean = _call(c)
+    c.q[3], c.q[m + 1, 1] = bad, bad
+    got = _call(c)
+    rows = torch.ones(2 * m, 2, dtype=torch.bool, device="cuda")
+    rows[3], rows[m + 1, 1] = False, False
+    assert torch.equal(got[rows].view(torch.int16), clean[rows].view(torch.int16))
+    assert bool(got[~rows].isnan().all()) and pa.pa_get_device_error() == 0
+
+
 def test_queries_past_the_bound_are_left():
     pa.pa_clear_device_error()
     c = Case(96, [70, 90], [40, 4], 4, 1, 128)
@@ -345,6 +360,8 @@ def test_refusals():
             call(**kw)
     with pytest.raises(pa.PAError):
         pa.CrossAttention(out, q, k, v, tables, sources, start, 4, 0.0)
+    with pytest.raises(pa.PAError):
+        call(out=q)
 
 
 def test_offsets_past_32_bits():

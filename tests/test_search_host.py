@@ -7,6 +7,7 @@ import pytest
 from paged_kv_cache_283_gb300 import pa
 
 F = ctypes.c_void_p(0x10000)
+FAR = ctypes.c_void_p(1 << 40)
 MIS8, MIS2 = ctypes.c_void_p(0x10008), ctypes.c_void_p(0x10002)
 BAD, SHAPE, OK = pa.PA_ERR_INVALID_ARG, pa.PA_ERR_UNSUPPORTED_SHAPE, pa.PA_OK
 
@@ -20,7 +21,7 @@ def lib():
 # reach a kernel.
 
 def test_cross_attention_refusals(lib):
-    def call(out=F, q=F, stride=1024, k=F, v=F, tables=F, mb=4, lens=F, start=F, max_q=3, n=2,
+    def call(out=FAR, q=F, stride=1024, k=F, v=F, tables=F, mb=4, lens=F, start=F, max_q=3, n=2,
              T=6, hq=8, hkv=4, d=128, bs=16, nb=10, scale=0.1, ws=F, ml=F, counters=F, ctas=8,
              prepare=False):
         args = (out, q, stride, k, v, tables, mb, lens, start, max_q, n, T, hq, hkv, d, bs, nb,
@@ -38,7 +39,11 @@ def test_cross_attention_refusals(lib):
                     dict(stride=1032 - 4), dict(stride=1016), dict(mb=0), dict(n=-1), dict(T=-1),
                     dict(max_q=-1), dict(hkv=3), dict(hkv=0), dict(nb=0), dict(scale=0.0),
                     dict(scale=-1.0), dict(scale=float("nan")), dict(ws=None), dict(ml=MIS8),
-                    dict(counters=None), dict(ctas=0), dict(ctas=(1 << 20) + 1), dict(nb=1 << 27), dict(mb=1 << 28)):
+                    dict(counters=None), dict(ctas=0), dict(ctas=(1 << 20) + 1), dict(nb=1 << 27),
+                    dict(mb=1 << 28), dict(out=F), dict(out=ctypes.c_void_p(0x10000 + 12288 - 16)),
+                    dict(out=F, q=ctypes.c_void_p(0x10000 + 12288 - 16)),
+                    dict(out=ctypes.c_void_p(0x10000 + 2 * (5 * 4096 + 1024) - 16),
+                         stride=4096)):
             assert call(prepare=prepare, **bad) == BAD, bad
         for shape in (dict(d=96), dict(d=256), dict(bs=32), dict(hq=64), dict(hq=12)):
             assert call(prepare=prepare, stride=1 << 14, **shape) == SHAPE, shape
@@ -61,9 +66,9 @@ def test_cross_attention_sizes(lib):
 
 
 def test_read_cache_refusals(lib):
-    far = ctypes.c_void_p(1 << 40)
+    beside = ctypes.c_void_p((1 << 40) + 1024)
 
-    def call(kind=1, ko=far, vo=far, stride=512, k=F, v=F, ks=F, vs=F, tables=F, mb=4, first=None,
+    def call(kind=1, ko=FAR, vo=beside, stride=512, k=F, v=F, ks=F, vs=F, tables=F, mb=4, first=None,
              start=F, rows=9, n=2, T=12, slots=None, nob=0, hkv=4, d=128, bs=16, nb=10,
              prepare=False):
         args = (kind, ko, vo, stride, k, v, ks, vs, tables, mb, first, start, rows, n, T, slots,
@@ -82,7 +87,7 @@ def test_read_cache_refusals(lib):
                     dict(stride=511), dict(stride=504), dict(stride=516), dict(mb=0),
                     dict(rows=-1), dict(n=-1), dict(T=-1), dict(hkv=0), dict(nb=0),
                     dict(slots=F), dict(slots=ctypes.c_void_p(0x10004), nob=3), dict(mb=1 << 28),
-                    dict(ko=F), dict(vo=ctypes.c_void_p(0x10000 + 10 * 16 * 512 - 16)),
+                    dict(ko=F), dict(vo=FAR), dict(vo=ctypes.c_void_p(0x10000 + 10 * 16 * 512 - 16)),
                     dict(ko=ctypes.c_void_p(0x10000 - 16)),
                     dict(ko=ctypes.c_void_p(0x10000 - 16), slots=F, nob=1)):
             assert call(prepare=prepare, **bad) == BAD, bad
@@ -95,7 +100,7 @@ def test_read_cache_refusals(lib):
 
 
 def test_beam_select_refusals(lib):
-    def call(out=F, parents=F, tokens=F, fin_out=None, logits=F, stride=100, dtype=0, scores=F,
+    def call(out=F, parents=F, tokens=F, fin_out=None, logits=F, stride=100, dtype=0, scores=FAR,
              fin=None, eos=-1, n=2, beams=4, keep=8, vocab=100, ws=F, counters=F, flags=0,
              prepare=False):
         args = (out, parents, tokens, fin_out, logits, stride, dtype, scores, fin, eos, n, beams,
@@ -116,7 +121,10 @@ def test_beam_select_refusals(lib):
                     dict(beams=0), dict(keep=0), dict(vocab=0), dict(flags=2),
                     dict(flags=pa.PA_BEAM_IN_PLACE),
                     dict(out=ctypes.c_void_p(0x20000), scores=ctypes.c_void_p(0x20000)),
-                    dict(out=ctypes.c_void_p(0x20000), fin=F, fin_out=F, eos=3)):
+                    dict(out=ctypes.c_void_p(0x20000), fin=F, fin_out=F, eos=3),
+                    dict(scores=F, keep=4, out=ctypes.c_void_p(0x10000 + 4)),
+                    dict(scores=ctypes.c_void_p(0x10000 + 28), keep=4),
+                    dict(keep=4, fin=F, fin_out=ctypes.c_void_p(0x10000 + 7), eos=3)):
             assert call(prepare=prepare, **bad) == BAD, bad
         for shape in (dict(beams=33), dict(keep=65), dict(n=20000),
                       dict(vocab=(1 << 27) + 1, stride=1 << 28)):
@@ -137,7 +145,7 @@ def test_beam_select_workspace(lib):
 
 
 def test_reorder_refusals(lib):
-    def call(states=(0x10000,), parents=F, groups=2, beams=4, row=64, stride=64, n=None,
+    def call(states=(0x10000,), parents=FAR, groups=2, beams=4, row=64, stride=64, n=None,
              prepare=False):
         ptrs = None if states is None else (ctypes.c_void_p * max(1, len(states)))(*states)
         n = len(states or ()) if n is None else n
@@ -152,7 +160,13 @@ def test_reorder_refusals(lib):
     for prepare in (False, True):
         for bad in (dict(states=None, n=1), dict(states=(0x10000, None)), dict(parents=None),
                     dict(parents=MIS2), dict(groups=-1), dict(beams=0), dict(row=-1),
-                    dict(stride=63), dict(n=-1)):
+                    dict(stride=63), dict(n=-1), dict(states=(0x10000, 0x10000)),
+                    dict(states=(0x30000, 0x10000, 0x30000 + 511)),
+                    dict(states=(0x10000, 0x10000 + 128), stride=100),
+                    dict(states=(0x10000, 0x10000 + 64), stride=127),
+                    dict(states=(0x10000, 0x10000 + 7 * 100 + 63), stride=100),
+                    dict(parents=ctypes.c_void_p(0x10000 + 508)),
+                    dict(parents=ctypes.c_void_p(0x10000 - 28))):
             assert call(prepare=prepare, **bad) == BAD, bad
         for shape in (dict(beams=33), dict(groups=65536), dict(row=1 << 41, stride=1 << 41)):
             assert call(prepare=prepare, **shape) == SHAPE, shape
