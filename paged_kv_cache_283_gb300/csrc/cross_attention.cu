@@ -19,7 +19,8 @@
 //    of chunks whatever units it begins and ends in: ragged sources, few long ones
 //    and many short ones all keep every SM busy to the end.  A unit's beginning and end
 //    count as kUnitCost chunks (64 x 4 beams of sources of 128 to 2048 keys 75 ->
-//    62 us, 16 x 512 prompts 466 -> 445, against counting the chunks alone).  The
+//    62 us, 16 x 512 prompts 466 -> 445, against counting the chunks alone, when
+//    that was measured; 58.2 and 381 with four, 60.8 and 388 with one now).  The
 //    lengths are read on the device, so a captured call follows them.
 //  * A CTA is 4 softmax warps, a row a thread, and a warp each for the MMAs of
 //    Q K^T and of P V and for the copies of K and of V: a warp's waits take it
@@ -96,7 +97,7 @@ constexpr int kScoreWarp = 4, kMixWarp = 5, kCopyWarp = 6;  // Q K^T, P V, copie
 constexpr int kSumFloats = 4 * 32 * 20;  // room for 16 columns of every row's copies
 constexpr int kMinChunks = 4;  // of a unit's part, on average: less is not worth a join
 constexpr int kAhead = 2;      // batches of block ids that run ahead of their copies
-constexpr int kUnitCost = 2;   // of a unit's beginning and end, in chunks
+constexpr int kUnitCost = 4;   // of a unit's beginning and end, in chunks
 constexpr int kMaxParts = 64;  // CTAs that share a unit, on average at most
 constexpr uint32_t kTO = 2 * kKeys;     // O's first column, after two S buffers
 constexpr uint32_t kTmemCols = 256;
@@ -358,58 +359,67 @@ __device__ void cut(const CrossParams& p, Plan* plan, Run* out, int64_t* warp_su
 
 // The rows of a unit from its parts' (m, l, o): part k lies in the place of CTA
 // c0 + k, the first one in that of the unit its CTA ends in.  A thread takes 4
-// dims of a row at a time, four such pieces and two parts of each in flight.
-template <int D>
+// dims of a row at a time, P such pieces and E parts of each in flight.
+template <int D, int P, int E>
 __device__ __forceinline__ void join(const CrossParams& p, const Part& it, int c0, int parts) {
-  constexpr int kPieces = 4, kCols = D / 4;
+  constexpr int kCols = D / 4;
   const int shift = 31 - __clz(p.group);
   const int rows = min(kRows, (it.seq.n - it.i0) << shift);
   auto at = [&](int k, int row) {
     return (static_cast<int64_t>(c0 + k) * 2 + (k == 0)) * p.ws_rows + row;
   };
   const int pieces = rows * kCols;
-  for (int q0 = threadIdx.x; q0 < pieces; q0 += kPieces * kSoftmaxThreads) {
-    float m[kPieces], l[kPieces];
-    float4 acc[kPieces];
+#pragma unroll 1
+  for (int q0 = threadIdx.x; q0 < pieces; q0 += P * kSoftmaxThreads) {
+    float m[P], l[P];
+    float4 acc[P];
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
+    for (int j = 0; j < P; ++j) {
       m[j] = -INFINITY;
       l[j] = 0.f;
       acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int k0 = 0; k0 < parts; k0 += 2) {
-      float2 ml[kPieces][2];
-      float4 o[kPieces][2];
+#pragma unroll 1
+    for (int k0 = 0; k0 < parts; k0 += E) {
+      float2 ml[P][E];
+      float4 o[P][E];
       // (loads without conditions, so that none waits for another: past the end the
       // last piece or part again, without weight)
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j)
+      for (int j = 0; j < P; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < E; ++e) {
           const int q = min(q0 + j * kSoftmaxThreads, pieces - 1);
           const int64_t r = at(min(k0 + e, parts - 1), q / kCols);
           ml[j][e] = __ldcg(p.ws_ml + r);
           o[j][e] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + r * D) + q % kCols);
         }
-      if (k0 + 1 >= parts) {
 #pragma unroll
-        for (int j = 0; j < kPieces; ++j) ml[j][1] = make_float2(-INFINITY, 0.f);
-      }
+      for (int j = 0; j < P; ++j) {
+        float top = m[j];
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        const float top = fmaxf(m[j], fmaxf(ml[j][0].x, ml[j][1].x));
+        for (int e = 0; e < E; ++e) {
+          if (k0 + e >= parts) ml[j][e] = make_float2(-INFINITY, 0.f);
+          top = fmaxf(top, ml[j][e].x);
+        }
         const float ref = top == -INFINITY ? 0.f : top;
-        const float a = ex2(m[j] - ref), b = ex2(ml[j][0].x - ref), c = ex2(ml[j][1].x - ref);
+        const float a = ex2(m[j] - ref);
         m[j] = top;
-        l[j] = fmaf(l[j], a, fmaf(ml[j][0].y, b, ml[j][1].y * c));
-        acc[j].x = fmaf(acc[j].x, a, fmaf(o[j][0].x, b, o[j][1].x * c));
-        acc[j].y = fmaf(acc[j].y, a, fmaf(o[j][0].y, b, o[j][1].y * c));
-        acc[j].z = fmaf(acc[j].z, a, fmaf(o[j][0].z, b, o[j][1].z * c));
-        acc[j].w = fmaf(acc[j].w, a, fmaf(o[j][0].w, b, o[j][1].w * c));
+        l[j] *= a;
+        acc[j] = make_float4(acc[j].x * a, acc[j].y * a, acc[j].z * a, acc[j].w * a);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float b = ex2(ml[j][e].x - ref);
+          l[j] = fmaf(ml[j][e].y, b, l[j]);
+          acc[j].x = fmaf(o[j][e].x, b, acc[j].x);
+          acc[j].y = fmaf(o[j][e].y, b, acc[j].y);
+          acc[j].z = fmaf(o[j][e].z, b, acc[j].z);
+          acc[j].w = fmaf(o[j][e].w, b, acc[j].w);
+        }
       }
     }
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
+    for (int j = 0; j < P; ++j) {
       const int q = q0 + j * kSoftmaxThreads, r = q / kCols;
       if (q >= pieces) continue;
       const float z = l[j] > 0.f ? 1.f / l[j] : 0.f;
@@ -927,7 +937,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                        : "memory");
         asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
         if (*last_slot + 1 == static_cast<unsigned>(shares)) {
-          join<D>(p, it, c0, shares);
+          // (few rows, as of a long source's step, may have many parts)
+          if (R > 1 && ((it.seq.n - it.i0) << shift) * (D / 4) <= kSoftmaxThreads)
+            join<D, 1, 8>(p, it, c0, shares);
+          else
+            join<D, 4, 2>(p, it, c0, shares);
           if (tid == 0) p.counters[c0] = 0;
         }
       }
