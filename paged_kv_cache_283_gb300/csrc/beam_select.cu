@@ -295,6 +295,7 @@ __device__ __forceinline__ void best_of_room(int count, int k) {
   if (count <= kRank) {
     const int seg = threadIdx.x & 3;
     for (int c0 = 0; c0 < count; c0 += kThreads / 4) {
+      if (c0 + static_cast<int>(threadIdx.x >> 5) * 8 >= count) break;  // none for the warp
       const int c = c0 + static_cast<int>(threadIdx.x >> 2);
       const Key mine = c < count ? Key{sh.v[c], sh.i[c]} : nothing();
       int rank = 0;
