@@ -31,6 +31,8 @@
 #include <float.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "device.cuh"
 #include "internal.h"
 
@@ -42,6 +44,11 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtas = 4;      // an SM
 constexpr int kRoom = 1024;   // candidates that a CTA can hold
+constexpr int kHits = 512;    // blocks of a thread that can hold candidates
+constexpr int kMaxBlocks = 16;  // of a part
+#ifndef TARGET
+#define TARGET 608
+#endif
 constexpr int kRank = 192;    // up to this many are ranked by counting
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -203,6 +210,8 @@ __device__ __forceinline__ double log64(double s) {
 }
 
 struct Shared {
+  uint32_t tops[kMaxBlocks][kThreads];  // the maximum of each thread's logits of a block
+  uint16_t hit[kHits];
   uint64_t v[kRoom];
   uint64_t i[kRoom];
   Key best[kWarps];
@@ -216,7 +225,7 @@ struct Shared {
   int state[kBeamMaxBeams];  // of a beam: 0 ended in nothing, 1 goes on, 2 finished
   int place[kBeamMaxKeep];
   uint64_t bound;
-  int count;
+  int count, hits;
   unsigned arrived;
 };
 __device__ __forceinline__ Shared& shared() {
@@ -568,8 +577,8 @@ __device__ __forceinline__ void load8_shifted(const T* row, int e, int end, uint
   }
 }
 
-// grid (parts, rows).  V: pieces of eight logits a thread.
-template <typename T, int V>
+// grid (parts, rows).  P: pieces of eight logits that a thread takes of a block.
+template <typename T, int P>
 __global__ void __launch_bounds__(kThreads, kCtas)
     beam_select_kernel(const __grid_constant__ BeamParams p) {
   using W = Words<T>;
@@ -583,47 +592,67 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   if (part == 0 && tid == 0 && !isfinite(score) && score != -INFINITY)
     raise_error(p.err, PA_DEVERR_LOGITS);
   if (isfinite(score) && !(p.finished && p.finished[row])) {
+    constexpr int kBlock = P * kThreads * 8;
     const int begin = part * p.part_len, end = min(begin + p.part_len, p.vocab);
     const T* logits = static_cast<const T*>(p.logits);
     const T* mine = logits + row * p.row_stride;
-    uint32_t w[V][W::N];
-    if ((reinterpret_cast<uintptr_t>(mine) & 15) == 0) {  // (begin is a multiple of 8)
-      const T* at = mine + begin + tid * 8;
+    const bool aligned = (reinterpret_cast<uintptr_t>(mine) & 15) == 0;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(logits);
+    const uintptr_t hi = reinterpret_cast<uintptr_t>(
+        logits + (static_cast<int64_t>(gridDim.y) - 1) * p.row_stride + p.vocab);
+    auto load = [&](int e, uint32_t (&w)[W::N]) {  // (begin is a multiple of 8)
+      if (!aligned)
+        load8_shifted<T>(mine, e, end, lo, hi, w);
+      else if (e + 8 <= end)
+        load8_aligned<T>(mine + e, w);
+      else
+        load8_each<T>(mine, e, end, w);
+    };
+    // the thread's maximum, and its sum of exp(x - maximum); NaN where a logit is NaN
+    // or +inf
+    float tm = -INFINITY;
+    float2 s4[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+    const float2 unit = make_float2(kLog2e, kLog2e);
+    const int blocks = (end - begin + kBlock - 1) / kBlock;
+#pragma unroll 1
+    for (int b = 0; b < blocks; ++b) {
+      const int e = begin + b * kBlock + tid * 8;
+      uint32_t w[P][W::N];
+      if (aligned && begin + (b + 1) * kBlock <= end) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (begin + (j * kThreads + tid) * 8 + 8 <= end)
-          load8_aligned<T>(at + j * kThreads * 8, w[j]);
-        else
-          load8_each<T>(mine, begin + (j * kThreads + tid) * 8, end, w[j]);
+        for (int j = 0; j < P; ++j) load8_aligned<T>(mine + e + j * kThreads * 8, w[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < P; ++j) load(e + j * kThreads * 8, w[j]);
       }
-    } else {
-      const uintptr_t lo = reinterpret_cast<uintptr_t>(logits);
-      const uintptr_t hi = reinterpret_cast<uintptr_t>(
-          logits + (static_cast<int64_t>(gridDim.y) - 1) * p.row_stride + p.vocab);
+      typename W::Top top = W::none();
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        load8_shifted<T>(mine, begin + (j * kThreads + tid) * 8, end, lo, hi, w[j]);
+      for (int j = 0; j < P; ++j) W::raise(top, w[j]);
+      sh.tops[b][tid] = *reinterpret_cast<const uint32_t*>(&top);
+      const float bm = W::value(top);
+      if (bm > tm) {
+        const float a = ex2((tm - bm) * kLog2e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s4[i] = make_float2(s4[i].x * a, s4[i].y * a);
+        tm = bm;
+      }
+      const float ref = tm == -INFINITY ? 0.f : -tm;
+      const float2 ref2 = make_float2(ref, ref);
+#pragma unroll
+      for (int j = 0; j < P; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 d = __fmul2_rn(__fadd2_rn(W::pair(w[j], i), ref2), unit);
+          s4[i] = __fadd2_rn(s4[i], make_float2(ex2(d.x), ex2(d.y)));
+        }
     }
-    // the thread's maximum, and the warp's
-    typename W::Top top = W::none();
-#pragma unroll
-    for (int j = 0; j < V; ++j) W::raise(top, w[j]);
-    float tm = W::value(top), wm = tm;
+    const float2 a2 = __fadd2_rn(__fadd2_rn(s4[0], s4[1]), __fadd2_rn(s4[2], s4[3]));
+    // the warp's
+    float wm = tm;
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) wm = fmaxf(wm, __shfl_xor_sync(kFullMask, wm, m));
-    // the warp's sum of exp(x - its maximum); NaN where a logit is NaN or +inf
-    const float ref = wm == -INFINITY ? 0.f : -wm;
-    const float2 ref2 = make_float2(ref, ref), unit = make_float2(kLog2e, kLog2e);
-    float2 s4[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 d = __fmul2_rn(__fadd2_rn(W::pair(w[j], i), ref2), unit);
-        s4[i] = __fadd2_rn(s4[i], make_float2(ex2(d.x), ex2(d.y)));
-      }
-    const float2 a2 = __fadd2_rn(__fadd2_rn(s4[0], s4[1]), __fadd2_rn(s4[2], s4[3]));
     float ws = a2.x + a2.y;
+    if (tm > -INFINITY) ws *= ex2((tm - wm) * kLog2e);
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) ws += __shfl_xor_sync(kFullMask, ws, m);
     // the groups' maxima
@@ -635,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       sh.m[warp] = wm;
       sh.s[warp] = ws;
     }
-    if (tid == 0) sh.count = 0;
+    if (tid == 0) sh.count = sh.hits = 0;
     if (__syncthreads_or(!(ws < INFINITY))) {
       // A NaN or +inf is no token: the part once more from memory, which hides them.
       if (tid == 0) raise_error(p.err, PA_DEVERR_LOGITS);
@@ -662,20 +691,31 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       const float bound =
           fmaxf(__uint_as_float(static_cast<uint32_t>(sh.bound)), Words<T>::kLowest);
       if (tm >= bound) {
-        uint32_t bits[V];
-        int n = 0;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          bits[j] = W::reach(w[j], bound);
-          n += __popc(bits[j]);
+        for (int b = 0; b < blocks; ++b) {
+          const uint32_t top = sh.tops[b][tid];
+          if (W::value(*reinterpret_cast<const typename W::Top*>(&top)) < bound) continue;
+          const int at = atomicAdd(&sh.hits, 1);
+          if (at < kHits) sh.hit[at] = static_cast<uint16_t>(b * kThreads + tid);
         }
-        int at = atomicAdd(&sh.count, n);
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          for (; bits[j] != 0; bits[j] &= bits[j] - 1, ++at)
-            if (at < kRoom)
-              sh.i[at] = static_cast<uint64_t>(begin + (j * kThreads + tid) * 8 +
-                                               logit_of<T>(__ffs(bits[j]) - 1));
+      }
+      __syncthreads();
+      // those blocks' pieces once more, a thread each
+      const int hits = sh.hits;
+      for (int c = tid; c < min(hits, kHits) * P; c += kThreads) {
+        const int at_block = sh.hit[c / P], j = c % P;
+        const int e = begin + (at_block / kThreads) * kBlock +
+                      (j * kThreads + at_block % kThreads) * 8;
+        uint32_t w[W::N];
+        load(e, w);
+        uint32_t bits = W::reach(w, bound);
+        if (bits == 0) continue;
+        int at = atomicAdd(&sh.count, hits <= kHits ? __popc(bits) : kRoom + 1);
+        for (; bits != 0; bits &= bits - 1, ++at)
+          if (at < kRoom) {
+            const int i = e + logit_of<T>(__ffs(bits) - 1);
+            sh.i[at] = static_cast<uint64_t>(i);
+            sh.v[at] = ordered(static_cast<float>(mine[i]));
+          }
       }
       __syncthreads();
     }
@@ -688,10 +728,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       p.ws_sums[row * p.parts + part] = make_float2(m, s);
     }
     const int count = sh.count;
-    if (count <= kRoom) {  // (their values once more: they are in the nearest cache)
-      for (int c = tid; c < count; c += kThreads)
-        sh.v[c] = ordered(static_cast<float>(mine[sh.i[c]]));
-      __syncthreads();
+    if (count <= kRoom) {
       best_of_room(count, K);
     } else {
       one_by_one_of_row(mine, begin, end, K);
@@ -714,52 +751,40 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   if (tid == 0) p.counters[search] = 0;
 }
 
-template <typename T, int V>
+template <typename T, int P>
 cudaError_t launch(const BeamParams& p, cudaStream_t stream) {
   const dim3 grid(p.parts, p.searches * p.beams);
-  return launch_pdl(beam_select_kernel<T, V>, grid, dim3(kThreads), 0, stream, p);
+  return launch_pdl(beam_select_kernel<T, P>, grid, dim3(kThreads), 0, stream, p);
 }
 
 template <typename T>
-cudaError_t launch_t(const BeamParams& p, int pieces, cudaStream_t stream) {
-  switch (pieces) {
-    case 1: return launch<T, 1>(p, stream);
-    case 2: return launch<T, 2>(p, stream);
-    case 4: return launch<T, 4>(p, stream);
-    default:
-      if constexpr (sizeof(T) == 2) return launch<T, 8>(p, stream);
-      return launch<T, 4>(p, stream);
-  }
+cudaError_t launch_t(const BeamParams& p, cudaStream_t stream) {
+  if (p.part_len <= kThreads * 8) return launch<T, 1>(p, stream);
+  return launch<T, sizeof(T) == 4 ? 2 : 4>(p, stream);
+}
+
+// Length of the parts that a row is cut into.
+int beam_part_len(int rows, int vocab, int dtype) {
+  const int least = kThreads * 8, most = (dtype == 2 ? 2 : 4) * least * kMaxBlocks;
+  const int parts = std::max(1, std::min(TARGET / std::max(rows, 1), (vocab + least - 1) / least));
+  return std::min(((vocab + parts - 1) / parts + 7) / 8 * 8, most);
 }
 
 }  // namespace
 
-// Pieces of eight logits a thread: as many as leave the GPU enough CTAs.
-int beam_pieces(int rows, int vocab, int dtype) {
-  const int most = dtype == 2 ? 4 : 8;
-  int v = 1;
-  while (v < most && static_cast<int64_t>(rows) * ((vocab + kThreads * 16 * v - 1) /
-                                                    (kThreads * 16 * v)) >= 608)
-    v *= 2;
-  return v;
-}
-
 int beam_parts(int rows, int vocab, int dtype) {
-  const int per = kThreads * 8 * beam_pieces(rows, vocab, dtype);
-  return (vocab + per - 1) / per;
+  const int len = beam_part_len(rows, vocab, dtype);
+  return (vocab + len - 1) / len;
 }
 
 cudaError_t launch_beam_select(BeamParams p, int dtype, cudaStream_t stream) {
-  const int rows = p.searches * p.beams;
-  const int pieces = beam_pieces(rows, p.vocab, dtype);
-  // parts of equal length, whole pieces
-  p.part_len = (((p.vocab + p.parts - 1) / p.parts) + 7) / 8 * 8;
+  p.part_len = beam_part_len(p.searches * p.beams, p.vocab, dtype);
   p.groups = 8;
   while (p.groups < p.keep) p.groups *= 2;
   switch (dtype) {
-    case 0: return launch_t<__nv_bfloat16>(p, pieces, stream);
-    case 1: return launch_t<__half>(p, pieces, stream);
-    default: return launch_t<float>(p, pieces, stream);
+    case 0: return launch_t<__nv_bfloat16>(p, stream);
+    case 1: return launch_t<__half>(p, stream);
+    default: return launch_t<float>(p, stream);
   }
 }
 
