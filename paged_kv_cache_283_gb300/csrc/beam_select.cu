@@ -9,12 +9,17 @@
 // and the K largest logits of each part of the row; the totals are needed for
 // those alone.
 //
-//  * A CTA takes a part of a row, E logits a thread, all in registers before
-//    any is used.  256 threads form G >= K groups; the K-th largest of the
-//    groups' maxima is a bound that at least K logits reach, and hardly more do
-//    (of independent values some G ln G): those go to shared memory, where each
-//    counts how many precede it.  Where many are equal (or G ln G is far above K)
-//    more may reach the bound: then the K largest are taken one by one.
+//  * A CTA takes a part of a row, block by block, P pieces of eight logits a thread
+//    in flight, and leaves each thread's maximum of each block in shared memory.
+//    256 threads form G >= K groups; the K-th largest of the groups' maxima is a
+//    bound that at least K logits reach, and hardly more do (of independent values
+//    some G ln G): only the blocks whose maximum reaches it are read again, and what
+//    reaches it goes to shared memory, where each counts how many precede it.
+//    Where many are equal (or G ln G is far above K) more may reach the bound: then
+//    the K largest are taken one by one.
+//  * 64 x 4 beams of 128,256 bf16 tokens: 17.9 us, 3.7 TB/s (short parts whose logits
+//    all stay in registers take 25.2: the phases after a part's sums cost two thirds
+//    of its instructions).  The next block's loads ahead of this one's use: 19.4.
 //  * Which thread holds which logit goes by its index in the row alone, not by
 //    the row's alignment, so equal rows have equal sums, bit for bit, and equal
 //    totals: ties go to the lower beam, then to the lower token.
@@ -43,12 +48,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtas = 4;      // an SM
+constexpr int kWave = 4 * 152;  // CTAs of a wave
 constexpr int kRoom = 1024;   // candidates that a CTA can hold
 constexpr int kHits = 512;    // blocks of a thread that can hold candidates
 constexpr int kMaxBlocks = 16;  // of a part
-#ifndef TARGET
-#define TARGET 608
-#endif
 constexpr int kRank = 192;    // up to this many are ranked by counting
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -614,10 +617,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     float2 s4[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
     const float2 unit = make_float2(kLog2e, kLog2e);
     const int blocks = (end - begin + kBlock - 1) / kBlock;
+    uint32_t w[P][W::N];
 #pragma unroll 1
     for (int b = 0; b < blocks; ++b) {
       const int e = begin + b * kBlock + tid * 8;
-      uint32_t w[P][W::N];
       if (aligned && begin + (b + 1) * kBlock <= end) {
 #pragma unroll
         for (int j = 0; j < P; ++j) load8_aligned<T>(mine + e + j * kThreads * 8, w[j]);
@@ -690,32 +693,39 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       // (at least the type's lowest number: what is hidden reaches nothing)
       const float bound =
           fmaxf(__uint_as_float(static_cast<uint32_t>(sh.bound)), Words<T>::kLowest);
-      if (tm >= bound) {
-        for (int b = 0; b < blocks; ++b) {
-          const uint32_t top = sh.tops[b][tid];
-          if (W::value(*reinterpret_cast<const typename W::Top*>(&top)) < bound) continue;
-          const int at = atomicAdd(&sh.hits, 1);
-          if (at < kHits) sh.hit[at] = static_cast<uint16_t>(b * kThreads + tid);
-        }
-      }
-      __syncthreads();
-      // those blocks' pieces once more, a thread each
-      const int hits = sh.hits;
-      for (int c = tid; c < min(hits, kHits) * P; c += kThreads) {
-        const int at_block = sh.hit[c / P], j = c % P;
-        const int e = begin + (at_block / kThreads) * kBlock +
-                      (j * kThreads + at_block % kThreads) * 8;
-        uint32_t w[W::N];
-        load(e, w);
+      auto find = [&](const uint32_t (&w)[W::N], int e, int found) {
         uint32_t bits = W::reach(w, bound);
-        if (bits == 0) continue;
-        int at = atomicAdd(&sh.count, hits <= kHits ? __popc(bits) : kRoom + 1);
+        if (bits == 0) return;
+        int at = atomicAdd(&sh.count, found > 0 ? found : __popc(bits));
         for (; bits != 0; bits &= bits - 1, ++at)
           if (at < kRoom) {
             const int i = e + logit_of<T>(__ffs(bits) - 1);
             sh.i[at] = static_cast<uint64_t>(i);
             sh.v[at] = ordered(static_cast<float>(mine[i]));
           }
+      };
+      if constexpr (P == 1) {  // (the part is one piece a thread, still in registers)
+        if (tm >= bound) find(w[0], begin + tid * 8, 0);
+      } else {
+        if (tm >= bound) {
+          for (int b = 0; b < blocks; ++b) {
+            const uint32_t top = sh.tops[b][tid];
+            if (W::value(*reinterpret_cast<const typename W::Top*>(&top)) < bound) continue;
+            const int at = atomicAdd(&sh.hits, 1);
+            if (at < kHits) sh.hit[at] = static_cast<uint16_t>(b * kThreads + tid);
+          }
+        }
+        __syncthreads();
+        // those blocks' pieces once more, a thread each (too many: one by one below)
+        const int hits = sh.hits;
+        for (int c = tid; c < min(hits, kHits) * P; c += kThreads) {
+          const int at_block = sh.hit[c / P], j = c % P;
+          const int e = begin + (at_block / kThreads) * kBlock +
+                        (j * kThreads + at_block % kThreads) * 8;
+          uint32_t again[W::N];
+          load(e, again);
+          find(again, e, hits > kHits ? kRoom + 1 : 0);
+        }
       }
       __syncthreads();
     }
@@ -763,10 +773,13 @@ cudaError_t launch_t(const BeamParams& p, cudaStream_t stream) {
   return launch<T, sizeof(T) == 4 ? 2 : 4>(p, stream);
 }
 
-// Length of the parts that a row is cut into.
+// Length of the parts that a row is cut into: one wave of CTAs, where that leaves a
+// thread a piece and no part more than kMaxBlocks blocks.  (64 x 4 beams of 128,256
+// tokens in 2, 4, 7 and 9 parts a row: 17.9, 20.1, 28.0 and 29.1 us; five and six CTAs an
+// SM 21.0 and 28.3.)
 int beam_part_len(int rows, int vocab, int dtype) {
   const int least = kThreads * 8, most = (dtype == 2 ? 2 : 4) * least * kMaxBlocks;
-  const int parts = std::max(1, std::min(TARGET / std::max(rows, 1), (vocab + least - 1) / least));
+  const int parts = std::max(1, std::min(kWave / std::max(rows, 1), (vocab + least - 1) / least));
   return std::min(((vocab + parts - 1) / parts + 7) / 8 * 8, most);
 }
 
