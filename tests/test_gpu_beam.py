@@ -10,9 +10,10 @@ from paged_kv_cache_283_gb300 import pa
 
 pytestmark = pytest.mark.gpu
 
-# A total's error: the exponentials (2^-22 of each) and the sums of at most 64 terms a
-# thread and 32 x 8 x parts of them (2^-24 each) move the log-sum by less than 1e-5 of 1;
-# the total is rounded to fp32 (2^-24 of itself).
+# A total's error: the exponentials (2^-22 of each), the sums of at most 64 terms (2^-24
+# each) under at most 16 changes of a thread's reference (2^-22 + 2^-24 each) and those of
+# the threads, warps and parts move the log-sum by less than 1e-5 of 1; the total is
+# rounded to fp32 (2^-24 of itself).
 ATOL = 1e-5
 T = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 
@@ -104,19 +105,47 @@ def test_many_rows(n, beams, vocab, dtype):
     """As many rows as make threads take more logits each."""
     pa.pa_clear_device_error()
     s = Search(n + vocab, n, beams, beams, vocab, dtype, finished=0.1)
-    got = s.call()
-    take = np.random.default_rng(0).choice(n, 12, replace=False)
+    check_some(s, s.call(), np.random.default_rng(0).choice(n, 12, replace=False))
+    assert pa.pa_get_device_error() == 0
+
+
+def check_some(s, got, take):
+    """Searches `take` of s alone."""
     few = Search.__new__(Search)
     few.__dict__ = dict(s.__dict__)
-    rows = (take[:, None] * beams + np.arange(beams)).reshape(-1)
-    few.n = 12
+    rows = (take[:, None] * s.beams + np.arange(s.beams)).reshape(-1)
+    few.n = len(take)
     few.logits, few.scores = s.logits[rows], s.scores[rows]
-    few.finished = s.finished[rows]
-    shift = (take - np.arange(12))[:, None] * beams
+    few.finished = None if s.finished is None else s.finished[rows]
+    shift = (take - np.arange(len(take)))[:, None] * s.beams
     part = [g[take] for g in got]
     part[1] = np.where(part[1] >= 0, part[1] - shift, -1)
     few.check(part)
+
+
+@pytest.mark.parametrize("dtype", sorted(T))
+@pytest.mark.parametrize("pad", [0, 1, 7])
+def test_long_parts(dtype, pad):
+    """Rows whose parts have many blocks of logits: of any values, rising, equal, all but a
+    few hidden, and bad in a last block."""
+    pa.pa_clear_device_error()
+    s = Search(pad, 128, 4, 6, 61003, dtype, pad=pad)
+    s.logits[8:12] = torch.linspace(-9, 9, 61003, device="cuda").to(T[dtype])
+    s.logits[16:20] = 0.25
+    s.scores[16:20] = -1.0
+    s.logits[24:28] = -float("inf")
+    s.logits[25, 60000:60004] = 1.0
+    got = s.call()
+    check_some(s, got, np.array([0, 2, 4, 6, 7, 127]))
+    assert got[1][4].tolist() == [16] * 6 and got[2][4].tolist() == list(range(6))
+    assert got[2][6].tolist() == [60000, 60001, 60002, 60003, -1, -1]
     assert pa.pa_get_device_error() == 0
+    s.logits[33, 60990], s.logits[34, 5], s.logits[35, 61002] = (float("nan"), float("inf"),
+                                                                 float("nan"))
+    got = s.call()
+    assert pa.pa_get_device_error() == pa.PA_DEVERR_LOGITS
+    pa.pa_clear_device_error()
+    check_some(s, got, np.array([7, 8, 9]))
 
 
 @pytest.mark.parametrize("pad", [0, 1, 3, 4, 5, 8])
