@@ -11,12 +11,12 @@
 //
 //  * A CTA takes a part of a row, block by block, P pieces of eight logits a thread
 //    in flight, and leaves each thread's maximum of each block in shared memory.
-//    256 threads form G >= K groups; the K-th largest of the groups' maxima is a
+//    256 threads form G >= 2 K groups; the K-th largest of the groups' maxima is a
 //    bound that at least K logits reach, and hardly more do (of independent values
-//    some G ln G): only the blocks whose maximum reaches it are read again, and what
+//    some 1.4 K): only the blocks whose maximum reaches it are read again, and what
 //    reaches it goes to shared memory, where each counts how many precede it.
-//    Where many are equal (or G ln G is far above K) more may reach the bound: then
-//    the K largest are taken one by one.
+//    Where many are equal more may reach the bound: then the K largest are taken one
+//    by one.
 //  * 64 x 4 beams of 128,256 bf16 tokens: 17.9 us, 3.7 TB/s (short parts whose logits
 //    all stay in registers take 25.2: the phases after a part's sums cost two thirds
 //    of its instructions).  The next block's loads ahead of this one's use: 19.4.
@@ -52,6 +52,7 @@ constexpr int kWave = 4 * 152;  // CTAs of a wave
 constexpr int kRoom = 1024;   // candidates that a CTA can hold
 constexpr int kHits = 512;    // blocks of a thread that can hold candidates
 constexpr int kMaxBlocks = 16;  // of a part
+constexpr int kGroups = 128;  // at most
 constexpr int kRank = 192;    // up to this many are ranked by counting
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -219,8 +220,8 @@ struct Shared {
   uint64_t i[kRoom];
   Key best[kWarps];
   Key last;
-  float group_max[64];
-  uint64_t group_key[64], warp_key[kWarps][32];
+  float group_max[kGroups];
+  uint64_t group_key[kGroups], warp_key[kWarps][32];
   float m[kWarps], s[kWarps];
   uint64_t out_v[kBeamMaxKeep];  // the K found, first to last
   uint64_t out_i[kBeamMaxKeep];
@@ -388,12 +389,15 @@ __device__ __forceinline__ void merge(const BeamParams& p, int search) {
   const int total = W * p.parts * K;
   const uint64_t* parts = p.ws_keys + static_cast<int64_t>(search) * total;
   // Thread t takes candidates t, t + 256, .. of the parts' firsts, then their seconds
-  // and so on, and group g of `groups` the threads t = g mod groups: every group has
-  // firsts of every beam, and the bound below is a good one.
+  // and so on, and group g of `groups` the threads t = g mod groups.  The list of a
+  // part moves on by an odd number of groups from one rank to the next, so that the
+  // many finds of one good beam lie in many groups, and the bound below is a good one
+  // (32 beams of 128,256 tokens, K = 64, lists of one group each: ms).
   const int lists = W * p.parts;
+  const bool turn = ((lists & (p.groups - 1)) & 1) == 0;
   auto place = [&](int c) {
-    const int r = c / lists;
-    return (c - r * lists) * K + r;
+    const int r = c / lists, l = c - r * lists;
+    return (turn ? (l + r) % lists : l) * K + r;
   };
   constexpr int kHeld = 2;  // candidates of a thread that stay in registers
   uint64_t raw[kHeld];
@@ -451,9 +455,9 @@ __device__ __forceinline__ void merge(const BeamParams& p, int search) {
   }
   sh.warp_key[tid >> 5][tid & 31] = gm;
   __syncthreads();
-  if (tid < p.groups) {  // (64 groups: of every second warp)
+  if (tid < p.groups) {  // (above 32 groups: of every second warp, or fourth)
     uint64_t x = 0;
-    for (int w = tid >> 5; w < kWarps; w += p.groups > 32 ? 2 : 1) {
+    for (int w = tid >> 5; w < kWarps; w += p.groups > 32 ? p.groups / 32 : 1) {
       const uint64_t o = sh.warp_key[w][tid & 31];
       x = o > x ? o : x;
     }
@@ -792,8 +796,11 @@ int beam_parts(int rows, int vocab, int dtype) {
 
 cudaError_t launch_beam_select(BeamParams p, int dtype, cudaStream_t stream) {
   p.part_len = beam_part_len(p.searches * p.beams, p.vocab, dtype);
-  p.groups = 8;
-  while (p.groups < p.keep) p.groups *= 2;
+  // (of G groups' maxima the K-th largest is reached by some G ln(G / (G - K)) logits:
+  // twice K, 1.4 K; as many as K, K ln K and more than can be ranked by counting)
+  static_assert(2 * kBeamMaxKeep <= kGroups, "groups");
+  p.groups = 16;
+  while (p.groups < 2 * p.keep) p.groups *= 2;
   switch (dtype) {
     case 0: return launch_t<__nv_bfloat16>(p, stream);
     case 1: return launch_t<__half>(p, stream);
