@@ -17,9 +17,9 @@
 //    reaches it goes to shared memory, where each counts how many precede it.
 //    Where many are equal more may reach the bound: then the K largest are taken one
 //    by one.
-//  * 64 x 4 beams of 128,256 bf16 tokens: 17.9 us, 3.7 TB/s (short parts whose logits
+//  * 64 x 4 beams of 128,256 bf16 tokens: 17.4 us, 3.8 TB/s (short parts whose logits
 //    all stay in registers take 25.2: the phases after a part's sums cost two thirds
-//    of its instructions).  The next block's loads ahead of this one's use: 19.4.
+//    of its instructions).  The next block's loads ahead of this one's use: 19.4 against 17.9.
 //  * Which thread holds which logit goes by its index in the row alone, not by
 //    the row's alignment, so equal rows have equal sums, bit for bit, and equal
 //    totals: ties go to the lower beam, then to the lower token.
@@ -390,14 +390,15 @@ __device__ __forceinline__ void merge(const BeamParams& p, int search) {
   const uint64_t* parts = p.ws_keys + static_cast<int64_t>(search) * total;
   // Thread t takes candidates t, t + 256, .. of the parts' firsts, then their seconds
   // and so on, and group g of `groups` the threads t = g mod groups.  The list of a
-  // part moves on by an odd number of groups from one rank to the next, so that the
-  // many finds of one good beam lie in many groups, and the bound below is a good one
-  // (32 beams of 128,256 tokens, K = 64, lists of one group each: ms).
+  // part moves on by an odd number of groups, 5/8 of them, from one rank to the next,
+  // so that the many finds of one good beam lie in many groups and the bound below is
+  // a good one (1910 candidates reach it of 32 beams in 4 parts, K = 64, where lists
+  // keep to a group, 77 so).
   const int lists = W * p.parts;
-  const bool turn = ((lists & (p.groups - 1)) & 1) == 0;
+  const int turn = (lists - (p.groups * 5 / 8 | 1)) & (p.groups - 1);
   auto place = [&](int c) {
-    const int r = c / lists, l = c - r * lists;
-    return (turn ? (l + r) % lists : l) * K + r;
+    const int r = c / lists;
+    return (c - r * lists + r * turn) % lists * K + r;
   };
   constexpr int kHeld = 2;  // candidates of a thread that stay in registers
   uint64_t raw[kHeld];

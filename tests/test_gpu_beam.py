@@ -123,6 +123,19 @@ def check_some(s, got, take):
     few.check(part)
 
 
+@pytest.mark.parametrize("n,beams,keep,vocab", [(4, 32, 64, 30011), (8, 16, 32, 20000),
+                                                (2, 32, 33, 9000), (1, 1, 64, 120000),
+                                                (3, 24, 64, 50257)])
+def test_wide_searches(n, beams, keep, vocab):
+    """Many finds of many parts, most of them of a good beam or two."""
+    pa.pa_clear_device_error()
+    s = Search(vocab + keep, n, beams, keep, vocab, "fp32")
+    s.check(s.call())
+    s.scores[::beams] += 10.0
+    s.check(s.call())
+    assert pa.pa_get_device_error() == 0
+
+
 @pytest.mark.parametrize("dtype", sorted(T))
 @pytest.mark.parametrize("pad", [0, 1, 7])
 def test_long_parts(dtype, pad):
