@@ -412,7 +412,7 @@ __device__ __forceinline__ void merge(const BeamParams& p, int search) {
   for (int w = tid >> 5; w < W; w += kWarps) {  // each row's log-sum from its parts
     const int64_t row = static_cast<int64_t>(search) * W + w;
     const float2* ms = p.ws_sums + row * p.parts;
-    const float score = p.scores[row];
+    const float score = load_after_wait(p.scores + row);
     const bool finished = p.finished && p.finished[row];
     const float2 mine = (tid & 31) < p.parts ? __ldcg(ms + (tid & 31)) : make_float2(-INFINITY, 0.f);
     float top = mine.x;
@@ -529,7 +529,7 @@ template <typename T>
 __device__ __forceinline__ void load8_aligned(const T* at, uint32_t (&w)[Words<T>::N]) {
 #pragma unroll
   for (int k = 0; k < Words<T>::N / 4; ++k) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(at) + k);
+    const uint4 q = load_after_wait(reinterpret_cast<const uint4*>(at) + k);
     w[4 * k] = q.x;
     w[4 * k + 1] = q.y;
     w[4 * k + 2] = q.z;
@@ -563,7 +563,7 @@ __device__ __forceinline__ void load8_shifted(const T* row, int e, int end, uint
     const uint4* a = reinterpret_cast<const uint4*>(addr - off);
 #pragma unroll
     for (int k = 0; k < N / 4 + 1; ++k) {
-      const uint4 q = __ldg(a + k);
+      const uint4 q = load_after_wait(a + k);
       u[4 * k] = q.x;
       u[4 * k + 1] = q.y;
       u[4 * k + 2] = q.z;
@@ -596,10 +596,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = p.keep;
   const int64_t row = blockIdx.y;
   const int part = blockIdx.x, search = static_cast<int>(row / p.beams);
-  const float score = p.scores[row];
+  const float score = load_after_wait(p.scores + row);
   if (part == 0 && tid == 0 && !isfinite(score) && score != -INFINITY)
     raise_error(p.err, PA_DEVERR_LOGITS);
-  if (isfinite(score) && !(p.finished && p.finished[row])) {
+  if (isfinite(score) && !(p.finished && load_after_wait(p.finished + row))) {
     constexpr int kBlock = P * kThreads * 8;
     const int begin = part * p.part_len, end = min(begin + p.part_len, p.vocab);
     const T* logits = static_cast<const T*>(p.logits);

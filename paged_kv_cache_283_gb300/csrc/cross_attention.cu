@@ -146,9 +146,9 @@ struct Seq {
 };
 __device__ __forceinline__ Seq read_seq(const CrossParams& p, int b) {
   Seq s;
-  s.q0 = __ldg(p.query_start + b);
-  const int q1 = __ldg(p.query_start + b + 1);
-  s.src = __ldg(p.source_lens + b);
+  s.q0 = load_after_wait(p.query_start + b);
+  const int q1 = load_after_wait(p.query_start + b + 1);
+  s.src = load_after_wait(p.source_lens + b);
   s.bad = s.q0 < 0 || q1 < s.q0 || q1 > p.total_q || s.src < 0 ||
           s.src > p.max_blocks_per_seq * kBS;
   s.n = s.bad ? 0 : min(q1 - s.q0, p.max_query_len);
@@ -587,8 +587,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       a.kvh = it.kvh;
       if (c == 0) a.q_row = it.seq.q0 + it.i0;
       if (lane < a.blocks)
-        a.id = __ldg(p.block_tables + static_cast<int64_t>(it.b) * p.max_blocks_per_seq + block +
-                     lane);
+        a.id = load_after_wait(p.block_tables +
+                               static_cast<int64_t>(it.b) * p.max_blocks_per_seq + block + lane);
       c += chunks;
       if (c == it.count) {
         some = walk.next(p, it);

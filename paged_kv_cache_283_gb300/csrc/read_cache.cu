@@ -53,19 +53,25 @@ struct Rows {
   const ReadCacheParams& p;
   int h, t_lo, t_hi;  // tokens [t_lo, t_hi) of the block are asked for
   int64_t row0;       // row of token 0 of the block (may be before the first row)
+  int64_t slot_at;    // with slots: the offset of token lane % 16's row
 
-  // Element offset of token t's row in the outputs, or -1: not asked for, or no slot.
-  __device__ __forceinline__ int64_t at(int t) const {
-    if (t < t_lo || t >= t_hi) return -1;
-    const int64_t r = row0 + t;
-    if (!p.slots) return r * p.out_stride + h * D;
-    const int64_t s = __ldg(p.slots + r);
-    if (s < 0) return -1;
-    if (s >= p.num_out_slots) {
+  // The slots of the block's rows, a lane each, fetched with its tiles.
+  __device__ __forceinline__ void read_slots(int lane) {
+    slot_at = -1;
+    const int t = lane % kBS;
+    if (!p.slots || t < t_lo || t >= t_hi) return;
+    const int64_t s = load_after_wait(p.slots + row0 + t);
+    if (s < 0) return;
+    if (s >= p.num_out_slots)
       raise_error(p.err, PA_DEVERR_SLOT);
-      return -1;
-    }
-    return ((s / kBS * p.num_kv_heads + h) * kBS + s % kBS) * D;
+    else
+      slot_at = ((s / kBS * p.num_kv_heads + h) * kBS + s % kBS) * D;
+  }
+  // Element offset of token t's row in the outputs, or -1: not asked for, or no slot.
+  // (By the whole warp.)
+  __device__ __forceinline__ int64_t at(int t) const {
+    if (p.slots) return __shfl_sync(kFullMask, slot_at, t);
+    return t < t_lo || t >= t_hi ? -1 : (row0 + t) * p.out_stride + h * D;
   }
 };
 
@@ -76,8 +82,8 @@ __global__ void __launch_bounds__(32 * kWarps) read_cache_kernel(const ReadCache
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
-  const int64_t r0 = __ldg(p.row_start + b), r1 = __ldg(p.row_start + b + 1);
-  const int64_t first = p.first ? __ldg(p.first + b) : 0;
+  const int64_t r0 = load_after_wait(p.row_start + b), r1 = load_after_wait(p.row_start + b + 1);
+  const int64_t first = p.first ? load_after_wait(p.first + b) : 0;
   if (r0 < 0 || r1 < r0 || r1 > p.total_rows || first < 0 ||
       first + (r1 - r0) > static_cast<int64_t>(p.max_blocks_per_seq) * kBS) {
     if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(p.err, PA_DEVERR_CONTEXT_LEN);
@@ -91,15 +97,15 @@ __global__ void __launch_bounds__(32 * kWarps) read_cache_kernel(const ReadCache
   const int64_t pos0 = static_cast<int64_t>(tb) * kBS;
   if (n <= 0 || pos0 >= first + n) return;
   if (lane == 0 && blk == 0 && h == 0 && n < r1 - r0) raise_error(p.err, PA_DEVERR_CONTEXT_LEN);
-  int id = __ldg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq + tb);
+  int id = load_after_wait(p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq + tb);
   if (id < 0 || id >= p.num_blocks) {  // never dereferenced: block 0 is read instead
     if (lane == 0) raise_error(p.err, PA_DEVERR_BLOCK_ID);
     id = 0;
   }
   const int64_t tile = static_cast<int64_t>(id) * p.num_kv_heads + h;
-  const Rows<D> rows{p, h, static_cast<int>(max(first - pos0, static_cast<int64_t>(0))),
-                     static_cast<int>(min(first + n - pos0, static_cast<int64_t>(kBS))),
-                     r0 + pos0 - first};
+  Rows<D> rows{p, h, static_cast<int>(max(first - pos0, static_cast<int64_t>(0))),
+               static_cast<int>(min(first + n - pos0, static_cast<int64_t>(kBS))),
+               r0 + pos0 - first, -1};
   constexpr int LR = D / 8;        // lanes that hold a row, 8 dims each
   constexpr int RI = 32 / LR;      // rows of one pass of the warp
   constexpr int NI = kBS / RI;     // passes over a tile
@@ -114,9 +120,10 @@ __global__ void __launch_bounds__(32 * kWarps) read_cache_kernel(const ReadCache
     uint4 kr[NI], vr[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      kr[i] = __ldg(k + i * 32 + lane);
-      vr[i] = __ldg(v + i * 32 + lane);
+      kr[i] = load_after_wait(k + i * 32 + lane);
+      vr[i] = load_after_wait(v + i * 32 + lane);
     }
+    rows.read_slots(lane);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int64_t at = rows.at(i * RI + tr);
@@ -135,8 +142,9 @@ __global__ void __launch_bounds__(32 * kWarps) read_cache_kernel(const ReadCache
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const int c = i * 32 + lane;
-      if (c < 2 * PIECES) w[i] = __ldg(c < PIECES ? k + c : v + (c - PIECES));
+      if (c < 2 * PIECES) w[i] = load_after_wait(c < PIECES ? k + c : v + (c - PIECES));
     }
+    rows.read_slots(lane);
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const int c = i * 32 + lane;
@@ -168,6 +176,9 @@ __global__ void __launch_bounds__(32 * kWarps) read_cache_kernel(const ReadCache
     // V: a word holds dims 16 c + i (low nibbles) and 16 c + i + 8 of four tokens
     // (bytes 0 .. 3: 2 tig, 2 tig + 8, 2 tig + 1, 2 tig + 9)
     const int tig = lane & 3, c = lane >> 2;
+    int64_t to[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) to[e] = rows.at(2 * tig + (e >> 1) + 8 * (e & 1));
     if (c < D / 16) {
       uint32_t word[8];
 #pragma unroll
@@ -185,10 +196,9 @@ __global__ void __launch_bounds__(32 * kWarps) read_cache_kernel(const ReadCache
           lo[i] = pack_bf16(value(a & 15u, par), value(d & 15u, par));
           hi[i] = pack_bf16(value((a >> 4) & 15u, par), value((d >> 4) & 15u, par));
         }
-        const int64_t at = rows.at(t);
-        if (at >= 0) {
-          put(p.v_out, at + 16 * c, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-          put(p.v_out, at + 16 * c + 8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        if (to[e] >= 0) {
+          put(p.v_out, to[e] + 16 * c, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          put(p.v_out, to[e] + 16 * c + 8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
         }
       }
     }
@@ -203,16 +213,18 @@ __global__ void __launch_bounds__(32 * kWarps) read_cache_kernel(const ReadCache
     uint2 kr[NI];
     float kscale[NI];
 #pragma unroll
-    for (int i = 0; i < PL; ++i) w[i] = __ldg(v + i * 32 + lane);
+    for (int i = 0; i < PL; ++i) w[i] = load_after_wait(v + i * 32 + lane);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      kr[i] = __ldg(k + i * 32 + lane);
-      kscale[i] = __ldg(ksc + i * RI + tr);
+      kr[i] = load_after_wait(k + i * 32 + lane);
+      kscale[i] = load_after_wait(ksc + i * RI + tr);
     }
     const int tig = lane & 3;
     float vscale[4];  // of tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
 #pragma unroll
-    for (int e = 0; e < 4; ++e) vscale[e] = __ldg(vsc + 2 * tig + (e & 1) + 8 * (e >> 1));
+    for (int e = 0; e < 4; ++e)
+      vscale[e] = load_after_wait(vsc + 2 * tig + (e & 1) + 8 * (e >> 1));
+    rows.read_slots(lane);
 #pragma unroll
     for (int i = 0; i < PL; ++i) buf[warp][i * 32 + lane] = w[i];
     __syncwarp();

@@ -52,7 +52,7 @@ __device__ __forceinline__ void read_parents(const ReorderParams& p, int64_t gro
   const int lane = threadIdx.x, W = p.beams;
   int par = -1;
   if (lane < W) {
-    const int64_t g = __ldg(p.parents + group * W + lane);
+    const int64_t g = load_after_wait(p.parents + group * W + lane);
     const int64_t local = g - group * W;
     if (g >= 0) {
       if (local < 0 || local >= W) {  // another group's row, or none: left as it is
