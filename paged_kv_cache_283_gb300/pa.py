@@ -1796,11 +1796,12 @@ class BlockAllocator:
 
     def reorder(self, seqs, parents):
         """The sequences become copies of their parents (entries of `seqs`; negative:
-        unchanged), sharing their blocks: a beam search's step."""
+        unchanged), sharing their blocks: a beam search's step.  Either may be flat or
+        [searches, beams], as pa_beam_select's parents are."""
         np = self._np
-        ids = np.ascontiguousarray(seqs, dtype=np.intc)
-        par = np.ascontiguousarray(parents, dtype=np.int32)
-        if par.shape != ids.shape or ids.ndim != 1:
+        ids = np.ascontiguousarray(seqs, dtype=np.intc).reshape(-1)
+        par = np.ascontiguousarray(parents, dtype=np.int32).reshape(-1)
+        if par.shape != ids.shape:
             raise ValueError("reorder: one parent per sequence")
         _check(lib().pa_alloc_reorder(self._h, ids.ctypes.data_as(_vp), par.ctypes.data_as(_vp),
                                       ids.shape[0]), "pa_alloc_reorder")
