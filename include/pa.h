@@ -711,9 +711,9 @@ pa_status pa_prefill_biased(void* out, const void* q, const void* k_cache, const
  * the PV product as two bf16 parts, which keep 2^-16 of them).  V of a source
  * position must be finite; what the cache holds past the source changes nothing.
  * head_dim 64 or 128, block_size 16, Hq / Hkv in {1, 2, 4, 8} (else
- * PA_ERR_UNSUPPORTED_SHAPE), scale > 0.  Device-side checks: 0 <= S <=
- * max_blocks_per_seq * 16 and rows within T (else PA_DEVERR_CONTEXT_LEN and the
- * sequence is skipped); bad block ids as pa_decode.  Asynchronous on `stream`.
+ * PA_ERR_UNSUPPORTED_SHAPE), scale > 0, max_blocks_per_seq * 16 <= 2^31 - 65.
+ * Device-side checks: 0 <= S <= max_blocks_per_seq * 16 and rows within T (else
+ * PA_DEVERR_CONTEXT_LEN and the sequence is skipped); bad block ids as pa_decode.  Asynchronous on `stream`.
  */
 int pa_cross_attention_supported(int head_dim, int group, int block_size);
 int pa_cross_attention_ctas(int num_sms);

@@ -1159,7 +1159,9 @@ pa_status cross_impl(void* out, const void* q, int64_t q_stride, const void* k_c
   if (!aligned_ptr(ws_out, 16) || !aligned_ptr(ws_ml, 16) || !aligned_ptr(counters, 4))
     return PA_ERR_INVALID_ARG;
   const int64_t rows = static_cast<int64_t>(num_blocks) * num_kv_heads * kBS;
-  if (rows > 0x7fffffffll || static_cast<int64_t>(max_blocks_per_seq) * kBS > 0x7fffffffll)
+  // (a source's length, rounded up to whole chunks, stays within 31 bits)
+  if (rows > 0x7fffffffll ||
+      static_cast<int64_t>(max_blocks_per_seq) * kBS > 0x7fffffffll - kKeys)
     return PA_ERR_INVALID_ARG;
   CrossParams p{};
   p.group = group;
