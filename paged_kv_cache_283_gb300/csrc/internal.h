@@ -172,6 +172,20 @@ inline bool ranges_meet(const void* a, int64_t a_bytes, const void* b, int64_t b
          y < x + static_cast<uintptr_t>(a_bytes);
 }
 
+// Whether rows of two tensors of one shape, `rows` of row_bytes, row_stride apart, share
+// bytes.  (Rows may alternate, as views of one tensor.)
+inline bool rows_meet(const void* a, const void* b, int64_t rows, int64_t row_bytes,
+                      int64_t row_stride) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t apart = x < y ? y - x : x - y;
+  const uintptr_t row = static_cast<uintptr_t>(row_bytes);
+  const uintptr_t stride = static_cast<uintptr_t>(row_stride);
+  if (apart >= static_cast<uintptr_t>(rows - 1) * stride + row) return false;
+  const uintptr_t past = apart % stride;  // into a row's stride
+  const bool last = apart / stride == static_cast<uintptr_t>(rows - 1);
+  return past < row || (!last && stride - past < row);
+}
+
 // Positions of a cache read back (read_cache.cu).
 struct ReadCacheParams {
   __nv_bfloat16* k_out;           // rows of Hkv * D at out_stride, or (slots) a bf16 pool

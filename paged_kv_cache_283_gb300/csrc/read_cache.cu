@@ -360,7 +360,10 @@ pa_status read_impl(int kv_kind, void* k_out, void* v_out, int64_t out_stride,
   for (const void* o : outs)
     for (const void* c : pools)
       if (ranges_meet(o, written, c, pool)) return PA_ERR_INVALID_ARG;
-  if (k_out == v_out) return PA_ERR_INVALID_ARG;
+  // (K and V rows may alternate, as views of one tensor)
+  if (slot_mapping ? ranges_meet(k_out, written, v_out, written)
+                   : rows_meet(k_out, v_out, total_rows, 2 * row, 2 * out_stride))
+    return PA_ERR_INVALID_ARG;
   p.k_out = static_cast<__nv_bfloat16*>(k_out);
   p.v_out = static_cast<__nv_bfloat16*>(v_out);
   p.k_cache = k_cache;

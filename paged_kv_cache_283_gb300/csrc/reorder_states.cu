@@ -210,26 +210,21 @@ struct Launches {
 };
 
 // Whether two tensors' rows, or a row and the parents, share bytes: each tensor is
-// moved by CTAs of its own, and none may change what another still reads.  (Rows of
-// two tensors may alternate, as views of one.)
-bool rows_meet(void* const* states, int num_tensors, const int32_t* parents, int64_t rows,
-               int64_t row_bytes, int64_t row_stride) {
-  const uintptr_t stride = static_cast<uintptr_t>(row_stride);
-  const uintptr_t extent = static_cast<uintptr_t>((rows - 1) * row_stride + row_bytes);
+// moved by CTAs of its own, and none may change what another still reads.
+bool any_meet(void* const* states, int num_tensors, const int32_t* parents, int64_t rows,
+              int64_t row_bytes, int64_t row_stride) {
+  const int64_t extent = (rows - 1) * row_stride + row_bytes;
   std::vector<uintptr_t> at(num_tensors);
   for (int t = 0; t < num_tensors; ++t) {
     at[t] = reinterpret_cast<uintptr_t>(states[t]);
-    if (ranges_meet(states[t], static_cast<int64_t>(extent), parents, 4 * rows)) return true;
+    if (ranges_meet(states[t], extent, parents, 4 * rows)) return true;
   }
   std::sort(at.begin(), at.end());
   for (int i = 0; i < num_tensors; ++i)
-    for (int j = i + 1; j < num_tensors && at[j] - at[i] < extent; ++j) {
-      const uintptr_t past = (at[j] - at[i]) % stride;  // into a row's stride
-      const bool last = (at[j] - at[i]) / stride == static_cast<uintptr_t>(rows - 1);
-      if (past < static_cast<uintptr_t>(row_bytes) ||
-          (!last && stride - past < static_cast<uintptr_t>(row_bytes)))
+    for (int j = i + 1; j < num_tensors && at[j] - at[i] < static_cast<uintptr_t>(extent); ++j)
+      if (rows_meet(reinterpret_cast<void*>(at[i]), reinterpret_cast<void*>(at[j]), rows,
+                    row_bytes, row_stride))
         return true;
-    }
   return false;
 }
 
@@ -251,8 +246,8 @@ pa_status reorder_impl(void* const* states, int num_tensors, const int32_t* pare
     bits |= reinterpret_cast<uintptr_t>(states[t]);
   }
   try {
-    if (rows_meet(states, num_tensors, parents, static_cast<int64_t>(num_groups) * num_beams,
-                  row_bytes, row_stride))
+    if (any_meet(states, num_tensors, parents, static_cast<int64_t>(num_groups) * num_beams,
+                 row_bytes, row_stride))
       return PA_ERR_INVALID_ARG;
   } catch (const std::bad_alloc&) {
     return PA_ERR_INVALID_ARG;

@@ -25,3 +25,23 @@ def test_cross_attention_tables_past_31_bits(prepare):
 
     for mb in ((1 << 27) - 1, (1 << 27) - 2, (1 << 27) - 3, (1 << 27) - 4, 1 << 27):
         assert call(mb) == BAD, mb
+
+
+@pytest.mark.parametrize("prepare", [False, True])
+def test_read_cache_outputs_that_meet(prepare):
+    """K and V rows that share bytes are refused, also where neither begins with the other:
+    which of the two a place would end with is nobody's choice."""
+    def call(apart, stride=1024, slots=None, nob=0, T=12):
+        ko, vo = (1 << 40, (1 << 40) + apart) if apart >= 0 else ((1 << 40) - apart, 1 << 40)
+        args = (1, ko, vo, stride, F, F, F, F, F, 4, None, F, 9, 2, T, slots, nob, 4, 128, 16, 10)
+        if prepare:
+            return pa.lib().pa_prepare_read_cache(ctypes.byref(ctypes.c_void_p()), *args)
+        return pa.lib().pa_read_cache(*args, None)
+
+    # 12 rows of 1024 bytes, 2048 apart
+    for apart in (0, 16, 1008, 1040, 2032, 2048, 2064, 4096, 11 * 2048, 11 * 2048 + 1008):
+        assert call(apart) == BAD and call(-apart) == BAD, apart
+    for apart in (512, 1008, 11 * 1024 + 16):               # and with nothing between them
+        assert call(apart, stride=512) == BAD and call(-apart, stride=512) == BAD, apart
+    for apart in (16, 3 * 16384 - 16):                      # pools of 3 blocks of 16 KiB
+        assert call(apart, slots=F, nob=3) == BAD and call(-apart, slots=F, nob=3) == BAD, apart
