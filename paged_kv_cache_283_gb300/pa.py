@@ -1500,6 +1500,8 @@ class ReorderStates(_FixedCall):
     marshalled once."""
 
     def __init__(self, states, parents, num_beams, stream=None):
+        # (a list of its own: the caller's may change, or be an iterator)
+        states = [states] if isinstance(states, _torch().Tensor) else list(states)
         self._fix("ReorderStates: pa_reorder_states", "pa_prepare_reorder_states",
                   _reorder_args(states, parents, num_beams), stream, [states, parents])
 

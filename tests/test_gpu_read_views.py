@@ -32,6 +32,6 @@ def test_keys_and_values_may_alternate(d, hkv):
         with pytest.raises(pa.PAError):                      # a head of K is one of V
             pa.pa_read_cache(flat[:, :hkv], flat[:, hkv - 1:2 * hkv - 1], k, v, tables, start, 37)
         with pytest.raises(pa.PAError):                      # V's row is K's next one
-            pa.pa_read_cache(whole[:39, 0], whole[1:, 0], k, v, tables, start[:2], 37)
+            pa.pa_read_cache(whole[:39, 0], whole[1:, 0], k, v, tables[:1], start[:2], 37)
         assert torch.equal(whole, before)
     assert pa.pa_get_device_error() == 0

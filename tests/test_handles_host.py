@@ -1,0 +1,51 @@
+"""What the handles of the search operators keep, on the CPU: a stand-in for the prepared
+call takes the addresses and launches nothing."""
+import gc
+import weakref
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from paged_kv_cache_283_gb300 import pa
+
+
+@pytest.fixture
+def prepared(monkeypatch):
+    """The calls that handles made."""
+    calls = []
+
+    class Call:
+        def __init__(self, name, *args):
+            calls.append((name, args))
+
+        def run(self, stream):
+            return pa.PA_OK
+
+    monkeypatch.setattr(pa, "_Prepared", Call)
+    return calls
+
+
+def _states():
+    return [torch.zeros(8, 5) for _ in range(3)]
+
+
+@pytest.mark.parametrize("how", ["iterator", "cleared list", "list", "one"])
+def test_reordering_keeps_its_states(monkeypatch, prepared, how):
+    """The call holds their addresses: they live as long as the handle, whatever becomes of
+    what the caller handed over."""
+    monkeypatch.setattr(pa, "_reorder_args", lambda states, parents, beams: tuple(
+        t.data_ptr() for t in ([states] if isinstance(states, torch.Tensor) else list(states))))
+    tensors = _states()[:1] if how == "one" else _states()
+    refs = [weakref.ref(t) for t in tensors]
+    given = {"iterator": iter, "one": lambda t: t[0]}.get(how, list)(tensors)
+    call = pa.ReorderStates(given, torch.zeros(8, dtype=torch.int32), 4)
+    if how == "cleared list":
+        given.clear()
+    del tensors, given
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    assert prepared[0][1] == tuple(r().data_ptr() for r in refs)
+    del call
+    gc.collect()
+    assert all(r() is None for r in refs)
