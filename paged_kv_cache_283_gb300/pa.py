@@ -1151,23 +1151,37 @@ class _FixedCall:
     """A prepared call on fixed device buffers (`prepare`: its pa_prepare_* function
     and arguments); each call is one bare launch.  The buffers' contents may change
     between calls, their shapes and addresses may not.  `made`: buffers made here on
-    the current stream, which the first call's stream awaits."""
+    the current stream, which the first call's stream awaits.  They are the handle's:
+    a captured graph that holds its calls needs the handle as long as it replays."""
 
-    def _fix(self, what, prepare, args, stream, keep, made=False):
+    def _fix(self, what, prepare, args, stream, keep, made=()):
         torch = _torch()
         self._what = what
         self._call = _Prepared(prepare, *args)
         self._stream = None if stream is None else ctypes.c_void_p(stream.cuda_stream)
         self._keep = keep
         self._ready = None
-        if made and not torch.cuda.is_current_stream_capturing():
+        self._made = list(made)
+        self._used_on = set()
+        if self._made and not torch.cuda.is_current_stream_capturing():
             self._ready = torch.cuda.current_stream().record_event()
+
+    def _hold_made(self, stream):
+        """The buffers made here are not given to others, once the handle is gone, before
+        the calls on `stream` have ended."""
+        at = getattr(stream, "value", stream) or 0
+        if at not in self._used_on:
+            self._used_on.add(at)
+            for t in self._made:
+                t.record_stream(_torch().cuda.ExternalStream(at, device=t.device))
 
     def __call__(self, stream=None):
         s = self._stream if stream is None and self._stream is not None else _stream(stream)
         if self._ready is not None:
             _check(lib().pa_await_event(self._ready.cuda_event, s), self._what)
             self._ready = None
+        if self._made:
+            self._hold_made(s)
         st = self._call.run(s)
         if st != PA_OK:
             _check(st, self._what)
@@ -1260,7 +1274,8 @@ class CrossAttention(_FixedCall):
                            max_query_len, scale, workspace)
         self._fix("CrossAttention: pa_cross_attention", "pa_prepare_cross_attention", args,
                   stream, [out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc,
-                           workspace], made)
+                           workspace],
+                  [workspace.ws_out, workspace.ws_ml, workspace.counters] if made else ())
 
 
 def _read_args(k_out, v_out, k_cache, v_cache, block_tables, row_start_loc, max_rows,
@@ -1451,7 +1466,7 @@ class BeamSelect(_FixedCall):
                           finished, eos_token, finished_out, in_place, workspace)
         self._fix("BeamSelect: pa_beam_select", "pa_prepare_beam_select", args, stream,
                   [scores_out, parents_out, tokens_out, logits, scores, finished, finished_out,
-                   workspace], made)
+                   workspace], workspace if made else ())
 
 
 def _reorder_args(states, parents, num_beams):

@@ -2,6 +2,7 @@
 call takes the addresses and launches nothing."""
 import gc
 import weakref
+from types import SimpleNamespace
 
 import pytest
 
@@ -49,3 +50,35 @@ def test_reordering_keeps_its_states(monkeypatch, prepared, how):
     del call
     gc.collect()
     assert all(r() is None for r in refs)
+
+
+def test_own_buffers_are_held_for_the_streams_that_used_them(monkeypatch, prepared):
+    """A workspace that a handle made goes back to its allocator with the handle: every
+    stream that it ran on is told of first, once."""
+    told = []
+
+    class Made:
+        device = "cuda:0"
+
+        def record_stream(self, stream):
+            told.append(stream)
+
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda at, device: (at, device))
+    one, other = (SimpleNamespace(cuda_stream=at) for at in (77, 78))
+    call = pa._FixedCall()
+    call._fix("a call", "pa_prepare_beam_select", (), one, [], [Made()])
+    assert told == []
+    call()
+    call()
+    call(stream=one)
+    assert told == [(77, "cuda:0")]
+    call(stream=other)
+    call(stream=other)
+    call(stream=SimpleNamespace(cuda_stream=0))
+    assert told == [(77, "cuda:0"), (78, "cuda:0"), (0, "cuda:0")]
+    # the caller's workspace is the caller's
+    call = pa._FixedCall()
+    call._fix("a call", "pa_prepare_beam_select", (), one, [object()])
+    call()
+    assert len(told) == 3
