@@ -104,7 +104,7 @@ __device__ __forceinline__ void load_row_words(const __nv_bfloat16* row, int lan
                                                uint32_t (&w)[D / 64]) {
 #pragma unroll
   for (int i = 0; i < D / 64; ++i)
-    w[i] = __ldg(reinterpret_cast<const unsigned int*>(row + lane * (D / 32)) + i);
+    w[i] = load_after_wait(reinterpret_cast<const unsigned int*>(row + lane * (D / 32)) + i);
 }
 
 // Quantises and stores one token's K and V rows of one KV head (kw / vw: the

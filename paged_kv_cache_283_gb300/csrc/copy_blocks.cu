@@ -30,8 +30,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const CopyBlo
   const int pair = blockIdx.x;
   const int layer = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
-  const int64_t src = __ldg(p.block_mapping + 2 * static_cast<int64_t>(pair));
-  const int64_t dst = __ldg(p.block_mapping + 2 * static_cast<int64_t>(pair) + 1);
+  const int64_t src = load_after_wait(p.block_mapping + 2 * static_cast<int64_t>(pair));
+  const int64_t dst = load_after_wait(p.block_mapping + 2 * static_cast<int64_t>(pair) + 1);
   if (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_blocks) {
     if (threadIdx.x == 0) raise_error(p.err, PA_DEVERR_BLOCK_ID);
     return;
@@ -43,14 +43,22 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const CopyBlo
   const int64_t n = p.block_bytes / 16;
   int64_t i = threadIdx.x;
   for (; i + 3 * kCopyThreads < n; i += 4 * kCopyThreads) {
-    const uint4 a = __ldg(s + i), b = __ldg(s + i + kCopyThreads);
-    const uint4 c = __ldg(s + i + 2 * kCopyThreads), e = __ldg(s + i + 3 * kCopyThreads);
+    const uint4 a = load_after_wait(s + i), b = load_after_wait(s + i + kCopyThreads);
+    const uint4 c = load_after_wait(s + i + 2 * kCopyThreads);
+    const uint4 e = load_after_wait(s + i + 3 * kCopyThreads);
     d[i] = a;
     d[i + kCopyThreads] = b;
     d[i + 2 * kCopyThreads] = c;
     d[i + 3 * kCopyThreads] = e;
   }
-  for (; i < n; i += kCopyThreads) d[i] = __ldg(s + i);
+  // at most three more: loaded before any is stored
+  uint4 rest[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (i + k * kCopyThreads < n) rest[k] = load_after_wait(s + i + k * kCopyThreads);
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (i + k * kCopyThreads < n) d[i + k * kCopyThreads] = rest[k];
 }
 
 }  // namespace

@@ -153,15 +153,15 @@ template <int D, int Q>
 __device__ __forceinline__ bool fused_cache_write(const DecodeParams& p, int b, int kvh, int ctx,
                                                   const int32_t* tbl, int lane,
                                                   unsigned char* stage) {
-  const int64_t slot = __ldg(p.slot_mapping + b);
+  const int64_t slot = load_after_wait(p.slot_mapping + b);
   const size_t src = (static_cast<size_t>(b) * p.num_kv_heads + kvh) * D;
   constexpr int C = D / 8;  // 16-byte chunks of a bf16 row
   uint4 x = make_uint4(0, 0, 0, 0);
   uint32_t kw[D / 64], vw[D / 64];
   if constexpr (Q == 0) {  // lanes [0, C) hold K chunks, [C, 2C) V chunks
     if (lane < 2 * C)
-      x = __ldg(reinterpret_cast<const uint4*>((lane >= C ? p.new_value : p.new_key) + src) +
-                (lane % C));
+      x = load_after_wait(
+          reinterpret_cast<const uint4*>((lane >= C ? p.new_value : p.new_key) + src) + lane % C);
   } else {
     load_row_words<D>(p.new_key + src, lane, kw);
     load_row_words<D>(p.new_value + src, lane, vw);
@@ -169,7 +169,7 @@ __device__ __forceinline__ bool fused_cache_write(const DecodeParams& p, int b, 
   if (slot < 0) return false;
   int64_t want = -1;
   if (ctx >= 1) {
-    const int id = __ldg(tbl + (ctx - 1) / kBlockSize);
+    const int id = load_after_wait(tbl + (ctx - 1) / kBlockSize);
     if (id >= 0 && id < p.num_blocks)
       want = static_cast<int64_t>(id) * kBlockSize + (ctx - 1) % kBlockSize;
   }
@@ -275,7 +275,7 @@ __device__ __forceinline__ void load_q_bf16(const DecodeParams& p, int b, int kv
   uint4 qw[G];
 #pragma unroll
   for (int g = 0; g < G; ++g)
-    qw[g] = __ldg(reinterpret_cast<const uint4*>(qb + static_cast<size_t>(g) * D));
+    qw[g] = load_after_wait(reinterpret_cast<const uint4*>(qb + static_cast<size_t>(g) * D));
   const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll
   for (int g = 0; g < G; ++g) {
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
   // range is refused (the item it displaced does not run: the error says so)
   int b = blockIdx.y, part = blockIdx.z + (SPLIT ? p.first_partition : 0);
   if (SPLIT && p.order != nullptr) {  // (items over the partitions from first_partition)
-    const int item = __ldg(p.order + blockIdx.y);
+    const int item = load_after_wait(p.order + blockIdx.y);
     if (item < 0 || item >= p.num_seqs * (p.max_partitions - p.first_partition)) {
       if (threadIdx.x == 0) raise_error(p.err, PA_DEVERR_ORDER);
       if (p.early_read || after_prefix) griddep_wait();
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
   // partition_blocks each from block prefix_blocks.
   // With a window the partitions start at the first visible token's block
   // (win_blk), so the ids wait for the length there.
-  int ctx = __ldg(p.context_lens + b);
+  int ctx = load_after_wait(p.context_lens + b);
   int lo_tok = 0;
   if constexpr (RULE) {
     if (p.rule.window > 0)
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
       const int n = win * 32 + lane;
       j = part_first + (warp + static_cast<int64_t>(n / SB) * NW) * SB + n % SB;
     }
-    return j < tbl_end ? __ldg(tbl + j) : 0;
+    return j < tbl_end ? load_after_wait(tbl + j) : 0;
   };
   int ids_cur = load_ids(0);
   float2 q2[G][4];
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
           E * tig;
   #pragma unroll
       for (int u = 0; u < E / 8; ++u) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(qh) + u);
+        const uint4 w = load_after_wait(reinterpret_cast<const uint4*>(qh) + u);
         const float2 a = bf16x2_to_float2(w.x), c = bf16x2_to_float2(w.y);
         const float2 d = bf16x2_to_float2(w.z), e = bf16x2_to_float2(w.w);
         f[8 * u] = a.x; f[8 * u + 1] = a.y; f[8 * u + 2] = c.x; f[8 * u + 3] = c.y;
@@ -465,11 +465,12 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
             lane * E;
         float f[E];
         if constexpr (E == 4) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(qh));
+          const uint2 w = load_after_wait(reinterpret_cast<const uint2*>(qh));
           const float2 a = bf16x2_to_float2(w.x), c = bf16x2_to_float2(w.y);
           f[0] = a.x; f[1] = a.y; f[2] = c.x; f[3] = c.y;
         } else {
-          const float2 a = bf16x2_to_float2(__ldg(reinterpret_cast<const unsigned int*>(qh)));
+          const float2 a =
+              bf16x2_to_float2(load_after_wait(reinterpret_cast<const unsigned int*>(qh)));
           f[0] = a.x; f[1] = a.y;
         }
         float amax = 0.f;
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(NW * 32, (min_blocks<D, NW, G, Q, SB>()))
       raise_error(p.err, PA_DEVERR_CONTEXT_LEN);
     if (part_first >= nblk) {  // past the end of this sequence; CTA-uniform, nothing issued
       if (p.early_read || after_prefix) griddep_wait();
-      if (writer_cta && threadIdx.x == 0 && __ldg(p.slot_mapping + b) >= 0)
+      if (writer_cta && threadIdx.x == 0 && load_after_wait(p.slot_mapping + b) >= 0)
         raise_error(p.err, PA_DEVERR_SLOT);  // a new token for an empty sequence
       if (p.counters != nullptr && nblk == 0 && part == 0) {
         // merged output of an empty sequence: zeros, as the merge gives

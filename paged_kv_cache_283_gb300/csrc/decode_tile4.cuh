@@ -91,7 +91,7 @@ struct Warp4 {
 #pragma unroll
     for (int u = 0; u < D / 32; ++u) {
       const uint4 w =
-          __ldg(reinterpret_cast<const uint4*>(qh + kInt4Group * (u / 2) + 8 * (u % 2)));
+          load_after_wait(reinterpret_cast<const uint4*>(qh + kInt4Group * (u / 2) + 8 * (u % 2)));
       const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
       const float2 c = bf16x2_to_float2(w.z), d = bf16x2_to_float2(w.w);
       f[8 * u] = a.x; f[8 * u + 1] = a.y; f[8 * u + 2] = b.x; f[8 * u + 3] = b.y;

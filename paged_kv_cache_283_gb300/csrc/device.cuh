@@ -161,6 +161,11 @@ __device__ __forceinline__ int32_t load_after_wait(const int32_t* p) {
   asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t load_after_wait(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ int64_t load_after_wait(const int64_t* p) {
   int64_t v;
   asm volatile("ld.global.s64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
@@ -170,6 +175,14 @@ __device__ __forceinline__ uint8_t load_after_wait(const uint8_t* p) {
   uint32_t v;
   asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return static_cast<uint8_t>(v);
+}
+__device__ __forceinline__ float4 load_after_wait(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ uint2 load_after_wait(const uint2* p) {
   uint2 v;

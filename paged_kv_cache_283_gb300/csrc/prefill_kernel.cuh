@@ -359,9 +359,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
   // Lengths live in device memory: check them (CTA-uniform).  A shared
   // prefix split: every query sees the split's keys (sizes checked on the host).
-  const int q0 = shared_prefix ? 0 : __ldg(p.query_start + b);
-  const int q1 = shared_prefix ? p.total_q : __ldg(p.query_start + b + 1);
-  const int ctx = shared_prefix ? p.split_blocks * kBS : __ldg(p.context_lens + b);
+  const int q0 = shared_prefix ? 0 : load_after_wait(p.query_start + b);
+  const int q1 = shared_prefix ? p.total_q : load_after_wait(p.query_start + b + 1);
+  const int ctx = shared_prefix ? p.split_blocks * kBS : load_after_wait(p.context_lens + b);
   const int n = q1 - q0;
   if (!shared_prefix &&
       (q0 < 0 || q1 > p.total_q || n < 0 || n > ctx || ctx > p.max_blocks_per_seq * kBS)) {
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   int key0 = 0, vlo = 0, prefix = 0;  // vlo: hidden keys of the first block
   if constexpr (RULE) {
     if (p.prefix_lens != nullptr) {
-      prefix = __ldg(p.prefix_lens + b);
+      prefix = load_after_wait(p.prefix_lens + b);
       if (prefix < 0 || prefix > ctx) {
         if (tid == 0 && tile == 0 && kvh == 0) raise_error(p.err, PA_DEVERR_PREFIX);
         return;
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     auto fetch_id = [&](int c) -> int {
       const int kc = chunk_at(c);
       if (c >= nchunks || lane >= min(kChunkBlocks, nblk_all - kc * kChunkBlocks)) return 0;
-      return __ldg(tbl + kc * kChunkBlocks + lane);
+      return load_after_wait(tbl + kc * kChunkBlocks + lane);
     };
     // K (or V) of chunk c into stage c % 3, one block per lane
     auto load = [&](int c, bool is_v, int id) {
@@ -523,11 +523,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll 4
       for (int e = lane; e < pairs; e += 32) {
         const int t = e / p.split_blocks, j = e - t * p.split_blocks;
-        bad |= __ldg(row0 + static_cast<size_t>(i0 + t) * p.max_blocks_per_seq + j) !=
-               __ldg(row0 + j);
+        bad |= load_after_wait(row0 + static_cast<size_t>(i0 + t) * p.max_blocks_per_seq + j) !=
+               load_after_wait(row0 + j);
       }
       if (split == 0)
-        for (int t = lane; t < seqs; t += 32) bad |= __ldg(p.context_lens + i0 + t) <= prefix_tokens;
+        for (int t = lane; t < seqs; t += 32)
+          bad |= load_after_wait(p.context_lens + i0 + t) <= prefix_tokens;
       if (__any_sync(kFullMask, bad) && lane == 0) raise_error(p.err, PA_DEVERR_PREFIX);
     }
     // Copies this warp issued land before the CTA's shared memory is given up
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       rr.twice = 2.8853900817779268f * k;
       rr.cap2 = p.rule.softcap * 1.4426950408889634f;
       if constexpr ((RULE & kBias) != 0)
-        rr.slope2 = __ldg(p.rule.slopes + kvh * G + r % G) * 1.4426950408889634f;
+        rr.slope2 = load_after_wait(p.rule.slopes + kvh * G + r % G) * 1.4426950408889634f;
     }
     float m_used = -INFINITY;  // reference maximum of the exponentials (base 2)
     float l_sum = 0.f;

@@ -37,9 +37,9 @@ __global__ void __launch_bounds__(256) reshape_and_cache_kernel(const CacheWrite
   const int64_t t = row / p.num_kv_heads;
   // the new K/V chunk and its slot are independent loads: issue them together
   const int64_t src = row * p.head_dim + c * 8;
-  const uint4 kv = __ldg(reinterpret_cast<const uint4*>(p.key + src));
-  const uint4 vv = __ldg(reinterpret_cast<const uint4*>(p.value + src));
-  const int64_t slot = __ldg(p.slot_mapping + t);
+  const uint4 kv = load_after_wait(reinterpret_cast<const uint4*>(p.key + src));
+  const uint4 vv = load_after_wait(reinterpret_cast<const uint4*>(p.value + src));
+  const int64_t slot = load_after_wait(p.slot_mapping + t);
   if (slot < 0) return;
   if (slot >= p.num_slots) {
     if (c == 0) raise_error(p.err, PA_DEVERR_SLOT);
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(256) reshape_and_cache_int8_kernel(const Cache
   uint32_t kw[D / 64], vw[D / 64];
   load_row_words<D>(p.key + row * D, lane, kw);
   load_row_words<D>(p.value + row * D, lane, vw);
-  const int64_t slot = __ldg(p.slot_mapping + t);
+  const int64_t slot = load_after_wait(p.slot_mapping + t);
   if (slot < 0) return;
   if (slot >= p.num_slots) {
     if (lane == 0) raise_error(p.err, PA_DEVERR_SLOT);

@@ -59,8 +59,8 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
 }
 
 __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = load_after_wait(reinterpret_cast<const float4*>(p));
+  const float4 b = load_after_wait(reinterpret_cast<const float4*>(p) + 1);
   f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const RopeAppe
     wa[u] = load16(src + 8 * (is_v ? 2 * j : ra));
     wb[u] = load16(src + 8 * (is_v ? 2 * j + 1 : rb));
   }
-  const int pos = p.positions != nullptr ? __ldg(p.positions + t) : 0;
-  const int64_t slot = __ldg(p.slot_mapping + t);
+  const int pos = p.positions != nullptr ? load_after_wait(p.positions + t) : 0;
+  const int64_t slot = load_after_wait(p.slot_mapping + t);
   if (pos < 0) return;  // a padding token
   if (pos >= p.max_position) {
     if (s == 0 && j == 0) raise_error(p.err, PA_DEVERR_POSITION);
@@ -286,10 +286,10 @@ __global__ void __launch_bounds__(kThreads, 4) rope_append_kernel(const RopeAppe
     const float* tab = p.cos_sin + static_cast<int64_t>(pos) * p.rotary_dim;
     const int half = p.rotary_dim / 2;
     if (p.interleaved) {  // chunk c holds pairs 4 c .. 4 c + 3
-      const float4 ca4 = __ldg(reinterpret_cast<const float4*>(tab + 4 * ra));
-      const float4 cb4 = __ldg(reinterpret_cast<const float4*>(tab + 4 * rb));
-      const float4 sa4 = __ldg(reinterpret_cast<const float4*>(tab + half + 4 * ra));
-      const float4 sb4 = __ldg(reinterpret_cast<const float4*>(tab + half + 4 * rb));
+      const float4 ca4 = load_after_wait(reinterpret_cast<const float4*>(tab + 4 * ra));
+      const float4 cb4 = load_after_wait(reinterpret_cast<const float4*>(tab + 4 * rb));
+      const float4 sa4 = load_after_wait(reinterpret_cast<const float4*>(tab + half + 4 * ra));
+      const float4 sb4 = load_after_wait(reinterpret_cast<const float4*>(tab + half + 4 * rb));
       cs[0] = ca4.x; cs[1] = ca4.y; cs[2] = ca4.z; cs[3] = ca4.w;
       cs[4] = cb4.x; cs[5] = cb4.y; cs[6] = cb4.z; cs[7] = cb4.w;
       sn[0] = sa4.x; sn[1] = sa4.y; sn[2] = sa4.z; sn[3] = sa4.w;

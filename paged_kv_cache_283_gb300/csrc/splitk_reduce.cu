@@ -38,12 +38,12 @@ __global__ void __launch_bounds__(D) splitk_reduce_kernel(const ReduceParams p) 
 #pragma unroll
   for (int i = 0; i < kSpecParts; ++i) {
     if (i < p.max_partitions) {
-      ms[i] = __ldg(m + i);
-      ls[i] = __ldg(l + i);
-      os[i] = __ldg(o + static_cast<size_t>(i) * D);
+      ms[i] = load_after_wait(m + i);
+      ls[i] = load_after_wait(l + i);
+      os[i] = load_after_wait(o + static_cast<size_t>(i) * D);
     }
   }
-  int ctx = __ldg(p.context_lens + b);
+  int ctx = load_after_wait(p.context_lens + b);
   if (p.window > 0 && ctx > p.window)  // the tokens from the first visible one's block on
     ctx -= (ctx - p.window) / 16 * 16;
   const int64_t cap = static_cast<int64_t>(p.max_partitions) * p.partition_size;
