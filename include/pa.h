@@ -704,16 +704,21 @@ pa_status pa_prefill_biased(void* out, const void* q, const void* k_cache, const
  *   counters        : [ws_ctas], zero before the first call; each call leaves
  *                     them zero.  Calls that may run at the same time (two
  *                     streams, two replayed graphs) must not share workspace or
- *                     counters.
+ *                     counters; calls that follow one another, as a stream's layers,
+ *                     can.
  *   ws_ctas         : how many CTAs the call may use, 1 to 2^20; pa_cross_attention_ctas(
  *                     num_sms) fills the GPU.
+ * How a tile is filled follows max_query_len: single steps beside one long prompt
+ * go in full tiles as it does.  (One call of 63 steps of 4 beams and a prompt of 512
+ * queries takes 75 us, a call for each 111; with a prompt of 40 queries 103 and 99.)
  * Runs on the tensor cores (bf16 in, fp32 accumulate; the softmax weights enter
  * the PV product as two bf16 parts, which keep 2^-16 of them).  V of a source
  * position must be finite; what the cache holds past the source changes nothing.
  * head_dim 64 or 128, block_size 16, Hq / Hkv in {1, 2, 4, 8} (else
  * PA_ERR_UNSUPPORTED_SHAPE), scale > 0, max_blocks_per_seq * 16 <= 2^31 - 65.
  * Device-side checks: 0 <= S <= max_blocks_per_seq * 16 and rows within T (else
- * PA_DEVERR_CONTEXT_LEN and the sequence is skipped); bad block ids as pa_decode.  Asynchronous on `stream`.
+ * PA_DEVERR_CONTEXT_LEN and the sequence is skipped); bad block ids as pa_decode.
+ * Asynchronous on `stream`.
  */
 int pa_cross_attention_supported(int head_dim, int group, int block_size);
 int pa_cross_attention_ctas(int num_sms);
@@ -766,19 +771,25 @@ pa_status pa_read_cache(int kv_kind, void* k_out, void* v_out, int64_t out_strid
  * continuations' totals are
  *   scores[r] + logits[r, v] - log sum_u exp(logits[r, u]),  0 <= v < vocab
  * and a finished beam (finished[r] != 0) has one continuation, eos_token, with
- * total scores[r].  Totals are compared in 64 bits.  The num_keep largest of a
- * search, largest first (equal ones: the lower beam first, of one beam the larger
- * logit, then the lower token), go to
+ * total scores[r].  Totals are taken and compared in 64 bits from a row's log-sum of
+ * fp32 exponentials, which is off by less than 2e-5 (3e-7 at most in rows of random
+ * logits): a row's continuations are in the order of their logits, exactly; those of
+ * two beams whose totals lie closer than twice that may stand either way.  Rows of equal
+ * logits have equal log-sums.  The num_keep largest of a search, largest first (equal
+ * totals: the lower beam first, of one beam the larger logit, then the lower token),
+ * go to
  *   scores_out  [num_searches, num_keep] fp32,
  *   parents_out [num_searches, num_keep] int32: the row r that it continues,
  *   tokens_out  [num_searches, num_keep] int32,
  *   finished_out (may be NULL) uint8: the beam was finished, or the token is
  *               eos_token.
- * A logit of -inf is no continuation; a row of
- * nothing else, or a beam whose score is -inf, has none.  A NaN or +inf logit, or
- * such a score, sets PA_DEVERR_LOGITS and counts as -inf.  Where a search has fewer
- * continuations than num_keep, the rest get score -inf, parent and token -1, not
- * finished.
+ * A logit of -inf is no continuation; a row of nothing else, or a beam whose score is
+ * -inf, has none.  Mask with -inf: a finite mask (the type's lowest number, -1e4) makes
+ * continuations, which count where fewer than num_keep others are left, and, as rows of
+ * equal logits, take num_keep passes over the row (64 x 4 beams of 128,256 tokens,
+ * num_keep 8: 556 us against 17).  A NaN or +inf logit, or such a score, sets
+ * PA_DEVERR_LOGITS and counts as -inf.  Where a search has fewer continuations than
+ * num_keep, the rest get score -inf, parent and token -1, not finished.
  *   flags: 0, or PA_BEAM_IN_PLACE (num_keep == num_beams): entry i of a search is
  *     its place i, and a beam that goes on keeps its place: the best continuation
  *     of beam w stands at place w, every other one, in order, at the first place
@@ -814,9 +825,10 @@ pa_status pa_beam_select(float* scores_out, int32_t* parents_out, int32_t* token
  * (device), row numbers.  A row's parent lies in its own group of num_beams rows
  * (rows g * num_beams ..; else PA_DEVERR_PARENT and the row is left); a negative
  * parent, or its own, leaves the row as it is.  Rows may be of any type: block
- * tables, recurrent states, token histories.  The tensors' rows share no bytes with
- * one another or with parents.  Only changed rows and their parents
- * are touched.  num_beams <= 32, num_groups <= 65535 (else
+ * tables, recurrent states, token histories.  Rows whose addresses, bytes and stride
+ * are multiples of 16 go fastest, of 4 nearly so; odd ones take twice the time and more.
+ * The tensors' rows share no bytes with one another or with parents.  Only changed rows
+ * and their parents are touched.  num_beams <= 32, num_groups <= 65535 (else
  * PA_ERR_UNSUPPORTED_SHAPE).  Asynchronous on `stream`; up to 64 tensors a launch.
  */
 pa_status pa_reorder_states(void* const* states, int num_tensors, const int32_t* parents,

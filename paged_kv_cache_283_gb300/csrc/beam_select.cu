@@ -16,16 +16,22 @@
 //    some 1.4 K): only the blocks whose maximum reaches it are read again, and what
 //    reaches it goes to shared memory, where each counts how many precede it.
 //    Where many are equal more may reach the bound: then the K largest are taken one
-//    by one.
-//  * 64 x 4 beams of 128,256 bf16 tokens: 17.4 us, 3.8 TB/s (short parts whose logits
-//    all stay in registers take 25.2: the phases after a part's sums cost two thirds
-//    of its instructions).  The next block's loads ahead of this one's use: 19.4 against 17.9.
+//    by one: each of the K passes reads the part again, an element a load.  Rows of equal
+//    logits, or all but K of them masked with a finite number, go that way (64 x 4
+//    beams of 128,256 tokens, K = 8: 556 us against 17.5; one search 31 to 36 against 16).
+//    What is masked with -inf is no candidate (16.5 us).
+//  * 64 x 4 beams of 128,256 bf16 tokens, 66 MB that fit L2: 20.7 us, 3.2 TB/s, with new
+//    logits each call, 17.4 to 17.8 the same ones again.  The phases after a part's sums
+//    cost as much as its logits, so parts are long.
 //  * Which thread holds which logit goes by its index in the row alone, not by
 //    the row's alignment, so equal rows have equal sums, bit for bit, and equal
 //    totals: ties go to the lower beam, then to the lower token.
 //  * The last CTA of a search to arrive (a counter, zeroed again by it) joins
-//    the parts.  Totals are taken and compared in 64 bits: sums of different
-//    beams lie closer than fp32's 1e-6 often enough to be seen.
+//    the parts.  Totals are taken and compared in 64 bits, so that fp32's rounding of a
+//    sum (1e-6 of a score of -10) joins no two of them.  Within a row their order is the
+//    logits' own, exactly.  Between beams it is as good as the rows' log-sums, of which
+//    the exponentials (2^-22), their arguments and the parts' sums are taken in fp32:
+//    off by less than 2e-5, by at most 3e-7 in rows of 1000 to 2^20 random logits.
 //
 // A row whose address is no multiple of 16 bytes (an odd vocabulary) is read in
 // aligned 16-byte words, shifted into place in registers.
@@ -414,7 +420,8 @@ __device__ __forceinline__ void merge(const BeamParams& p, int search) {
     const float2* ms = p.ws_sums + row * p.parts;
     const float score = load_after_wait(p.scores + row);
     const bool finished = p.finished && p.finished[row];
-    const float2 mine = (tid & 31) < p.parts ? __ldcg(ms + (tid & 31)) : make_float2(-INFINITY, 0.f);
+    const float2 mine =
+        (tid & 31) < p.parts ? __ldcg(ms + (tid & 31)) : make_float2(-INFINITY, 0.f);
     float top = mine.x;
     for (int c = (tid & 31) + 32; c < p.parts; c += 32) top = fmaxf(top, __ldcg(ms + c).x);
 #pragma unroll
@@ -780,8 +787,10 @@ cudaError_t launch_t(const BeamParams& p, cudaStream_t stream) {
 
 // Length of the parts that a row is cut into: one wave of CTAs, where that leaves a
 // thread a piece and no part more than kMaxBlocks blocks.  (64 x 4 beams of 128,256
-// tokens in 2, 4, 7 and 9 parts a row: 17.9, 20.1, 28.0 and 29.1 us; five and six CTAs an
-// SM 21.0 and 28.3.)
+// tokens in 2 parts a row: 20.7 us; in 1 and 4, as waves of half and of twice as many
+// would cut them: 24.6 and 23.8; 33 x 5 of 50,257 fp32 15.9, 21.0 and 17.8.)  Whole
+// parts leave steps beside the wave's size: 304 rows 17.7 us, 308 25.4; 608 33.5, 612 46.6
+// (0.058, 0.083, 0.055 and 0.076 us a row).
 int beam_part_len(int rows, int vocab, int dtype) {
   const int least = kThreads * 8, most = (dtype == 2 ? 2 : 4) * least * kMaxBlocks;
   const int parts = std::max(1, std::min(kWave / std::max(rows, 1), (vocab + least - 1) / least));

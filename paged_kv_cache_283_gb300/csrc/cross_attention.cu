@@ -18,10 +18,9 @@
 //    another, is cut evenly among persistent CTAs (two an SM), each taking one run
 //    of chunks whatever units it begins and ends in: ragged sources, few long ones
 //    and many short ones all keep every SM busy to the end.  A unit's beginning and end
-//    count as kUnitCost chunks (64 x 4 beams of sources of 128 to 2048 keys 75 ->
-//    62 us, 16 x 512 prompts 466 -> 445, against counting the chunks alone, when
-//    that was measured; 58.2 and 381 with four, 60.8 and 388 with one now).  The
-//    lengths are read on the device, so a captured call follows them.
+//    count as kUnitCost chunks (four: 64 x 4 beams of sources of 128 to 2048 keys 59.1 us,
+//    16 x 512 prompts 424; one: 61.6 and 432), and one CTA an SM takes 72.2 and 532.
+//    The lengths are read on the device, so a captured call follows them.
 //  * A CTA is 4 softmax warps, a row a thread, and a warp each for the MMAs of
 //    Q K^T and of P V and for the copies of K and of V: a warp's waits take it
 //    longer than what it waits to issue.  The warps walk their CTA's run on their
@@ -33,20 +32,28 @@
 //  * The softmax takes a chunk's maximum first and its weights against the row's
 //    reference, which follows (and O is rescaled in tensor memory) only where it is
 //    more than 2^8 too low.  The weights then go to tensor memory 16 keys at a time
-//    and none is held.  (Weights first, maxima only where their sum asks for them,
-//    keep 64 of them in registers past a branch: ragged prompts 46 us against 40.)
+//    and none is held.
 //  * The weights enter P V as two bf16 parts, hi + lo, which keep 2^-16 of them;
 //    their sum is taken before, in fp32.  One part would be off by up to 2^-9 of
 //    the weighted mean of |V|, far more than the rounding of an output whose terms
-//    cancel.  It would save a fourth of the time of long prompts (16 x 512 queries
-//    of 512 to 4096 keys: 343 us against 470, both measured then).
+//    cancel.  It would save a fourth of the time of long prompts.
 //  * Few rows (beams of one step): a softmax thread's way through its row of 64
 //    scores takes longer than the copies of their keys.  With 32 rows or fewer
 //    the tile holds four copies of them, each of which takes a quarter of every
 //    chunk's keys (zero weights for the others) and so a quarter of the time, and
-//    ends with a share of the row's (m, l, O); with 64, two copies.
+//    ends with a share of the row's (m, l, O); with 64, two copies.  (64 x 4 beams
+//    59.1 us and 3 x 5 beams of 8K to 64K keys 81.0, against 63.2 and 98.6 of one copy
+//    each; one short source 7.9 against 7.6.)  The longest sequence decides for its call:
+//    63 x 4 beams beside a prompt of 512 queries, all in full tiles, take 75 us, and 111 in
+//    a call for the beams and one for the prompt (61.7 and 32.8 us alone); with a
+//    prompt of 40 queries 103 and 99.
 //  * Warps whose rows are all past the tile's queries (a step of few beams) do
 //    no work but keep the barriers' counts.
+//
+// What bounds it: copies where rows are few (64 x 4 beams 0.74 of the copy rate, the long
+// sources 0.87, with the start and the joins), the softmax threads' chain where tiles are
+// full (16 x 512 prompts of 512 to 4096 keys 412 to 424 us, 378 the same call after
+// itself: 0.91 to 1.0 PFLOP/s), and for ragged prompts the ends of units (35.5 us).
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -104,7 +111,7 @@ constexpr uint32_t kTmemCols = 256;
 
 // mbar_wait_bounded, whose clock and loop stay out of the code of the waits, nearly
 // all of which end in a sleeping try: the roles' loops then fit the instruction
-// caches that they share (16 x 512 prompts 465 -> 396 us).
+// caches that they share (16 x 512 prompts 424 us, 467 with the loops in line).
 __device__ __noinline__ bool wait_long(uint64_t* bar, unsigned parity, unsigned* err) {
   return mbar_wait_bounded(bar, parity, err);
 }
@@ -362,8 +369,7 @@ __device__ void cut(const CrossParams& p, Plan* plan, Run* out, int64_t* warp_su
 // their order, whichever CTA does it.
 //
 // Full tiles: a thread a row, whose pieces of 4 dims lie beside the other rows' in the
-// workspace, and this CTA's own part still in tensor memory (16 x 512 prompts 384 ->
-// 372 us against the way of few rows).
+// workspace, and this CTA's own part still in tensor memory.
 template <int D>
 __device__ __forceinline__ float4* column_piece(const CrossParams& p, int64_t place, int piece,
                                                 int row) {

@@ -15,8 +15,10 @@
 // words that hold four tokens of a dim, so that each lane ends with runs of 8 or
 // 16 dims of four tokens and stores them in 16-byte pieces.  Neighbouring warps
 // take neighbouring heads: their rows are contiguous in a [T, Hkv, D] output.
-// 16 prefixes of 512 to 8192 tokens of a 4-bit cache (8 heads of 128): 62.7 us, 0.95
-// of the copy rate; three short ranges of an INT8 cache 4.8 us, round trips to memory.
+// 16 prefixes of 512 to 8192 tokens (8 heads of 128): a 4-bit cache 61.7 us, 0.96 of the
+// copy rate; INT8 and FP8 69, bf16 86, each some 2 us more into slots.  Three short
+// ranges of an INT8 cache 3.0 us: round trips to memory (range, block id, then tile and
+// slots together).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

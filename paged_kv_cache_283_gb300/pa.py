@@ -1261,7 +1261,8 @@ def pa_cross_attention(out, q, k_cache, v_cache, block_tables, source_lens, quer
 class CrossAttention(_FixedCall):
     """pa_cross_attention of one layer on fixed device buffers, its arguments checked
     and marshalled once.  Without a workspace it makes its own (of two such handles'
-    calls, each may then run beside the other's; one handle's may not)."""
+    calls, each may then run beside the other's; one handle's may not): 40 MB for prompts
+    of 128 dims.  The layers of one stream can share one CrossWorkspace."""
 
     def __init__(self, out, q, k_cache, v_cache, block_tables, source_lens, query_start_loc,
                  max_query_len, scale, workspace=None, stream=None):
@@ -1444,8 +1445,9 @@ def pa_beam_select(scores_out, parents_out, tokens_out, logits, scores, num_beam
     logits [searches * num_beams, vocab] bf16, fp16 or fp32 (rows strided or not);
     scores and finished (bool) hold one entry per row; outputs [searches, num_keep]:
     scores fp32, parents (rows of the beams they continue) and tokens int32,
-    finished_out bool.  in_place (num_keep = num_beams): beams that go on keep their
-    places.  workspace = beam_select_workspace(...)."""
+    finished_out bool.  Hidden tokens are -inf (a finite mask is slow, pa.h).  in_place
+    (num_keep = num_beams): beams that go on keep their places.
+    workspace = beam_select_workspace(...)."""
     args = _beam_args(scores_out, parents_out, tokens_out, logits, scores, num_beams, finished,
                       eos_token, finished_out, in_place, workspace)
     _check(lib().pa_beam_select(*args, _stream(stream)), "pa_beam_select")
