@@ -1147,6 +1147,22 @@ class PrefillStep:
             _check(st, "PrefillStep: prefill")
 
 
+class _Made:
+    """Buffers that a handle made: they are not given to others, once the handle is gone,
+    before its calls have ended on the streams that they ran on."""
+
+    def __init__(self, tensors):
+        self._tensors = tensors
+        self._used_on = set()
+
+    def use_on(self, stream):
+        at = getattr(stream, "value", stream) or 0
+        if at not in self._used_on:
+            self._used_on.add(at)
+            for t in self._tensors:
+                t.record_stream(_torch().cuda.ExternalStream(at, device=t.device))
+
+
 class _FixedCall:
     """A prepared call on fixed device buffers (`prepare`: its pa_prepare_* function
     and arguments); each call is one bare launch.  The buffers' contents may change
@@ -1161,27 +1177,17 @@ class _FixedCall:
         self._stream = None if stream is None else ctypes.c_void_p(stream.cuda_stream)
         self._keep = keep
         self._ready = None
-        self._made = list(made)
-        self._used_on = set()
-        if self._made and not torch.cuda.is_current_stream_capturing():
+        self._made = _Made(list(made)) if made else None
+        if made and not torch.cuda.is_current_stream_capturing():
             self._ready = torch.cuda.current_stream().record_event()
-
-    def _hold_made(self, stream):
-        """The buffers made here are not given to others, once the handle is gone, before
-        the calls on `stream` have ended."""
-        at = getattr(stream, "value", stream) or 0
-        if at not in self._used_on:
-            self._used_on.add(at)
-            for t in self._made:
-                t.record_stream(_torch().cuda.ExternalStream(at, device=t.device))
 
     def __call__(self, stream=None):
         s = self._stream if stream is None and self._stream is not None else _stream(stream)
         if self._ready is not None:
             _check(lib().pa_await_event(self._ready.cuda_event, s), self._what)
             self._ready = None
-        if self._made:
-            self._hold_made(s)
+        if self._made is not None:
+            self._made.use_on(s)
         st = self._call.run(s)
         if st != PA_OK:
             _check(st, self._what)
@@ -1569,6 +1575,7 @@ class DecodeStep:
         torch = _torch()
         self.fused = bool(fused)
         self._ready = None  # the event behind the counters and workspace made here
+        own = []            # buffers made here
         four = k_cache.dtype == torch.uint8 and k_cache.dim() == 3
         block = 16 if four else k_cache.shape[2]
         if not self.fused and (four or softcap or alibi_slopes is not None or window):
@@ -1608,6 +1615,7 @@ class DecodeStep:
                 partition_size = plan.partition_size
                 if order is None and plan.order is not None:
                     order = torch.from_numpy(plan.order).to(q.device)
+                    own.append(order)
             elif partition_size is None:
                 partition_size = 512
             self.partition_size = partition_size
@@ -1618,8 +1626,10 @@ class DecodeStep:
                     if window:
                         mc = min(mc, cover)
                     workspace = splitk_workspace(B, hq, d, mc, partition_size, q.device)
+                    own += workspace
                 if counters is None:
                     counters = step_counters(B, hkv, q.device)
+                    own.append(counters)
                 if made and not torch.cuda.is_current_stream_capturing():
                     # the first call may go to another stream, or into a graph that
                     # is replayed on one: it awaits what was enqueued here
@@ -1632,6 +1642,7 @@ class DecodeStep:
             self._keep = [key, value, k_cache, v_cache, slot_mapping, q, block_tables,
                           context_lens, out, workspace, counters, k_scales, v_scales, order,
                           alibi_slopes]
+            self._made = _Made(own) if own else None
             self._call = None
             if four or softcap or alibi_slopes is not None or window:
                 # out q key value slots | pools | tables .. scale | rule | the rest
@@ -1676,6 +1687,7 @@ class DecodeStep:
             if workspace is None:
                 mc = int(max_context_len) if max_context_len is not None else mb * bs
                 workspace = splitk_workspace(B, hq, d, mc, partition_size, q.device)
+                own += workspace
             ws_o, ws_m, ws_l = workspace
             maxp = ws_m.shape[2]
             if ws_o.shape != (B, hq, maxp, d) or ws_l.shape != ws_m.shape:
@@ -1690,6 +1702,7 @@ class DecodeStep:
             self._rd = (po, wo, wm, wl, maxp, pc, B, hq, d, int(partition_size))
         else:
             self._dc = (po, pq) + kvp + (pt, mb, pc, B, hq, hkv, d, bs, nb, float(scale))
+        self._made = _Made(own) if own else None
         L = lib()
         if self.fp8:
             self._f_write, self._f_split, self._f_whole = (
@@ -1716,6 +1729,8 @@ class DecodeStep:
 
     def __call__(self, stream=None):
         s = self._stream if stream is None and self._stream is not None else _stream(stream)
+        if self._made is not None:
+            self._made.use_on(s)
         if self.fused:
             if self._ready is not None:
                 self._await_made(s)

@@ -71,3 +71,40 @@ def test_selection_on_another_stream():
     s.check([x.cpu().numpy() for x in out] + [None])
     assert all(bool((t == 123).all()) for t in held) and busy is not None
     assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fused", [True, False])
+def test_decode_step_on_another_stream(fused):
+    pa.pa_clear_device_error()
+    g = torch.Generator(device="cuda").manual_seed(33)
+    b, hq, hkv, d, mb = 6, 8, 2, 128, 40
+    kc, vc = (torch.randn((b * mb, hkv, 16, d), generator=g, device="cuda").bfloat16()
+              for _ in "kv")
+    tables = torch.randperm(b * mb, generator=g, device="cuda").to(torch.int32).view(b, mb)
+    lens = torch.tensor([600, 1, 64, 333, 16, 510], dtype=torch.int32, device="cuda")
+    q = torch.randn((b, hq, d), generator=g, device="cuda").bfloat16()
+    key, value = (torch.randn((b, hkv, d), generator=g, device="cuda").bfloat16() for _ in "kv")
+    at = (lens - 1).long()
+    slots = tables[torch.arange(b, device="cuda"), at // 16].long() * 16 + at % 16
+    outs = []
+    for drop in (False, True):
+        out = torch.full_like(q, float("nan"))
+        k, v = kc.clone(), vc.clone()
+        side = torch.cuda.Stream()
+        busy = _kept_busy(side)
+        step = pa.DecodeStep(key, value, k, v, slots, q, tables, lens, out, d ** -0.5,
+                             partition_size=64, fused=fused)
+        if not drop:
+            torch.cuda.synchronize()
+        step(stream=side)
+        shapes = [(t.shape, t.dtype) for t in step.workspace]
+        if fused:
+            shapes.append((step.counters.shape, step.counters.dtype))
+        if drop:
+            del step
+        held = _dirty(shapes)
+        torch.cuda.synchronize()
+        assert all(bool((t == 123).all()) for t in held) and busy is not None
+        outs.append(out)
+    assert torch.isfinite(outs[0]).all() and torch.equal(*outs)
+    assert pa.pa_get_device_error() == 0

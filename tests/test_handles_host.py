@@ -82,3 +82,43 @@ def test_own_buffers_are_held_for_the_streams_that_used_them(monkeypatch, prepar
     call._fix("a call", "pa_prepare_beam_select", (), one, [object()])
     call()
     assert len(told) == 3
+
+
+@pytest.mark.parametrize("fused", [True, False])
+def test_a_decode_step_holds_its_own_buffers_too(monkeypatch, fused):
+    told = []
+
+    class Made:
+        device, shape = "cuda:0", (2, 4, 1, 64)
+
+        def record_stream(self, stream):
+            told.append((self, stream))
+
+    made = [Made() for _ in range(4)]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda at, device: at)
+    monkeypatch.setattr(pa, "splitk_workspace", lambda *a: tuple(made[:3]))
+    monkeypatch.setattr(pa, "step_counters", lambda *a: made[3])
+    monkeypatch.setattr(pa, "_step_args", lambda *a: (lambda *b: pa.PA_OK, ()))
+    monkeypatch.setattr(pa, "_dev", lambda *a: None)
+    q, kv = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 16, 64).bfloat16()
+    new = torch.zeros(2, 2, 64).bfloat16()
+    ints = torch.zeros(2, 1, dtype=torch.int32)
+
+    def step(**kw):
+        return pa.DecodeStep(new, new, kv, kv, ints[:, 0].long(), q, ints, ints[:, 0], q, 0.1,
+                             stream=SimpleNamespace(cuda_stream=77), fused=fused, **kw)
+
+    # (a step of separate launches calls these)
+    monkeypatch.setattr(pa, "_lib", SimpleNamespace(**{
+        f: lambda *a: pa.PA_OK for f in ("pa_reshape_and_cache", "pa_decode_splitk", "pa_decode",
+                                         "pa_splitk_reduce")}))
+    call = step()
+    call()
+    call()
+    call(stream=SimpleNamespace(cuda_stream=78))
+    of = made if fused else made[:3]
+    assert told == [(t, at) for at in (77, 78) for t in of]
+    # the caller's are the caller's
+    step(workspace=tuple(made[:3]), counters=made[3])()
+    assert len(told) == 2 * len(of)
