@@ -1,5 +1,4 @@
 """Handles that are gone before their calls have run."""
-import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")

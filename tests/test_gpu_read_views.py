@@ -1,5 +1,4 @@
 """Reading a cache back into views of one tensor."""
-import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
